@@ -15,6 +15,8 @@ Modules (each cites the passages it follows):
   step       the three composed
   draft      the draft side: draft-token draw (Philox stream 1) and one draft
              position (single-row attention, append, draw)
+  rope       rotary positions of block rows, E4M3 rounding
+  logits     penalties, biases and grammar masks on logits rows; the token table
 """
 from .philox import philox4x32, verify_uniforms, word_to_uniform
 from .sampling import (process_row, accept, residual, sample_index, verify_sequence,
@@ -25,3 +27,5 @@ from .attention import attention_row, verify_attention
 from .append import kv_append
 from .step import verify_step
 from .draft import draft_sample, draft_step
+from .rope import (rope_frequencies, rope_rows, row_positions, e4m3_nearest)
+from .logits import (count_tokens, seen_bits, adjust_logits, adjust_row, allowed_tokens)

@@ -15,6 +15,9 @@ SV_OK, SV_ERR_INVALID, SV_ERR_WORKSPACE, SV_ERR_CUDA, SV_ERR_UNSUPPORTED = range
 SV_F32, SV_BF16, SV_E4M3 = 0, 1, 2
 DEV_CAPACITY, DEV_BAD_TOKEN, DEV_NONFINITE, DEV_EMPTY_RESIDUAL, DEV_BAD_LENGTH = 1, 2, 4, 8, 16
 DEV_TIMEOUT, DEV_BAD_PARAM = 32, 64
+ROPE_HALF, ROPE_INTERLEAVED = 0, 1
+ROPE_PLAIN, ROPE_LINEAR, ROPE_NTK, ROPE_YARN, ROPE_BANDED = range(5)
+COUNT_PROMPT, COUNT_RESET = 1, 2
 
 _p = ctypes.c_void_p
 
@@ -59,6 +62,57 @@ class DraftArgs(ctypes.Structure):
     ]
 
 
+class RopeArgs(ctypes.Structure):
+    """Mirror of sv_rope_args."""
+    _fields_ = [
+        ("batch", ctypes.c_int32), ("num_q_heads", ctypes.c_int32),
+        ("num_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+        ("rot_dim", ctypes.c_int32), ("layout", ctypes.c_int32), ("dtype", ctypes.c_int32),
+        ("kv_dtype", ctypes.c_int32), ("num_rows", ctypes.c_int64),
+        ("max_q_rows", ctypes.c_int32), ("mscale", ctypes.c_float), ("k_scale", ctypes.c_float),
+        ("v_scale", ctypes.c_float), ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64),
+        ("v_stride", ctypes.c_int64), ("turns", _p), ("cu_q", _p), ("kv_len", _p),
+        ("positions", _p), ("q", _p), ("k", _p), ("v", _p), ("q_out", _p), ("k_out", _p),
+        ("v_out", _p), ("dev_status", _p),
+    ]
+
+
+class RopeScaling(ctypes.Structure):
+    """Mirror of sv_rope_scaling."""
+    _fields_ = [
+        ("kind", ctypes.c_int32), ("trained_len", ctypes.c_int32), ("base", ctypes.c_double),
+        ("factor", ctypes.c_double), ("beta_fast", ctypes.c_double),
+        ("beta_slow", ctypes.c_double), ("low_freq", ctypes.c_double),
+        ("high_freq", ctypes.c_double),
+    ]
+
+
+class CountArgs(ctypes.Structure):
+    """Mirror of sv_count_args."""
+    _fields_ = [
+        ("batch", ctypes.c_int32), ("vocab", ctypes.c_int32), ("num_slots", ctypes.c_int32),
+        ("flags", ctypes.c_int32), ("num_tokens", ctypes.c_int64), ("start", _p), ("tokens", _p),
+        ("num_accepted", _p), ("slots", _p), ("counts", _p), ("seen", _p), ("dev_status", _p),
+    ]
+
+
+class AdjustArgs(ctypes.Structure):
+    """Mirror of sv_adjust_args."""
+    _fields_ = [
+        ("batch", ctypes.c_int32), ("vocab", ctypes.c_int32), ("dtype", ctypes.c_int32),
+        ("max_q_rows", ctypes.c_int32), ("num_rows", ctypes.c_int64), ("cu_q", _p),
+        ("target", _p), ("target_out", _p), ("draft", _p), ("draft_out", _p),
+        ("draft_tokens", _p), ("counts", _p), ("seen", _p), ("num_slots", ctypes.c_int32),
+        ("num_ctx", ctypes.c_int32), ("slots", _p), ("ctx_tokens", _p),
+        ("ctx_stride", ctypes.c_int64), ("repetition", ctypes.c_float),
+        ("presence", ctypes.c_float), ("frequency", ctypes.c_float),
+        ("num_masks", ctypes.c_int32), ("repetitions", _p), ("presences", _p),
+        ("frequencies", _p), ("bias_start", _p), ("bias_tokens", _p), ("bias_values", _p),
+        ("num_bias", ctypes.c_int64), ("mask", _p), ("mask_stride", ctypes.c_int64),
+        ("mask_rows", _p), ("dev_status", _p),
+    ]
+
+
 def _load():
     if not os.path.exists(LIB_PATH):
         raise ImportError(
@@ -93,6 +147,19 @@ def _load():
     lib.kv_append_ragged.restype = ctypes.c_int
     lib.spec_verify_step.argtypes = [P(AttnArgs), P(SampleArgs), _p, _p, _p, ctypes.c_size_t, _p]
     lib.spec_verify_step.restype = ctypes.c_int
+    lib.spec_rope_rows.argtypes = [P(RopeArgs), _p]
+    lib.spec_rope_rows.restype = ctypes.c_int
+    lib.sv_rope_turns.argtypes = [P(RopeScaling), ctypes.c_int32, P(ctypes.c_uint64),
+                                  P(ctypes.c_float)]
+    lib.sv_rope_turns.restype = ctypes.c_int
+    lib.spec_count_tokens.argtypes = [P(CountArgs), _p]
+    lib.spec_count_tokens.restype = ctypes.c_int
+    lib.spec_adjust_logits.argtypes = [P(AdjustArgs), _p]
+    lib.spec_adjust_logits.restype = ctypes.c_int
+    lib.sv_ops_version.argtypes = []
+    lib.sv_ops_version.restype = ctypes.c_int32
+    lib.sv_ops_struct_size.argtypes = [ctypes.c_int32]
+    lib.sv_ops_struct_size.restype = ctypes.c_size_t
     lib.sv_last_error.argtypes = []
     lib.sv_last_error.restype = ctypes.c_char_p
     lib.sv_abi_version.argtypes = []
@@ -103,6 +170,9 @@ def _load():
             lib.sv_struct_size(1) != ctypes.sizeof(SampleArgs) or \
             lib.sv_struct_size(2) != ctypes.sizeof(DraftArgs):
         raise ImportError("libspecverify.so struct layout does not match this binding")
+    if any(lib.sv_ops_struct_size(i) != ctypes.sizeof(c)
+           for i, c in enumerate((RopeArgs, RopeScaling, CountArgs, AdjustArgs))):
+        raise ImportError("libspecverify.so operator structs do not match this binding")
     return lib
 
 

@@ -55,7 +55,7 @@ def build(verbose=False, extra_flags=()):
             os.remove(LIB)
         with open(stamp, "w") as fh:
             fh.write(host)
-    headers = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cuh", ".h"))]
+    headers = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cuh", ".h", ".inl"))]
     headers += [os.path.join(INCLUDE, f) for f in os.listdir(INCLUDE)]
     objs, jobs = [], []
     for src in sources():

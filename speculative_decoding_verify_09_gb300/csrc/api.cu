@@ -12,6 +12,7 @@
 #include <cuda.h>
 
 #include "kernels.h"
+#include "ops_host.inl"
 
 namespace {
 
@@ -331,6 +332,25 @@ sv::SamplerLaunch sampler_launch(const sv_sample_args *sample, const Layout &L, 
 }
 
 }  // namespace
+
+namespace sv {
+
+sv_status record_error(sv_status st, const char *fmt, ...) {
+  char buf[512];
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(buf, sizeof(buf), fmt, ap);
+  va_end(ap);
+  try {
+    g_err = buf;
+  } catch (...) {      // out of memory: the status alone is returned
+  }
+  return st;
+}
+
+int device_sms() { return num_sms_current(); }
+
+}  // namespace sv
 
 // Scratch of spec_verify_attn_static: a fixed array in the library's own device
 // image instead of a caller workspace.  It exists for callers that may not
