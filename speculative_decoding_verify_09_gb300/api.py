@@ -267,16 +267,27 @@ def _rows_stride(t, name):
     return t.stride(0)
 
 
-def _ops_stream(args, stream):
-    """The stream to launch on: of the device that holds the tensors, which has to be the
-    current one."""
-    s = stream if stream is not None else torch.cuda.current_stream()
-    if args._device is not None and (
-            s.device_index != args._device or
-            (stream is not None and torch.cuda.current_device() != args._device)):
-        raise ValueError(f"tensors are on cuda:{args._device}, the call on cuda:{s.device_index} "
-                         f"with current device cuda:{torch.cuda.current_device()}")
-    return ctypes.c_void_p(s.cuda_stream)
+def _launch(fn, args, stream):
+    """Calls fn on `stream` or the current one; the tensors' device has to be the current one.
+    (The raw stream: a torch.cuda.Stream object costs more than the launch.)"""
+    device = args._device
+    if torch._C._cuda_getDevice() != device:
+        raise ValueError(f"tensors are on cuda:{device}, not on the current device")
+    if stream is None:
+        raw = torch._C._cuda_getCurrentRawStream(device)
+    elif stream.device_index != device:
+        raise ValueError(f"tensors are on cuda:{device}, the stream on cuda:{stream.device_index}")
+    else:
+        raw = stream.cuda_stream
+    st = fn(ctypes.byref(args), raw)
+    if st:
+        _check(st)
+
+
+def _finish(a, c):
+    """Keeps the tensors of an argument struct alive with it."""
+    a._keep, a._device = c.keep, c.device.index
+    return a
 
 
 def rope_turns(rot_dim, *, base=10000.0, scaling="plain", factor=1.0, trained_len=1,
@@ -352,13 +363,12 @@ def rope_args(q, k, v, q_out, k_out, v_out, turns, *, cu_q=None, kv_len=None, po
         a.cu_q = c.add(cu_q, "cu_q", torch.int32)
         a.kv_len = c.add(kv_len, "kv_len", torch.int32, shape=(a.batch,))
     a.dev_status = c.add(dev_status, "dev_status", _WORDS, at_least=1)
-    a._keep, a._device = c.keep, c.device.index
-    return a
+    return _finish(a, c)
 
 
 def spec_rope_rows(rope, stream=None):
     """Rotates q and k (and turns k and v into cache codes) of every row."""
-    _check(lib.spec_rope_rows(ctypes.byref(rope), _ops_stream(rope, stream)))
+    _launch(lib.spec_rope_rows, rope, stream)
 
 
 class TokenCounts:
@@ -392,13 +402,12 @@ def count_args(counts, seen, tokens, start, *, num_accepted=None, slots=None, pr
     a.num_accepted = c.add(num_accepted, "num_accepted", torch.int32, shape=(B,))
     a.slots = c.add(slots, "slots", torch.int32, shape=(B,))
     a.dev_status = c.add(dev_status, "dev_status", _WORDS, at_least=1)
-    a._keep, a._device = c.keep, c.device.index
-    return a
+    return _finish(a, c)
 
 
 def spec_count_tokens(count, stream=None):
     """Adds a batch's tokens to the table."""
-    _check(lib.spec_count_tokens(ctypes.byref(count), _ops_stream(count, stream)))
+    _launch(lib.spec_count_tokens, count, stream)
 
 
 def adjust_args(target, target_out, cu_q, *, max_q_rows, draft=None, draft_out=None,
@@ -463,10 +472,9 @@ def adjust_args(target, target_out, cu_q, *, max_q_rows, draft=None, draft_out=N
         a.mask = c.add(mask, "mask", _WORDS)
         a.mask_rows = c.add(mask_rows, "mask_rows", torch.int32, shape=(R,))
     a.dev_status = c.add(dev_status, "dev_status", _WORDS, at_least=1)
-    a._keep, a._device = c.keep, c.device.index
-    return a
+    return _finish(a, c)
 
 
 def spec_adjust_logits(adjust, stream=None):
     """Penalties, biases and grammar masks on the target (and draft) rows."""
-    _check(lib.spec_adjust_logits(ctypes.byref(adjust), _ops_stream(adjust, stream)))
+    _launch(lib.spec_adjust_logits, adjust, stream)
