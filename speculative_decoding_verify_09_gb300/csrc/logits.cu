@@ -6,16 +6,16 @@
 // and written once, 2 V elements per row) is what the time goes into; the
 // exceptions are few: the tokens of the history, the biased ones and the
 // block's drafts, a few thousand of V per sequence, but spread so that most
-// warps of a row would meet one.  So they are kept out of the copy: a CTA
-// takes a share of the vocabulary for one sequence, copies its part of the
-// rows with the masks alone, lists the share's exceptions once (the table's
-// bits say where they are, so its counts are read only there), and then works
-// the list off for all rows.  In place the copy falls away and only masked
-// rows and listed tokens are touched.
-//
-// A CTA's share is 8 tiles of 256 tokens (one per warp) that lie gridDim.x
-// tiles apart, not one run: tokens of small index are the frequent ones, and a
-// run of them would give one CTA a list of thousands.
+// 512-byte pieces of a row hold one.  What has to stay small is the number of
+// instructions per byte.  A CTA takes a chunk of the vocabulary (4 KB of a row)
+// for one sequence and lists the chunk's exceptions once: the table's bits say
+// where they are, so its counts are read only there.  From then on every warp
+// works alone, a row's chunk at a time: 16-byte cp.async copies into a ring of
+// shared memory (kRing rows deep), the listed tokens changed there, a lane per
+// token, and the chunk written out.  In place nothing streams: masked rows are
+// written where a token is barred, and the listed tokens of every row are
+// changed in global memory.
+#include <atomic>
 #include <cmath>
 
 #include "common.cuh"
@@ -26,12 +26,12 @@ namespace sv {
 
 namespace {
 
-constexpr int kNT = 256;
-constexpr int kWarps = kNT / 32;
-constexpr int kTile = 256;                 // tokens of one warp
-constexpr int kTileWords = kTile / 32;
-constexpr int kShare = kWarps * kTile;     // tokens of one CTA
-constexpr int kBatch = 4;                  // rows whose vectors are in flight together
+constexpr int kNT = 256;                   // threads of the table's kernels
+constexpr int kWarps = 4;                  // of an adjusting CTA
+constexpr int kThreads = kWarps * 32;
+constexpr int kChunkBytes = 4096;          // of a row, per CTA
+constexpr int kRing = 2;                   // row chunks in flight per warp
+constexpr int kBatch = 4;                  // (in place) rows in flight per warp
 
 // ---------------------------------------------------------------- adjust
 template <typename T>
@@ -56,61 +56,74 @@ struct AdjustParams {
   int seen_words;
 };
 
-// n rows of a sequence, V elements apart: block rows j0 .. of the target's
-// logits or of the draft's.
-template <typename T>
-struct Rows {
-  const T *in;
-  T *out;
-  int n, j0;
-  uint32_t index;                // of the first row in its tensor (its alignment)
-};
-
-// The kPer bits of tokens t .. of a mask row (token u at bit u % 8 of byte u / 8).
+// The kPer bits from bit b of mask bytes on; bytes: how many there are.
 template <int kPer>
-__device__ __forceinline__ uint32_t mask_bits(const uint8_t *m, int t, int64_t mask_bytes) {
-  const int64_t b = t >> 3;
-  uint32_t w = m[b];
-  if ((t & 7) + kPer > 8 && b + 1 < mask_bytes) w |= static_cast<uint32_t>(m[b + 1]) << 8;
-  return (w >> (t & 7)) & ((1u << kPer) - 1);
+__device__ __forceinline__ uint32_t mask_bits(const uint8_t *m, int b, int64_t bytes) {
+  uint32_t w = m[b >> 3];
+  if ((b & 7) + kPer > 8 && (b >> 3) + 1 < bytes) w |= static_cast<uint32_t>(m[(b >> 3) + 1]) << 8;
+  return (w >> (b & 7)) & ((1u << kPer) - 1);
 }
 
-// One vector of a row: from its mask's bits to its new value.
+// One vector of a row; the tokens whose bit is 0 are barred.
 template <typename T, int kPer>
-struct Piece {
-  union { uint4 w; T e[kPer]; };
-  uint32_t allow;                // all bits: as it is
-  __device__ __forceinline__ void bar() {
-    if (allow == (1u << kPer) - 1) return;
+union Piece {
+  uint4 w;
+  T e[kPer];
+  __device__ __forceinline__ void bar(uint32_t allow) {
 #pragma unroll
     for (int k = 0; k < kPer; ++k)
       if (!((allow >> k) & 1u)) e[k] = Elem<T>::kNegInf;
   }
 };
 
-// RAGGED: V is no multiple of a 16-byte vector's elements, so rows differ in
-// alignment: a tile's vectors start at each row's first aligned token, and the
-// up to kPer - 1 tokens at either end go one by one.
+// A row that the CTA works on, at the chunk's first token.
+template <typename T>
+struct alignas(16) Line {
+  const T *in;
+  T *out;
+  const uint8_t *mask;           // the row's mask from the chunk's first token on, or null
+  int j, mis;                    // block row; elements from the 16-byte boundary before it
+};
+
+template <typename T>
+struct Chunk {
+  static constexpr int kPer = 16 / static_cast<int>(sizeof(T));       // elements of a vector
+  static constexpr int kTokens = kChunkBytes / static_cast<int>(sizeof(T));
+  static constexpr int kWords = kTokens / 32;
+  static constexpr int kVecs = kChunkBytes / 16 / 32;                 // vectors per lane
+  static constexpr int kMaskAt = kChunkBytes + 16;                    // (a misaligned row's last vector)
+  static constexpr int kSlot = kMaskAt + kWords * 4;                  // a row in the ring, its mask
+  static_assert(kSlot % 16 == 0, "vectors of every slot are 16-byte aligned");
+};
+
+constexpr uint16_t kOutside = 0x8000u, kBiased = 0x4000u;   // flags of a listed token: counted
+                                                            // outside the table, has a bias
+
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void *src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;\n" ::"r"(dst), "l"(src) : "memory");
+}
+
+// RAGGED: V is no multiple of a vector's elements, so rows differ in alignment.
 template <typename T, bool IN_PLACE, bool RAGGED>
-__global__ void __launch_bounds__(kNT, 4) adjust_kernel(const __grid_constant__ AdjustParams P) {
+__global__ void __launch_bounds__(kThreads) adjust_kernel(const __grid_constant__ AdjustParams P) {
   using E = Elem<T>;
-  constexpr int kPer = 16 / static_cast<int>(sizeof(T));     // elements of a vector
-  constexpr int kVecs = kTile / kPer / 32;                   // vectors per lane and row
+  using C = Chunk<T>;
+  constexpr int kPer = C::kPer;
   constexpr uint32_t kAll = (1u << kPer) - 1;
   const sv_adjust_args &a = P.a;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, i = blockIdx.y;
-  const int V = a.vocab, shares = gridDim.x;
-  const int t0 = (blockIdx.x + warp * shares) * kTile, t1 = min(V, t0 + kTile);   // t1 <= t0: none
+  const int V = a.vocab, t0 = blockIdx.x * C::kTokens, width = min(V - t0, C::kTokens);
   const bool head = blockIdx.x == 0 && blockIdx.z == 0;      // this CTA reports the sequence
 
-  __shared__ uint32_t s_extra[kShare / 32];                  // ctx, draft and bias tokens
-  __shared__ int32_t s_mask[16];                             // mask rows of the block rows
-  __shared__ int s_n, s_masked;
-  __shared__ uint32_t s_tok[kShare];                         // listed token, and above it bit b:
-                                                             // draft b + 1 is this token
-  __shared__ uint32_t s_word[kShare];                        // its table word, with ctx
-  __shared__ float s_bias[kShare];
-  __shared__ __align__(16) int32_t s_last[kShare];           // 1 + last bias entry of a token
+  extern __shared__ __align__(16) unsigned char s_ring[];    // (out of place) kWarps x kRing slots
+  __shared__ Line<T> s_line[32];                             // target rows, then draft rows
+  __shared__ uint32_t s_extra[C::kWords];                    // bits of ctx, draft and bias tokens
+  __shared__ __align__(16) int32_t s_last[C::kTokens];       // 1 + last bias entry of a token; then
+                                                             // its bias, as bits
+  __shared__ uint32_t s_word[C::kTokens];                    // table words of the list, with ctx
+  __shared__ uint16_t s_tok[C::kTokens];                     // the list: tokens in the chunk, flags
+  __shared__ int32_t s_draft[16];                            // the block's drafts in the chunk
+  __shared__ int s_n;
 
   const int r0 = a.cu_q[i], Ri = a.cu_q[i + 1] - r0;
   if (r0 < i || Ri < 1 || Ri > a.max_q_rows || r0 + Ri > a.num_rows ||
@@ -118,21 +131,9 @@ __global__ void __launch_bounds__(kNT, 4) adjust_kernel(const __grid_constant__ 
     if (head && tid == 0) set_status(a.dev_status, SV_DEV_BAD_LENGTH);
     return;
   }
-  const int lines = Ri + (a.draft != nullptr ? Ri - 1 : 0);  // target rows, then draft rows
-  const int l0 = blockIdx.z * P.lines_per_part, l1 = min(lines, l0 + P.lines_per_part);
-  if (l0 >= l1) return;
-  auto rows_of = [&](const void *in, void *out, int first, int last, int row0) {
-    Rows<T> R;
-    R.j0 = first;
-    R.n = max(last - first, 0);
-    R.index = static_cast<uint32_t>(row0 + first);
-    const int64_t off = static_cast<int64_t>(row0 + first) * V;
-    R.in = static_cast<const T *>(in) + off;
-    R.out = static_cast<T *>(out) + off;
-    return R;
-  };
-  const Rows<T> parts[2] = {rows_of(a.target, a.target_out, min(l0, Ri), min(l1, Ri), r0),
-                            rows_of(a.draft, a.draft_out, max(l0 - Ri, 0), max(l1 - Ri, 0), r0 - i)};
+  const int all = Ri + (a.draft != nullptr ? Ri - 1 : 0);
+  const int l0 = blockIdx.z * P.lines_per_part, lines = min(all - l0, P.lines_per_part);
+  if (lines <= 0) return;
 
   // the sequence's values
   const float rep = a.repetitions ? a.repetitions[i] : a.repetition;
@@ -146,234 +147,239 @@ __global__ void __launch_bounds__(kNT, 4) adjust_kernel(const __grid_constant__ 
   }
   int bad = !(rep > 0.0f) || !isfinite(rep) || !isfinite(pres) || !isfinite(freq) || slot < -1 ||
             slot >= max(a.num_slots, 0) || b0 < 0 || b1 < b0 || b1 > a.num_bias;
-  if (warp == 0) {
-    int m = -1;
-    if (a.mask && lane < Ri) {
-      m = a.mask_rows ? a.mask_rows[r0 + lane] : r0 + lane;
-      bad |= m < -1 || m >= a.num_masks;
-    }
-    if (lane < 16) s_mask[lane] = m;
-    const uint32_t masked = __ballot_sync(0xffffffffu, m >= 0);
-    if (lane == 0) {
-      s_masked = static_cast<int>(masked);
-      s_n = 0;
-    }
-  }
-  if (tid < kShare / 32) s_extra[tid] = 0;
   const int nb = b1 - b0;
+  if (tid < Ri && a.mask) {                                  // every row's, for one verdict
+    const int m = a.mask_rows ? a.mask_rows[r0 + tid] : r0 + tid;
+    bad |= m < -1 || m >= a.num_masks;
+  }
+  if (tid < lines) {
+    const int l = l0 + tid;
+    Line<T> L;
+    L.j = l < Ri ? l : l - Ri;
+    const int64_t row = l < Ri ? r0 + l : r0 - i + L.j;
+    L.in = static_cast<const T *>(l < Ri ? a.target : a.draft) + row * V + t0;
+    L.out = static_cast<T *>(l < Ri ? a.target_out : a.draft_out) + row * V + t0;
+    L.mis = RAGGED ? static_cast<int>((static_cast<uint32_t>(row) * static_cast<uint32_t>(V)) & (kPer - 1)) : 0;
+    L.mask = nullptr;
+    if (a.mask) {
+      const int m = a.mask_rows ? a.mask_rows[r0 + L.j] : r0 + L.j;
+      if (m >= 0) L.mask = reinterpret_cast<const uint8_t *>(a.mask) + m * P.mask_bytes + (t0 >> 3);
+    }
+    s_line[tid] = L;
+  }
+  if (tid < C::kWords) s_extra[tid] = 0;
+  if (tid == 0) s_n = 0;
   if (nb > 0)
-    for (int t = tid; t < kShare / 4; t += kNT)
+    for (int t = tid; t < C::kTokens / 4; t += kThreads)
       reinterpret_cast<int4 *>(s_last)[t] = make_int4(0, 0, 0, 0);
   bad = __syncthreads_or(bad);
 
   if (bad) {                      // rows the sampler fails the sequence on
     if (head && tid == 0) set_status(a.dev_status, SV_DEV_BAD_PARAM);
-    for (const Rows<T> &R : parts)
-      for (int r = 0; r < R.n; ++r)
-        for (int t = t0 + lane; t < t1; t += 32) R.out[static_cast<int64_t>(r) * V + t] = E::put(NAN);
+    for (int l = warp; l < lines; l += kWarps)
+      for (int t = lane; t < width; t += 32) s_line[l].out[t] = E::put(NAN);
     return;
   }
 
+  // Row chunk `line` into its slot of this warp's ring: 16-byte vectors from
+  // the boundary at or before the chunk's first token up to its last one, and
+  // the chunk's mask words.
+  unsigned char *my_ring = s_ring + warp * (kRing * C::kSlot);
+  auto issue = [&](int line, int s) {
+    if (line < lines) {
+      const Line<T> L = s_line[line];
+      const uint32_t dst = smem_u32(my_ring + s * C::kSlot) + lane * 16;
+      const T *src = L.in - L.mis + lane * kPer;
+      const int left = width + L.mis - lane * kPer;          // elements from this lane's first on
+#pragma unroll
+      for (int q = 0; q < C::kVecs; ++q)
+        if (left > q * 32 * kPer)
+          cp_async16(dst + q * 512, src + q * 32 * kPer,
+                     min(16, (left - q * 32 * kPer) * static_cast<int>(sizeof(T))));
+      if (RAGGED && lane == 0 && left > C::kTokens)
+        cp_async16(dst + kChunkBytes, src + C::kTokens, (left - C::kTokens) * static_cast<int>(sizeof(T)));
+      if (L.mask)
+        for (int w = lane; w * 32 < width; w += 32)
+          cp_async4(smem_u32(my_ring + s * C::kSlot + C::kMaskAt) + w * 4, L.mask + w * 4);
+    }
+    cp_async_commit();
+  };
+  if constexpr (!IN_PLACE)
+    for (int s = 0; s < kRing; ++s) issue(warp + s * kWarps, s);
+
   const bool penal = rep != 1.0f || pres != 0.0f || freq != 0.0f;
   const int drafts = penal && a.draft_tokens ? Ri - 1 : 0;
-  const int32_t *draft_tokens = a.draft_tokens + (r0 - i);
+  const int ctx = penal ? a.num_ctx : 0;
   const int64_t ctx_stride = a.ctx_stride ? a.ctx_stride : a.batch;
 
-  // the table's bits of this warp's tile: word q in lane q
+  // the table's bits of the chunk: a word per thread
   uint32_t known = 0;
-  if (penal && slot >= 0 && lane < kTileWords && t0 + lane * 32 < t1)
-    known = a.seen[static_cast<int64_t>(slot) * P.seen_words + (t0 >> 5) + lane];
+  if (penal && slot >= 0 && tid < C::kWords && tid * 32 < width)
+    known = a.seen[static_cast<int64_t>(slot) * P.seen_words + (t0 >> 5) + tid];
+  static_assert(C::kWords <= kThreads, "a word per thread");
 
-  // tokens outside the table: index in the share, or -1
-  auto local_of = [&](int t) {
-    if (t < 0 || t >= V) return -1;
-    const int tile = t / kTile, w = tile / shares;
-    return tile - w * shares == static_cast<int>(blockIdx.x) ? w * kTile + t % kTile : -1;
-  };
-  auto mark = [&](int local) { atomicOr(&s_extra[local >> 5], 1u << (local & 31)); };
+  // tokens outside the table
+  auto mark = [&](int t) { atomicOr(&s_extra[t >> 5], 1u << (t & 31)); };
+  auto in_chunk = [&](int token) { return token >= t0 && token - t0 < width; };
   if (tid < drafts) {
-    const int local = local_of(draft_tokens[tid]);
-    if (local >= 0) mark(local);
+    const int t = a.draft_tokens[r0 - i + tid];
+    s_draft[tid] = in_chunk(t) ? t - t0 : -1;
+    if (in_chunk(t)) mark(t - t0);
   }
-  if (penal)
-    for (int c = tid; c < a.num_ctx; c += kNT) {
-      const int local = local_of(a.ctx_tokens[c * ctx_stride + i]);
-      if (local >= 0) mark(local);
-    }
-  for (int e = tid; e < nb; e += kNT) {
-    const int t = a.bias_tokens[b0 + e], local = local_of(t);
-    if (local >= 0) {
-      mark(local);
-      atomicMax(&s_last[local], e + 1);
+  for (int c = tid; c < ctx; c += kThreads) {
+    const int t = a.ctx_tokens[c * ctx_stride + i];
+    if (in_chunk(t)) mark(t - t0);
+  }
+  for (int e = tid; e < nb; e += kThreads) {
+    const int t = a.bias_tokens[b0 + e];
+    if (in_chunk(t)) {
+      mark(t - t0);
+      atomicMax(&s_last[t - t0], e + 1);
     } else if (head && (t < 0 || t >= V)) {
       set_status(a.dev_status, SV_DEV_BAD_TOKEN);
     }
   }
+  __syncthreads();
 
-  // the copy of up to kBatch rows, loads before stores; row r of R, its mask m
-  const uint8_t *masks = reinterpret_cast<const uint8_t *>(a.mask);
-  const uint32_t masked = static_cast<uint32_t>(s_masked);
-  auto copy = [&](const Rows<T> &R, const int (&row)[kBatch], int n) {
-    Piece<T, kPer> x[kBatch][kVecs];
-    T edge[kBatch];
-    int edge_at[kBatch];
-#pragma unroll
-    for (int u = 0; u < kBatch; ++u) {
-      if (u >= n) break;
-      const T *in = R.in + static_cast<int64_t>(row[u]) * V;
-      const int m = masked ? s_mask[R.j0 + row[u]] : -1;
-      const uint8_t *bits = masks + m * P.mask_bytes;
-      const int mis = RAGGED ? ((R.index + row[u]) * static_cast<uint32_t>(V)) & (kPer - 1) : 0;
-      const int first = RAGGED ? min(t1, t0 + ((kPer - mis) & (kPer - 1))) : t0;
-#pragma unroll
-      for (int q = 0; q < kVecs; ++q) {
-        const int t = first + (lane + q * 32) * kPer;
-        x[u][q].allow = kAll;
-        if (t + kPer > t1) continue;
-        if (m >= 0) x[u][q].allow = mask_bits<kPer>(bits, t, P.mask_bytes);
-        if (x[u][q].allow != 0 && !(IN_PLACE && x[u][q].allow == kAll))
-          x[u][q].w = *reinterpret_cast<const uint4 *>(in + t);
-      }
-      if constexpr (RAGGED) {
-        const int tail = first + ((t1 - first) & ~(kPer - 1));
-        int t = lane < 16 ? (t0 + lane < first ? t0 + lane : -1)
-                          : (tail + lane - 16 < t1 ? tail + lane - 16 : -1);
-        if (t >= 0) {
-          const bool allowed = m < 0 || ((bits[t >> 3] >> (t & 7)) & 1u);
-          if (!allowed) edge[u] = E::kNegInf;
-          else if (IN_PLACE) t = -1;
-          else edge[u] = in[t];
-        }
-        edge_at[u] = t;
+  // the list: every thread its word's tokens
+  if (tid < C::kWords && tid * 32 < width) {
+    const uint32_t extra = s_extra[tid];
+    uint32_t any = known | extra;
+    if (width - tid * 32 < 32) any &= (1u << (width - tid * 32)) - 1;
+    int e = any ? atomicAdd(&s_n, __popc(any)) : 0;
+    while (any) {
+      const int b = __ffs(any) - 1;
+      any &= any - 1;
+      s_word[e] = (known >> b) & 1u;                         // read below
+      s_tok[e++] = static_cast<uint16_t>(tid * 32 + b) | (((extra >> b) & 1u) ? kOutside : 0);
+    }
+  }
+  __syncthreads();
+  const int n = s_n;
+  for (int e = tid; e < n; e += kThreads) {
+    const int tok = s_tok[e], t = tok & (C::kTokens - 1);
+    uint32_t word = 0;
+    if (s_word[e]) word = static_cast<uint32_t>(a.counts[static_cast<int64_t>(slot) * V + t0 + t]);
+    if (tok & kOutside) {
+      for (int c = 0; c < ctx; ++c) word += a.ctx_tokens[c * ctx_stride + i] == t0 + t;
+      if (nb > 0 && s_last[t]) {
+        s_last[t] = __float_as_int(a.bias_values[b0 + s_last[t] - 1]);
+        s_tok[e] = static_cast<uint16_t>(tok | kBiased);
       }
     }
-#pragma unroll
-    for (int u = 0; u < kBatch; ++u) {
-      if (u >= n) break;
-      T *out = R.out + static_cast<int64_t>(row[u]) * V;
-      const int mis = RAGGED ? ((R.index + row[u]) * static_cast<uint32_t>(V)) & (kPer - 1) : 0;
-      const int first = RAGGED ? min(t1, t0 + ((kPer - mis) & (kPer - 1))) : t0;
-#pragma unroll
-      for (int q = 0; q < kVecs; ++q) {
-        const int t = first + (lane + q * 32) * kPer;
-        if (t + kPer > t1 || (IN_PLACE && x[u][q].allow == kAll)) continue;
-        x[u][q].bar();
-        *reinterpret_cast<uint4 *>(out + t) = x[u][q].w;
-      }
-      if constexpr (RAGGED) {
-        if (edge_at[u] >= 0) out[edge_at[u]] = edge[u];
-      }
-    }
+    s_word[e] = word;
+  }
+  __syncthreads();
+
+  auto changed = [&](T x, int tok, uint32_t word, int j) {
+    uint32_t times = word & 0x7FFFFFFFu;
+    if (tok & kOutside)
+      for (int d = 0; d < min(j, drafts); ++d) times += s_draft[d] == (tok & (C::kTokens - 1));
+    float y = E::get(x);
+    if (times > 0 || (word >> 31)) y = y > 0.0f ? y / rep : y * rep;
+    if (times > 0) y -= fmaf(freq, static_cast<float>(times), pres);
+    if (tok & kBiased) y += __int_as_float(s_last[tok & (C::kTokens - 1)]);
+    return E::put(y);
   };
-  if (t0 < t1 && !(IN_PLACE && masked == 0)) {
+
+  if constexpr (!IN_PLACE) {
+    int s = 0;
+    for (int line = warp; line < lines; line += kWarps) {
+      cp_async_wait<kRing - 1>();
+      __syncwarp();
+      const Line<T> L = s_line[line];
+      unsigned char *row = my_ring + s * C::kSlot;
+      T *x = reinterpret_cast<T *>(row) + L.mis;             // the chunk's tokens
+      for (int e = lane; e < n; e += 32) {
+        const int tok = s_tok[e], t = tok & (C::kTokens - 1);
+        x[t] = changed(x[t], tok, s_word[e], L.j);
+      }
+      __syncwarp();
+      const uint8_t *bits = row + C::kMaskAt;
+      T *out = L.out - L.mis;                                // vectors as they were read
+      if (width == C::kTokens && L.mis == 0) {
 #pragma unroll
-    for (int kind = 0; kind < 2; ++kind) {
-      const Rows<T> &R = parts[kind];
-      if constexpr (IN_PLACE) {              // the masked rows alone
-        uint32_t left = R.n > 0 ? (masked >> R.j0) & ((1u << R.n) - 1) : 0u;
-        while (left) {
-          int row[kBatch] = {0, 0, 0, 0}, n = 0;
-#pragma unroll
-          for (int u = 0; u < kBatch; ++u)
-            if (left) {
-              row[u] = __ffs(left) - 1;
-              left &= left - 1;
-              n = u + 1;
-            }
-          copy(R, row, n);
+        for (int q = 0; q < C::kVecs; ++q) {
+          const int v = (lane + q * 32) * kPer;
+          Piece<T, kPer> piece;
+          piece.w = *reinterpret_cast<const uint4 *>(row + (lane + q * 32) * 16);
+          if (L.mask) piece.bar(mask_bits<kPer>(bits, v, C::kWords * 4));
+          *reinterpret_cast<uint4 *>(out + v) = piece.w;
         }
       } else {
-        for (int r = 0; r < R.n; r += kBatch) {
-          const int row[kBatch] = {r, r + 1, r + 2, r + 3};
-          copy(R, row, R.n - r);
-        }
-      }
-    }
-  }
-  __syncthreads();
-
-  // the list: lane b has bit b of the tile's words
-  if (t0 < t1) {
-    uint32_t any[kTileWords];
-    int count = 0;
+        for (int v = lane * kPer; v - L.mis < width; v += 32 * kPer) {
+          const int t = v - L.mis;
+          Piece<T, kPer> piece;
+          piece.w = *reinterpret_cast<const uint4 *>(row + v * static_cast<int>(sizeof(T)));
+          uint32_t allow = kAll;                             // bits past the chunk say nothing
+          if (L.mask) allow = t >= 0 ? mask_bits<kPer>(bits, t, C::kWords * 4)
+                                     : mask_bits<kPer>(bits, 0, C::kWords * 4) << -t;
+          piece.bar(allow);
+          if (t >= 0 && t + kPer <= width) {
+            *reinterpret_cast<uint4 *>(out + v) = piece.w;
+          } else {
 #pragma unroll
-    for (int q = 0; q < kTileWords; ++q) {
-      any[q] = __shfl_sync(0xffffffffu, known, q) | s_extra[warp * kTileWords + q];
-      if (t1 - t0 - q * 32 < 32) any[q] &= t1 - t0 > q * 32 ? (1u << (t1 - t0 - q * 32)) - 1 : 0u;
-      count += __popc(any[q]);
-    }
-    if (count) {
-      int at = 0;
-      if (lane == 0) at = atomicAdd(&s_n, count);
-      at = __shfl_sync(0xffffffffu, at, 0);
-      const int32_t *counts = a.counts + static_cast<int64_t>(slot) * V + t0;
-#pragma unroll
-      for (int q = 0; q < kTileWords; ++q) {
-        if (any[q] == 0) continue;
-        const uint32_t kw = __shfl_sync(0xffffffffu, known, q);
-        if ((any[q] >> lane) & 1u) {
-          const int in_tile = q * 32 + lane, local = warp * kTile + in_tile, t = t0 + in_tile;
-          uint32_t word = 0, after = 0;
-          float bias = 0.0f;
-          if ((kw >> lane) & 1u) word = static_cast<uint32_t>(counts[in_tile]);
-          if ((s_extra[warp * kTileWords + q] >> lane) & 1u) {
-            if (penal)
-              for (int c = 0; c < a.num_ctx; ++c) word += a.ctx_tokens[c * ctx_stride + i] == t;
-            for (int d = 0; d < drafts; ++d)
-              if (draft_tokens[d] == t) after |= 1u << d;
-            if (nb > 0 && s_last[local]) bias = a.bias_values[b0 + s_last[local] - 1];
+            for (int k = 0; k < kPer; ++k)
+              if (t + k >= 0 && t + k < width) out[v + k] = piece.e[k];
           }
-          const int e = at + __popc(any[q] & ((1u << lane) - 1));
-          s_tok[e] = static_cast<uint32_t>(local) | (after << 16);
-          s_word[e] = word;
-          s_bias[e] = bias;
         }
-        at += __popc(any[q]);
+      }
+      __syncwarp();                                          // the slot is free
+      issue(line + kRing * kWarps, s);
+      s = s + 1 == kRing ? 0 : s + 1;
+    }
+  } else {
+    // masked rows: barred tokens written, vectors that stay whole not touched
+    for (int line = warp; line < lines; line += kWarps) {
+      const Line<T> L = s_line[line];
+      if (!L.mask) continue;
+      const int first = RAGGED ? (kPer - L.mis) & (kPer - 1) : 0;
+      Piece<T, kPer> x[C::kVecs];
+      uint32_t allow[C::kVecs];
+#pragma unroll
+      for (int q = 0; q < C::kVecs; ++q) {
+        const int t = first + (lane + q * 32) * kPer;
+        allow[q] = t + kPer <= width ? mask_bits<kPer>(L.mask, t, (width + 7) >> 3) : kAll;
+      }
+#pragma unroll
+      for (int q = 0; q < C::kVecs; ++q)
+        if (allow[q] != 0 && allow[q] != kAll)
+          x[q].w = *reinterpret_cast<const uint4 *>(L.in + first + (lane + q * 32) * kPer);
+#pragma unroll
+      for (int q = 0; q < C::kVecs; ++q)
+        if (allow[q] != kAll) {
+          x[q].bar(allow[q]);
+          *reinterpret_cast<uint4 *>(L.out + first + (lane + q * 32) * kPer) = x[q].w;
+        }
+      if (RAGGED || width != C::kTokens) {                   // the ends, one by one
+        const int tail = first + (width > first ? (width - first) & ~(kPer - 1) : 0);
+        const int t = lane < 16 ? (lane < min(first, width) ? lane : -1)
+                                : (tail + lane - 16 < width ? tail + lane - 16 : -1);
+        if (t >= 0 && !((L.mask[t >> 3] >> (t & 7)) & 1u)) L.out[t] = E::kNegInf;
       }
     }
-  }
-  __syncthreads();
-
-  // the list for every row: threads share the entries, and the rows too where
-  // the entries are fewer than threads
-  const int n = s_n;
-  int span = kNT;                                            // threads that share the entries
-  while (span > 32 && n <= span / 2) span >>= 1;
-  const int step = kNT / span, group = tid / span;
-  for (int e = tid & (span - 1); e < n; e += span) {
-    const uint32_t tok = s_tok[e], word = s_word[e], after = tok >> 16;
-    const int local = tok & 0xFFFFu;
-    const int t = (blockIdx.x + (local / kTile) * shares) * kTile + local % kTile;
-    const float bias = s_bias[e];
-#pragma unroll
-    for (int kind = 0; kind < 2; ++kind) {
-      const Rows<T> &R = parts[kind];
-      for (int rb = group; rb < R.n; rb += step * kBatch) {
+    __syncwarp();
+    // the listed tokens of this warp's rows
+    for (int e = lane; e < n; e += 32) {
+      const int tok = s_tok[e], t = tok & (C::kTokens - 1);
+      const uint32_t word = s_word[e];
+      for (int lb = warp; lb < lines; lb += kBatch * kWarps) {
         T x[kBatch];
         bool allowed[kBatch];
-        const int64_t off = static_cast<int64_t>(rb) * V + t, next = static_cast<int64_t>(step) * V;
 #pragma unroll
         for (int u = 0; u < kBatch; ++u) {
-          if (rb + u * step >= R.n) break;
-          x[u] = R.in[off + u * next];
-          allowed[u] = true;
-          if (masked) {
-            const int m = s_mask[R.j0 + rb + u * step];
-            if (m >= 0) allowed[u] = (masks[m * P.mask_bytes + (t >> 3)] >> (t & 7)) & 1u;
+          allowed[u] = false;                                // (barred: written already)
+          if (lb + u * kWarps >= lines) continue;
+          const Line<T> &L = s_line[lb + u * kWarps];
+          x[u] = L.in[t];
+          allowed[u] = !L.mask || ((L.mask[t >> 3] >> (t & 7)) & 1u);
+        }
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u)
+          if (allowed[u]) {
+            const Line<T> &L = s_line[lb + u * kWarps];
+            L.out[t] = changed(x[u], tok, word, L.j);
           }
-        }
-#pragma unroll
-        for (int u = 0; u < kBatch; ++u) {
-          if (rb + u * step >= R.n) break;
-          if (!allowed[u]) continue;                         // written already
-          const uint32_t times = (word & 0x7FFFFFFFu) +
-                                 __popc(after & ((1u << (R.j0 + rb + u * step)) - 1));
-          float y = E::get(x[u]);
-          if (times > 0 || (word >> 31)) y = y > 0.0f ? y / rep : y * rep;
-          if (times > 0) y -= fmaf(freq, static_cast<float>(times), pres);
-          if (bias != 0.0f) y += bias;
-          R.out[off + u * next] = E::put(y);
-        }
       }
     }
   }
@@ -443,16 +449,32 @@ __global__ void __launch_bounds__(kNT) count_kernel(const __grid_constant__ Coun
 }
 
 // ---------------------------------------------------------------- host side
-template <typename T>
-void launch_adjust(bool in_place, dim3 grid, const AdjustParams &P, cudaStream_t s) {
-  const bool ragged = P.a.vocab % (16 / static_cast<int>(sizeof(T))) != 0;
-  if (in_place) {
-    if (ragged) adjust_kernel<T, true, true><<<grid, kNT, 0, s>>>(P);
-    else adjust_kernel<T, true, false><<<grid, kNT, 0, s>>>(P);
-  } else {
-    if (ragged) adjust_kernel<T, false, true><<<grid, kNT, 0, s>>>(P);
-    else adjust_kernel<T, false, false><<<grid, kNT, 0, s>>>(P);
+template <typename T, bool IN_PLACE, bool RAGGED>
+cudaError_t launch_adjust(dim3 grid, const AdjustParams &P, cudaStream_t s) {
+  constexpr int ring = IN_PLACE ? 0 : kWarps * kRing * Chunk<T>::kSlot;
+  if constexpr (!IN_PLACE) {      // once per device: the ring and the lists pass 48 KB
+    static std::atomic<uint64_t> ready{0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = uint64_t{1} << (dev & 63);
+    if (dev >= 64 || !(ready.load(std::memory_order_acquire) & bit)) {
+      e = cudaFuncSetAttribute(adjust_kernel<T, IN_PLACE, RAGGED>,
+                               cudaFuncAttributeMaxDynamicSharedMemorySize, ring);
+      if (e != cudaSuccess) return e;
+      ready.fetch_or(bit, std::memory_order_release);
+    }
   }
+  adjust_kernel<T, IN_PLACE, RAGGED><<<grid, kThreads, ring, s>>>(P);
+  return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t launch_adjust(bool in_place, dim3 grid, const AdjustParams &P, cudaStream_t s) {
+  const bool ragged = P.a.vocab % Chunk<T>::kPer != 0;
+  if (in_place)
+    return ragged ? launch_adjust<T, true, true>(grid, P, s) : launch_adjust<T, true, false>(grid, P, s);
+  return ragged ? launch_adjust<T, false, true>(grid, P, s) : launch_adjust<T, false, false>(grid, P, s);
 }
 
 sv_status check_adjust(const sv_adjust_args *a) {
@@ -531,22 +553,22 @@ SV_API sv_status spec_adjust_logits(const sv_adjust_args *a, void *stream) {
   if (P.a.repetition == 0.0f) P.a.repetition = 1.0f;
   P.seen_words = (a->vocab + 31) / 32;
   P.mask_bytes = 4 * (a->mask_stride ? a->mask_stride : P.seen_words);
-  const int tiles = (a->vocab + kTile - 1) / kTile, shares = (tiles + kWarps - 1) / kWarps;
+  const int chunk = a->dtype == SV_BF16 ? Chunk<uint16_t>::kTokens : Chunk<float>::kTokens;
+  const int chunks = (a->vocab + chunk - 1) / chunk;
   const int lines = a->draft ? 2 * a->max_q_rows - 1 : a->max_q_rows;
-  // Few CTAs: the rows are split as well, down to one batch of rows per CTA
-  // (each part repeats the list).
+  // Few CTAs: the rows are split as well, down to a row per warp (each part
+  // repeats the list).
   const int sms = device_sms();
   if (sms <= 0) return record_error(SV_ERR_CUDA, "adjust: no current CUDA device");
-  const int64_t ctas = static_cast<int64_t>(shares) * a->batch;
+  const int64_t ctas = static_cast<int64_t>(chunks) * a->batch;
   int parts = 1;
-  while (parts * kBatch < lines && ctas * (parts + 1) <= 4 * static_cast<int64_t>(sms)) ++parts;
+  while (parts * kWarps < lines && ctas * (parts + 1) <= 4 * static_cast<int64_t>(sms)) ++parts;
   P.lines_per_part = (lines + parts - 1) / parts;
-  const dim3 grid(shares, a->batch, (lines + P.lines_per_part - 1) / P.lines_per_part);
+  const dim3 grid(chunks, a->batch, (lines + P.lines_per_part - 1) / P.lines_per_part);
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool in_place = a->target == a->target_out;
-  if (a->dtype == SV_BF16) launch_adjust<uint16_t>(in_place, grid, P, s);
-  else launch_adjust<float>(in_place, grid, P, s);
-  const cudaError_t e = cudaGetLastError();
+  const cudaError_t e = a->dtype == SV_BF16 ? launch_adjust<uint16_t>(in_place, grid, P, s)
+                                            : launch_adjust<float>(in_place, grid, P, s);
   if (e != cudaSuccess) return record_error(SV_ERR_CUDA, "adjust launch: %s", cudaGetErrorString(e));
   return SV_OK;
 }
