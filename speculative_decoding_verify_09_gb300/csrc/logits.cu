@@ -7,16 +7,19 @@
 // exceptions are few: the tokens of the history, the biased ones and the
 // block's drafts, a few thousand of V per sequence, but spread so that most
 // 512-byte pieces of a row hold one.  What has to stay small is the number of
-// instructions per byte.  A CTA takes a chunk of the vocabulary (4 KB of a row)
-// for one sequence and lists the chunk's exceptions once: the table's bits say
-// where they are, so its counts are read only there.  From then on every warp
-// works alone, a row's chunk at a time: 16-byte cp.async copies into a ring of
-// shared memory (kRing rows deep), the listed tokens changed there, a lane per
-// token, and the chunk written out.  In place nothing streams: masked rows are
-// written where a token is barred, and the listed tokens of every row are
-// changed in global memory.
+// instructions per byte, and the chain of dependent loads before the first row
+// can be changed.  A CTA takes a chunk of the vocabulary (4 KB of a row, 1 KB
+// where that gives too few CTAs) for one sequence; each of its warps lists the
+// exceptions of its share of the chunk (the table's bits say where they are, so
+// its counts are read only there) while the first rows are on their way.  From
+// then on every warp works alone, a row's chunk at a time: 16-byte cp.async
+// copies into shared memory, the listed tokens changed there, a lane per token,
+// and the chunk written out.  In place nothing streams: masked rows are written
+// where a token is barred, and the listed tokens of every row are changed in
+// global memory.
 #include <atomic>
 #include <cmath>
+#include <type_traits>
 
 #include "common.cuh"
 #include "ops_host.inl"
@@ -27,11 +30,7 @@ namespace sv {
 namespace {
 
 constexpr int kNT = 256;                   // threads of the table's kernels
-constexpr int kWarps = 4;                  // of an adjusting CTA
-constexpr int kThreads = kWarps * 32;
-constexpr int kChunkBytes = 4096;          // of a row, per CTA
-constexpr int kRing = 2;                   // row chunks in flight per warp
-constexpr int kBatch = 4;                  // (in place) rows in flight per warp
+constexpr int kBatch = 5;                  // (in place) rows in flight per warp
 
 // ---------------------------------------------------------------- adjust
 template <typename T>
@@ -76,24 +75,24 @@ union Piece {
   }
 };
 
-// A row that the CTA works on, at the chunk's first token.
-template <typename T>
-struct alignas(16) Line {
-  const T *in;
-  T *out;
-  const uint8_t *mask;           // the row's mask from the chunk's first token on, or null
-  int j, mis;                    // block row; elements from the 16-byte boundary before it
-};
-
-template <typename T>
+// How a kernel cuts its work.  A CTA takes a chunk of BYTES of a row.  Out of
+// place its warps stream the rows' chunks in units of at most 2 KB, two units
+// of shared memory each, every unit with a list of its own; in place there is
+// one list, and few warps, for all they do is wait.
+template <typename T, int BYTES, bool IN_PLACE>
 struct Chunk {
   static constexpr int kPer = 16 / static_cast<int>(sizeof(T));       // elements of a vector
-  static constexpr int kTokens = kChunkBytes / static_cast<int>(sizeof(T));
-  static constexpr int kWords = kTokens / 32;
-  static constexpr int kVecs = kChunkBytes / 16 / 32;                 // vectors per lane
-  static constexpr int kMaskAt = kChunkBytes + 16;                    // (a misaligned row's last vector)
-  static constexpr int kSlot = kMaskAt + kWords * 4;                  // a row in the ring, its mask
-  static_assert(kSlot % 16 == 0, "vectors of every slot are 16-byte aligned");
+  static constexpr int kTokens = BYTES / static_cast<int>(sizeof(T));
+  static constexpr int kWarps = IN_PLACE ? 2 : 8, kThreads = kWarps * 32;
+  static constexpr int kUnitBytes = IN_PLACE || BYTES < 2048 ? BYTES : 2048;
+  static constexpr int kUnits = BYTES / kUnitBytes, kUnitTokens = kTokens / kUnits;
+  static constexpr int kWords = kTokens / 32 / kWarps;                // of each warp's share
+  static constexpr int kVecs = kUnitBytes / 16 / 32;                  // vectors per lane and unit
+  static constexpr int kMaskAt = kUnitBytes + 16;                     // (a misaligned row's last vector)
+  static constexpr int kSlot = kMaskAt + kUnitTokens / 8;             // a unit and its mask
+  static constexpr int kRing = 2;
+  static constexpr int kRingBytes = IN_PLACE ? 0 : kWarps * kRing * kSlot;
+  static_assert(kWords >= 1 && kWords <= 32 && kSlot % 16 == 0, "");
 };
 
 constexpr uint16_t kOutside = 0x8000u, kBiased = 0x4000u;   // flags of a listed token: counted
@@ -104,38 +103,27 @@ __device__ __forceinline__ void cp_async4(uint32_t dst, const void *src) {
 }
 
 // RAGGED: V is no multiple of a vector's elements, so rows differ in alignment.
-template <typename T, bool IN_PLACE, bool RAGGED>
-__global__ void __launch_bounds__(kThreads) adjust_kernel(const __grid_constant__ AdjustParams P) {
+template <typename T, int BYTES, bool IN_PLACE, bool RAGGED>
+__global__ void __launch_bounds__(Chunk<T, BYTES, IN_PLACE>::kThreads)
+adjust_kernel(const __grid_constant__ AdjustParams P) {
   using E = Elem<T>;
-  using C = Chunk<T>;
-  constexpr int kPer = C::kPer;
+  using C = Chunk<T, BYTES, IN_PLACE>;
+  constexpr int kPer = C::kPer, kWarps = C::kWarps, kThreads = C::kThreads;
   constexpr uint32_t kAll = (1u << kPer) - 1;
   const sv_adjust_args &a = P.a;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, i = blockIdx.y;
   const int V = a.vocab, t0 = blockIdx.x * C::kTokens, width = min(V - t0, C::kTokens);
   const bool head = blockIdx.x == 0 && blockIdx.z == 0;      // this CTA reports the sequence
 
-  extern __shared__ __align__(16) unsigned char s_ring[];    // (out of place) kWarps x kRing slots
-  __shared__ Line<T> s_line[32];                             // target rows, then draft rows
-  __shared__ uint32_t s_extra[C::kWords];                    // bits of ctx, draft and bias tokens
-  __shared__ __align__(16) int32_t s_last[C::kTokens];       // 1 + last bias entry of a token; then
-                                                             // its bias, as bits
-  __shared__ uint32_t s_word[C::kTokens];                    // table words of the list, with ctx
-  __shared__ uint16_t s_tok[C::kTokens];                     // the list: tokens in the chunk, flags
-  __shared__ int32_t s_draft[16];                            // the block's drafts in the chunk
-  __shared__ int s_n;
+  extern __shared__ __align__(16) unsigned char s_dyn[];     // the ring; with biases: s_last
+  int32_t *s_last = reinterpret_cast<int32_t *>(s_dyn + C::kRingBytes);   // 1 + last bias entry of
+                                                             // a token; then its bias, as bits
+  __shared__ uint32_t s_extra[C::kTokens / 32];              // bits of ctx, draft and bias tokens
+  __shared__ uint32_t s_word[C::kTokens];                    // table words of the lists, with ctx
+  __shared__ uint16_t s_tok[C::kTokens];                     // the lists: tokens in the chunk, flags
+  __shared__ int s_n[C::kUnits];
 
-  const int r0 = a.cu_q[i], Ri = a.cu_q[i + 1] - r0;
-  if (r0 < i || Ri < 1 || Ri > a.max_q_rows || r0 + Ri > a.num_rows ||
-      r0 + Ri - (i + 1) > a.num_rows - a.batch) {            // (its draft rows, too)
-    if (head && tid == 0) set_status(a.dev_status, SV_DEV_BAD_LENGTH);
-    return;
-  }
-  const int all = Ri + (a.draft != nullptr ? Ri - 1 : 0);
-  const int l0 = blockIdx.z * P.lines_per_part, lines = min(all - l0, P.lines_per_part);
-  if (lines <= 0) return;
-
-  // the sequence's values
+  const int r0 = a.cu_q[i], r1 = a.cu_q[i + 1];
   const float rep = a.repetitions ? a.repetitions[i] : a.repetition;
   const float pres = a.presences ? a.presences[i] : a.presence;
   const float freq = a.frequencies ? a.frequencies[i] : a.frequency;
@@ -144,137 +132,215 @@ __global__ void __launch_bounds__(kThreads) adjust_kernel(const __grid_constant_
   if (a.bias_start) {
     b0 = a.bias_start[i];
     b1 = a.bias_start[i + 1];
-  }
-  int bad = !(rep > 0.0f) || !isfinite(rep) || !isfinite(pres) || !isfinite(freq) || slot < -1 ||
-            slot >= max(a.num_slots, 0) || b0 < 0 || b1 < b0 || b1 > a.num_bias;
-  const int nb = b1 - b0;
-  if (tid < Ri && a.mask) {                                  // every row's, for one verdict
-    const int m = a.mask_rows ? a.mask_rows[r0 + tid] : r0 + tid;
-    bad |= m < -1 || m >= a.num_masks;
-  }
-  if (tid < lines) {
-    const int l = l0 + tid;
-    Line<T> L;
-    L.j = l < Ri ? l : l - Ri;
-    const int64_t row = l < Ri ? r0 + l : r0 - i + L.j;
-    L.in = static_cast<const T *>(l < Ri ? a.target : a.draft) + row * V + t0;
-    L.out = static_cast<T *>(l < Ri ? a.target_out : a.draft_out) + row * V + t0;
-    L.mis = RAGGED ? static_cast<int>((static_cast<uint32_t>(row) * static_cast<uint32_t>(V)) & (kPer - 1)) : 0;
-    L.mask = nullptr;
-    if (a.mask) {
-      const int m = a.mask_rows ? a.mask_rows[r0 + L.j] : r0 + L.j;
-      if (m >= 0) L.mask = reinterpret_cast<const uint8_t *>(a.mask) + m * P.mask_bytes + (t0 >> 3);
-    }
-    s_line[tid] = L;
-  }
-  if (tid < C::kWords) s_extra[tid] = 0;
-  if (tid == 0) s_n = 0;
-  if (nb > 0)
     for (int t = tid; t < C::kTokens / 4; t += kThreads)
       reinterpret_cast<int4 *>(s_last)[t] = make_int4(0, 0, 0, 0);
+  }
+  for (int w = tid; w < C::kTokens / 32; w += kThreads) s_extra[w] = 0;
+  if (tid < C::kUnits) s_n[tid] = 0;
+  __syncthreads();
+
+  const int Ri = r1 - r0;
+  if (r0 < i || Ri < 1 || Ri > a.max_q_rows || r0 + Ri > a.num_rows ||
+      r0 + Ri - (i + 1) > a.num_rows - a.batch) {            // (its draft rows, too)
+    if (head && tid == 0) set_status(a.dev_status, SV_DEV_BAD_LENGTH);
+    return;
+  }
+  const int all = Ri + (a.draft != nullptr ? Ri - 1 : 0);    // target rows, then draft rows
+  const int l0 = blockIdx.z * P.lines_per_part, lines = min(all - l0, P.lines_per_part);
+  if (lines <= 0) return;
+
+  // Row `line` of this part, at the chunk's first token.
+  auto block_row = [&](int line) { return l0 + line < Ri ? l0 + line : l0 + line - Ri; };
+  auto row_index = [&](int line) {
+    return static_cast<int64_t>(l0 + line < Ri ? r0 : r0 - i) + block_row(line);
+  };
+  auto row_in = [&](int line) {
+    return static_cast<const T *>(l0 + line < Ri ? a.target : a.draft) + row_index(line) * V + t0;
+  };
+  auto row_out = [&](int line) {
+    return static_cast<T *>(l0 + line < Ri ? a.target_out : a.draft_out) + row_index(line) * V + t0;
+  };
+  // elements from the 16-byte boundary before the chunk to the chunk
+  auto misaligned = [&](int line) {
+    return RAGGED ? static_cast<int>((static_cast<uint32_t>(row_index(line)) * static_cast<uint32_t>(V)) & (kPer - 1)) : 0;
+  };
+
+  // Unit u (row u / kUnits) into slot s of this warp's ring: 16-byte vectors
+  // from the boundary at or before the unit's first token up to its last one.
+  unsigned char *ring = s_dyn + warp * (C::kRing * C::kSlot);
+  const int units = lines * C::kUnits;
+  auto fetch = [&](int u, int s) {
+    const int line = u / C::kUnits, from = (u % C::kUnits) * C::kUnitTokens, uw = width - from;
+    if (uw <= 0) return;
+    const int mis = misaligned(line);
+    const uint32_t dst = smem_u32(ring + s * C::kSlot) + lane * 16;
+    const T *src = row_in(line) + from - mis + lane * kPer;
+    if (uw >= C::kUnitTokens) {
+#pragma unroll
+      for (int q = 0; q < C::kVecs; ++q) cp_async16(dst + q * 512, src + q * 32 * kPer, 16);
+      if (RAGGED && lane == 0 && mis)
+        cp_async16(dst + C::kUnitBytes, src + C::kUnitTokens, mis * static_cast<int>(sizeof(T)));
+    } else {
+      const int left = uw + mis - lane * kPer;               // elements from this lane's first on
+#pragma unroll 1
+      for (int q = 0; left > q * 32 * kPer; ++q)             // (at most kVecs + 1: the slot holds them)
+        cp_async16(dst + q * 512, src + q * 32 * kPer,
+                   min(16, (left - q * 32 * kPer) * static_cast<int>(sizeof(T))));
+    }
+  };
+  if constexpr (!IN_PLACE) {
+    if (warp < units) fetch(warp, 0);
+    if (warp + kWarps < units) fetch(warp + kWarps, 1);
+  }
+
+  const bool penal = rep != 1.0f || pres != 0.0f || freq != 0.0f;
+  const int nb = b1 - b0;
+  bool bad = !(rep > 0.0f) || !isfinite(rep) || !isfinite(pres) || !isfinite(freq) || slot < -1 ||
+             slot >= max(a.num_slots, 0) || b0 < 0 || b1 < b0 || b1 > a.num_bias;
+  int my_mask = -1;                                          // lane j: mask row of block row j
+  if (a.mask && lane < Ri) my_mask = a.mask_rows ? a.mask_rows[r0 + lane] : r0 + lane;
+  const int drafts = penal && a.draft_tokens ? Ri - 1 : 0;
+  int my_draft = -1;                                         // lane d: draft d + 1, in the chunk
+  if (lane < drafts) {
+    const int t = a.draft_tokens[r0 - i + lane];
+    my_draft = t >= t0 && t - t0 < width ? t - t0 : -1;
+  }
+  // the table's bits of this warp's share, a word per lane
+  const int w0 = warp * C::kWords;
+  uint32_t known = 0;
+  if (!bad && penal && slot >= 0 && lane < C::kWords && (w0 + lane) * 32 < width)
+    known = a.seen[static_cast<int64_t>(slot) * P.seen_words + (t0 >> 5) + w0 + lane];
+
+  // tokens outside the table, by the whole CTA
+  const int ctx = penal ? a.num_ctx : 0;
+  const int64_t ctx_stride = a.ctx_stride ? a.ctx_stride : a.batch;
+  auto mark = [&](int t) { atomicOr(&s_extra[t >> 5], 1u << (t & 31)); };
+  auto in_chunk = [&](int t) { return t >= t0 && t - t0 < width; };
+  if (!bad) {
+    for (int c = tid; c < ctx; c += kThreads) {
+      const int t = a.ctx_tokens[c * ctx_stride + i];
+      if (in_chunk(t)) mark(t - t0);
+    }
+#pragma unroll 4
+    for (int e = tid; e < nb; e += kThreads) {
+      const int t = a.bias_tokens[b0 + e];
+      if (in_chunk(t)) {
+        mark(t - t0);
+        atomicMax(&s_last[t - t0], e + 1);
+      } else if (head && (t < 0 || t >= V)) {
+        set_status(a.dev_status, SV_DEV_BAD_TOKEN);
+      }
+    }
+  }
+  if (warp == 0 && my_draft >= 0) mark(my_draft);
+  bad |= my_mask < -1 || (my_mask >= 0 && my_mask >= a.num_masks);
   bad = __syncthreads_or(bad);
 
   if (bad) {                      // rows the sampler fails the sequence on
     if (head && tid == 0) set_status(a.dev_status, SV_DEV_BAD_PARAM);
-    for (int l = warp; l < lines; l += kWarps)
-      for (int t = lane; t < width; t += 32) s_line[l].out[t] = E::put(NAN);
+    if constexpr (!IN_PLACE) {
+      cp_async_commit();
+      cp_async_wait<0>();
+    }
+    for (int line = warp; line < lines; line += kWarps) {
+      T *out = row_out(line);
+      for (int t = lane; t < width; t += 32) out[t] = E::put(NAN);
+    }
     return;
   }
-
-  // Row chunk `line` into its slot of this warp's ring: 16-byte vectors from
-  // the boundary at or before the chunk's first token up to its last one, and
-  // the chunk's mask words.
-  unsigned char *my_ring = s_ring + warp * (kRing * C::kSlot);
-  auto issue = [&](int line, int s) {
-    if (line < lines) {
-      const Line<T> L = s_line[line];
-      const uint32_t dst = smem_u32(my_ring + s * C::kSlot) + lane * 16;
-      const T *src = L.in - L.mis + lane * kPer;
-      const int left = width + L.mis - lane * kPer;          // elements from this lane's first on
-#pragma unroll
-      for (int q = 0; q < C::kVecs; ++q)
-        if (left > q * 32 * kPer)
-          cp_async16(dst + q * 512, src + q * 32 * kPer,
-                     min(16, (left - q * 32 * kPer) * static_cast<int>(sizeof(T))));
-      if (RAGGED && lane == 0 && left > C::kTokens)
-        cp_async16(dst + kChunkBytes, src + C::kTokens, (left - C::kTokens) * static_cast<int>(sizeof(T)));
-      if (L.mask)
-        for (int w = lane; w * 32 < width; w += 32)
-          cp_async4(smem_u32(my_ring + s * C::kSlot + C::kMaskAt) + w * 4, L.mask + w * 4);
-    }
-    cp_async_commit();
+  const uint32_t masked = __ballot_sync(0xffffffffu, my_mask >= 0);   // bit j: row j has a mask
+  auto mask_of = [&](int j) -> const uint8_t * {             // by all lanes
+    const int m = __shfl_sync(0xffffffffu, my_mask, j);
+    return m < 0 ? nullptr : reinterpret_cast<const uint8_t *>(a.mask) + m * P.mask_bytes + (t0 >> 3);
   };
-  if constexpr (!IN_PLACE)
-    for (int s = 0; s < kRing; ++s) issue(warp + s * kWarps, s);
-
-  const bool penal = rep != 1.0f || pres != 0.0f || freq != 0.0f;
-  const int drafts = penal && a.draft_tokens ? Ri - 1 : 0;
-  const int ctx = penal ? a.num_ctx : 0;
-  const int64_t ctx_stride = a.ctx_stride ? a.ctx_stride : a.batch;
-
-  // the table's bits of the chunk: a word per thread
-  uint32_t known = 0;
-  if (penal && slot >= 0 && tid < C::kWords && tid * 32 < width)
-    known = a.seen[static_cast<int64_t>(slot) * P.seen_words + (t0 >> 5) + tid];
-  static_assert(C::kWords <= kThreads, "a word per thread");
-
-  // tokens outside the table
-  auto mark = [&](int t) { atomicOr(&s_extra[t >> 5], 1u << (t & 31)); };
-  auto in_chunk = [&](int token) { return token >= t0 && token - t0 < width; };
-  if (tid < drafts) {
-    const int t = a.draft_tokens[r0 - i + tid];
-    s_draft[tid] = in_chunk(t) ? t - t0 : -1;
-    if (in_chunk(t)) mark(t - t0);
+  auto fetch_mask = [&](int u, int s) {                      // a unit's mask words, by all lanes
+    const int j = block_row(u / C::kUnits), from = (u % C::kUnits) * C::kUnitTokens;
+    if (!((masked >> j) & 1u)) return;
+    const uint8_t *mask = mask_of(j) + (from >> 3);
+    const uint32_t dst = smem_u32(ring + s * C::kSlot + C::kMaskAt);
+    for (int w = lane; w < C::kUnitTokens / 32 && from + w * 32 < width; w += 32)
+      cp_async4(dst + w * 4, mask + w * 4);
+  };
+  if constexpr (!IN_PLACE) {
+    if (warp < units) fetch_mask(warp, 0);
+    if (warp + kWarps < units) fetch_mask(warp + kWarps, 1);
+    cp_async_commit();                                       // both first units
+    cp_async_commit();
   }
-  for (int c = tid; c < ctx; c += kThreads) {
-    const int t = a.ctx_tokens[c * ctx_stride + i];
-    if (in_chunk(t)) mark(t - t0);
-  }
-  for (int e = tid; e < nb; e += kThreads) {
-    const int t = a.bias_tokens[b0 + e];
-    if (in_chunk(t)) {
-      mark(t - t0);
-      atomicMax(&s_last[t - t0], e + 1);
-    } else if (head && (t < 0 || t >= V)) {
-      set_status(a.dev_status, SV_DEV_BAD_TOKEN);
+
+  // the share's list: each lane its word's tokens where they are few, else a
+  // word at a time with a lane per bit
+  const int my_unit = w0 * 32 / C::kUnitTokens;
+  {
+    uint32_t extra = 0, any = 0;
+    if (lane < C::kWords) {
+      extra = s_extra[w0 + lane];
+      any = known | extra;
+      const int left = width - (w0 + lane) * 32;
+      if (left < 32) any &= left > 0 ? (1u << left) - 1 : 0u;
     }
-  }
-  __syncthreads();
-
-  // the list: every thread its word's tokens
-  if (tid < C::kWords && tid * 32 < width) {
-    const uint32_t extra = s_extra[tid];
-    uint32_t any = known | extra;
-    if (width - tid * 32 < 32) any &= (1u << (width - tid * 32)) - 1;
-    int e = any ? atomicAdd(&s_n, __popc(any)) : 0;
-    while (any) {
-      const int b = __ffs(any) - 1;
-      any &= any - 1;
-      s_word[e] = (known >> b) & 1u;                         // read below
-      s_tok[e++] = static_cast<uint16_t>(tid * 32 + b) | (((extra >> b) & 1u) ? kOutside : 0);
+    int count = __popc(any), before = count;                 // of this lane, of the lanes up to it
+    const int most = __reduce_max_sync(0xffffffffu, count);
+#pragma unroll
+    for (int o = 1; o < C::kWords; o <<= 1) {
+      const int c = __shfl_up_sync(0xffffffffu, before, o);
+      if (lane >= o) before += c;
     }
-  }
-  __syncthreads();
-  const int n = s_n;
-  for (int e = tid; e < n; e += kThreads) {
-    const int tok = s_tok[e], t = tok & (C::kTokens - 1);
-    uint32_t word = 0;
-    if (s_word[e]) word = static_cast<uint32_t>(a.counts[static_cast<int64_t>(slot) * V + t0 + t]);
-    if (tok & kOutside) {
-      for (int c = 0; c < ctx; ++c) word += a.ctx_tokens[c * ctx_stride + i] == t0 + t;
-      if (nb > 0 && s_last[t]) {
-        s_last[t] = __float_as_int(a.bias_values[b0 + s_last[t] - 1]);
+    const int total = __shfl_sync(0xffffffffu, before, C::kWords - 1);
+    before -= count;
+    int base = 0;
+    if (lane == 0 && total) base = my_unit * C::kUnitTokens + atomicAdd(&s_n[my_unit], total);
+    base = __shfl_sync(0xffffffffu, base, 0);
+    auto enter = [&](int e, int q, int b, bool in_table, bool out) {
+      s_word[e] = in_table;                                  // read below
+      s_tok[e] = static_cast<uint16_t>(((w0 + q) * 32 + b) | (out ? kOutside : 0));
+    };
+    if (most <= 4) {
+      int e = base + before;
+      while (any) {
+        const int b = __ffs(any) - 1;
+        any &= any - 1;
+        enter(e++, lane, b, (known >> b) & 1u, (extra >> b) & 1u);
+      }
+    } else {
+#pragma unroll 1
+      for (int q = 0; q < C::kWords; ++q) {
+        const uint32_t w = __shfl_sync(0xffffffffu, any, q), kw = __shfl_sync(0xffffffffu, known, q),
+                       ew = __shfl_sync(0xffffffffu, extra, q);
+        const int e = base + __shfl_sync(0xffffffffu, before, q) + __popc(w & ((1u << lane) - 1));
+        if ((w >> lane) & 1u) enter(e, q, lane, (kw >> lane) & 1u, (ew >> lane) & 1u);
+      }
+    }
+    __syncwarp();
+    const int32_t *counts = a.counts + static_cast<int64_t>(slot) * V + t0;
+#pragma unroll 4
+    for (int e = base + lane; e < base + total; e += 32) {
+      const int tok = s_tok[e], t = tok & (C::kTokens - 1);
+      const bool outside = tok & kOutside;
+      const int entry = outside && nb > 0 ? s_last[t] : 0;
+      const uint32_t word = s_word[e] ? static_cast<uint32_t>(counts[t]) : 0u;
+      const float bias = entry ? a.bias_values[b0 + entry - 1] : 0.0f;
+      uint32_t more = 0;
+      if (outside)
+        for (int c = 0; c < ctx; ++c) more += a.ctx_tokens[c * ctx_stride + i] == t0 + t;
+      s_word[e] = word + more;
+      if (entry) {
+        s_last[t] = __float_as_int(bias);
         s_tok[e] = static_cast<uint16_t>(tok | kBiased);
       }
     }
-    s_word[e] = word;
   }
   __syncthreads();
 
-  auto changed = [&](T x, int tok, uint32_t word, int j) {
+  // (drafts of a listed token: by all lanes, `on` those that have one)
+  auto times_of = [&](bool on, int tok, uint32_t word, int j) {
     uint32_t times = word & 0x7FFFFFFFu;
-    if (tok & kOutside)
-      for (int d = 0; d < min(j, drafts); ++d) times += s_draft[d] == (tok & (C::kTokens - 1));
+    if (__any_sync(0xffffffffu, on && (tok & kOutside)))
+      for (int d = 0; d < min(j, drafts); ++d)
+        times += __shfl_sync(0xffffffffu, my_draft, d) == (tok & (C::kTokens - 1));
+    return times;
+  };
+  auto changed = [&](T x, int tok, uint32_t word, uint32_t times) {
     float y = E::get(x);
     if (times > 0 || (word >> 31)) y = y > 0.0f ? y / rep : y * rep;
     if (times > 0) y -= fmaf(freq, static_cast<float>(times), pres);
@@ -284,102 +350,143 @@ __global__ void __launch_bounds__(kThreads) adjust_kernel(const __grid_constant_
 
   if constexpr (!IN_PLACE) {
     int s = 0;
-    for (int line = warp; line < lines; line += kWarps) {
-      cp_async_wait<kRing - 1>();
+#pragma unroll 1
+    for (int u = warp; u < units; u += kWarps, s ^= 1) {
+      cp_async_wait<1>();
       __syncwarp();
-      const Line<T> L = s_line[line];
-      unsigned char *row = my_ring + s * C::kSlot;
-      T *x = reinterpret_cast<T *>(row) + L.mis;             // the chunk's tokens
-      for (int e = lane; e < n; e += 32) {
-        const int tok = s_tok[e], t = tok & (C::kTokens - 1);
-        x[t] = changed(x[t], tok, s_word[e], L.j);
+      const int line = u / C::kUnits, unit = u % C::kUnits, j = block_row(line);
+      const int from = unit * C::kUnitTokens, uw = min(width - from, C::kUnitTokens);
+      const int mis = misaligned(line), n = s_n[unit];
+      unsigned char *row = ring + s * C::kSlot;
+      T *x = reinterpret_cast<T *>(row) + mis;               // the unit's tokens
+#pragma unroll 1
+      for (int eb = 0; eb < n; eb += 64) {                   // two entries per lane
+        int tok[2];
+        uint32_t word[2], times[2];
+        T old[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int e = eb + h * 32 + lane;
+          tok[h] = 0;
+          word[h] = 0;
+          if (e < n) {
+            tok[h] = s_tok[from + e];
+            word[h] = s_word[from + e];
+            old[h] = x[(tok[h] & (C::kTokens - 1)) - from];
+          }
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int e = eb + h * 32 + lane;
+          if (eb + h * 32 >= n) break;
+          times[h] = times_of(e < n, tok[h], word[h], j);
+          if (e < n) x[(tok[h] & (C::kTokens - 1)) - from] = changed(old[h], tok[h], word[h], times[h]);
+        }
       }
       __syncwarp();
+      const bool barred = (masked >> j) & 1u;
       const uint8_t *bits = row + C::kMaskAt;
-      T *out = L.out - L.mis;                                // vectors as they were read
-      if (width == C::kTokens && L.mis == 0) {
+      T *out = row_out(line) + from - mis;                   // vectors as they were read
+      if (uw == C::kUnitTokens && mis == 0) {
 #pragma unroll
         for (int q = 0; q < C::kVecs; ++q) {
           const int v = (lane + q * 32) * kPer;
           Piece<T, kPer> piece;
           piece.w = *reinterpret_cast<const uint4 *>(row + (lane + q * 32) * 16);
-          if (L.mask) piece.bar(mask_bits<kPer>(bits, v, C::kWords * 4));
+          if (barred) piece.bar(mask_bits<kPer>(bits, v, C::kUnitTokens / 8));
           *reinterpret_cast<uint4 *>(out + v) = piece.w;
         }
       } else {
-        for (int v = lane * kPer; v - L.mis < width; v += 32 * kPer) {
-          const int t = v - L.mis;
+#pragma unroll 1
+        for (int v = lane * kPer; v - mis < uw; v += 32 * kPer) {
+          const int t = v - mis;
           Piece<T, kPer> piece;
           piece.w = *reinterpret_cast<const uint4 *>(row + v * static_cast<int>(sizeof(T)));
-          uint32_t allow = kAll;                             // bits past the chunk say nothing
-          if (L.mask) allow = t >= 0 ? mask_bits<kPer>(bits, t, C::kWords * 4)
-                                     : mask_bits<kPer>(bits, 0, C::kWords * 4) << -t;
-          piece.bar(allow);
-          if (t >= 0 && t + kPer <= width) {
+          if (barred)                                        // (bits outside the unit say nothing)
+            piece.bar(t >= 0 ? mask_bits<kPer>(bits, t, C::kUnitTokens / 8)
+                             : mask_bits<kPer>(bits, 0, C::kUnitTokens / 8) << -t);
+          if (t >= 0 && t + kPer <= uw) {
             *reinterpret_cast<uint4 *>(out + v) = piece.w;
           } else {
 #pragma unroll
             for (int k = 0; k < kPer; ++k)
-              if (t + k >= 0 && t + k < width) out[v + k] = piece.e[k];
+              if (t + k >= 0 && t + k < uw) out[v + k] = piece.e[k];
           }
         }
       }
       __syncwarp();                                          // the slot is free
-      issue(line + kRing * kWarps, s);
-      s = s + 1 == kRing ? 0 : s + 1;
+      if (u + 2 * kWarps < units) {
+        fetch(u + 2 * kWarps, s);
+        fetch_mask(u + 2 * kWarps, s);
+      }
+      cp_async_commit();
     }
   } else {
     // masked rows: barred tokens written, vectors that stay whole not touched
-    for (int line = warp; line < lines; line += kWarps) {
-      const Line<T> L = s_line[line];
-      if (!L.mask) continue;
-      const int first = RAGGED ? (kPer - L.mis) & (kPer - 1) : 0;
-      Piece<T, kPer> x[C::kVecs];
-      uint32_t allow[C::kVecs];
+    if (masked)
+#pragma unroll 1
+      for (int line = warp; line < lines; line += kWarps) {
+        const uint8_t *mask = mask_of(block_row(line));
+        if (!mask) continue;
+        const int mis = misaligned(line), first = RAGGED ? (kPer - mis) & (kPer - 1) : 0;
+        T *row = row_out(line);
+        Piece<T, kPer> x[C::kVecs];
+        uint32_t allow[C::kVecs];
 #pragma unroll
-      for (int q = 0; q < C::kVecs; ++q) {
-        const int t = first + (lane + q * 32) * kPer;
-        allow[q] = t + kPer <= width ? mask_bits<kPer>(L.mask, t, (width + 7) >> 3) : kAll;
-      }
-#pragma unroll
-      for (int q = 0; q < C::kVecs; ++q)
-        if (allow[q] != 0 && allow[q] != kAll)
-          x[q].w = *reinterpret_cast<const uint4 *>(L.in + first + (lane + q * 32) * kPer);
-#pragma unroll
-      for (int q = 0; q < C::kVecs; ++q)
-        if (allow[q] != kAll) {
-          x[q].bar(allow[q]);
-          *reinterpret_cast<uint4 *>(L.out + first + (lane + q * 32) * kPer) = x[q].w;
+        for (int q = 0; q < C::kVecs; ++q) {
+          const int t = first + (lane + q * 32) * kPer;
+          allow[q] = t + kPer <= width ? mask_bits<kPer>(mask, t, (width + 7) >> 3) : kAll;
         }
-      if (RAGGED || width != C::kTokens) {                   // the ends, one by one
-        const int tail = first + (width > first ? (width - first) & ~(kPer - 1) : 0);
-        const int t = lane < 16 ? (lane < min(first, width) ? lane : -1)
-                                : (tail + lane - 16 < width ? tail + lane - 16 : -1);
-        if (t >= 0 && !((L.mask[t >> 3] >> (t & 7)) & 1u)) L.out[t] = E::kNegInf;
+#pragma unroll
+        for (int q = 0; q < C::kVecs; ++q)
+          if (allow[q] != 0 && allow[q] != kAll)
+            x[q].w = *reinterpret_cast<const uint4 *>(row + first + (lane + q * 32) * kPer);
+#pragma unroll
+        for (int q = 0; q < C::kVecs; ++q)
+          if (allow[q] != kAll) {
+            x[q].bar(allow[q]);
+            *reinterpret_cast<uint4 *>(row + first + (lane + q * 32) * kPer) = x[q].w;
+          }
+        if (RAGGED) {                                        // the ends, one by one
+          const int tail = first + (width > first ? (width - first) & ~(kPer - 1) : 0);
+          const int t = lane < 16 ? (lane < min(first, width) ? lane : -1)
+                                  : (tail + lane - 16 < width ? tail + lane - 16 : -1);
+          if (t >= 0 && !((mask[t >> 3] >> (t & 7)) & 1u)) row[t] = E::kNegInf;
+        }
       }
-    }
     __syncwarp();
     // the listed tokens of this warp's rows
-    for (int e = lane; e < n; e += 32) {
-      const int tok = s_tok[e], t = tok & (C::kTokens - 1);
-      const uint32_t word = s_word[e];
-      for (int lb = warp; lb < lines; lb += kBatch * kWarps) {
+    const int n = s_n[0];
+#pragma unroll 1
+    for (int lb = warp; lb < lines; lb += kBatch * kWarps) {
+      T *row[kBatch];
+      const uint8_t *mask[kBatch];
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u)
+        if (lb + u * kWarps < lines) {
+          row[u] = row_out(lb + u * kWarps);
+          mask[u] = mask_of(block_row(lb + u * kWarps));
+        }
+#pragma unroll 1
+      for (int eb = 0; eb < n; eb += 32) {
+        const bool on = eb + lane < n;
+        const int tok = on ? s_tok[eb + lane] : 0, t = tok & (C::kTokens - 1);
+        const uint32_t word = on ? s_word[eb + lane] : 0u;
         T x[kBatch];
         bool allowed[kBatch];
 #pragma unroll
         for (int u = 0; u < kBatch; ++u) {
-          allowed[u] = false;                                // (barred: written already)
-          if (lb + u * kWarps >= lines) continue;
-          const Line<T> &L = s_line[lb + u * kWarps];
-          x[u] = L.in[t];
-          allowed[u] = !L.mask || ((L.mask[t >> 3] >> (t & 7)) & 1u);
+          allowed[u] = on && lb + u * kWarps < lines;
+          if (!allowed[u]) continue;
+          x[u] = row[u][t];
+          if (mask[u]) allowed[u] = (mask[u][t >> 3] >> (t & 7)) & 1u;   // barred: written already
         }
 #pragma unroll
-        for (int u = 0; u < kBatch; ++u)
-          if (allowed[u]) {
-            const Line<T> &L = s_line[lb + u * kWarps];
-            L.out[t] = changed(x[u], tok, word, L.j);
-          }
+        for (int u = 0; u < kBatch; ++u) {
+          if (lb + u * kWarps >= lines) continue;
+          const uint32_t times = times_of(on, tok, word, block_row(lb + u * kWarps));
+          if (allowed[u]) row[u][t] = changed(x[u], tok, word, times);
+        }
       }
     }
   }
@@ -449,32 +556,53 @@ __global__ void __launch_bounds__(kNT) count_kernel(const __grid_constant__ Coun
 }
 
 // ---------------------------------------------------------------- host side
-template <typename T, bool IN_PLACE, bool RAGGED>
+template <typename T, int BYTES, bool IN_PLACE, bool RAGGED>
 cudaError_t launch_adjust(dim3 grid, const AdjustParams &P, cudaStream_t s) {
-  constexpr int ring = IN_PLACE ? 0 : kWarps * kRing * Chunk<T>::kSlot;
-  if constexpr (!IN_PLACE) {      // once per device: the ring and the lists pass 48 KB
-    static std::atomic<uint64_t> ready{0};
+  using C = Chunk<T, BYTES, IN_PLACE>;
+  constexpr int biases = C::kTokens * 4;                     // s_last
+  if constexpr (C::kRingBytes + biases + C::kTokens * 6 > 47 * 1024) {   // past the default
+    static std::atomic<uint64_t> ready{0};                   // once per device
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     const uint64_t bit = uint64_t{1} << (dev & 63);
     if (dev >= 64 || !(ready.load(std::memory_order_acquire) & bit)) {
-      e = cudaFuncSetAttribute(adjust_kernel<T, IN_PLACE, RAGGED>,
-                               cudaFuncAttributeMaxDynamicSharedMemorySize, ring);
+      e = cudaFuncSetAttribute(adjust_kernel<T, BYTES, IN_PLACE, RAGGED>,
+                               cudaFuncAttributeMaxDynamicSharedMemorySize, C::kRingBytes + biases);
       if (e != cudaSuccess) return e;
       ready.fetch_or(bit, std::memory_order_release);
     }
   }
-  adjust_kernel<T, IN_PLACE, RAGGED><<<grid, kThreads, ring, s>>>(P);
+  adjust_kernel<T, BYTES, IN_PLACE, RAGGED>
+      <<<grid, C::kThreads, C::kRingBytes + (P.a.bias_start ? biases : 0), s>>>(P);
   return cudaGetLastError();
 }
 
 template <typename T>
-cudaError_t launch_adjust(bool in_place, dim3 grid, const AdjustParams &P, cudaStream_t s) {
-  const bool ragged = P.a.vocab % Chunk<T>::kPer != 0;
-  if (in_place)
-    return ragged ? launch_adjust<T, true, true>(grid, P, s) : launch_adjust<T, true, false>(grid, P, s);
-  return ragged ? launch_adjust<T, false, true>(grid, P, s) : launch_adjust<T, false, false>(grid, P, s);
+cudaError_t launch_adjust(const sv_adjust_args &a, int sms, AdjustParams &P, cudaStream_t s) {
+  const bool in_place = a.target == a.target_out, ragged = a.vocab % (16 / static_cast<int>(sizeof(T))) != 0;
+  const int lines = a.draft ? 2 * a.max_q_rows - 1 : a.max_q_rows;
+  auto chunks = [&](int bytes) {
+    const int tokens = bytes / static_cast<int>(sizeof(T));
+    return (a.vocab + tokens - 1) / tokens;
+  };
+  // Few CTAs: small chunks, and the rows split as well, down to a row per warp
+  // (each part repeats the list).
+  const int64_t want = 4 * static_cast<int64_t>(sms);
+  const bool small = static_cast<int64_t>(chunks(4096)) * a.batch < want;
+  const int64_t ctas = static_cast<int64_t>(chunks(small ? 1024 : 4096)) * a.batch;
+  int parts = 1;
+  const int warps = in_place ? Chunk<T, 1024, true>::kWarps : Chunk<T, 1024, false>::kWarps;
+  while (parts * warps < lines && ctas * (parts + 1) <= want) ++parts;
+  P.lines_per_part = (lines + parts - 1) / parts;
+  const dim3 grid(chunks(small ? 1024 : 4096), a.batch, (lines + P.lines_per_part - 1) / P.lines_per_part);
+  auto pick = [&](auto bytes) {
+    constexpr int B = decltype(bytes)::value;
+    if (in_place)
+      return ragged ? launch_adjust<T, B, true, true>(grid, P, s) : launch_adjust<T, B, true, false>(grid, P, s);
+    return ragged ? launch_adjust<T, B, false, true>(grid, P, s) : launch_adjust<T, B, false, false>(grid, P, s);
+  };
+  return small ? pick(std::integral_constant<int, 1024>()) : pick(std::integral_constant<int, 4096>());
 }
 
 sv_status check_adjust(const sv_adjust_args *a) {
@@ -553,22 +681,11 @@ SV_API sv_status spec_adjust_logits(const sv_adjust_args *a, void *stream) {
   if (P.a.repetition == 0.0f) P.a.repetition = 1.0f;
   P.seen_words = (a->vocab + 31) / 32;
   P.mask_bytes = 4 * (a->mask_stride ? a->mask_stride : P.seen_words);
-  const int chunk = a->dtype == SV_BF16 ? Chunk<uint16_t>::kTokens : Chunk<float>::kTokens;
-  const int chunks = (a->vocab + chunk - 1) / chunk;
-  const int lines = a->draft ? 2 * a->max_q_rows - 1 : a->max_q_rows;
-  // Few CTAs: the rows are split as well, down to a row per warp (each part
-  // repeats the list).
   const int sms = device_sms();
   if (sms <= 0) return record_error(SV_ERR_CUDA, "adjust: no current CUDA device");
-  const int64_t ctas = static_cast<int64_t>(chunks) * a->batch;
-  int parts = 1;
-  while (parts * kWarps < lines && ctas * (parts + 1) <= 4 * static_cast<int64_t>(sms)) ++parts;
-  P.lines_per_part = (lines + parts - 1) / parts;
-  const dim3 grid(chunks, a->batch, (lines + P.lines_per_part - 1) / P.lines_per_part);
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const bool in_place = a->target == a->target_out;
-  const cudaError_t e = a->dtype == SV_BF16 ? launch_adjust<uint16_t>(in_place, grid, P, s)
-                                            : launch_adjust<float>(in_place, grid, P, s);
+  const cudaError_t e = a->dtype == SV_BF16 ? launch_adjust<uint16_t>(*a, sms, P, s)
+                                            : launch_adjust<float>(*a, sms, P, s);
   if (e != cudaSuccess) return record_error(SV_ERR_CUDA, "adjust launch: %s", cudaGetErrorString(e));
   return SV_OK;
 }
