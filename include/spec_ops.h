@@ -169,7 +169,7 @@ SV_API sv_status spec_count_tokens(const sv_count_args *count, void *stream);
  * sampler then fails its sequence with SV_DEV_NONFINITE). */
 typedef struct sv_adjust_args {
   int32_t batch;            /* B, 0..65535 */
-  int32_t vocab;            /* V >= 1 */
+  int32_t vocab;            /* V, 1..2^23 */
   int32_t dtype;            /* SV_F32 or SV_BF16: all logits */
   int32_t max_q_rows;       /* host bound on R_i, 1..16 */
   int64_t num_rows;         /* R = cu_q[B] (host copy) */

@@ -30,7 +30,8 @@ namespace sv {
 namespace {
 
 constexpr int kNT = 256;                   // threads of the table's kernels
-constexpr int kBatch = 5;                  // (in place) rows in flight per warp
+constexpr int kBatch = 3;                  // (in place) rows in flight per warp
+constexpr int kAhead = 4;                  // (in place) listed tokens in flight per lane
 
 // ---------------------------------------------------------------- adjust
 template <typename T>
@@ -83,7 +84,7 @@ template <typename T, int BYTES, bool IN_PLACE>
 struct Chunk {
   static constexpr int kPer = 16 / static_cast<int>(sizeof(T));       // elements of a vector
   static constexpr int kTokens = BYTES / static_cast<int>(sizeof(T));
-  static constexpr int kWarps = IN_PLACE ? 2 : 8, kThreads = kWarps * 32;
+  static constexpr int kWarps = IN_PLACE ? 4 : 8, kThreads = kWarps * 32;
   static constexpr int kUnitBytes = IN_PLACE || BYTES < 2048 ? BYTES : 2048;
   static constexpr int kUnits = BYTES / kUnitBytes, kUnitTokens = kTokens / kUnits;
   static constexpr int kWords = kTokens / 32 / kWarps;                // of each warp's share
@@ -104,16 +105,16 @@ __device__ __forceinline__ void cp_async4(uint32_t dst, const void *src) {
 
 // RAGGED: V is no multiple of a vector's elements, so rows differ in alignment.
 template <typename T, int BYTES, bool IN_PLACE, bool RAGGED>
-__global__ void __launch_bounds__(Chunk<T, BYTES, IN_PLACE>::kThreads)
+__global__ void __launch_bounds__(Chunk<T, BYTES, IN_PLACE>::kThreads, IN_PLACE ? 8 : 4)
 adjust_kernel(const __grid_constant__ AdjustParams P) {
   using E = Elem<T>;
   using C = Chunk<T, BYTES, IN_PLACE>;
   constexpr int kPer = C::kPer, kWarps = C::kWarps, kThreads = C::kThreads;
   constexpr uint32_t kAll = (1u << kPer) - 1;
   const sv_adjust_args &a = P.a;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, i = blockIdx.y;
-  const int V = a.vocab, t0 = blockIdx.x * C::kTokens, width = min(V - t0, C::kTokens);
-  const bool head = blockIdx.x == 0 && blockIdx.z == 0;      // this CTA reports the sequence
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, i = blockIdx.x;
+  const int V = a.vocab, t0 = blockIdx.y * C::kTokens, width = min(V - t0, C::kTokens);
+  const bool head = blockIdx.y == 0 && blockIdx.z == 0;      // this CTA reports the sequence
 
   extern __shared__ __align__(16) unsigned char s_dyn[];     // the ring; with biases: s_last
   int32_t *s_last = reinterpret_cast<int32_t *>(s_dyn + C::kRingBytes);   // 1 + last bias entry of
@@ -468,24 +469,34 @@ adjust_kernel(const __grid_constant__ AdjustParams P) {
           mask[u] = mask_of(block_row(lb + u * kWarps));
         }
 #pragma unroll 1
-      for (int eb = 0; eb < n; eb += 32) {
-        const bool on = eb + lane < n;
-        const int tok = on ? s_tok[eb + lane] : 0, t = tok & (C::kTokens - 1);
-        const uint32_t word = on ? s_word[eb + lane] : 0u;
-        T x[kBatch];
-        bool allowed[kBatch];
+      for (int eb = 0; eb < n; eb += 32 * kAhead) {
+        T x[kAhead][kBatch];
+        bool allowed[kAhead][kBatch];
+        int tok[kAhead];
 #pragma unroll
-        for (int u = 0; u < kBatch; ++u) {
-          allowed[u] = on && lb + u * kWarps < lines;
-          if (!allowed[u]) continue;
-          x[u] = row[u][t];
-          if (mask[u]) allowed[u] = (mask[u][t >> 3] >> (t & 7)) & 1u;   // barred: written already
+        for (int h = 0; h < kAhead; ++h) {
+          const int e = eb + h * 32 + lane;
+          tok[h] = e < n ? s_tok[e] : 0;
+          const int t = tok[h] & (C::kTokens - 1);
+#pragma unroll
+          for (int u = 0; u < kBatch; ++u) {
+            allowed[h][u] = e < n && lb + u * kWarps < lines;
+            if (!allowed[h][u]) continue;
+            x[h][u] = row[u][t];
+            if (mask[u]) allowed[h][u] = (mask[u][t >> 3] >> (t & 7)) & 1u;   // barred: written already
+          }
         }
 #pragma unroll
-        for (int u = 0; u < kBatch; ++u) {
-          if (lb + u * kWarps >= lines) continue;
-          const uint32_t times = times_of(on, tok, word, block_row(lb + u * kWarps));
-          if (allowed[u]) row[u][t] = changed(x[u], tok, word, times);
+        for (int h = 0; h < kAhead; ++h) {
+          if (eb + h * 32 >= n) break;
+          const int e = eb + h * 32 + lane, t = tok[h] & (C::kTokens - 1);
+          const uint32_t word = e < n ? s_word[e] : 0u;
+#pragma unroll
+          for (int u = 0; u < kBatch; ++u) {
+            if (lb + u * kWarps >= lines) break;
+            const uint32_t times = times_of(e < n, tok[h], word, block_row(lb + u * kWarps));
+            if (allowed[h][u]) row[u][t] = changed(x[h][u], tok[h], word, times);
+          }
         }
       }
     }
@@ -595,7 +606,8 @@ cudaError_t launch_adjust(const sv_adjust_args &a, int sms, AdjustParams &P, cud
   const int warps = in_place ? Chunk<T, 1024, true>::kWarps : Chunk<T, 1024, false>::kWarps;
   while (parts * warps < lines && ctas * (parts + 1) <= want) ++parts;
   P.lines_per_part = (lines + parts - 1) / parts;
-  const dim3 grid(chunks(small ? 1024 : 4096), a.batch, (lines + P.lines_per_part - 1) / P.lines_per_part);
+  // sequences first: the chunks of the frequent tokens, which have the long lists, start first
+  const dim3 grid(a.batch, chunks(small ? 1024 : 4096), (lines + P.lines_per_part - 1) / P.lines_per_part);
   auto pick = [&](auto bytes) {
     constexpr int B = decltype(bytes)::value;
     if (in_place)
@@ -610,8 +622,8 @@ sv_status check_adjust(const sv_adjust_args *a) {
   if (!a) return bad("null arguments");
   if (a->batch < 0 || a->batch > 65535)
     return record_error(SV_ERR_UNSUPPORTED, "adjust: batch %d outside [0, 65535]", a->batch);
-  if (a->vocab < 1 || a->vocab > (1 << 30))
-    return record_error(SV_ERR_INVALID, "adjust: vocab %d", a->vocab);
+  if (a->vocab < 1 || a->vocab > (1 << 23))
+    return record_error(SV_ERR_UNSUPPORTED, "adjust: vocab %d outside [1, 2^23]", a->vocab);
   if (a->dtype != SV_F32 && a->dtype != SV_BF16)
     return record_error(SV_ERR_INVALID, "adjust: dtype %d", a->dtype);
   if (a->max_q_rows < 1 || a->max_q_rows > 16)

@@ -113,7 +113,8 @@ def _adjust(b, **kw):
 
 
 @pytest.mark.parametrize("kw,status", [
-    (dict(batch=-1), UNSUPPORTED), (dict(batch=65536), UNSUPPORTED), (dict(vocab=0), INVALID),
+    (dict(batch=-1), UNSUPPORTED), (dict(batch=65536), UNSUPPORTED), (dict(vocab=0), UNSUPPORTED),
+    (dict(vocab=(1 << 23) + 1), UNSUPPORTED),
     (dict(dtype=2), INVALID), (dict(max_q_rows=0), INVALID), (dict(max_q_rows=17), INVALID),
     (dict(num_rows=1), INVALID), (dict(num_rows=11), INVALID),
     (dict(repetition=-1.0), INVALID), (dict(repetition=float("inf")), INVALID),
