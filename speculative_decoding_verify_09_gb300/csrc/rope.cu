@@ -13,6 +13,7 @@
 // memory (rot_dim / 2 pairs, one per thread), while the first 16-byte vectors
 // of the row are in flight, and each thread keeps the pairs of its vector
 // column in registers over all heads of the row.
+#include <algorithm>
 #include <cmath>
 
 #include "common.cuh"
@@ -28,13 +29,12 @@ constexpr int kMaxDim = 256;
 constexpr int kMinRowThreads = 64;                   // threads that share one row, at least
 constexpr int kMaxRows = kNT / kMinRowThreads;       // rows per CTA, at most
 
-// How a thread's 8 elements (or two times 8) of a head meet their partners.
-enum Shape {
-  kHalf = 0,      // half layout, rot_dim % 16 == 0 and D % 16 == 0: a thread holds the vectors
-                  // at 8 c and 8 c + rot_dim / 2, i.e. 8 whole pairs
-  kNeighbor = 1,  // interleaved: a vector holds 4 whole pairs
-  kRagged = 2     // half layout otherwise: a vector's partners are read one by one (L1 hits)
-};
+// How a thread's elements of a head meet their partners.  G = 8, 4, 2, 1 (the
+// half layout): G elements and the G that are rot_dim / 2 further on, i.e. G
+// whole pairs, where G is the largest that divides rot_dim / 2 and so keeps the
+// accesses aligned.  kNeighbor (the interleaved layout): two vectors of 8
+// elements, 4 whole pairs each.
+constexpr int kNeighbor = 0;
 
 struct RopeParams {
   int batch, max_q_rows, Hq, Hkv, D, rot;
@@ -44,6 +44,7 @@ struct RopeParams {
   int64_t num_rows, slots;
   int64_t q_stride, k_stride, v_stride;
   float mscale, k_scale, v_scale;
+  float k_inverse, v_inverse;   // reciprocals of scales that are powers of two, else 0
   const uint64_t *turns;
   const int32_t *cu_q, *kv_len;
   const int64_t *positions;
@@ -52,47 +53,43 @@ struct RopeParams {
   uint32_t *dev_status;
 };
 
-template <typename T>
-struct Vec8;                    // 8 elements as they lie in memory
-template <>
-struct Vec8<uint16_t> {         // bf16
-  uint4 w;
-  __device__ __forceinline__ void load(const uint16_t *p) { w = *reinterpret_cast<const uint4 *>(p); }
-  __device__ __forceinline__ void store(uint16_t *p) const { *reinterpret_cast<uint4 *>(p) = w; }
-  __device__ __forceinline__ void get(float (&x)[8]) const {
-    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+// N elements as they lie in memory.
+template <int BYTES> struct Raw;
+template <> struct Raw<32> { uint4 a, b; };
+template <> struct Raw<16> { uint4 a; };
+template <> struct Raw<8> { uint2 a; };
+template <> struct Raw<4> { uint32_t a; };
+template <> struct Raw<2> { uint16_t a; };
+
+template <typename T, int N>
+struct Vec {
+  union {
+    Raw<N * static_cast<int>(sizeof(T))> raw;
+    T e[N];
+  };
+  __device__ __forceinline__ void load(const T *p) { raw = *reinterpret_cast<const decltype(raw) *>(p); }
+  __device__ __forceinline__ void store(T *p) const { *reinterpret_cast<decltype(raw) *>(p) = raw; }
+  __device__ __forceinline__ void get(float (&x)[N]) const {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      x[2 * i] = __uint_as_float(u[i] << 16);
-      x[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
+    for (int i = 0; i < N; ++i) {
+      if constexpr (sizeof(T) == 2) x[i] = bf16_bits_to_f32(e[i]);
+      else x[i] = e[i];
     }
   }
-  __device__ __forceinline__ void set(const float (&x)[8]) {
-    w = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
-                   pack_bf16x2(x[6], x[7]));
+  __device__ __forceinline__ void set(const float (&x)[N]) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      if constexpr (sizeof(T) == 4) {
+        e[i] = x[i];
+      } else if (N % 2) {
+        e[i] = f32_to_bf16_rn(x[i]);
+      } else if (i % 2 == 0) {
+        const uint32_t two = pack_bf16x2(x[i], x[i + 1]);
+        e[i] = static_cast<uint16_t>(two);
+        e[i + 1] = static_cast<uint16_t>(two >> 16);
+      }
+    }
   }
-  static __device__ __forceinline__ float one(const uint16_t *p) { return bf16_bits_to_f32(*p); }
-};
-template <>
-struct Vec8<float> {
-  float4 a, b;
-  __device__ __forceinline__ void load(const float *p) {
-    a = reinterpret_cast<const float4 *>(p)[0];
-    b = reinterpret_cast<const float4 *>(p)[1];
-  }
-  __device__ __forceinline__ void store(float *p) const {
-    reinterpret_cast<float4 *>(p)[0] = a;
-    reinterpret_cast<float4 *>(p)[1] = b;
-  }
-  __device__ __forceinline__ void get(float (&x)[8]) const {
-    x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-    x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
-  }
-  __device__ __forceinline__ void set(const float (&x)[8]) {
-    a = make_float4(x[0], x[1], x[2], x[3]);
-    b = make_float4(x[4], x[5], x[6], x[7]);
-  }
-  static __device__ __forceinline__ float one(const float *p) { return *p; }
 };
 
 // Two floats -> two E4M3 codes (lo in the lower byte), nearest even, saturating.
@@ -102,11 +99,20 @@ __device__ __forceinline__ uint32_t e4m3x2_of(float lo, float hi) {
   return r;
 }
 
-__device__ __forceinline__ void store_codes(uint8_t *p, const float (&x)[8], float scale) {
-  uint32_t h[4];
+// Codes of x / scale; inverse: 1 / scale where that is exact (scale a power of two), else 0.
+template <int N>
+__device__ __forceinline__ void store_codes(uint8_t *p, const float (&x)[N], float scale, float inverse) {
+  float y[N];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) h[i] = e4m3x2_of(x[2 * i] / scale, x[2 * i + 1] / scale);
-  *reinterpret_cast<uint2 *>(p) = make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
+  for (int i = 0; i < N; ++i) y[i] = inverse != 0.0f ? x[i] * inverse : x[i] / scale;
+  if constexpr (N == 1) {
+    *p = static_cast<uint8_t>(e4m3x2_of(y[0], 0.0f));
+  } else {
+    Vec<uint16_t, N / 2> v;
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) v.e[i] = static_cast<uint16_t>(e4m3x2_of(y[2 * i], y[2 * i + 1]));
+    v.store(reinterpret_cast<uint16_t *>(p));
+  }
 }
 
 // Row and position of slot `slot`; false if there is no such row (or a bad one).
@@ -133,8 +139,15 @@ __device__ __forceinline__ bool find_row(const RopeParams &P, int64_t slot, int6
   return true;
 }
 
-template <typename T, int SHAPE, bool KV8>
-__global__ void __launch_bounds__(kNT) rope_kernel(const RopeParams P) {
+// CTAs per SM that the registers are capped for, as measured (32768 rows of 48 heads of 128: bf16 G = 8 122 us at 4, 134 at 3, 131 at 5; fp32
+// 237 us at 3, 253 at 4; with codes 131 us at 3, 165 at 5).
+template <typename T, int G, bool KV8>
+constexpr int min_ctas() {
+  return G == 8 || G == kNeighbor ? (KV8 || sizeof(T) == 4 ? 3 : 4) : G == 4 ? 4 : 6;
+}
+
+template <typename T, int G, bool KV8>
+__global__ void __launch_bounds__(kNT, min_ctas<T, G, KV8>()) rope_kernel(const RopeParams P) {
   __shared__ __align__(16) float s_cos[kMaxRows][kMaxDim / 2 + 4];
   __shared__ __align__(16) float s_sin[kMaxRows][kMaxDim / 2 + 4];
   const int row_threads = 1 << P.row_shift;
@@ -143,7 +156,6 @@ __global__ void __launch_bounds__(kNT) rope_kernel(const RopeParams P) {
   const int hstep = row_threads >> P.gshift;
   const int h_begin = blockIdx.y * P.heads_per_cta;
   const int h_end = min(P.heads, h_begin + P.heads_per_cta);
-  const int iters = (h_end - h_begin + hstep - 1) / hstep;
   const int half = P.rot >> 1;
 
   int64_t row = 0, pos = 0;
@@ -152,40 +164,32 @@ __global__ void __launch_bounds__(kNT) rope_kernel(const RopeParams P) {
                              pos, bad);
   if (bad && t == 0 && blockIdx.y == 0) set_status(P.dev_status, SV_DEV_BAD_LENGTH);
 
-  // this thread's vector column: element offsets inside a head
-  constexpr int NV = SHAPE == kHalf ? 2 : 1;
-  const bool column = live && c < P.D / (8 * NV);
-  const bool turn = SHAPE != kHalf || c < P.rot / 16;    // (kHalf) the column holds pairs
-  const int o0 = SHAPE == kHalf ? (turn ? 8 * c : P.rot + 16 * (c - P.rot / 16)) : 8 * c;
-  const int o1 = SHAPE == kHalf ? (turn ? o0 + half : o0 + 8) : 0;
+  // this thread's column: element offsets inside a head
+  constexpr int N = G == kNeighbor ? 8 : G;
+  const bool turn = G == kNeighbor ? 2 * N * c < P.rot : c < half / N;   // the column holds pairs
+  const int o0 = G == kNeighbor ? 2 * N * c : turn ? N * c : P.rot + 2 * N * (c - half / N);
+  const int o1 = G != kNeighbor && turn ? o0 + half : o0 + N;
+  const bool column = live && o0 < P.D;
+  const bool both = o1 < P.D;                            // (the last column may be single)
 
-  Vec8<T> cur[NV], nxt[NV];
-  float pcur[8], pnxt[8];                                // (kRagged) the partners
-  auto source = [&](int h) -> const T * {
-    if (h < P.nq) return static_cast<const T *>(P.q) + row * P.q_stride + static_cast<int64_t>(h) * P.D;
-    h -= P.nq;
-    if (h < P.nk) return static_cast<const T *>(P.k) + row * P.k_stride + static_cast<int64_t>(h) * P.D;
-    return static_cast<const T *>(P.v) + row * P.v_stride + static_cast<int64_t>(h - P.nk) * P.D;
-  };
-  auto fetch = [&](Vec8<T> (&v)[NV], float (&pv)[8], int h) {
+  Vec<T, N> cur[2], nxt[2];
+  // the row's heads, numbered through q, k, v: element h D of these
+  const int k0 = P.nq * P.D, v0 = (P.nq + P.nk) * P.D;
+  const T *in_q = static_cast<const T *>(P.q) + row * P.q_stride;
+  const T *in_k = static_cast<const T *>(P.k) + row * P.k_stride - k0;
+  const T *in_v = static_cast<const T *>(P.v) + row * P.v_stride - v0;
+  auto source = [&](int h) { return (h < P.nq ? in_q : h < P.nq + P.nk ? in_k : in_v) + h * P.D; };
+  auto fetch = [&](Vec<T, N> (&v)[2], int h) {
     if (!column || h >= h_end) return;
     const T *p = source(h);
     v[0].load(p + o0);
-    if constexpr (NV == 2) v[1].load(p + o1);
-    if constexpr (SHAPE == kRagged) {
-      if (h < P.nq + P.nk) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int e = o0 + i;
-          pv[i] = e < P.rot ? Vec8<T>::one(p + (e < half ? e + half : e - half)) : 0.0f;
-        }
-      }
-    }
+    if (both) v[1].load(p + o1);
   };
-  fetch(cur, pcur, h_begin + hl);
+  fetch(cur, h_begin + hl);
 
   // cos and sin of the row's pairs, by the threads that share the row
-  if (live && h_begin < P.nq + P.nk) {
+  const bool any_turn = h_begin < P.nq + P.nk;
+  if (live && any_turn) {
     for (int p = t; p < half; p += row_threads) {
       const uint64_t part = static_cast<uint64_t>(pos) * __ldg(P.turns + p);
       float sn, cs;
@@ -195,115 +199,82 @@ __global__ void __launch_bounds__(kNT) rope_kernel(const RopeParams P) {
     }
   }
   __syncthreads();
+  if (!column) return;
 
   // the pairs of this column
-  constexpr int NP = SHAPE == kNeighbor ? 4 : 8;
-  float cs[NP], sn[NP];
-  if (column && h_begin < P.nq + P.nk) {
+  float cs[N], sn[N];
+  if (any_turn && turn) {
 #pragma unroll
-    for (int i = 0; i < NP; ++i) {
-      int p;                                             // pair, or >= half: none
-      if constexpr (SHAPE == kHalf) p = turn ? 8 * c + i : half;
-      if constexpr (SHAPE == kNeighbor) p = 4 * c + i;
-      if constexpr (SHAPE == kRagged) {
-        const int e = 8 * c + i;
-        p = e < half ? e : e < P.rot ? e - half : half;
-      }
+    for (int i = 0; i < N; ++i) {
+      const int p = N * c + i;
       cs[i] = p < half ? s_cos[rl][p] : 1.0f;
       sn[i] = p < half ? s_sin[rl][p] : 0.0f;
     }
   }
+  const bool whole = N * c + N <= half;                  // (kNeighbor) nothing but pairs in the column
 
-  for (int it = 0; it < iters; ++it) {
-    const int h = h_begin + hl + it * hstep;
-    fetch(nxt, pnxt, h + hstep);
-    // kRagged in place: every lane of a head has read before one of them writes
-    if constexpr (SHAPE == kRagged) __syncwarp();
-    if (column && h < h_end) {
-      const bool rotated = h < P.nq + P.nk, is_q = h < P.nq;
-      float x[8], y[8];
-      if (rotated) {
-        cur[0].get(x);
-        if constexpr (SHAPE == kHalf) {
-          if (turn) {
-            float b[8];
-            cur[1].get(b);
+  const int64_t kv_row = row * P.Hkv * P.D;
+  T *out_q = static_cast<T *>(P.q_out) + row * P.Hq * P.D;
+  T *out_k = static_cast<T *>(P.k_out) + kv_row - k0, *out_v = static_cast<T *>(P.v_out) + kv_row - v0;
+  uint8_t *codes_k = static_cast<uint8_t *>(P.k_out) + kv_row - k0;
+  uint8_t *codes_v = static_cast<uint8_t *>(P.v_out) + kv_row - v0;
+  for (int h = h_begin + hl; h < h_end; h += hstep) {
+    fetch(nxt, h + hstep);
+    const bool is_q = h < P.nq, is_k = !is_q && h < P.nq + P.nk, codes = KV8 && !is_q;
+    float x[N], y[N];
+    if ((turn && (is_q || is_k)) || codes) {
+      cur[0].get(x);
+      cur[1].get(y);
+    }
+    if (turn && (is_q || is_k)) {
+      if constexpr (G != kNeighbor) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              y[i] = b[i] * cs[i] + x[i] * sn[i];
-              x[i] = x[i] * cs[i] - b[i] * sn[i];
-            }
-            if (!KV8 || is_q) {
-              cur[0].set(x);
-              cur[1].set(y);
-            }
-          } else if (KV8 && !is_q) {
-            cur[1].get(y);
-          }
+        for (int i = 0; i < N; ++i) {
+          const float a = x[i], b = y[i];
+          x[i] = a * cs[i] - b * sn[i];
+          y[i] = b * cs[i] + a * sn[i];
         }
-        if constexpr (SHAPE == kNeighbor) {
-          if (8 * c < P.rot) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float a = x[2 * i], b = x[2 * i + 1];
-              if (4 * c + i < half) {
-                x[2 * i] = a * cs[i] - b * sn[i];
-                x[2 * i + 1] = b * cs[i] + a * sn[i];
-              }
-            }
-            if (!KV8 || is_q) cur[0].set(x);
-          }
-        }
-        if constexpr (SHAPE == kRagged) {
-          if (8 * c < P.rot) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const int e = 8 * c + i;
-              if (e < half) x[i] = x[i] * cs[i] - pcur[i] * sn[i];
-              else if (e < P.rot) x[i] = x[i] * cs[i] + pcur[i] * sn[i];
-            }
-            if (!KV8 || is_q) cur[0].set(x);
-          }
-        }
-      } else if (KV8) {
-        cur[0].get(x);
-        if constexpr (NV == 2) cur[1].get(y);
-      }
-      if (KV8 && !is_q) {
-        const bool is_k = h < P.nq + P.nk;
-        const int hk = h - P.nq - (is_k ? 0 : P.nk);
-        uint8_t *o = static_cast<uint8_t *>(is_k ? P.k_out : P.v_out) +
-                     (row * P.Hkv + hk) * static_cast<int64_t>(P.D);
-        const float scale = is_k ? P.k_scale : P.v_scale;
-        store_codes(o + o0, x, scale);
-        if constexpr (NV == 2) store_codes(o + o1, y, scale);
       } else {
-        T *o;
-        if (is_q) {
-          o = static_cast<T *>(P.q_out) + (row * P.Hq + h) * static_cast<int64_t>(P.D);
-        } else {
-          const bool is_k = h < P.nq + P.nk;
-          const int hk = h - P.nq - (is_k ? 0 : P.nk);
-          o = static_cast<T *>(is_k ? P.k_out : P.v_out) + (row * P.Hkv + hk) * static_cast<int64_t>(P.D);
-        }
-        cur[0].store(o + o0);
-        if constexpr (NV == 2) cur[1].store(o + o1);
+        auto turn4 = [&](float (&z)[N], int first) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float a = z[2 * i], b = z[2 * i + 1];
+            if (whole || N * c + first + i < half) {
+              z[2 * i] = a * cs[first + i] - b * sn[first + i];
+              z[2 * i + 1] = b * cs[first + i] + a * sn[first + i];
+            }
+          }
+        };
+        turn4(x, 0);
+        turn4(y, 4);
+      }
+      if (!codes) {
+        cur[0].set(x);
+        cur[1].set(y);
       }
     }
-#pragma unroll
-    for (int n = 0; n < NV; ++n) cur[n] = nxt[n];
-    if constexpr (SHAPE == kRagged) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) pcur[i] = pnxt[i];
+    if (codes) {
+      uint8_t *o = (is_k ? codes_k : codes_v) + h * P.D;
+      const float scale = is_k ? P.k_scale : P.v_scale, inverse = is_k ? P.k_inverse : P.v_inverse;
+      store_codes(o + o0, x, scale, inverse);
+      if (both) store_codes(o + o1, y, scale, inverse);
+    } else {
+      T *o = (is_q ? out_q : is_k ? out_k : out_v) + h * P.D;
+      cur[0].store(o + o0);
+      if (both) cur[1].store(o + o1);
     }
+#pragma unroll
+    for (int n = 0; n < 2; ++n) cur[n] = nxt[n];
   }
 }
 
 template <typename T, bool KV8>
-void launch_shape(int shape, dim3 grid, const RopeParams &P, cudaStream_t s) {
-  if (shape == kHalf) rope_kernel<T, kHalf, KV8><<<grid, kNT, 0, s>>>(P);
-  else if (shape == kNeighbor) rope_kernel<T, kNeighbor, KV8><<<grid, kNT, 0, s>>>(P);
-  else rope_kernel<T, kRagged, KV8><<<grid, kNT, 0, s>>>(P);
+void launch_shape(int g, dim3 grid, const RopeParams &P, cudaStream_t s) {
+  if (g == kNeighbor) rope_kernel<T, kNeighbor, KV8><<<grid, kNT, 0, s>>>(P);
+  else if (g == 8) rope_kernel<T, 8, KV8><<<grid, kNT, 0, s>>>(P);
+  else if (g == 4) rope_kernel<T, 4, KV8><<<grid, kNT, 0, s>>>(P);
+  else if (g == 2) rope_kernel<T, 2, KV8><<<grid, kNT, 0, s>>>(P);
+  else rope_kernel<T, 1, KV8><<<grid, kNT, 0, s>>>(P);
 }
 
 bool positive(float x) { return std::isfinite(x) && x > 0.0f; }
@@ -387,6 +358,13 @@ SV_API sv_status spec_rope_rows(const sv_rope_args *a, void *stream) {
   P.mscale = a->mscale == 0.0f ? 1.0f : a->mscale;
   P.k_scale = a->k_scale == 0.0f ? 1.0f : a->k_scale;
   P.v_scale = a->v_scale == 0.0f ? 1.0f : a->v_scale;
+  auto inverse = [](float x) {
+    int e;
+    const float inv = 1.0f / x;
+    return std::frexp(x, &e) == 0.5f && std::isnormal(inv) ? inv : 0.0f;
+  };
+  P.k_inverse = inverse(P.k_scale);
+  P.v_inverse = inverse(P.v_scale);
   P.turns = a->turns;
   P.cu_q = a->cu_q;
   P.kv_len = a->kv_len;
@@ -403,29 +381,35 @@ SV_API sv_status spec_rope_rows(const sv_rope_args *a, void *stream) {
   P.heads = P.nq + P.nk + (a->v && a->v != a->v_out ? P.Hkv : 0);   // v onto itself: nothing to do
   if (a->num_rows == 0 || P.slots == 0 || P.heads == 0) return SV_OK;
 
-  const int shape = a->layout == SV_ROPE_INTERLEAVED ? kNeighbor
-                    : (P.rot % 16 == 0 && P.D % 16 == 0) ? kHalf : kRagged;
-  const int columns = shape == kHalf ? P.D / 16 : P.D / 8;
+  const int half = P.rot / 2;
+  int g = kNeighbor, columns = (P.D + 15) / 16;
+  if (a->layout == SV_ROPE_HALF) {
+    g = half % 8 == 0 ? 8 : half % 4 == 0 ? 4 : half % 2 == 0 ? 2 : 1;
+    columns = half / g + (P.D - P.rot + 2 * g - 1) / (2 * g);
+  }
   while ((1 << P.gshift) < columns) ++P.gshift;
-  // Many rows: kMinRowThreads threads per row, so that a thread keeps its pairs'
-  // cos and sin over many heads.  Few rows: a CTA per row and share of the heads.
   const int sms = device_sms();
   if (sms <= 0) return record_error(SV_ERR_CUDA, "rope: no current CUDA device");
-  const bool few = P.slots < 4 * static_cast<int64_t>(sms);
-  P.row_shift = few ? 8 : 6;
+  // A pass is one head per 1 << gshift threads; a CTA makes as many as leave about
+  // two CTAs per SM (576 rows of 48 heads, E4M3: one pass 6.9 us, all heads 3.8
+  // us; 8 rows of 96 heads: 2.3 against 2.7 us), its rows side by side: two, or
+  // four where there are rows enough (32768 rows of 48 heads, E4M3: 131 against
+  // 142 us; 1152 rows: 6.7 against 5.9 us for two).
+  const int64_t threads = (P.slots * P.heads) << P.gshift, room = 512 * static_cast<int64_t>(sms);
+  P.row_shift = std::max(P.slots >= 16 * static_cast<int64_t>(sms) ? 6 : 7, P.gshift);
   const int at_once = (1 << P.row_shift) >> P.gshift;
-  P.heads_per_cta = few ? at_once : P.heads;
+  P.heads_per_cta = static_cast<int>(std::min<int64_t>(P.heads, std::max<int64_t>(1, (threads + room - 1) / room) * at_once));
   const int rows_per_cta = kNT >> P.row_shift;
   const dim3 grid(static_cast<unsigned>((P.slots + rows_per_cta - 1) / rows_per_cta),
                   static_cast<unsigned>((P.heads + P.heads_per_cta - 1) / P.heads_per_cta));
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool kv8 = a->kv_dtype == SV_E4M3;
   if (a->dtype == SV_BF16) {
-    if (kv8) launch_shape<uint16_t, true>(shape, grid, P, s);
-    else launch_shape<uint16_t, false>(shape, grid, P, s);
+    if (kv8) launch_shape<uint16_t, true>(g, grid, P, s);
+    else launch_shape<uint16_t, false>(g, grid, P, s);
   } else {
-    if (kv8) launch_shape<float, true>(shape, grid, P, s);
-    else launch_shape<float, false>(shape, grid, P, s);
+    if (kv8) launch_shape<float, true>(g, grid, P, s);
+    else launch_shape<float, false>(g, grid, P, s);
   }
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return record_error(SV_ERR_CUDA, "rope launch: %s", cudaGetErrorString(e));
