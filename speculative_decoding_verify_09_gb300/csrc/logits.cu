@@ -17,6 +17,7 @@
 // and the chunk written out.  In place nothing streams: masked rows are written
 // where a token is barred, and the listed tokens of every row are changed in
 // global memory.
+#include <algorithm>
 #include <atomic>
 #include <cmath>
 
@@ -515,37 +516,45 @@ adjust_kernel(const __grid_constant__ AdjustParams P) {
 }
 
 // ---------------------------------------------------------------- count
+constexpr int kTokens = 8;                 // of its sequence that a resetting thread has in flight
+constexpr int kMaxStart = 4096;            // sequences whose start values are kept in shared memory
+
 struct CountParams {
   sv_count_args a;
   int words;                      // of a slot's bits
 };
 
-// Clears the batch's slots: the counts that the bits point at, then the bits.
-__global__ void __launch_bounds__(kNT) clear_kernel(const __grid_constant__ CountParams P) {
+// One token into the table.  Frequent tokens fall on the same words: a mark that
+// is there already is not written again, and additions return nothing.
+__device__ __forceinline__ void enter_token(const CountParams &P, int slot, int t) {
   const sv_count_args &a = P.a;
-  const int i = blockIdx.y;
-  const int slot = a.slots ? a.slots[i] : i;
-  if (slot < 0 || slot >= a.num_slots) return;                // reported by count_kernel
-  const int w = blockIdx.x * kNT + threadIdx.x;
-  if (w >= P.words) return;
-  uint32_t *seen = a.seen + static_cast<int64_t>(slot) * P.words + w;
-  uint32_t bits = *seen;
-  if (bits == 0) return;
-  int32_t *counts = a.counts + static_cast<int64_t>(slot) * a.vocab + w * 32;
-  while (bits) {
-    const int b = __ffs(bits) - 1;
-    bits &= bits - 1;
-    if (w * 32 + b < a.vocab) counts[b] = 0;
+  uint32_t *word = reinterpret_cast<uint32_t *>(a.counts) + static_cast<int64_t>(slot) * a.vocab + t;
+  uint32_t *seen = a.seen + static_cast<int64_t>(slot) * P.words + (t >> 5);
+  const uint32_t bit = 1u << (t & 31), bits = __ldcg(seen);
+  if (a.flags & SV_COUNT_PROMPT) {
+    if (!(__ldcg(word) >> 31)) atomicOr(word, 0x80000000u);
+  } else {
+    atomicAdd(word, 1u);
   }
-  *seen = 0;
+  if (!(bits & bit)) atomicOr(seen, bit);
 }
 
+// One token per thread; its sequence is searched in shared memory.
 __global__ void __launch_bounds__(kNT) count_kernel(const __grid_constant__ CountParams P) {
   const sv_count_args &a = P.a;
+  extern __shared__ __align__(16) uint32_t s_word[];
+  int32_t *s_start = reinterpret_cast<int32_t *>(s_word);     // start, where it fits
   const int64_t at = static_cast<int64_t>(blockIdx.x) * kNT + threadIdx.x;
+  const int32_t *start = a.start;
+  const int t = at < a.num_tokens ? a.tokens[at] : 0;
+  if (a.batch <= kMaxStart) {
+    for (int i = threadIdx.x; i <= a.batch; i += kNT) s_start[i] = a.start[i];
+    start = s_start;
+    __syncthreads();
+  }
   if (at < a.batch) {             // one thread per sequence reports
     const int i = static_cast<int>(at);
-    const int s0 = a.start[i], s1 = a.start[i + 1], slot = a.slots ? a.slots[i] : i;
+    const int s0 = start[i], s1 = start[i + 1], slot = a.slots ? a.slots[i] : i;
     if (s0 < 0 || s1 < s0 || s1 > a.num_tokens) set_status(a.dev_status, SV_DEV_BAD_LENGTH);
     if (slot < -1 || slot >= a.num_slots) set_status(a.dev_status, SV_DEV_BAD_PARAM);
   }
@@ -554,27 +563,102 @@ __global__ void __launch_bounds__(kNT) count_kernel(const __grid_constant__ Coun
   int lo = 0, hi = a.batch;
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
-    if (a.start[mid] <= at) lo = mid; else hi = mid;
+    if (start[mid] <= at) lo = mid; else hi = mid;
   }
-  const int i = lo, s0 = a.start[i], s1 = a.start[i + 1];
+  const int i = lo, s0 = start[i], s1 = start[i + 1];
   if (s0 < 0 || at < s0 || at >= s1 || s1 > a.num_tokens) return;
-  if (a.num_accepted && at - s0 > a.num_accepted[i]) return;
   const int slot = a.slots ? a.slots[i] : i;
+  if (a.num_accepted && at - s0 > a.num_accepted[i]) return;
   if (slot < 0 || slot >= a.num_slots) return;
-  const int t = a.tokens[at];
-  if (t < 0 || t >= a.vocab) {
-    set_status(a.dev_status, SV_DEV_BAD_TOKEN);
-    return;
+  if (t < 0 || t >= a.vocab) set_status(a.dev_status, SV_DEV_BAD_TOKEN);
+  else enter_token(P, slot, t);
+}
+
+// Clearing and counting: a CTA owns a slice of one slot's vocabulary and takes
+// the sequence's tokens that fall into it (of all sequences that share the
+// slot, by the first of them) together in shared memory, as bits for a prompt,
+// as counts too otherwise.  Frequent tokens meet there, and what is or was not
+// 0 in the table is written once.  Every slice reads all of its sequence's
+// tokens, from L2.
+template <int NT, bool PROMPT>
+__global__ void __launch_bounds__(NT) reset_kernel(const __grid_constant__ CountParams P) {
+  const sv_count_args &a = P.a;
+  constexpr int kSlice = 32 * NT;                             // a word of bits per thread
+  __shared__ uint32_t s_bits[NT];
+  __shared__ __align__(16) uint32_t s_word[PROMPT ? 4 : kSlice];
+  const int i = blockIdx.x, tid = threadIdx.x, lane = tid & 31;
+  const int t0 = blockIdx.y * kSlice, width = min(kSlice, a.vocab - t0);
+  const bool head = blockIdx.y == 0;
+  const int slot = a.slots ? a.slots[i] : i;
+  auto segment = [&](int j, int &s0, int &n) {                // tokens of sequence j
+    s0 = a.start[j];
+    const int s1 = a.start[j + 1];
+    const bool good = s0 >= 0 && s1 >= s0 && s1 <= a.num_tokens;
+    n = good ? s1 - s0 : 0;
+    if (good && a.num_accepted) n = min(n, max(a.num_accepted[j], -1) + 1);
+    return good;
+  };
+  int s0, n;
+  const bool good = segment(i, s0, n);
+  if (head && tid == 0) {
+    if (!good) set_status(a.dev_status, SV_DEV_BAD_LENGTH);
+    if (slot < -1 || slot >= a.num_slots) set_status(a.dev_status, SV_DEV_BAD_PARAM);
   }
-  uint32_t *word = reinterpret_cast<uint32_t *>(a.counts) + static_cast<int64_t>(slot) * a.vocab + t;
-  if (a.flags & SV_COUNT_PROMPT) {
-    if (!(__ldcg(word) >> 31)) atomicOr(word, 0x80000000u);
-  } else {
-    atomicAdd(word, 1u);
+  if (slot < 0 || slot >= a.num_slots) return;
+  // loads first: the table's bits, a thread's first tokens, the other slots
+  uint32_t *seen = a.seen + static_cast<int64_t>(slot) * P.words + t0 / 32;
+  const uint32_t old = tid * 32 < width ? seen[tid] : 0u;
+  int t[kTokens];
+  auto load = [&](int k0) {
+#pragma unroll
+    for (int u = 0; u < kTokens; ++u) t[u] = k0 + u * NT < n ? __ldg(a.tokens + s0 + k0 + u * NT) : t0;
+  };
+  load(tid);
+  bool before = false, after = false;                         // others that share the slot
+  if (a.slots)
+    for (int j = tid; j < a.batch; j += NT)
+      if (j != i && a.slots[j] == slot) (j < i ? before : after) = true;
+  s_bits[tid] = 0;
+  if constexpr (!PROMPT)
+    for (int w = tid; w < kSlice / 4; w += NT) reinterpret_cast<uint4 *>(s_word)[w] = make_uint4(0, 0, 0, 0);
+  const int shared = __syncthreads_or(before || after);
+  if (shared && __syncthreads_or(before)) return;             // the first of them does it
+  for (int j = i;;) {
+#pragma unroll 1
+    for (int k0 = tid; k0 < n;) {
+#pragma unroll
+      for (int u = 0; u < kTokens; ++u) {
+        if (k0 + u * NT >= n) break;
+        if (t[u] >= t0 && t[u] - t0 < width) {
+          const int at = t[u] - t0;
+          if (!((s_bits[at >> 5] >> (at & 31)) & 1u)) atomicOr(&s_bits[at >> 5], 1u << (at & 31));
+          if constexpr (!PROMPT) atomicAdd(&s_word[at], 1u);
+        } else if (head && (t[u] < 0 || t[u] >= a.vocab)) {
+          set_status(a.dev_status, SV_DEV_BAD_TOKEN);
+        }
+      }
+      k0 += NT * kTokens;
+      load(k0);
+    }
+    if (!shared) break;
+    do ++j; while (j < a.batch && a.slots[j] != slot);
+    if (j >= a.batch) break;
+    segment(j, s0, n);
+    load(tid);
   }
-  uint32_t *seen = a.seen + static_cast<int64_t>(slot) * P.words + (t >> 5);
-  const uint32_t bit = 1u << (t & 31);
-  if (!(__ldcg(seen) & bit)) atomicOr(seen, bit);
+  __syncthreads();
+  // of each warp's words those with tokens one after the other, a lane per token
+  uint32_t *counts = reinterpret_cast<uint32_t *>(a.counts) + static_cast<int64_t>(slot) * a.vocab + t0;
+  const uint32_t now = s_bits[tid], any = now | old;
+  uint32_t left = __ballot_sync(0xffffffffu, any != 0);
+  while (left) {
+    const int q = __ffs(left) - 1, at = ((tid & ~31) + q) * 32 + lane;
+    left &= left - 1;
+    const uint32_t change = __shfl_sync(0xffffffffu, any, q), set = __shfl_sync(0xffffffffu, now, q);
+    if (((change >> lane) & 1u) && at < width)
+      counts[at] = PROMPT ? ((set >> lane) & 1u) << 31 : s_word[at];
+  }
+  if (now != old) seen[tid] = now;
 }
 
 // ---------------------------------------------------------------- host side
@@ -735,10 +819,18 @@ SV_API sv_status spec_count_tokens(const sv_count_args *a, void *stream) {
   P.a = *a;
   P.words = (a->vocab + 31) / 32;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (a->flags & SV_COUNT_RESET)
-    clear_kernel<<<dim3((P.words + kNT - 1) / kNT, a->batch), kNT, 0, s>>>(P);
-  const int64_t threads = a->num_tokens > a->batch ? a->num_tokens : a->batch;
-  count_kernel<<<static_cast<unsigned>((threads + kNT - 1) / kNT), kNT, 0, s>>>(P);
+  if (a->flags & SV_COUNT_RESET) {
+    // For a prompt the slices are as large as a CTA can be (64 prompts of 1024 to
+    // 4096 tokens, V = 128256: 9.3 us with 8192 tokens a slice); counts take
+    // shared memory.
+    auto slices = [&](int threads) { return static_cast<unsigned>((a->vocab + 32 * threads - 1) / (32 * threads)); };
+    if (a->flags & SV_COUNT_PROMPT) reset_kernel<1024, true><<<dim3(a->batch, slices(1024)), 1024, 0, s>>>(P);
+    else reset_kernel<256, false><<<dim3(a->batch, slices(256)), 256, 0, s>>>(P);
+  } else {
+    const int64_t threads = a->num_tokens > a->batch ? a->num_tokens : a->batch;
+    count_kernel<<<static_cast<unsigned>((threads + kNT - 1) / kNT), kNT,
+                   a->batch <= kMaxStart ? (a->batch + 1) * 4 : 0, s>>>(P);
+  }
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return record_error(SV_ERR_CUDA, "count launch: %s", cudaGetErrorString(e));
   return SV_OK;
