@@ -50,8 +50,8 @@ enum { SV_ROPE_HALF = 0, SV_ROPE_INTERLEAVED = 1 };
 
 typedef struct sv_rope_args {
   int32_t batch;            /* B >= 0 (ignored with positions) */
-  int32_t num_q_heads;      /* Hq >= 0; 0: no q */
-  int32_t num_kv_heads;     /* Hkv >= 0; 0: no k and v */
+  int32_t num_q_heads;      /* Hq, 0..16384; 0: no q */
+  int32_t num_kv_heads;     /* Hkv, 0..16384; 0: no k and v */
   int32_t head_dim;         /* D: a multiple of 8, 8..256 */
   int32_t rot_dim;          /* even, 2..D */
   int32_t layout;           /* SV_ROPE_HALF or SV_ROPE_INTERLEAVED */
@@ -90,7 +90,8 @@ typedef struct sv_rope_args {
  * are rounded to nearest even and saturate at +-448 code values; NaN stays
  * NaN.  A sequence whose cu_q / kv_len are inconsistent with the host bounds,
  * or a row whose position is out of range, is left unwritten with
- * SV_DEV_BAD_LENGTH. */
+ * SV_DEV_BAD_LENGTH (with max_q_rows > 16, a cu_q that does not ascend may leave
+ * other sequences' rows unwritten too).  Rows behind cu_q[B] stay as they are. */
 SV_API sv_status spec_rope_rows(const sv_rope_args *rope, void *stream);
 
 /* Frequencies of the pairs, with the usual changes for contexts longer than
@@ -130,8 +131,8 @@ enum { SV_COUNT_PROMPT = 1,  /* the tokens are a prompt's: marked, not counted *
        SV_COUNT_RESET = 2 }; /* clear the batch's slots first (new requests) */
 
 typedef struct sv_count_args {
-  int32_t batch;            /* B >= 0 */
-  int32_t vocab;            /* V >= 1 */
+  int32_t batch;            /* B, 0..65535 */
+  int32_t vocab;            /* V, 1..2^23 */
   int32_t num_slots;        /* rows of the table, >= 1 */
   int32_t flags;            /* SV_COUNT_* */
   int64_t num_tokens;       /* T, the tokens in `tokens`; < 2^31 */
@@ -151,8 +152,8 @@ typedef struct sv_count_args {
 /* Adds the batch's tokens to the table.  A token outside [0, V) is skipped
  * with SV_DEV_BAD_TOKEN, a sequence with a slot outside [-1, num_slots) with
  * SV_DEV_BAD_PARAM.  start values that do not ascend within [0, num_tokens] set
- * SV_DEV_BAD_LENGTH and may leave any of the batch's tokens uncounted.  Counts
- * are exact up to 2^31 - 1. */
+ * SV_DEV_BAD_LENGTH and may leave any of the batch's tokens uncounted (slots are
+ * cleared all the same).  Counts are exact up to 2^31 - 1. */
 SV_API sv_status spec_count_tokens(const sv_count_args *count, void *stream);
 
 /* ---------------------------------------------------------------- logits
@@ -175,8 +176,7 @@ typedef struct sv_adjust_args {
   int64_t num_rows;         /* R = cu_q[B] (host copy) */
   const int32_t *cu_q;      /* [dev] [B+1] (0..B: single rows, as at a draft position) */
   const void *target;       /* [dev] [R, V] */
-  void *target_out;         /* [dev] [R, V]; may be target itself (in place: only
-                               what changes is read and written) */
+  void *target_out;         /* [dev] [R, V]; may be target itself (in place) */
   const void *draft;        /* [dev] [R - B, V] or NULL */
   void *draft_out;          /* [dev] [R - B, V] or NULL; draft itself if and only if
                                target_out is target */
@@ -194,11 +194,11 @@ typedef struct sv_adjust_args {
                                a draft position); outside [0, V): not counted */
   int64_t ctx_stride;       /* elements between ctx positions; 0 -> B */
   /* penalties */
-  float repetition;         /* > 0; 0 -> 1 (off) */
+  float repetition;         /* in [2^-64, 2^64]; 0 -> 1 (off) */
   float presence;           /* finite */
   float frequency;          /* finite */
   int32_t num_masks;        /* rows of mask (0 without one) */
-  const float *repetitions; /* [dev] [B] per-sequence values (> 0) or NULL */
+  const float *repetitions; /* [dev] [B] per-sequence values (not 0) or NULL */
   const float *presences;   /* [dev] [B] or NULL */
   const float *frequencies; /* [dev] [B] or NULL */
   /* biases */
@@ -218,7 +218,7 @@ typedef struct sv_adjust_args {
 
 /* Adjusts the target (and draft) rows.  Logits tensors 16-byte aligned.  A
  * sequence with a bad cu_q is skipped with SV_DEV_BAD_LENGTH (rows unwritten).
- * A sequence with a bad per-sequence value (repetition not > 0 or not finite,
+ * A sequence with a bad per-sequence value (repetition out of range,
  * presence or frequency not finite), slot, bias range or mask row gets rows of
  * NaN with SV_DEV_BAD_PARAM, so that the sampler fails it too; a bias token
  * outside [0, V) is ignored with SV_DEV_BAD_TOKEN. */

@@ -57,7 +57,8 @@ def seen_bits(counts):
 
 def allowed_tokens(words, V):
     """Truth per token of one mask row of 32-bit words."""
-    return np.array([(int(words[t >> 5]) >> (t & 31)) & 1 for t in range(V)], dtype=bool)
+    w = np.ascontiguousarray(words).astype("<i4").view(np.uint8)
+    return np.unpackbits(w, bitorder="little")[:V].astype(bool)
 
 
 def adjust_row(x, prompt, times, repetition, presence, frequency, bias, allowed):
@@ -95,7 +96,7 @@ def adjust_logits(target, cu_q, draft=None, draft_tokens=None, counts=None, slot
         rep, pres, freq = of(repetition, i), of(presence, i), of(frequency, i)
         slot = -1 if counts is None else i if slots is None else int(slots[i])
         rows = [r if mask_rows is None else int(mask_rows[r]) for r in range(r0, r1)]
-        fails = not (rep > 0 and all(map(math.isfinite, (rep, pres, freq)))) or slot < -1 or \
+        fails = not (2.0 ** -64 <= rep <= 2.0 ** 64 and all(map(math.isfinite, (pres, freq)))) or slot < -1 or \
             (counts is not None and slot >= len(counts)) or \
             (mask is not None and any(not -1 <= m < len(mask) for m in rows))
         word = np.zeros(V, dtype=np.int64)

@@ -30,6 +30,7 @@ namespace sv {
 namespace {
 
 constexpr int kNT = 256;                   // threads of the table's kernels
+constexpr float kMinRepetition = 0x1p-64f, kMaxRepetition = 0x1p64f;   // (its reciprocal is used)
 constexpr int kBatch = 3;                  // (sparse) rows in flight per warp
 constexpr int kAhead = 4;                  // listed tokens in flight per lane and row
 constexpr int kMaskVecs = 4;               // (sparse) vectors of a masked row in flight per lane
@@ -200,8 +201,8 @@ adjust_kernel(const __grid_constant__ AdjustParams P) {
 
   const bool penal = rep != 1.0f || pres != 0.0f || freq != 0.0f;
   const int nb = b1 - b0;
-  bool bad = !(rep > 0.0f) || !isfinite(rep) || !isfinite(pres) || !isfinite(freq) || slot < -1 ||
-             slot >= max(a.num_slots, 0) || b0 < 0 || b1 < b0 || b1 > a.num_bias;
+  bool bad = !(rep >= kMinRepetition && rep <= kMaxRepetition) || !isfinite(pres) || !isfinite(freq) ||
+             slot < -1 || slot >= max(a.num_slots, 0) || b0 < 0 || b1 < b0 || b1 > a.num_bias;
   int my_mask = -1;                                          // lane j: mask row of block row j
   if (a.mask && lane < Ri) my_mask = a.mask_rows ? a.mask_rows[r0 + lane] : r0 + lane;
   const int drafts = penal && a.draft_tokens ? Ri - 1 : 0;
@@ -595,7 +596,7 @@ __global__ void __launch_bounds__(NT) reset_kernel(const __grid_constant__ Count
     const int s1 = a.start[j + 1];
     const bool good = s0 >= 0 && s1 >= s0 && s1 <= a.num_tokens;
     n = good ? s1 - s0 : 0;
-    if (good && a.num_accepted) n = min(n, max(a.num_accepted[j], -1) + 1);
+    if (good && a.num_accepted && a.num_accepted[j] < n) n = max(a.num_accepted[j] + 1, 0);
     return good;
   };
   int s0, n;
@@ -739,8 +740,8 @@ sv_status check_adjust(const sv_adjust_args *a) {
   if (a->num_rows < a->batch || a->num_rows > static_cast<int64_t>(a->batch) * a->max_q_rows)
     return record_error(SV_ERR_INVALID, "adjust: num_rows %lld inconsistent with batch %d and max_q_rows %d",
                         static_cast<long long>(a->num_rows), a->batch, a->max_q_rows);
-  if (!std::isfinite(a->repetition) || a->repetition < 0.0f)
-    return bad("repetition must be finite and > 0 (0 = off)");
+  if (a->repetition != 0.0f && !(a->repetition >= kMinRepetition && a->repetition <= kMaxRepetition))
+    return bad("repetition outside [2^-64, 2^64] (0 = off)");
   if (!std::isfinite(a->presence) || !std::isfinite(a->frequency))
     return bad("presence and frequency must be finite");
   if (a->num_ctx < 0 || a->num_ctx > 1024)
@@ -773,8 +774,8 @@ sv_status check_count(const sv_count_args *a) {
   if (!a) return bad("null arguments");
   if (a->batch < 0 || a->batch > 65535)
     return record_error(SV_ERR_UNSUPPORTED, "count: batch %d outside [0, 65535]", a->batch);
-  if (a->vocab < 1 || a->vocab > (1 << 30))
-    return record_error(SV_ERR_INVALID, "count: vocab %d", a->vocab);
+  if (a->vocab < 1 || a->vocab > (1 << 23))
+    return record_error(SV_ERR_UNSUPPORTED, "count: vocab %d outside [1, 2^23]", a->vocab);
   if (a->num_slots < 1) return record_error(SV_ERR_INVALID, "count: num_slots %d", a->num_slots);
   if (a->flags & ~(SV_COUNT_PROMPT | SV_COUNT_RESET))
     return record_error(SV_ERR_INVALID, "count: flags %d", a->flags);

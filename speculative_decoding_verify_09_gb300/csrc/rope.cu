@@ -26,6 +26,7 @@ namespace {
 
 constexpr int kNT = 256;
 constexpr int kMaxDim = 256;
+constexpr int kMaxHeads = 16384;                     // of q, and of k and v
 constexpr int kMinRowThreads = 64;                   // threads that share one row, at least
 constexpr int kMaxRows = kNT / kMinRowThreads;       // rows per CTA, at most
 
@@ -41,7 +42,8 @@ struct RopeParams {
   int nq, nk, heads;            // q heads, k heads, all heads of a row (q, k, then v)
   int gshift, row_shift;        // log2 threads per head, per row
   int heads_per_cta;
-  int64_t num_rows, slots;
+  int64_t num_rows, slots;      // slots: rows, or max_q_rows for every sequence
+  int by_row;                   // slots are rows, whose sequences are searched
   int64_t q_stride, k_stride, v_stride;
   float mscale, k_scale, v_scale;
   float k_inverse, v_inverse;   // reciprocals of scales that are powers of two, else 0
@@ -115,6 +117,12 @@ __device__ __forceinline__ void store_codes(uint8_t *p, const float (&x)[N], flo
   }
 }
 
+// Whether sequence i's rows agree with the host's bounds.
+__device__ __forceinline__ bool good_sequence(const RopeParams &P, int i) {
+  const int r0 = P.cu_q[i], r1 = P.cu_q[i + 1];
+  return r0 >= 0 && r1 >= r0 && r1 <= P.num_rows && r1 - r0 <= P.max_q_rows && P.kv_len[i] >= 0;
+}
+
 // Row and position of slot `slot`; false if there is no such row (or a bad one).
 __device__ __forceinline__ bool find_row(const RopeParams &P, int64_t slot, int64_t &row,
                                          int64_t &pos, bool &bad) {
@@ -126,14 +134,25 @@ __device__ __forceinline__ bool find_row(const RopeParams &P, int64_t slot, int6
     bad = pos <= -(int64_t{1} << 31) || pos >= (int64_t{1} << 31);
     return !bad;
   }
-  const int i = static_cast<int>(static_cast<uint32_t>(slot) / static_cast<uint32_t>(P.max_q_rows));
-  const int j = static_cast<int>(slot) - i * P.max_q_rows;
+  int i, j;
+  if (P.by_row) {                 // the last sequence that starts at or before the row
+    int lo = 0, hi = P.batch;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (P.cu_q[mid] <= slot) lo = mid; else hi = mid;
+    }
+    i = lo;
+    j = static_cast<int>(slot) - P.cu_q[i];
+  } else {
+    i = static_cast<int>(static_cast<uint32_t>(slot) / static_cast<uint32_t>(P.max_q_rows));
+    j = static_cast<int>(slot) - i * P.max_q_rows;
+  }
   const int r0 = P.cu_q[i], r1 = P.cu_q[i + 1], L = P.kv_len[i];
-  if (r0 < 0 || r1 < r0 || r1 > P.num_rows || r1 - r0 > P.max_q_rows || L < 0) {
+  if (!good_sequence(P, i)) {
     bad = true;
     return false;
   }
-  if (j >= r1 - r0) return false;
+  if (j < 0 || j >= r1 - r0) return false;
   row = r0 + j;
   pos = static_cast<int64_t>(L) + j;
   return true;
@@ -163,6 +182,10 @@ __global__ void __launch_bounds__(kNT, min_ctas<T, G, KV8>()) rope_kernel(const 
   const bool live = find_row(P, static_cast<int64_t>(blockIdx.x) * (kNT >> P.row_shift) + rl, row,
                              pos, bad);
   if (bad && t == 0 && blockIdx.y == 0) set_status(P.dev_status, SV_DEV_BAD_LENGTH);
+  if (P.by_row && blockIdx.y == 0)                       // (a bad sequence need not be found by a row)
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * kNT + threadIdx.x; i < P.batch;
+         i += static_cast<int64_t>(gridDim.x) * kNT)
+      if (!good_sequence(P, static_cast<int>(i))) set_status(P.dev_status, SV_DEV_BAD_LENGTH);
 
   // this thread's column: element offsets inside a head
   constexpr int N = G == kNeighbor ? 8 : G;
@@ -286,9 +309,9 @@ sv_status check_rope(const sv_rope_args *a) {
     return record_error(SV_ERR_INVALID, "rope: dtype %d", a->dtype);
   if (a->kv_dtype != 0 && a->kv_dtype != SV_E4M3)
     return record_error(SV_ERR_INVALID, "rope: kv_dtype %d (0 or SV_E4M3)", a->kv_dtype);
-  if (a->num_q_heads < 0 || a->num_q_heads > 65535 || a->num_kv_heads < 0 || a->num_kv_heads > 65535)
-    return record_error(SV_ERR_INVALID, "rope: heads Hq=%d Hkv=%d outside [0, 65535]",
-                        a->num_q_heads, a->num_kv_heads);
+  if (a->num_q_heads < 0 || a->num_q_heads > kMaxHeads || a->num_kv_heads < 0 || a->num_kv_heads > kMaxHeads)
+    return record_error(SV_ERR_INVALID, "rope: heads Hq=%d Hkv=%d outside [0, %d]", a->num_q_heads,
+                        a->num_kv_heads, kMaxHeads);
   if (a->head_dim < 8 || a->head_dim > kMaxDim || a->head_dim % 8)
     return record_error(SV_ERR_UNSUPPORTED, "rope: head_dim %d (built: multiples of 8 up to %d)",
                         a->head_dim, kMaxDim);
@@ -350,7 +373,11 @@ SV_API sv_status spec_rope_rows(const sv_rope_args *a, void *stream) {
   P.D = a->head_dim;
   P.rot = a->rot_dim;
   P.num_rows = a->num_rows;
+  // Every sequence has max_q_rows slots, as in a step, unless most would stay
+  // empty (prompts of different lengths): then a row searches its sequence.
   P.slots = a->positions ? a->num_rows : static_cast<int64_t>(a->batch) * a->max_q_rows;
+  P.by_row = !a->positions && a->max_q_rows > 16 && P.slots > a->num_rows + a->num_rows / 4;
+  if (P.by_row) P.slots = a->num_rows;
   const int64_t D = a->head_dim;
   P.q_stride = a->q_stride ? a->q_stride : P.Hq * D;
   P.k_stride = a->k_stride ? a->k_stride : P.Hkv * D;

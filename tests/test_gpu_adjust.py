@@ -1,9 +1,9 @@
 """GPU parity of spec_adjust_logits with the float64 oracle.
 
-Tolerance per value: the quotient or product by the repetition penalty, the
-fused frequency * times + presence (times rounded to fp32), the subtraction and
-the bias sum round at 2^-24 of their results each, all bounded by
-S = |x| max(r, 1 / r) + |f| times + |p| + |bias|: below 5 * 2^-24 S; the store
+Tolerance per value: the repetition penalty's reciprocal and the product with
+it, the fused frequency * times + presence, the subtraction and the bias sum
+round at 2^-24 of their results each, all bounded by
+S = |x| max(r, 1 / r) + |f| times + |p| + |bias|: at most 5 * 2^-24 S; the store
 rounds by half a step, 2^-8 of the value for bf16.  Values that nothing touches
 keep their bits."""
 import numpy as np
@@ -185,6 +185,24 @@ def test_large_vocabulary(api):
     c.run(in_place=True)
 
 
+@pytest.mark.parametrize("V,dtype", [(65536, "bf16"), (65541, "bf16"), (70003, "f32")])
+@pytest.mark.parametrize("kw", [dict(ctx=2, bias=40, masked=0.4, hist=3000), dict(masked=1.0, allow=0.02),
+                                dict(penal=False, bias=3), dict(hist=60000, draft=False)])
+def test_in_place_of_many_long_rows(api, V, dtype, kw):
+    """Sequences and vocabulary enough that single tokens are changed in memory:
+    thin and dense lists, single rows and whole blocks, parts of a block's rows."""
+    c = Case(api, [1, 3, 2] * 10, V, dtype, seed=V, **kw)
+    c.run(in_place=True)
+
+
+@pytest.mark.parametrize("rows", [[16, 2], [9] * 13])
+@pytest.mark.parametrize("V", [4097, 33001])
+def test_rows_split_over_ctas(api, rows, V):
+    """Few sequences with many rows: the rows of a block are worked on in parts."""
+    for in_place in (False, True):
+        Case(api, rows, V, seed=3, ctx=1, bias=9, masked=0.3, hist=300).run(in_place)
+
+
 def test_scalar_penalties(api):
     c = Case(api, [2, 3], 3001, "f32", seed=4, penal=False)
     c.ref.update(repetition=1.25, presence=0.5, frequency=-0.125)
@@ -265,7 +283,7 @@ def test_biases_twice_out_of_range_and_infinite(api):
 
 
 @pytest.mark.parametrize("what,value", [
-    ("repetitions", 0.0), ("repetitions", -1.0), ("repetitions", np.nan), ("repetitions", np.inf),
+    ("repetitions", 0.0), ("repetitions", -1.0), ("repetitions", 1e-20), ("repetitions", 1e20), ("repetitions", np.nan), ("repetitions", np.inf),
     ("presences", np.nan), ("frequencies", -np.inf), ("slots", 9), ("slots", -2),
     ("mask_rows", 99), ("mask_rows", -2)])
 @pytest.mark.parametrize("in_place", [False, True])

@@ -75,6 +75,21 @@ def test_one_token_many_times(api):
     assert t.ref[1, 7] == np.int32(-2 ** 31 + (tok == 7).sum())
 
 
+@pytest.mark.parametrize("prompt", [False, True])
+@pytest.mark.parametrize("V", [8191, 8193, 32769, 70000])
+def test_reset_over_slices(api, V, prompt):
+    """Vocabularies of several slices, prompts longer than a CTA takes at once,
+    and three sequences on one slot."""
+    rng = np.random.default_rng(V)
+    t = Table(api, 4, V, rng)
+    lens = [9000, 0, 31, 17000, 1]
+    start = np.concatenate([[0], np.cumsum(lens)])
+    tok = (rng.random(start[-1]) ** 3 * V).astype(np.int64)
+    t.add(tok, start, slots=[1, 3, 1, 0, 1], prompt=prompt, reset=True)
+    n = np.array([2 ** 31 - 1, -1, 3, -2 ** 31, 0])
+    t.add(tok, start, slots=[0, 2, 1, 3, 1], prompt=prompt, reset=True, num_accepted=n)
+
+
 def test_shared_and_absent_slots(api):
     t = Table(api, 3, 50, np.random.default_rng(3))
     t.add([1, 2, 3, 4, 5, 6], [0, 2, 4, 6], slots=[2, -1, 2], reset=True)

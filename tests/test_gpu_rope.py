@@ -198,6 +198,34 @@ def test_inconsistent_sequences_are_skipped(api, how):
         assert bool((c.out[p][skipped] == 123).all()), (how, p)
 
 
+@pytest.mark.parametrize("cu", [[0, 30, 10, 40, 60], [0, 20, 70, 71, 60], [-5, 20, 40, 50, 60],
+                                [0, 20, 20, 20, 60], [0, 0, 0, 0, 0]])
+def test_rows_that_search_their_sequence(api, cu):
+    """A bound of 60 rows on four sequences of 60 rows in all: rows of sequences
+    that are consistent are right or (where cu_q does not ascend) untouched."""
+    c = Case(api, [20, 20, 10, 10], 3, 1, 64, 64, seed=6)
+    a = np.array(cu)
+    good = (a[:-1] >= 0) & (a[1:] >= a[:-1]) & (a[1:] <= 60)
+    pos = np.zeros(60, dtype=np.int64)
+    owner = np.full(60, -1)
+    for i in range(4):
+        if good[i]:
+            owner[a[i]:a[i + 1]] = i
+            pos[a[i]:a[i + 1]] = c.kv_len[i] + np.arange(a[i + 1] - a[i])
+    api.spec_rope_rows(c.args(cu_q=dev(a.astype(np.int32)), max_q_rows=60))
+    torch.cuda.synchronize()
+    assert int(c.status.item()) == (0 if good.all() else oracle.DEV_BAD_LENGTH)
+    touched = (c.out["v"] != 123).flatten(1).any(1).cpu().numpy()
+    assert not touched[owner < 0].any()
+    if good.all():
+        assert touched[owner >= 0].all()
+    if (np.bincount(np.concatenate([np.arange(a[i], a[i + 1]) for i in range(4) if good[i]] + [[0]])
+                    .astype(int)) <= 2).all() and touched.any():
+        alone = [r for r in np.flatnonzero(touched)
+                 if sum(good[i] and a[i] <= r < a[i + 1] for i in range(4)) == 1]
+        c.check(positions=pos, rows=alone)
+
+
 def test_rows_behind_the_last_sequence_stay(api):
     for rows in ([2, 3], [400, 500]):
         c = Case(api, rows, 4, 2, 128, 128, extra_rows=9)

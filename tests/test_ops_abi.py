@@ -48,7 +48,7 @@ INVALID, UNSUPPORTED = 1, 4
 
 @pytest.mark.parametrize("kw,status", [
     (dict(dtype=2), INVALID), (dict(dtype=9), INVALID), (dict(kv_dtype=1), INVALID),
-    (dict(num_q_heads=-1), INVALID), (dict(num_kv_heads=70000), INVALID),
+    (dict(num_q_heads=-1), INVALID), (dict(num_kv_heads=16385), INVALID), (dict(num_q_heads=16385), INVALID),
     (dict(head_dim=12), UNSUPPORTED), (dict(head_dim=0), UNSUPPORTED),
     (dict(head_dim=264, rot_dim=64), UNSUPPORTED),
     (dict(rot_dim=3), INVALID), (dict(rot_dim=0), INVALID), (dict(rot_dim=130), INVALID),
@@ -89,8 +89,8 @@ def _count(b, **kw):
 
 
 @pytest.mark.parametrize("kw,status", [
-    (dict(batch=-1), UNSUPPORTED), (dict(batch=65536), UNSUPPORTED), (dict(vocab=0), INVALID),
-    (dict(num_slots=0), INVALID), (dict(flags=4), INVALID), (dict(num_tokens=-1), INVALID),
+    (dict(batch=-1), UNSUPPORTED), (dict(batch=65536), UNSUPPORTED), (dict(vocab=0), UNSUPPORTED),
+    (dict(vocab=(1 << 23) + 1), UNSUPPORTED), (dict(num_slots=0), INVALID), (dict(flags=4), INVALID), (dict(num_tokens=-1), INVALID),
     (dict(num_tokens=1 << 31), INVALID), (dict(start=0), INVALID), (dict(tokens=0), INVALID),
     (dict(counts=0), INVALID), (dict(seen=0), INVALID),
 ])
@@ -118,7 +118,7 @@ def _adjust(b, **kw):
     (dict(dtype=2), INVALID), (dict(max_q_rows=0), INVALID), (dict(max_q_rows=17), INVALID),
     (dict(num_rows=1), INVALID), (dict(num_rows=11), INVALID),
     (dict(repetition=-1.0), INVALID), (dict(repetition=float("inf")), INVALID),
-    (dict(repetition=float("nan")), INVALID), (dict(presence=float("inf")), INVALID),
+    (dict(repetition=float("nan")), INVALID), (dict(repetition=1e-20), INVALID), (dict(presence=float("inf")), INVALID),
     (dict(frequency=float("nan")), INVALID), (dict(num_ctx=-1), INVALID),
     (dict(num_ctx=1025), INVALID), (dict(ctx_stride=-1), INVALID), (dict(ctx_tokens=0), INVALID),
     (dict(num_bias=-1), INVALID), (dict(num_bias=1 << 31), INVALID),

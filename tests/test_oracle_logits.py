@@ -62,3 +62,5 @@ def test_bits_round_trip():
     assert seen.shape == (3, 3)
     for s in range(3):
         assert np.array_equal(oracle.allowed_tokens(seen[s], 77), counts[s] != 0)
+        by_hand = [(int(seen[s, t >> 5]) >> (t & 31)) & 1 for t in range(77)]
+        assert by_hand == (counts[s] != 0).astype(int).tolist()
