@@ -395,14 +395,20 @@ adjust_kernel(const __grid_constant__ AdjustParams P) {
       const bool barred = (masked >> j) & 1u;
       const uint8_t *bits = row + C::kMaskAt;
       T *out = row_out(line) + from - mis;                   // vectors as they were read
-      if (uw == C::kUnitTokens && mis == 0) {
+      if (uw == C::kUnitTokens) {
 #pragma unroll
         for (int q = 0; q < C::kVecs; ++q) {
-          const int v = (lane + q * 32) * kPer;
+          const int v = (lane + q * 32) * kPer, t = v - mis;
+          if (RAGGED && t < 0) continue;                     // (shared with the tokens before)
           Piece<T, kPer> piece;
           piece.w = *reinterpret_cast<const uint4 *>(row + (lane + q * 32) * 16);
-          if (barred) piece.bar(mask_bits<kPer>(bits, v, C::kUnitTokens / 8));
+          if (barred) piece.bar(mask_bits<kPer>(bits, t, C::kUnitTokens / 8));
           *reinterpret_cast<uint4 *>(out + v) = piece.w;
+        }
+        if (RAGGED && mis && lane < kPer) {                  // the two ends, an element per lane
+          const int t = lane >= mis ? lane - mis : C::kUnitTokens - mis + lane;
+          const bool allowed = !barred || ((bits[t >> 3] >> (t & 7)) & 1u);
+          out[t + mis] = allowed ? x[t] : E::kNegInf;
         }
       } else {
 #pragma unroll 1
