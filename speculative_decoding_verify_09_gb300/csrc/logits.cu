@@ -523,7 +523,7 @@ adjust_kernel(const __grid_constant__ AdjustParams P) {
 }
 
 // ---------------------------------------------------------------- count
-constexpr int kTokens = 8;                 // of its sequence that a resetting thread has in flight
+constexpr int kTokens = 4;                 // of its sequence that a resetting thread has in flight
 constexpr int kMaxStart = 4096;            // sequences whose start values are kept in shared memory
 
 struct CountParams {
@@ -638,7 +638,7 @@ __global__ void __launch_bounds__(NT) reset_kernel(const __grid_constant__ Count
         if (k0 + u * NT >= n) break;
         if (t[u] >= t0 && t[u] - t0 < width) {
           const int at = t[u] - t0;
-          if (!((s_bits[at >> 5] >> (at & 31)) & 1u)) atomicOr(&s_bits[at >> 5], 1u << (at & 31));
+          atomicOr(&s_bits[at >> 5], 1u << (at & 31));
           if constexpr (!PROMPT) atomicAdd(&s_word[at], 1u);
         } else if (head && (t[u] < 0 || t[u] >= a.vocab)) {
           set_status(a.dev_status, SV_DEV_BAD_TOKEN);
