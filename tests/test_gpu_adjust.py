@@ -273,6 +273,32 @@ def test_special_values(api):
         assert np.array_equal(host_bits(plain.ot).view(np.uint8), x.view(np.uint8))
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_rows_of_the_lowest_value(api, dtype):
+    """Masks by the type's lowest finite value: a known token's product beyond the type is -inf
+    (which the sampler reads as masked), everything else keeps the value."""
+    V = 1500
+    c = Case(api, [2, 2], V, dtype, seed=18, draft=False, hist=300)
+    low = f32_to_bf16_bits(np.float32([-3.3895314e38]))[0] if dtype == "bf16" else \
+        np.finfo(np.float32).min
+    c.target = np.full_like(c.target, low)
+    c.kw["repetitions"] = c.ref["repetition"] = np.array([1.5, 0.5], np.float32)
+    for in_place in (False, True):
+        api.spec_adjust_logits(c.args(in_place))
+        torch.cuda.synchronize()
+        want, _, st = oracle.adjust_logits(c.target, c.cu, None, c.tokens, **c.ref)
+        got = oracle.to_f64(host_bits(c.ot))
+        most = 3.39e38 if dtype == "bf16" else float(np.finfo(np.float32).max)
+        over = want < -most * 1.01
+        assert over.any() and np.all(got[over] == -np.inf)
+        assert np.all(np.abs(got[~over] - want[~over]) <= 2.0 ** -8 * np.abs(want[~over]))
+        assert int(c.status.item()) == st == 0
+
+
+def test_many_sequences(api):
+    Case(api, [1] * 3000 + [2] * 2100, 130, seed=20, hist=20, ctx=1, bias=3, masked=0.2).run()
+
+
 def test_biases_twice_out_of_range_and_infinite(api):
     c = Case(api, [2, 1, 1, 1], 2100, "f32", seed=10, draft=False)
     c.set_bias([[(5, 1.0), (5, -2.0), (2099, 3.0)], [(2100, 1.0), (-1, 1.0), (7, 0.0), (8, 4.0)],

@@ -97,6 +97,18 @@ def test_shared_and_absent_slots(api):
     t.add([1, 2, 3], [0, 1, 2, 3])              # no slots: sequence i has row i
 
 
+def test_many_sequences(api):
+    """More sequences than start values are kept in shared memory for."""
+    B = 5000
+    rng = np.random.default_rng(9)
+    t = Table(api, B, 40, rng)
+    start = np.concatenate([[0], np.cumsum(rng.integers(0, 4, B))])
+    tok = rng.integers(0, 40, start[-1])
+    t.add(tok, start, slots=rng.integers(-1, B, B))
+    t.add(tok, start, slots=rng.permutation(B), reset=True, prompt=True)
+    t.add(tok, start, slots=rng.integers(0, 7, B), reset=True)
+
+
 def test_bad_tokens_and_slots(api):
     t = Table(api, 3, 50, np.random.default_rng(4))
     t.add([1, 50, -1, 4, 2 ** 31 - 1, 6], [0, 2, 4, 6], slots=[0, 1, 2],

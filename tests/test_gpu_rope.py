@@ -152,6 +152,18 @@ def test_heads_and_absent_tensors(api, Hq, Hkv, parts, rows):
     c.check()
 
 
+@pytest.mark.parametrize("longest", [3, 90])
+def test_many_sequences(api, longest):
+    rng = np.random.default_rng(longest)
+    rows = rng.integers(0, 4, 5000).tolist()
+    rows[77] = longest
+    c = Case(api, rows, 2, 1, 16, 8, seed=3)
+    api.spec_rope_rows(c.args())
+    c.check(rows=np.concatenate([np.arange(40), np.arange(c.live - 40, c.live)]))
+    assert int(c.status.item()) == 0
+    assert bool((c.out["q"] != 123).flatten(1).any(1).all())
+
+
 @pytest.mark.parametrize("n", [1, 5, 2000])
 @pytest.mark.parametrize("layout", ["half", "interleaved"])
 def test_positions_near_and_far(api, n, layout):
