@@ -27,8 +27,7 @@ namespace {
 constexpr int kNT = 256;
 constexpr int kMaxDim = 256;
 constexpr int kMaxHeads = 16384;                     // of q, and of k and v
-constexpr int kMinRowThreads = 64;                   // threads that share one row, at least
-constexpr int kMaxRows = kNT / kMinRowThreads;       // rows per CTA, at most
+constexpr int kPasses = 6;                           // heads that one thread works on, about
 
 // How a thread's elements of a head meet their partners.  G = 8, 4, 2, 1 (the
 // half layout): G elements and the G that are rot_dim / 2 further on, i.e. G
@@ -40,7 +39,9 @@ constexpr int kNeighbor = 0;
 struct RopeParams {
   int batch, max_q_rows, Hq, Hkv, D, rot;
   int nq, nk, heads;            // q heads, k heads, all heads of a row (q, k, then v)
-  int gshift, row_shift;        // log2 threads per head, per row
+  int columns, per_column;      // threads that share a head, and 2^16 / columns rounded up: (x *
+                                // per_column) >> 16 is x / columns for x up to 256
+  int row_shift, pairs;         // log2 threads that share a row; its room for cos and for sin
   int heads_per_cta;
   int64_t num_rows, slots;      // slots: rows, or max_q_rows for every sequence
   int by_row;                   // slots are rows, whose sequences are searched
@@ -158,21 +159,28 @@ __device__ __forceinline__ bool find_row(const RopeParams &P, int64_t slot, int6
   return true;
 }
 
-// CTAs per SM that the registers are capped for, as measured (32768 rows of 48 heads of 128: bf16 G = 8 122 us at 4, 134 at 3, 131 at 5; fp32
-// 237 us at 3, 253 at 4; with codes 131 us at 3, 165 at 5).
+// Heads that a thread has in flight (and as many that it works on): narrow
+// columns load little at a time.  CTAs per SM that the registers are capped for.
+// As measured (32768 rows of 48 heads of 128): bf16 G = 8 122 us at 4 CTAs, 134 at
+// 3, 131 at 5; fp32 237 us at 3, 253 at 4; with codes 131 us at 3, 165 at 5; one,
+// two, four heads at G = 1 304, 266, 232 us, at G = 2 180, 168, 150 us, one and two
+// at G = 4 162 and 134 us.
+template <int G, bool KV8>
+struct InFlight {
+  static constexpr int kHeads = G == 1 || G == 2 ? (KV8 ? 2 : 4) : G == 4 ? 2 : 1;
+};
 template <typename T, int G, bool KV8>
 constexpr int min_ctas() {
-  return G == 8 || G == kNeighbor ? (KV8 || sizeof(T) == 4 ? 3 : 4) : G == 4 ? 4 : 6;
+  return (G == 8 || G == kNeighbor) && (KV8 || sizeof(T) == 4) ? 3 : 4;
 }
 
 template <typename T, int G, bool KV8>
 __global__ void __launch_bounds__(kNT, min_ctas<T, G, KV8>()) rope_kernel(const RopeParams P) {
-  __shared__ __align__(16) float s_cos[kMaxRows][kMaxDim / 2 + 4];
-  __shared__ __align__(16) float s_sin[kMaxRows][kMaxDim / 2 + 4];
+  extern __shared__ __align__(16) float s_turn[];        // [rows][cos, sin][pairs]
   const int row_threads = 1 << P.row_shift;
   const int rl = threadIdx.x >> P.row_shift, t = threadIdx.x & (row_threads - 1);
-  const int c = t & ((1 << P.gshift) - 1), hl = t >> P.gshift;
-  const int hstep = row_threads >> P.gshift;
+  const int hl = (t * P.per_column) >> 16, c = t - hl * P.columns;
+  const int hstep = (row_threads * P.per_column) >> 16;
   const int h_begin = blockIdx.y * P.heads_per_cta;
   const int h_end = min(P.heads, h_begin + P.heads_per_cta);
   const int half = P.rot >> 1;
@@ -192,10 +200,11 @@ __global__ void __launch_bounds__(kNT, min_ctas<T, G, KV8>()) rope_kernel(const 
   const bool turn = G == kNeighbor ? 2 * N * c < P.rot : c < half / N;   // the column holds pairs
   const int o0 = G == kNeighbor ? 2 * N * c : turn ? N * c : P.rot + 2 * N * (c - half / N);
   const int o1 = G != kNeighbor && turn ? o0 + half : o0 + N;
-  const bool column = live && o0 < P.D;
+  const bool column = live && hl < hstep;
   const bool both = o1 < P.D;                            // (the last column may be single)
 
-  Vec<T, N> cur[2], nxt[2];
+  constexpr int U = InFlight<G, KV8>::kHeads;
+  Vec<T, N> cur[U][2], nxt[U][2];
   // the row's heads, numbered through q, k, v: element h D of these
   const int k0 = P.nq * P.D, v0 = (P.nq + P.nk) * P.D;
   const T *in_q = static_cast<const T *>(P.q) + row * P.q_stride;
@@ -208,17 +217,19 @@ __global__ void __launch_bounds__(kNT, min_ctas<T, G, KV8>()) rope_kernel(const 
     v[0].load(p + o0);
     if (both) v[1].load(p + o1);
   };
-  fetch(cur, h_begin + hl);
+#pragma unroll
+  for (int u = 0; u < U; ++u) fetch(cur[u], h_begin + hl + u * hstep);
 
   // cos and sin of the row's pairs, by the threads that share the row
+  float *s_cos = s_turn + rl * 2 * P.pairs, *s_sin = s_cos + P.pairs;
   const bool any_turn = h_begin < P.nq + P.nk;
   if (live && any_turn) {
     for (int p = t; p < half; p += row_threads) {
       const uint64_t part = static_cast<uint64_t>(pos) * __ldg(P.turns + p);
       float sn, cs;
       sincospif(__ll2float_rn(static_cast<int64_t>(part)) * 0x1p-63f, &sn, &cs);
-      s_cos[rl][p] = cs * P.mscale;
-      s_sin[rl][p] = sn * P.mscale;
+      s_cos[p] = cs * P.mscale;
+      s_sin[p] = sn * P.mscale;
     }
   }
   __syncthreads();
@@ -230,8 +241,8 @@ __global__ void __launch_bounds__(kNT, min_ctas<T, G, KV8>()) rope_kernel(const 
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       const int p = N * c + i;
-      cs[i] = p < half ? s_cos[rl][p] : 1.0f;
-      sn[i] = p < half ? s_sin[rl][p] : 0.0f;
+      cs[i] = p < half ? s_cos[p] : 1.0f;
+      sn[i] = p < half ? s_sin[p] : 0.0f;
     }
   }
   const bool whole = N * c + N <= half;                  // (kNeighbor) nothing but pairs in the column
@@ -241,13 +252,12 @@ __global__ void __launch_bounds__(kNT, min_ctas<T, G, KV8>()) rope_kernel(const 
   T *out_k = static_cast<T *>(P.k_out) + kv_row - k0, *out_v = static_cast<T *>(P.v_out) + kv_row - v0;
   uint8_t *codes_k = static_cast<uint8_t *>(P.k_out) + kv_row - k0;
   uint8_t *codes_v = static_cast<uint8_t *>(P.v_out) + kv_row - v0;
-  for (int h = h_begin + hl; h < h_end; h += hstep) {
-    fetch(nxt, h + hstep);
+  auto finish = [&](Vec<T, N> (&v)[2], int h) {
     const bool is_q = h < P.nq, is_k = !is_q && h < P.nq + P.nk, codes = KV8 && !is_q;
     float x[N], y[N];
     if ((turn && (is_q || is_k)) || codes) {
-      cur[0].get(x);
-      cur[1].get(y);
+      v[0].get(x);
+      v[1].get(y);
     }
     if (turn && (is_q || is_k)) {
       if constexpr (G != kNeighbor) {
@@ -272,8 +282,8 @@ __global__ void __launch_bounds__(kNT, min_ctas<T, G, KV8>()) rope_kernel(const 
         turn4(y, 4);
       }
       if (!codes) {
-        cur[0].set(x);
-        cur[1].set(y);
+        v[0].set(x);
+        v[1].set(y);
       }
     }
     if (codes) {
@@ -283,21 +293,31 @@ __global__ void __launch_bounds__(kNT, min_ctas<T, G, KV8>()) rope_kernel(const 
       if (both) store_codes(o + o1, y, scale, inverse);
     } else {
       T *o = (is_q ? out_q : is_k ? out_k : out_v) + h * P.D;
-      cur[0].store(o + o0);
-      if (both) cur[1].store(o + o1);
+      v[0].store(o + o0);
+      if (both) v[1].store(o + o1);
     }
+  };
+  for (int h = h_begin + hl; h < h_end; h += U * hstep) {
 #pragma unroll
-    for (int n = 0; n < 2; ++n) cur[n] = nxt[n];
+    for (int u = 0; u < U; ++u) fetch(nxt[u], h + (U + u) * hstep);
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (h + u * hstep < h_end) finish(cur[u], h + u * hstep);
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int n = 0; n < 2; ++n) cur[u][n] = nxt[u][n];
   }
 }
 
 template <typename T, bool KV8>
 void launch_shape(int g, dim3 grid, const RopeParams &P, cudaStream_t s) {
-  if (g == kNeighbor) rope_kernel<T, kNeighbor, KV8><<<grid, kNT, 0, s>>>(P);
-  else if (g == 8) rope_kernel<T, 8, KV8><<<grid, kNT, 0, s>>>(P);
-  else if (g == 4) rope_kernel<T, 4, KV8><<<grid, kNT, 0, s>>>(P);
-  else if (g == 2) rope_kernel<T, 2, KV8><<<grid, kNT, 0, s>>>(P);
-  else rope_kernel<T, 1, KV8><<<grid, kNT, 0, s>>>(P);
+  const size_t smem = static_cast<size_t>(kNT >> P.row_shift) * 2 * P.pairs * sizeof(float);
+  if (g == kNeighbor) rope_kernel<T, kNeighbor, KV8><<<grid, kNT, smem, s>>>(P);
+  else if (g == 8) rope_kernel<T, 8, KV8><<<grid, kNT, smem, s>>>(P);
+  else if (g == 4) rope_kernel<T, 4, KV8><<<grid, kNT, smem, s>>>(P);
+  else if (g == 2) rope_kernel<T, 2, KV8><<<grid, kNT, smem, s>>>(P);
+  else rope_kernel<T, 1, KV8><<<grid, kNT, smem, s>>>(P);
 }
 
 bool positive(float x) { return std::isfinite(x) && x > 0.0f; }
@@ -409,22 +429,26 @@ SV_API sv_status spec_rope_rows(const sv_rope_args *a, void *stream) {
   if (a->num_rows == 0 || P.slots == 0 || P.heads == 0) return SV_OK;
 
   const int half = P.rot / 2;
-  int g = kNeighbor, columns = (P.D + 15) / 16;
+  int g = kNeighbor;
+  P.columns = (P.D + 15) / 16;
   if (a->layout == SV_ROPE_HALF) {
     g = half % 8 == 0 ? 8 : half % 4 == 0 ? 4 : half % 2 == 0 ? 2 : 1;
-    columns = half / g + (P.D - P.rot + 2 * g - 1) / (2 * g);
+    P.columns = half / g + (P.D - P.rot + 2 * g - 1) / (2 * g);
   }
-  while ((1 << P.gshift) < columns) ++P.gshift;
   const int sms = device_sms();
   if (sms <= 0) return record_error(SV_ERR_CUDA, "rope: no current CUDA device");
-  // A pass is one head per 1 << gshift threads; a CTA makes as many as leave about
+  // A pass is one head per P.columns threads; a CTA makes as many as leave about
   // two CTAs per SM (576 rows of 48 heads, E4M3: one pass 6.9 us, all heads 3.8
   // us; 8 rows of 96 heads: 2.3 against 2.7 us), its rows side by side: two, or
-  // four where there are rows enough (32768 rows of 48 heads, E4M3: 131 against
-  // 142 us; 1152 rows: 6.7 against 5.9 us for two).
-  const int64_t threads = (P.slots * P.heads) << P.gshift, room = 512 * static_cast<int64_t>(sms);
-  P.row_shift = std::max(P.slots >= 16 * static_cast<int64_t>(sms) ? 6 : 7, P.gshift);
-  const int at_once = (1 << P.row_shift) >> P.gshift;
+  // more where there are rows enough.
+  const int64_t threads = P.slots * P.heads * P.columns, room = 512 * static_cast<int64_t>(sms);
+  P.row_shift = 7;
+  if (P.slots >= 16 * static_cast<int64_t>(sms))
+    for (P.row_shift = 4; P.row_shift < 7 && ((1 << P.row_shift) < P.columns || (kPasses << P.row_shift) < P.heads * P.columns);)
+      ++P.row_shift;
+  P.per_column = 65536 / P.columns + 1;
+  P.pairs = (half + 7) / 4 * 4;
+  const int at_once = (1 << P.row_shift) / P.columns;
   P.heads_per_cta = static_cast<int>(std::min<int64_t>(P.heads, std::max<int64_t>(1, (threads + room - 1) / room) * at_once));
   const int rows_per_cta = kNT >> P.row_shift;
   const dim3 grid(static_cast<unsigned>((P.slots + rows_per_cta - 1) / rows_per_cta),
