@@ -439,11 +439,14 @@ SV_API sv_status spec_rope_rows(const sv_rope_args *a, void *stream) {
   if (sms <= 0) return record_error(SV_ERR_CUDA, "rope: no current CUDA device");
   // A pass is one head per P.columns threads; a CTA makes as many as leave about
   // two CTAs per SM (576 rows of 48 heads, E4M3: one pass 6.9 us, all heads 3.8
-  // us; 8 rows of 96 heads: 2.3 against 2.7 us), its rows side by side: two, or
-  // more where there are rows enough.
+  // us; 8 rows of 96 heads: 2.3 against 2.7 us).  Its rows lie side by side: two,
+  // or, once pairs of rows fill the SMs, as many as about kPasses heads per
+  // thread give (1152 rows of 48 heads, E4M3: 7.5 against 6.7 us; 2210 fp32 rows of
+  // 12 heads of 64: 5.6 against 4.0 us).
   const int64_t threads = P.slots * P.heads * P.columns, room = 512 * static_cast<int64_t>(sms);
   P.row_shift = 7;
-  if (P.slots >= 16 * static_cast<int64_t>(sms))
+  const int resident = a->kv_dtype == SV_E4M3 || a->dtype == SV_F32 ? 3 : 4;   // CTAs per SM (min_ctas)
+  if (P.slots > 2 * resident * static_cast<int64_t>(sms))
     for (P.row_shift = 4; P.row_shift < 7 && ((1 << P.row_shift) < P.columns || (kPasses << P.row_shift) < P.heads * P.columns);)
       ++P.row_shift;
   P.per_column = 65536 / P.columns + 1;
