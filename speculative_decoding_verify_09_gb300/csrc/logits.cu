@@ -129,6 +129,7 @@ adjust_kernel(const __grid_constant__ AdjustParams P) {
   __shared__ uint16_t s_tok[C::kTokens];                     // the lists: tokens in the chunk, flags
   __shared__ int s_n[C::kUnits];
 
+  wait_for_previous();
   const int r0 = a.cu_q[i], r1 = a.cu_q[i + 1];
   const float rep = a.repetitions ? a.repetitions[i] : a.repetition;
   const float pres = a.presences ? a.presences[i] : a.presence;
@@ -551,6 +552,7 @@ __global__ void __launch_bounds__(kNT) count_kernel(const __grid_constant__ Coun
   const sv_count_args &a = P.a;
   extern __shared__ __align__(16) uint32_t s_word[];
   int32_t *s_start = reinterpret_cast<int32_t *>(s_word);     // start, where it fits
+  wait_for_previous();
   const int64_t at = static_cast<int64_t>(blockIdx.x) * kNT + threadIdx.x;
   const int32_t *start = a.start;
   const int t = at < a.num_tokens ? a.tokens[at] : 0;
@@ -596,6 +598,7 @@ __global__ void __launch_bounds__(NT) reset_kernel(const __grid_constant__ Count
   const int i = blockIdx.x, tid = threadIdx.x, lane = tid & 31;
   const int t0 = blockIdx.y * kSlice, width = min(kSlice, a.vocab - t0);
   const bool head = blockIdx.y == 0;
+  wait_for_previous();
   const int slot = a.slots ? a.slots[i] : i;
   auto segment = [&](int j, int &s0, int &n) {                // tokens of sequence j
     s0 = a.start[j];
@@ -686,9 +689,8 @@ cudaError_t launch_adjust(dim3 grid, const AdjustParams &P, cudaStream_t s) {
       ready.fetch_or(bit, std::memory_order_release);
     }
   }
-  adjust_kernel<T, BYTES, UNIT, RAGGED>
-      <<<grid, C::kThreads, C::kRingBytes + (P.a.bias_start ? biases : 0), s>>>(P);
-  return cudaGetLastError();
+  return launch_behind(adjust_kernel<T, BYTES, UNIT, RAGGED>, grid, C::kThreads,
+                       C::kRingBytes + (P.a.bias_start ? biases : 0), s, P);
 }
 
 template <typename T, int BYTES, int UNIT>
@@ -826,19 +828,21 @@ SV_API sv_status spec_count_tokens(const sv_count_args *a, void *stream) {
   P.a = *a;
   P.words = (a->vocab + 31) / 32;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaError_t e;
   if (a->flags & SV_COUNT_RESET) {
     // For a prompt the slices are as large as a CTA can be (64 prompts of 1024 to
-    // 4096 tokens, V = 128256: 9.3 us with 8192 tokens a slice); counts take
-    // shared memory.
+    // 4096 tokens, V = 128256: 9.3 us with 8192 tokens a slice, 7.7 us so); counts
+    // take shared memory.
     auto slices = [&](int threads) { return static_cast<unsigned>((a->vocab + 32 * threads - 1) / (32 * threads)); };
-    if (a->flags & SV_COUNT_PROMPT) reset_kernel<1024, true><<<dim3(a->batch, slices(1024)), 1024, 0, s>>>(P);
-    else reset_kernel<256, false><<<dim3(a->batch, slices(256)), 256, 0, s>>>(P);
+    if (a->flags & SV_COUNT_PROMPT)
+      e = launch_behind(reset_kernel<1024, true>, dim3(a->batch, slices(1024)), 1024, 0, s, P);
+    else
+      e = launch_behind(reset_kernel<256, false>, dim3(a->batch, slices(256)), 256, 0, s, P);
   } else {
     const int64_t threads = a->num_tokens > a->batch ? a->num_tokens : a->batch;
-    count_kernel<<<static_cast<unsigned>((threads + kNT - 1) / kNT), kNT,
-                   a->batch <= kMaxStart ? (a->batch + 1) * 4 : 0, s>>>(P);
+    e = launch_behind(count_kernel, dim3(static_cast<unsigned>((threads + kNT - 1) / kNT)), kNT,
+                      a->batch <= kMaxStart ? (a->batch + 1) * 4 : 0, s, P);
   }
-  const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return record_error(SV_ERR_CUDA, "count launch: %s", cudaGetErrorString(e));
   return SV_OK;
 }

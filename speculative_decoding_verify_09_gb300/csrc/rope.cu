@@ -184,6 +184,7 @@ __global__ void __launch_bounds__(kNT, min_ctas<T, G, KV8>()) rope_kernel(const 
   const int h_begin = blockIdx.y * P.heads_per_cta;
   const int h_end = min(P.heads, h_begin + P.heads_per_cta);
   const int half = P.rot >> 1;
+  wait_for_previous();
 
   int64_t row = 0, pos = 0;
   bool bad;
@@ -311,13 +312,13 @@ __global__ void __launch_bounds__(kNT, min_ctas<T, G, KV8>()) rope_kernel(const 
 }
 
 template <typename T, bool KV8>
-void launch_shape(int g, dim3 grid, const RopeParams &P, cudaStream_t s) {
+cudaError_t launch_shape(int g, dim3 grid, const RopeParams &P, cudaStream_t s) {
   const size_t smem = static_cast<size_t>(kNT >> P.row_shift) * 2 * P.pairs * sizeof(float);
-  if (g == kNeighbor) rope_kernel<T, kNeighbor, KV8><<<grid, kNT, smem, s>>>(P);
-  else if (g == 8) rope_kernel<T, 8, KV8><<<grid, kNT, smem, s>>>(P);
-  else if (g == 4) rope_kernel<T, 4, KV8><<<grid, kNT, smem, s>>>(P);
-  else if (g == 2) rope_kernel<T, 2, KV8><<<grid, kNT, smem, s>>>(P);
-  else rope_kernel<T, 1, KV8><<<grid, kNT, smem, s>>>(P);
+  if (g == kNeighbor) return launch_behind(rope_kernel<T, kNeighbor, KV8>, grid, kNT, smem, s, P);
+  if (g == 8) return launch_behind(rope_kernel<T, 8, KV8>, grid, kNT, smem, s, P);
+  if (g == 4) return launch_behind(rope_kernel<T, 4, KV8>, grid, kNT, smem, s, P);
+  if (g == 2) return launch_behind(rope_kernel<T, 2, KV8>, grid, kNT, smem, s, P);
+  return launch_behind(rope_kernel<T, 1, KV8>, grid, kNT, smem, s, P);
 }
 
 bool positive(float x) { return std::isfinite(x) && x > 0.0f; }
@@ -458,14 +459,10 @@ SV_API sv_status spec_rope_rows(const sv_rope_args *a, void *stream) {
                   static_cast<unsigned>((P.heads + P.heads_per_cta - 1) / P.heads_per_cta));
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool kv8 = a->kv_dtype == SV_E4M3;
-  if (a->dtype == SV_BF16) {
-    if (kv8) launch_shape<uint16_t, true>(g, grid, P, s);
-    else launch_shape<uint16_t, false>(g, grid, P, s);
-  } else {
-    if (kv8) launch_shape<float, true>(g, grid, P, s);
-    else launch_shape<float, false>(g, grid, P, s);
-  }
-  const cudaError_t e = cudaGetLastError();
+  const cudaError_t e =
+      a->dtype == SV_BF16
+          ? (kv8 ? launch_shape<uint16_t, true>(g, grid, P, s) : launch_shape<uint16_t, false>(g, grid, P, s))
+          : (kv8 ? launch_shape<float, true>(g, grid, P, s) : launch_shape<float, false>(g, grid, P, s));
   if (e != cudaSuccess) return record_error(SV_ERR_CUDA, "rope launch: %s", cudaGetErrorString(e));
   return SV_OK;
 }

@@ -199,3 +199,50 @@ def test_a_step_captured_as_one_graph(api):
             assert torch.equal(getattr(d1, name), getattr(d2, name)), (seed, name)
         assert torch.equal(t1.counts, t2.counts) and torch.equal(t1.seen, t2.seen)
         assert int(t1.counts.sum()) > 0 and d1.status_bits() == d2.status_bits() == 0
+
+
+def test_calls_in_the_shadow_of_other_kernels(api):
+    """The operators' launches are worked on while the kernel before still runs: what
+    it wrote has to be there, and what comes after has to see all of theirs, whether
+    the neighbours are torch kernels, the attention, or each other."""
+    inp = W.make_inputs(W.workload("bass_b8", B=4, V=40001, Hq=8, Hkv=8, L_lo=900, L_hi=2000,
+                                   gen_seed=71, cap_slack=20))
+    d = DeviceStep(inp, api)
+    table = api.TokenCounts(4, 40001)
+    turns, _ = api.rope_turns(128)
+    x, y = torch.empty_like(d.q), torch.empty_like(d.q)
+    logits, adjusted = torch.empty_like(d.tgt), torch.empty_like(d.tgt)
+    tok = torch.zeros(4 * 700, dtype=torch.int32, device="cuda")
+    start = torch.arange(5, dtype=torch.int32, device="cuda") * 700
+    rope = api.rope_args(x, None, None, y, None, None, turns, cu_q=d.cu_q, kv_len=d.kv_len,
+                         max_q_rows=d.max_q_rows)
+    adjust = api.adjust_args(logits, adjusted, d.cu_q, max_q_rows=d.max_q_rows, counts=table.counts,
+                             seen=table.seen, presence=1.0, frequency=0.5)
+    reset = api.count_args(table.counts, table.seen, tok, start, reset=True)
+    count = api.count_args(table.counts, table.seen, tok, start)
+    big = torch.zeros(1 << 26, device="cuda")
+    gen = torch.Generator(device="cuda").manual_seed(0)
+    seen, want, turned = [], [], []
+    for k in range(40):
+        big.add_(1)                                     # a long kernel before
+        tok.copy_(torch.randint(0, 40001, tok.shape, generator=gen, device="cuda"))
+        api.spec_count_tokens(reset)
+        api.spec_count_tokens(count)
+        x.fill_(float(k + 1))
+        api.spec_rope_rows(rope)
+        api.spec_verify_attn(d.attn, d.ws)
+        logits.fill_(float(k))
+        api.spec_adjust_logits(adjust)
+        seen.append(adjusted.clone())
+        turned.append(y.clone())
+        n = torch.zeros(4, 40001, device="cuda").scatter_add_(
+            1, tok.view(4, 700).long(), torch.full((4, 700), 2.0, device="cuda"))
+        less = torch.where(n > 0, 0.5 * n + 1.0, torch.zeros_like(n))
+        want.append((float(k) - less).to(torch.bfloat16))
+    torch.cuda.synchronize()
+    rows = torch.repeat_interleave(torch.arange(4), torch.from_numpy(np.diff(inp["cu_q"])).long())
+    for k in range(40):
+        assert torch.equal(seen[k], want[k][rows.cuda()]), k
+        # every pair (k + 1)(1, 1) turned keeps its length: sqrt(2) (k + 1), halves of steps apart
+        pair = torch.hypot(turned[k][..., :64].float(), turned[k][..., 64:].float()) / (k + 1)
+        assert float((pair - 2 ** 0.5).abs().max()) <= 2 ** 0.5 * 2.0 ** -8 + 1e-5, k
