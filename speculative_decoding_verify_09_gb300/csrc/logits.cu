@@ -14,9 +14,9 @@
 // its counts are read only there) while the first rows are on their way.  From
 // then on every warp works alone, a row's chunk at a time: 16-byte cp.async
 // copies into shared memory, the listed tokens changed there, a lane per token,
-// and the chunk written out.  In place nothing streams: masked rows are written
-// where a token is barred, and the listed tokens of every row are changed in
-// global memory.
+// and the chunk written out.  Many long rows in place are not streamed: masked
+// rows are written where a token is barred, and the listed tokens of every row
+// are changed in global memory.
 #include <algorithm>
 #include <atomic>
 #include <cmath>

@@ -34,7 +34,9 @@ inline cudaError_t launch_behind(void (*kernel)(Params), dim3 grid, int threads,
   cfg.stream = s;
   cfg.attrs = &early;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, params);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, params);
+  if (e != cudaSuccess) cudaGetLastError();     // reported by the caller, not left for another call
+  return e;
 }
 
 // Waits until the kernel before has completed and its writes are visible.

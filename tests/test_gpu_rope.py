@@ -115,7 +115,8 @@ class Case:
 
 
 SHAPES = [(128, 128), (64, 64), (128, 64), (128, 32), (64, 20), (80, 80), (8, 2), (16, 16),
-          (256, 96), (256, 256), (128, 30), (40, 38), (96, 48)]
+          (256, 96), (256, 256), (128, 30), (40, 38), (96, 48), (24, 16), (72, 64), (128, 120),
+          (256, 250), (256, 2)]
 
 
 @pytest.mark.parametrize("D,rot", SHAPES)
