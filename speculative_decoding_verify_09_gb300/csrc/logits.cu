@@ -96,12 +96,15 @@ struct Chunk {
   static constexpr int kSlot = kMaskAt + kUnitTokens / 8;             // a unit and its mask
   static constexpr int kRing = 2;
   static constexpr int kRingBytes = kSparse ? 0 : kWarps * kRing * kSlot;
-  static_assert(kWords >= 1 && kWords <= 32 && kTokens <= 16384, "");
+  static_assert(kWords >= 1 && kWords <= 32 && kTokens <= 2048, "");
   static_assert(kSparse || (kSlot % 16 == 0 && kUnitTokens % (kWords * 32) == 0), "");
 };
 
-constexpr uint16_t kOutside = 0x8000u, kBiased = 0x4000u;   // flags of a listed token: counted
-                                                            // outside the table, has a bias
+// A listed token: its place in the chunk; above kDraft: 1 + the first of the
+// block's drafts that it is (its row of s_after), or 0; and one flag, that it is
+// counted outside the table until its list is complete, that it has a bias then.
+constexpr uint16_t kFlag = 0x800u, kPlace = 0x7FFu;
+constexpr int kDraft = 12;
 
 __device__ __forceinline__ void cp_async4(uint32_t dst, const void *src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4;\n" ::"r"(dst), "l"(src) : "memory");
@@ -126,7 +129,8 @@ adjust_kernel(const __grid_constant__ AdjustParams P) {
                                                              // a token; then its bias, as bits
   __shared__ uint32_t s_extra[C::kTokens / 32];              // bits of ctx, draft and bias tokens
   __shared__ uint32_t s_word[C::kTokens];                    // table words of the lists, with ctx
-  __shared__ uint16_t s_tok[C::kTokens];                     // the lists: tokens in the chunk, flags
+  __shared__ uint16_t s_tok[C::kTokens];                     // the lists
+  __shared__ uint32_t s_after[16];                           // [1 + d]: bit e: draft e + 1 is draft d + 1
   __shared__ int s_n[C::kUnits];
 
   wait_for_previous();
@@ -239,7 +243,15 @@ adjust_kernel(const __grid_constant__ AdjustParams P) {
       }
     }
   }
-  if (warp == 0 && my_draft >= 0) mark(my_draft);
+  if (warp == 0) {
+    const uint32_t same = __match_any_sync(0xffffffffu, my_draft);
+    if (lane < 16) s_after[lane] = 0;
+    __syncwarp();
+    if (my_draft >= 0) {
+      mark(my_draft);
+      s_after[1 + lane] = same;
+    }
+  }
   bad |= my_mask < -1 || (my_mask >= 0 && my_mask >= a.num_masks);
   bad = __syncthreads_or(bad);
 
@@ -300,7 +312,7 @@ adjust_kernel(const __grid_constant__ AdjustParams P) {
     base = __shfl_sync(0xffffffffu, base, 0);
     auto enter = [&](int e, int q, int b, bool in_table, bool out) {
       s_word[e] = in_table;                                  // read below
-      s_tok[e] = static_cast<uint16_t>(((w0 + q) * 32 + b) | (out ? kOutside : 0));
+      s_tok[e] = static_cast<uint16_t>(((w0 + q) * 32 + b) | (out ? kFlag : 0));
     };
     if (most <= 4) {
       int e = base + before;
@@ -321,38 +333,38 @@ adjust_kernel(const __grid_constant__ AdjustParams P) {
     __syncwarp();
     const int32_t *counts = a.counts + static_cast<int64_t>(slot) * V + t0;
 #pragma unroll 4
-    for (int e = base + lane; e < base + total; e += 32) {
-      const int tok = s_tok[e], t = tok & (C::kTokens - 1);
-      const bool outside = tok & kOutside;
-      const int entry = outside && nb > 0 ? s_last[t] : 0;
-      const uint32_t word = s_word[e] ? static_cast<uint32_t>(counts[t]) : 0u;
-      const float bias = entry ? a.bias_values[b0 + entry - 1] : 0.0f;
-      uint32_t more = 0;
-      if (outside)
-        for (int c = 0; c < ctx; ++c) more += a.ctx_tokens[c * ctx_stride + i] == t0 + t;
-      s_word[e] = word + more;
-      if (entry) {
-        s_last[t] = __float_as_int(bias);
-        s_tok[e] = static_cast<uint16_t>(tok | kBiased);
+    for (int e0 = 0; e0 < total; e0 += 32) {
+      const int e = base + e0 + lane;
+      const bool on = e0 + lane < total;
+      const int tok = on ? s_tok[e] : 0, t = tok & kPlace;
+      uint32_t word = on && s_word[e] ? static_cast<uint32_t>(counts[t]) : 0u;
+      if (__any_sync(0xffffffffu, tok & kFlag)) {
+        int entry = t;
+        if ((tok & kFlag) && nb > 0 && s_last[t]) {
+          s_last[t] = __float_as_int(a.bias_values[b0 + s_last[t] - 1]);
+          entry |= kFlag;
+        }
+        if (tok & kFlag)
+          for (int c = 0; c < ctx; ++c) word += a.ctx_tokens[c * ctx_stride + i] == t0 + t;
+        for (int d = drafts - 1; d >= 0; --d)
+          if (__shfl_sync(0xffffffffu, my_draft, d) == t) entry = (entry & (kFlag | kPlace)) | ((1 + d) << kDraft);
+        if (on) s_tok[e] = static_cast<uint16_t>(entry);
       }
+      if (on) s_word[e] = word;
     }
   }
   __syncthreads();
 
-  // One listed token of a row, by all lanes (`on`: those that have one).  The
-  // quotient by the repetition penalty is the product with its reciprocal, both
-  // rounded: within 2^-23 of it, and without a division's branches.
+  // One listed token of block row j.  The quotient by the repetition penalty is
+  // the product with its reciprocal, both rounded: within 2^-23 of it, and
+  // without a division's branches.
   const float inverse = 1.0f / rep;
-  auto changed = [&](bool on, T old, int tok, uint32_t word, int j) {
-    const bool outside = __any_sync(0xffffffffu, on && (tok & kOutside));
-    uint32_t times = word & 0x7FFFFFFFu;
-    if (outside)
-      for (int d = 0; d < min(j, drafts); ++d)
-        times += __shfl_sync(0xffffffffu, my_draft, d) == (tok & (C::kTokens - 1));
+  auto changed = [&](T old, int tok, uint32_t word, int j) {
+    const uint32_t times = (word & 0x7FFFFFFFu) + __popc(s_after[tok >> kDraft] & ((1u << j) - 1));
     float y = E::get(old);
-    if (word != 0 || times != 0) y *= y > 0.0f ? inverse : rep;
+    if ((word | times) != 0) y *= y > 0.0f ? inverse : rep;
     if (times != 0) y -= fmaf(freq, static_cast<float>(times), pres);
-    if (outside && (tok & kBiased)) y += __int_as_float(s_last[tok & (C::kTokens - 1)]);
+    if (tok & kFlag) y += __int_as_float(s_last[tok & kPlace]);
     return E::put(y);
   };
 
@@ -376,20 +388,17 @@ adjust_kernel(const __grid_constant__ AdjustParams P) {
         for (int h = 0; h < kAhead; ++h) {
           if (eb + h * 32 >= n) break;
           const int e = eb + h * 32 + lane;
-          tok[h] = 0;
-          word[h] = 0;
           if (e < n) {
             tok[h] = s_tok[from + e];
             word[h] = s_word[from + e];
-            old[h] = x[(tok[h] & (C::kTokens - 1)) - from];
+            old[h] = x[(tok[h] & kPlace) - from];
           }
         }
 #pragma unroll
         for (int h = 0; h < kAhead; ++h) {
           if (eb + h * 32 >= n) break;
-          const bool on = eb + h * 32 + lane < n;
-          const T y = changed(on, old[h], tok[h], word[h], j);
-          if (on) x[(tok[h] & (C::kTokens - 1)) - from] = y;
+          if (eb + h * 32 + lane < n)
+            x[(tok[h] & kPlace) - from] = changed(old[h], tok[h], word[h], j);
         }
       }
       __syncwarp();
@@ -497,7 +506,7 @@ adjust_kernel(const __grid_constant__ AdjustParams P) {
         for (int h = 0; h < kAhead; ++h) {
           const int e = eb + h * 32 + lane;
           tok[h] = e < n ? s_tok[e] : 0;
-          const int t = tok[h] & (C::kTokens - 1);
+          const int t = tok[h] & kPlace;
 #pragma unroll
           for (int u = 0; u < kBatch; ++u) {
             allowed[h][u] = e < n && lb + u * apart < lines;
@@ -509,13 +518,12 @@ adjust_kernel(const __grid_constant__ AdjustParams P) {
 #pragma unroll
         for (int h = 0; h < kAhead; ++h) {
           if (eb + h * 32 >= n) break;
-          const int e = eb + h * 32 + lane, t = tok[h] & (C::kTokens - 1);
+          const int e = eb + h * 32 + lane, t = tok[h] & kPlace;
           const uint32_t word = e < n ? s_word[e] : 0u;
 #pragma unroll
           for (int u = 0; u < kBatch; ++u) {
             if (lb + u * apart >= lines) break;
-            const T y = changed(e < n, x[h][u], tok[h], word, block_row(lb + u * apart));
-            if (allowed[h][u]) row[u][t] = y;
+            if (allowed[h][u]) row[u][t] = changed(x[h][u], tok[h], word, block_row(lb + u * apart));
           }
         }
       }
