@@ -730,14 +730,14 @@ cudaError_t launch_adjust(int sms, AdjustParams &P, cudaStream_t s) {
   // thousand listed tokens are thin in the row and there are CTAs enough to
   // hide its longer chain of loads (bf16, 9 rows a sequence, 2048 tokens of
   // history, a quarter of the rows masked; this against streaming the rows
-  // through: V = 128256 at B = 64 50 against 62 us, B = 16 20 against 21 us,
-  // B = 8 13 against 11 us; V = 32000 at B = 64 34 against 22 us, B = 8 10.5
-  // against 7.2 us).
+  // through: V = 128256 at B = 64 45 against 62 us, B = 16 17 against 19 us,
+  // B = 8 13 against 11 us; V = 32000, 11 rows, at B = 64 30 against 22 us, B = 8
+  // 13.5 against 7.3 us).
   if (a.target == a.target_out && a.vocab >= 65536 && big >= 6 * static_cast<int64_t>(sms))
     return launch_adjust<T, 4096, 0>(split(big, 4, 16), P, s);
   // Streaming: 1 KB chunks until the 4 KB ones (fewer repeated starts) give
-  // about two CTAs per SM (bf16, V = 32000: 11 rows a sequence at B = 8 6.9
-  // against 8.4 us, B = 16 9.7 against 11.7 us; at B = 32 20.3 against 19.3 us).
+  // about two CTAs per SM (bf16, V = 32000, 11 rows a sequence: at B = 8 6.4
+  // against 7.3 us, at B = 16 8.8 both, at B = 32 20.1 against 16.3 us).
   if (big < 2 * static_cast<int64_t>(sms)) return launch_adjust<T, 1024, 1024>(split(small, 8, 4), P, s);
   return launch_adjust<T, 4096, 2048>(split(big, 4, 8), P, s);
 }
