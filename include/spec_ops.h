@@ -135,7 +135,7 @@ typedef struct sv_count_args {
   int32_t vocab;            /* V, 1..2^23 */
   int32_t num_slots;        /* rows of the table, >= 1 */
   int32_t flags;            /* SV_COUNT_* */
-  int64_t num_tokens;       /* T, the tokens in `tokens`; < 2^31 */
+  int64_t num_tokens;       /* T, the tokens in `tokens`; 0..2^30 */
   const int32_t *start;     /* [dev] [B+1] tokens of sequence i: start[i] ..
                                start[i+1]-1 (a step's cu_q; may be none) */
   const int32_t *tokens;    /* [dev] [T] (a step's out_tokens) */
@@ -206,7 +206,7 @@ typedef struct sv_adjust_args {
   const int32_t *bias_tokens;  /* [dev] [num_bias]; of a token named twice by one
                                sequence the last entry holds */
   const float *bias_values; /* [dev] [num_bias] */
-  int64_t num_bias;         /* < 2^31 */
+  int64_t num_bias;         /* 0..2^30 */
   /* grammar masks */
   const uint32_t *mask;     /* [dev] [num_masks, mask_stride] bit t % 32 of word t / 32 is 1
                                where token t is allowed; NULL: none */

@@ -31,6 +31,7 @@ namespace {
 
 constexpr int kNT = 256;                   // threads of the table's kernels
 constexpr float kMinRepetition = 0x1p-64f, kMaxRepetition = 0x1p64f;   // (its reciprocal is used)
+constexpr int64_t kMaxEntries = int64_t{1} << 30;   // tokens, biases: a strided int index stays one
 constexpr int kBatch = 3;                  // (sparse) rows in flight per warp
 constexpr int kAhead = 4;                  // listed tokens in flight per lane and row
 constexpr int kMaskVecs = 4;               // (sparse) vectors of a masked row in flight per lane
@@ -763,7 +764,7 @@ sv_status check_adjust(const sv_adjust_args *a) {
   if (a->num_ctx < 0 || a->num_ctx > 1024)
     return record_error(SV_ERR_INVALID, "adjust: num_ctx %d outside [0, 1024]", a->num_ctx);
   if (a->ctx_stride < 0) return bad("negative ctx_stride");
-  if (a->num_bias < 0 || a->num_bias >= (int64_t{1} << 31)) return bad("num_bias outside [0, 2^31)");
+  if (a->num_bias < 0 || a->num_bias > kMaxEntries) return bad("num_bias outside [0, 2^30]");
   if (a->num_slots < 0 || a->num_masks < 0) return bad("negative num_slots or num_masks");
   if (a->mask_stride != 0 && a->mask_stride < (a->vocab + 31) / 32)
     return bad("mask_stride below ceil(vocab / 32)");
@@ -795,7 +796,7 @@ sv_status check_count(const sv_count_args *a) {
   if (a->num_slots < 1) return record_error(SV_ERR_INVALID, "count: num_slots %d", a->num_slots);
   if (a->flags & ~(SV_COUNT_PROMPT | SV_COUNT_RESET))
     return record_error(SV_ERR_INVALID, "count: flags %d", a->flags);
-  if (a->num_tokens < 0 || a->num_tokens >= (int64_t{1} << 31)) return bad("num_tokens outside [0, 2^31)");
+  if (a->num_tokens < 0 || a->num_tokens > kMaxEntries) return bad("num_tokens outside [0, 2^30]");
   if (a->batch == 0) return SV_OK;
   if (!a->start || !a->counts || !a->seen) return bad("null start, counts or seen");
   if (a->num_tokens > 0 && !a->tokens) return bad("null tokens");

@@ -175,3 +175,21 @@ def test_header_compiles_as_plain_c_and_cxx(tmp_path, std, compiler, lang):
                         "-x", lang, "-fsyntax-only", "-I", os.path.join(ROOT, "include"),
                         str(src)], capture_output=True, text=True)
     assert r.returncode == 0, r.stderr
+
+
+def test_as_many_tokens_or_biases_as_an_index_holds(binding):
+    """The kernels step through both with a 32-bit index that must not wrap."""
+    most = 1 << 30
+    a = _count(binding, num_tokens=most + 1)
+    assert binding.lib.spec_count_tokens(ctypes.byref(a), None) == INVALID
+    assert "num_tokens" in binding.last_error()
+    a = _adjust(binding, num_bias=most + 1)
+    assert binding.lib.spec_adjust_logits(ctypes.byref(a), None) == INVALID
+    assert "num_bias" in binding.last_error()
+    # the largest that is allowed passes this check and meets the next one
+    a = _count(binding, num_tokens=most, start=0)
+    assert binding.lib.spec_count_tokens(ctypes.byref(a), None) == INVALID
+    assert "start" in binding.last_error()
+    a = _adjust(binding, num_bias=most, num_slots=-1)
+    assert binding.lib.spec_adjust_logits(ctypes.byref(a), None) == INVALID
+    assert "num_slots" in binding.last_error()
