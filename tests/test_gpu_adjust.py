@@ -433,3 +433,59 @@ def test_torch_call_refusals(api):
         api.spec_adjust_logits(call(mask=d["mask"][:, :2].contiguous(), mask_rows=d["mask_rows"]))
     with pytest.raises(SpecVerifyError, match="num_masks"):
         api.spec_adjust_logits(call(mask=d["mask"][:2].contiguous()))
+
+
+# Shapes that every way of cutting the work takes: short chunks, long ones,
+# single tokens changed in memory (in place, with sequences enough).
+CUTS = [(6, 5003, False), (20, 32000, False), (20, 33001, False), (30, 65536, True), (30, 70003, True)]
+
+
+@pytest.mark.parametrize("B,V,in_place", CUTS)
+@pytest.mark.parametrize("few", [1, 40])
+def test_blocks_of_repeated_drafts(api, B, V, in_place, few):
+    """Blocks of 16 rows whose drafts are one token, or a few, next to the table's
+    and the biased ones: each row counts the drafts before it alone."""
+    c = Case(api, ([16, 1, 9] * B)[:B], V, seed=few, hist=200, ctx=2, bias=8, masked=0.2)
+    near = c.rng.integers(0, V - 40)
+    c.tokens[:] = near + c.rng.integers(0, few, len(c.tokens))
+    c.kw["ctx_tokens"][0] = near
+    c.set_bias([[(near, 0.5), (near + few, -1.0)]] * B)
+    c.run(in_place)
+
+
+@pytest.mark.parametrize("B,V,in_place", CUTS)
+def test_failing_and_skipped_sequences_among_others(api, B, V, in_place):
+    """A value, a slot and a mask row out of range give rows of NaN, and only there."""
+    c = Case(api, ([2, 1, 3] * B)[:B], V, seed=V, hist=300, masked=0.3, bias=4)
+    c.kw["repetitions"][1] = c.ref["repetition"][1] = np.nan
+    slots = c.kw["slots"].copy()
+    slots[2] = B + 2
+    c.kw["slots"] = c.ref["slots"] = slots
+    c.kw["mask_rows"][c.cu[4]] = c.ref["mask_rows"][c.cu[4]] = len(c.kw["mask"])
+    c.run(in_place, status=oracle.DEV_BAD_PARAM)
+
+
+@pytest.mark.parametrize("B,V,in_place", CUTS)
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_infinities_and_nan_in_rows(api, B, V, in_place, dtype):
+    """Listed, plain and barred places that hold infinities, NaN or the lowest value."""
+    c = Case(api, ([2, 1] * B)[:B], V, dtype, seed=3, hist=2000, masked=0.5, penal=False)
+    ones = np.ones(B, np.float32)
+    c.kw.update(repetitions=ones * 2, presences=ones * 0.5)
+    c.ref.update(repetition=ones * 2, presence=ones * 0.5)
+    low = np.float32(-3.3895314e38)             # the lowest bf16; a quarter, so that twice it is finite
+    vals = np.array([np.inf, -np.inf, np.nan, low / 4, 0.0, -0.0], np.float32)
+    x = vals[c.rng.integers(0, len(vals), c.target.shape)]
+    at = c.rng.random(c.target.shape) < 0.2
+    c.target = np.where(at, f32_to_bf16_bits(x) if dtype == "bf16" else x, c.target)
+    c.run(in_place)
+
+
+@pytest.mark.parametrize("B,V,in_place", CUTS)
+def test_the_same_call_twice_gives_the_same_bits(api, B, V, in_place):
+    c = Case(api, ([5, 2] * B)[:B], V, seed=8, hist=1500, ctx=3, bias=100, masked=0.3)
+    got = []
+    for _ in range(2):
+        api.spec_adjust_logits(c.args(in_place))
+        got.append((host_bits(c.ot).copy(), host_bits(c.od).copy()))
+    assert all(np.array_equal(a, b) for a, b in zip(*got))
