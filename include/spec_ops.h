@@ -165,8 +165,9 @@ SV_API sv_status spec_count_tokens(const sv_count_args *count, void *stream);
  *   always:  l = l - (frequency * n + (n > 0 ? presence : 0))
  *            l = l + bias            (the row's sequence's, where it has one)
  *   barred:  l = -inf                (the mask's bit is 0; whatever l was)
- * Tokens that nothing of this touches keep their bits.  Draft row j takes what
- * target row j takes.  A row whose mask bars everything is all -inf (the
+ * Tokens that nothing of this touches keep their bits (a NaN where a later
+ * draft's token stands remains some NaN).  Draft row j takes what target row j
+ * takes.  A row whose mask bars everything is all -inf (the
  * sampler then fails its sequence with SV_DEV_NONFINITE). */
 typedef struct sv_adjust_args {
   int32_t batch;            /* B, 0..65535 */
