@@ -151,12 +151,13 @@ adjust_kernel(const __grid_constant__ AdjustParams P) {
   if (tid < C::kUnits) s_n[tid] = 0;
   __syncthreads();
 
-  const int Ri = r1 - r0;
-  if (r0 < i || Ri < 1 || Ri > a.max_q_rows || r0 + Ri > a.num_rows ||
-      r0 + Ri - (i + 1) > a.num_rows - a.batch) {            // (its draft rows, too)
+  // (compared before they are subtracted: far apart, the difference wraps)
+  if (r0 < i || r1 <= r0 || r1 > a.num_rows || r1 - r0 > a.max_q_rows ||
+      r1 - (i + 1) > a.num_rows - a.batch) {                 // (its draft rows, too)
     if (head && tid == 0) set_status(a.dev_status, SV_DEV_BAD_LENGTH);
     return;
   }
+  const int Ri = r1 - r0;
   const int all = Ri + (a.draft != nullptr ? Ri - 1 : 0);    // target rows, then draft rows
   const int l0 = blockIdx.z * P.lines_per_part, lines = min(all - l0, P.lines_per_part);
   if (lines <= 0) return;

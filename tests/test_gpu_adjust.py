@@ -489,3 +489,21 @@ def test_the_same_call_twice_gives_the_same_bits(api, B, V, in_place):
         api.spec_adjust_logits(c.args(in_place))
         got.append((host_bits(c.ot).copy(), host_bits(c.od).copy()))
     assert all(np.array_equal(a, b) for a, b in zip(*got))
+
+
+@pytest.mark.parametrize("cu,skipped", [([2 ** 31 - 1, -2 ** 31 + 1, 4, 6], [0, 1, 2, 3]),
+                                        ([2 ** 31 - 1, -2 ** 31, 4, 6], [0, 1, 2, 3]),
+                                        ([0, 2 ** 31 - 1, -2 ** 31 + 2, 6], [0, 1, 2, 3, 4, 5])])
+def test_row_bounds_whose_difference_wraps(api, cu, skipped):
+    """Bounds so far apart that their 32-bit difference is a plausible number of rows."""
+    c = Case(api, [2, 2, 2], 300, seed=23, table=False, penal=False, draft=False)
+    c.max_rows = 3
+    api.spec_adjust_logits(c.args(cu=dev(np.array(cu, np.int32))))
+    torch.cuda.synchronize()
+    assert int(c.status.item()) == oracle.DEV_BAD_LENGTH
+    got = host_bits(c.ot)
+    for r in range(6):
+        if r in skipped:
+            assert bool((c.ot[r] == 77).all()), r
+        else:
+            assert np.array_equal(got[r], c.target[r])
