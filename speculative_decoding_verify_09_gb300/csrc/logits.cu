@@ -631,7 +631,7 @@ __global__ void __launch_bounds__(NT) reset_kernel(const __grid_constant__ Count
   int t[kTokens];
   auto load = [&](int k0) {
 #pragma unroll
-    for (int u = 0; u < kTokens; ++u) t[u] = k0 + u * NT < n ? __ldg(a.tokens + s0 + k0 + u * NT) : t0;
+    for (int u = 0; u < kTokens; ++u) t[u] = k0 + u * NT < n ? a.tokens[s0 + k0 + u * NT] : t0;
   };
   load(tid);
   bool before = false, after = false;                         // others that share the slot

@@ -19,8 +19,11 @@ int device_sms();
 // stream still runs (programmatic dependent launch): between small kernels on a
 // stream that saves about 2 us each (bass_b8 verify rows adjusted 9.0 -> 7.0 us a
 // call, 176 rotary rows 6.1 -> 5.1 us).  Such a kernel begins with
-// wait_for_previous(), before it touches global memory; none of them lets its
-// successor start before it is done, which would put waiting CTAs on its SMs.
+// wait_for_previous(), before it touches global memory, and reads by ordinary loads
+// (or from L2): it may be resident while the kernel before still writes, and the
+// read-only path (__ldg) is only for data that nobody writes while it runs.  None of
+// them lets its successor start before it is done, which would put waiting CTAs
+// on its SMs.
 template <typename Params>
 inline cudaError_t launch_behind(void (*kernel)(Params), dim3 grid, int threads, size_t smem,
                                  cudaStream_t s, const Params &params) {

@@ -226,7 +226,7 @@ __global__ void __launch_bounds__(kNT, min_ctas<T, G, KV8>()) rope_kernel(const 
   const bool any_turn = h_begin < P.nq + P.nk;
   if (live && any_turn) {
     for (int p = t; p < half; p += row_threads) {
-      const uint64_t part = static_cast<uint64_t>(pos) * __ldg(P.turns + p);
+      const uint64_t part = static_cast<uint64_t>(pos) * P.turns[p];
       float sn, cs;
       sincospif(__ll2float_rn(static_cast<int64_t>(part)) * 0x1p-63f, &sn, &cs);
       s_cos[p] = cs * P.mscale;

@@ -246,3 +246,42 @@ def test_calls_in_the_shadow_of_other_kernels(api):
         # every pair (k + 1)(1, 1) turned keeps its length: sqrt(2) (k + 1), halves of steps apart
         pair = torch.hypot(turned[k][..., :64].float(), turned[k][..., 64:].float()) / (k + 1)
         assert float((pair - 2 ** 0.5).abs().max()) <= 2 ** 0.5 * 2.0 ** -8 + 1e-5, k
+
+
+def test_inputs_written_by_the_kernel_just_before(api):
+    """Each call reads what the launch before it on the stream has written (frequencies,
+    tokens, logits), in buffers that the call before that one has read too."""
+    n, V = 64, 5000
+    g = torch.Generator(device="cuda").manual_seed(9)
+    x = torch.randn(n, 2, 64, device="cuda", generator=g)
+    pos = torch.arange(1, n + 1, device="cuda", dtype=torch.int64)
+    tables = [api.rope_turns(64, base=b)[0] for b in (1e4, 1e6)]
+    turns, y = torch.empty_like(tables[0]), torch.empty_like(x)
+    rope = api.rope_args(x, None, None, y, None, None, turns, positions=pos)
+    want = []
+    for t in tables:
+        turns.copy_(t)
+        torch.cuda.synchronize()
+        api.spec_rope_rows(rope)
+        torch.cuda.synchronize()
+        want.append(y.clone())
+    assert not torch.equal(*want)
+    prompts = torch.randint(0, V, (2, 4096), device="cuda", generator=g, dtype=torch.int32)
+    start = torch.tensor([0, 4096], dtype=torch.int32, device="cuda")
+    tokens, table = torch.empty_like(prompts[0]), api.TokenCounts(1, V)
+    count = api.count_args(table.counts, table.seen, tokens, start, prompt=True, reset=True)
+    marked = torch.zeros(2, V, dtype=torch.bool, device="cuda")
+    for k in range(2):
+        marked[k, prompts[k].long()] = True
+    got_y, got_c = [], []
+    for k in range(40):
+        torch.mul(tables[k % 2], 1, out=turns)          # a kernel, not a copy
+        api.spec_rope_rows(rope)
+        got_y.append(y.clone())
+        torch.add(prompts[k % 2], 0, out=tokens)
+        api.spec_count_tokens(count)
+        got_c.append(table.counts[0] < 0)
+    torch.cuda.synchronize()
+    for k in range(40):
+        assert torch.equal(got_y[k], want[k % 2]), k
+        assert torch.equal(got_c[k], marked[k % 2]), k

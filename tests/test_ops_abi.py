@@ -193,3 +193,17 @@ def test_as_many_tokens_or_biases_as_an_index_holds(binding):
     a = _adjust(binding, num_bias=most, num_slots=-1)
     assert binding.lib.spec_adjust_logits(ctypes.byref(a), None) == INVALID
     assert "num_slots" in binding.last_error()
+
+
+def test_kernels_launched_behind_another_read_by_ordinary_loads():
+    """They may be resident while the kernel before them still writes what they
+    read: the read-only path is not for them."""
+    csrc = os.path.join(ROOT, "speculative_decoding_verify_09_gb300", "csrc")
+    found = 0
+    for name in sorted(os.listdir(csrc)):
+        with open(os.path.join(csrc, name)) as fh:
+            code = "\n".join(ln.split("//")[0] for ln in fh)
+        if "launch_behind(" in code and name.endswith(".cu"):
+            found += 1
+            assert "__ldg" not in code and "ld.global.nc" not in code, name
+    assert found == 2
