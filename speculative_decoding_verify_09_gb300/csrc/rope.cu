@@ -32,9 +32,14 @@ constexpr int kPasses = 6;                           // heads that one thread wo
 // How a thread's elements of a head meet their partners.  G = 8, 4, 2, 1 (the
 // half layout): G elements and the G that are rot_dim / 2 further on, i.e. G
 // whole pairs, where G is the largest that divides rot_dim / 2 and so keeps the
-// accesses aligned.  kNeighbor (the interleaved layout): two vectors of 8
-// elements, 4 whole pairs each.
-constexpr int kNeighbor = 0;
+// accesses aligned.  kNeighbor (the interleaved layout, rot_dim a multiple of 16): two
+// vectors of 8 elements, 4 whole pairs each.  kMixed (any other rot_dim): the same, but
+// one column holds the last pairs and copied elements; those keep their bits, so its
+// pairs are turned in place, one by one.  In one kernel the selects cost the other
+// columns registers (176 rows of 48 heads, half of each turned: 2.9 us so, 3.1 to 3.7 us
+// by where they stand in a common one; 32768 rows of 48 heads of 128, bf16: 126 us,
+// with rot_dim 40 130 us).
+constexpr int kNeighbor = 0, kMixed = -1;
 
 struct RopeParams {
   int batch, max_q_rows, Hq, Hkv, D, rot;
@@ -91,6 +96,19 @@ struct Vec {
         e[i] = static_cast<uint16_t>(two);
         e[i + 1] = static_cast<uint16_t>(two >> 16);
       }
+    }
+  }
+  // The pair of elements i (even) and i + 1 turned in place, or left as it is.
+  __device__ __forceinline__ void turn_pair(int i, float cs, float sn, bool on) {
+    if constexpr (sizeof(T) == 2) {
+      const float a = bf16_bits_to_f32(e[i]), b = bf16_bits_to_f32(e[i + 1]);
+      const uint32_t two = pack_bf16x2(a * cs - b * sn, b * cs + a * sn);
+      e[i] = on ? static_cast<uint16_t>(two) : e[i];
+      e[i + 1] = on ? static_cast<uint16_t>(two >> 16) : e[i + 1];
+    } else {
+      const float a = e[i], b = e[i + 1];
+      e[i] = on ? a * cs - b * sn : a;
+      e[i + 1] = on ? b * cs + a * sn : b;
     }
   }
 };
@@ -171,7 +189,7 @@ struct InFlight {
 };
 template <typename T, int G, bool KV8>
 constexpr int min_ctas() {
-  return (G == 8 || G == kNeighbor) && (KV8 || sizeof(T) == 4) ? 3 : 4;
+  return (G == 8 || G <= kNeighbor) && (KV8 || sizeof(T) == 4) ? 3 : 4;
 }
 
 template <typename T, int G, bool KV8>
@@ -197,10 +215,11 @@ __global__ void __launch_bounds__(kNT, min_ctas<T, G, KV8>()) rope_kernel(const 
       if (!good_sequence(P, static_cast<int>(i))) set_status(P.dev_status, SV_DEV_BAD_LENGTH);
 
   // this thread's column: element offsets inside a head
-  constexpr int N = G == kNeighbor ? 8 : G;
-  const bool turn = G == kNeighbor ? 2 * N * c < P.rot : c < half / N;   // the column holds pairs
-  const int o0 = G == kNeighbor ? 2 * N * c : turn ? N * c : P.rot + 2 * N * (c - half / N);
-  const int o1 = G != kNeighbor && turn ? o0 + half : o0 + N;
+  constexpr bool kBeside = G <= kNeighbor;               // a pair's elements stand side by side
+  constexpr int N = kBeside ? 8 : G;
+  const bool turn = kBeside ? 2 * N * c < P.rot : c < half / N;   // the column holds pairs
+  const int o0 = kBeside ? 2 * N * c : turn ? N * c : P.rot + 2 * N * (c - half / N);
+  const int o1 = !kBeside && turn ? o0 + half : o0 + N;
   const bool column = live && hl < hstep;
   const bool both = o1 < P.D;                            // (the last column may be single)
 
@@ -246,7 +265,6 @@ __global__ void __launch_bounds__(kNT, min_ctas<T, G, KV8>()) rope_kernel(const 
       sn[i] = p < half ? s_sin[p] : 0.0f;
     }
   }
-  const bool whole = N * c + N <= half;                  // (kNeighbor) nothing but pairs in the column
 
   const int64_t kv_row = row * P.Hkv * P.D;
   T *out_q = static_cast<T *>(P.q_out) + row * P.Hq * P.D;
@@ -256,12 +274,20 @@ __global__ void __launch_bounds__(kNT, min_ctas<T, G, KV8>()) rope_kernel(const 
   auto finish = [&](Vec<T, N> (&v)[2], int h) {
     const bool is_q = h < P.nq, is_k = !is_q && h < P.nq + P.nk, codes = KV8 && !is_q;
     float x[N], y[N];
-    if ((turn && (is_q || is_k)) || codes) {
+    bool done = false;
+    if constexpr (G == kMixed) {                         // pair by pair, the copied elements not touched
+      done = !codes;
+      if (done && turn && (is_q || is_k)) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i / 4].turn_pair(i % 4 * 2, cs[i], sn[i], N * c + i < half);
+      }
+    }
+    if (!done && ((turn && (is_q || is_k)) || codes)) {
       v[0].get(x);
       v[1].get(y);
     }
-    if (turn && (is_q || is_k)) {
-      if constexpr (G != kNeighbor) {
+    if (!done && turn && (is_q || is_k)) {
+      if constexpr (!kBeside) {
 #pragma unroll
         for (int i = 0; i < N; ++i) {
           const float a = x[i], b = y[i];
@@ -273,7 +299,7 @@ __global__ void __launch_bounds__(kNT, min_ctas<T, G, KV8>()) rope_kernel(const 
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const float a = z[2 * i], b = z[2 * i + 1];
-            if (whole || N * c + first + i < half) {
+            if (G == kNeighbor || N * c + first + i < half) {
               z[2 * i] = a * cs[first + i] - b * sn[first + i];
               z[2 * i + 1] = b * cs[first + i] + a * sn[first + i];
             }
@@ -315,6 +341,7 @@ template <typename T, bool KV8>
 cudaError_t launch_shape(int g, dim3 grid, const RopeParams &P, cudaStream_t s) {
   const size_t smem = static_cast<size_t>(kNT >> P.row_shift) * 2 * P.pairs * sizeof(float);
   if (g == kNeighbor) return launch_behind(rope_kernel<T, kNeighbor, KV8>, grid, kNT, smem, s, P);
+  if (g == kMixed) return launch_behind(rope_kernel<T, kMixed, KV8>, grid, kNT, smem, s, P);
   if (g == 8) return launch_behind(rope_kernel<T, 8, KV8>, grid, kNT, smem, s, P);
   if (g == 4) return launch_behind(rope_kernel<T, 4, KV8>, grid, kNT, smem, s, P);
   if (g == 2) return launch_behind(rope_kernel<T, 2, KV8>, grid, kNT, smem, s, P);
@@ -430,7 +457,7 @@ SV_API sv_status spec_rope_rows(const sv_rope_args *a, void *stream) {
   if (a->num_rows == 0 || P.slots == 0 || P.heads == 0) return SV_OK;
 
   const int half = P.rot / 2;
-  int g = kNeighbor;
+  int g = P.rot % 16 ? kMixed : kNeighbor;
   P.columns = (P.D + 15) / 16;
   if (a->layout == SV_ROPE_HALF) {
     g = half % 8 == 0 ? 8 : half % 4 == 0 ? 4 : half % 2 == 0 ? 2 : 1;

@@ -384,3 +384,31 @@ def test_torch_call_refusals(api):
         with pytest.raises(ValueError):
             f()
             pytest.fail(f"call {i} was not refused")
+
+
+@pytest.mark.parametrize("D,rot", [(64, 20), (128, 30), (40, 38), (72, 64), (256, 250), (24, 2), (64, 8), (128, 120)])
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_copied_elements_keep_any_bits(api, D, rot, layout, dtype):
+    """Every bit pattern (NaN payloads, infinities, subnormals) behind the rotated part."""
+    c = Case(api, [3, 70], 5, 2, D, rot, dtype, layout, seed=rot)
+    rng = np.random.default_rng(D)
+    word = np.uint16 if dtype == "bf16" else np.uint32
+    x = c.x.view(word).copy()
+    tail = rng.integers(0, 2 ** (8 * word().itemsize), x[..., rot:].shape, dtype=np.uint64).astype(word)
+    nan = rng.random(tail.shape) < 0.3              # exponent all ones, some payload
+    tail[nan] |= word(0x7F80 if dtype == "bf16" else 0x7F800000)
+    x[..., rot:] = tail
+    c.x = x.view(c.x.dtype)
+    c.dx.copy_(dev(c.x))
+    api.spec_rope_rows(c.args())
+    torch.cuda.synchronize()
+    for p in "qk":
+        got = host_bits(c.out[p]).view(word)
+        assert np.array_equal(got[..., rot:], tail[:, c.heads[p]]), p
+        x[..., rot:] = 0                            # the turned part as always
+    c.x = x.view(c.x.dtype)
+    for p in "qk":
+        c.out[p][..., rot:] = 0
+    c.out["v"].copy_(dev(c.x)[:, c.heads["v"]])
+    c.check()
