@@ -5,8 +5,9 @@
 // sin x), x = t f_p.  What has to be exact is x modulo a turn: at t = 2^20 an
 // fp32 product is off by 2^-4 radians.  f_p / (2 pi) is kept as a 64-bit
 // fraction of a turn, so t times it modulo 2^64 -- one integer multiplication
-// -- is the exact fraction of a turn (up to t * 2^-65 from rounding f_p), whose
-// signed value feeds sincospif.
+// -- is the exact fraction of a turn (up to t * 2^-65 from rounding f_p).  The
+// nearest quarter turn is taken off as an integer too, so that the one rounding
+// of the angle to fp32 (for sincospif) is of an eighth of a turn at most.
 //
 // The kernel is one pass over the rows: bytes bound for prompts, launch bound
 // for a step's rows.  A row's cos and sin are computed once per CTA into shared
@@ -246,10 +247,13 @@ __global__ void __launch_bounds__(kNT, min_ctas<T, G, KV8>()) rope_kernel(const 
   if (live && any_turn) {
     for (int p = t; p < half; p += row_threads) {
       const uint64_t part = static_cast<uint64_t>(pos) * P.turns[p];
-      float sn, cs;
-      sincospif(__ll2float_rn(static_cast<int64_t>(part)) * 0x1p-63f, &sn, &cs);
-      s_cos[p] = cs * P.mscale;
-      s_sin[p] = sn * P.mscale;
+      const uint64_t quarter = (part + (uint64_t{1} << 61)) >> 62;      // the nearest, 0..3
+      const int64_t rest = static_cast<int64_t>(part - (quarter << 62));
+      float s0, c0;                                                   // of the rest, then of the angle
+      sincospif(__ll2float_rn(rest) * 0x1p-63f, &s0, &c0);
+      const float sn = quarter & 1 ? c0 : s0, cs = quarter & 1 ? s0 : c0;
+      s_cos[p] = ((quarter + 1) & 2 ? -cs : cs) * P.mscale;
+      s_sin[p] = (quarter & 2 ? -sn : sn) * P.mscale;
     }
   }
   __syncthreads();

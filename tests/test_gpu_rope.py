@@ -412,3 +412,45 @@ def test_copied_elements_keep_any_bits(api, D, rot, layout, dtype):
         c.out[p][..., rot:] = 0
     c.out["v"].copy_(dev(c.x)[:, c.heads["v"]])
     c.check()
+
+
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+def test_cos_and_sin_are_as_exact_as_fp32_has_them(api, layout):
+    """Rows of (1, 0) pairs come out as (cos, sin).  The angle's only rounding is that of
+    its distance x from the nearest quarter turn (2^-24 of pi |x|, which moves the value
+    by that times its derivative), and sincospif is within 2 ulp (2^-22 of the value): near
+    a half turn, where rounding the whole angle would cost 9e-8, the sine is good to its
+    last bits."""
+    R, pairs = 4096, 8
+    rng = np.random.default_rng(17)
+    f = rng.integers(0, 2 ** 63, pairs, dtype=np.uint64)
+    f[0] = (1 << 63) + (1 << 46) + 12345        # a half turn and a little
+    f[1] = (1 << 62) - (1 << 45) + 777          # a quarter turn less a little
+    f[2] = (1 << 63) - (1 << 40) - 1
+    f[3] = (1 << 61) + (1 << 47) + 99           # between the quarters
+    f[4] = 1 << 62                              # quarter turns exactly
+    pos = np.concatenate([np.arange(R - 8), [2 ** 31 - 1, -(2 ** 31) + 1, -1, -2, -3, -4, -5, 2 ** 30]])
+    x = torch.zeros(R, 1, 2 * pairs, device="cuda")
+    if layout == "half":
+        x[..., :pairs] = 1.0
+    else:
+        x[..., 0::2] = 1.0
+    y = torch.empty_like(x)
+    api.spec_rope_rows(api.rope_args(x, None, None, y, None, None, dev(f.view(np.int64)), layout=layout,
+                                     positions=dev(pos.astype(np.int64))))
+    torch.cuda.synchronize()
+    got = y[:, 0].cpu().numpy().astype(np.float64)
+    cos, sin = (got[:, :pairs], got[:, pairs:]) if layout == "half" else (got[:, 0::2], got[:, 1::2])
+    for p in range(pairs):
+        part = [int(t) * int(f[p]) % 2 ** 64 for t in pos]
+        quarter = [(v + 2 ** 61 >> 62) % 4 for v in part]
+        rest = np.array([(v - (q << 62) + 2 ** 63) % 2 ** 64 - 2 ** 63 for v, q in zip(part, quarter)],
+                        dtype=np.float64) * 2.0 ** -63              # half turns, at most 1 / 4
+        assert np.abs(rest).max() <= 0.25
+        s0, c0 = np.sin(np.pi * rest), np.cos(np.pi * rest)
+        q = np.array(quarter)
+        want_s = np.choose(q, [s0, c0, -s0, -c0])
+        want_c = np.choose(q, [c0, -s0, -c0, s0])
+        moved = np.pi * np.abs(rest) * 2.0 ** -24
+        for g, w, d in ((sin[:, p], want_s, want_c), (cos[:, p], want_c, want_s)):
+            assert np.all(np.abs(g - w) <= 2.0 ** -22 * np.abs(w) + moved * np.abs(d)), p
