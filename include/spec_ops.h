@@ -160,11 +160,14 @@ SV_API sv_status spec_count_tokens(const sv_count_args *count, void *stream);
  * Row j of sequence i (block rows as in spec_verify.h) follows the tokens of
  * the table, the ctx tokens and drafts 1..j of its block; n is how often a
  * token was emitted among them, and a token is known if n > 0 or the prompt
- * holds it.  For every token, in fp32 and rounded once:
+ * holds it.  For every token:
  *   known:   l = l > 0 ? l / repetition : l * repetition
- *   always:  l = l - (frequency * n + (n > 0 ? presence : 0))
- *            l = l + bias            (the row's sequence's, where it has one)
+ *   n > 0:   l = l - (frequency * n + presence)
+ *   biased:  l = l + bias
  *   barred:  l = -inf                (the mask's bit is 0; whatever l was)
+ * Each line's result is rounded to nearest in fp32 (the bracket before it, too: one
+ * rounding), the last one to the logits' type.  Quotients of l outside [2^-60, 2^60] are
+ * within 2^-23 of the exact value instead of 2^-24.
  * Tokens that nothing of this touches keep their bits (a NaN where a later
  * draft's token stands remains some NaN).  Draft row j takes what target row j
  * takes.  A row whose mask bars everything is all -inf (the

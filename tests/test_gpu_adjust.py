@@ -12,7 +12,7 @@ import torch
 
 import oracle
 from gpu_util import dev, host_bits
-from workloads import f32_to_bf16_bits
+from workloads import bf16_bits_to_f32, f32_to_bf16_bits
 
 pytestmark = pytest.mark.gpu
 
@@ -507,3 +507,58 @@ def test_row_bounds_whose_difference_wraps(api, cu, skipped):
             assert bool((c.ot[r] == 77).all()), r
         else:
             assert np.array_equal(got[r], c.target[r])
+
+
+@pytest.mark.parametrize("B,V,in_place", CUTS)
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_the_repetition_quotient_is_rounded_once(api, B, V, in_place, dtype):
+    """Prompt tokens under a repetition penalty alone: the fp32 product, and for logits
+    between 2^-60 and 2^60 the fp32 quotient, to the bit (rounded again to bf16 there); a
+    logit that equals the penalty becomes 1.  Farther positive logits are multiplied by
+    the rounded reciprocal: two roundings of 2^-24 (or half of the least subnormal)."""
+    c = Case(api, ([2, 1] * B)[:B], V, dtype, seed=31, draft=False, penal=False, hist=1)
+    rng = c.rng
+    r = np.exp(rng.uniform(-1, 1, B)).astype(np.float32)
+    r[:4] = [1.1, 2.0 ** -64, 2.0 ** 64, 1.3]
+    if dtype == "bf16":
+        r[4:] = bf16_bits_to_f32(f32_to_bf16_bits(r[4:]))
+    counts = np.where(rng.random((B + 2, V)) < 0.05, np.int32(-2 ** 31), 0).astype(np.int32)
+    c.kw.update(counts=counts, seen=oracle.seen_bits(counts), repetitions=r)
+    seq = np.repeat(np.arange(B), np.diff(c.cu))
+    x = rng.standard_normal((c.R, V), dtype=np.float32) * np.float32(3)
+    far = rng.random(x.shape) < 0.2
+    x[far] *= np.exp2(rng.uniform(-140, 124, far.sum())).astype(np.float32)
+    own = rng.random(x.shape) < 0.1
+    x = np.where(own, r[seq][:, None], x)
+    if dtype == "bf16":
+        c.target = f32_to_bf16_bits(x)
+        x = bf16_bits_to_f32(c.target)
+    else:
+        c.target = x
+    api.spec_adjust_logits(c.args(in_place))
+    torch.cuda.synchronize()
+    with np.errstate(over="ignore", under="ignore"):
+        want = np.where(x > 0, x / r[seq][:, None], x * r[seq][:, None])
+    known = counts[c.kw["slots"][seq]] != 0
+    for i in np.flatnonzero(np.diff(c.cu) == 2):        # the second row of a block knows its draft
+        known[c.cu[i] + 1, c.tokens[c.cu[i] - i]] = True
+    want = np.where(known, want, x)
+    got = host_bits(c.ot)
+    if dtype == "bf16":
+        got = bf16_bits_to_f32(got)
+        big = np.abs(want) >= np.float32(3.3961775e38)      # rounds past the largest bf16
+        want = np.where(big, np.copysign(np.float32(np.inf), want),
+                        bf16_bits_to_f32(f32_to_bf16_bits(np.where(big, 0, want))))
+    far = known & (x > 0) & ((x < 2.0 ** -60) | (x > 2.0 ** 60))
+    assert far.any() and np.array_equal(got[~far], want[~far])
+    got, exact = got[far].astype(np.float64), (x.astype(np.float64) / r[seq][:, None])[far]
+    top, half, least = (2.0 ** 128 * (1 - 2.0 ** -9), 2.0 ** -8, 2.0 ** -134) if dtype == "bf16" else \
+        (2.0 ** 128 * (1 - 2.0 ** -25), 0.0, 0.0)
+    two = 2.0 ** -23 * (1 + 2.0 ** -24)
+    assert np.all(exact[np.isinf(got)] >= top * (1 - two))
+    assert np.all(got[exact >= top * (1 + two)] == np.inf)
+    fin = np.isfinite(got)
+    assert np.all(np.abs(got - exact)[fin] <= ((two + half) * exact + 2.0 ** -149 + least)[fin])
+    got = bf16_bits_to_f32(host_bits(c.ot)) if dtype == "bf16" else host_bits(c.ot)
+    assert bool((got[known & own & (x == r[seq][:, None])] == 1).all())
+    assert int(c.status.item()) == 0
