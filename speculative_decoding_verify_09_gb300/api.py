@@ -444,6 +444,8 @@ def adjust_args(target, target_out, cu_q, *, max_q_rows, draft=None, draft_out=N
         raise ValueError("counts and seen go together")
     if counts is not None:
         a.num_slots = counts.shape[0]
+        if a.num_slots < 1:
+            raise ValueError("counts has no row")
         a.counts = c.add(counts, "counts", torch.int32, shape=(a.num_slots, V))
         a.seen = c.add(seen, "seen", _WORDS, shape=(a.num_slots, (V + 31) // 32))
         a.slots = c.add(slots, "slots", torch.int32, shape=(B,))
@@ -471,6 +473,8 @@ def adjust_args(target, target_out, cu_q, *, max_q_rows, draft=None, draft_out=N
         a.num_masks, a.mask_stride = mask.shape
         a.mask = c.add(mask, "mask", _WORDS)
         a.mask_rows = c.add(mask_rows, "mask_rows", torch.int32, shape=(R,))
+        if not a.mask:          # no rows: an empty tensor's null would mean no mask, whatever
+            a.mask = a.cu_q     # rows mask_rows names (of num_masks = 0 rows none is read)
     a.dev_status = c.add(dev_status, "dev_status", _WORDS, at_least=1)
     return _finish(a, c)
 

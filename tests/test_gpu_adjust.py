@@ -562,3 +562,19 @@ def test_the_repetition_quotient_is_rounded_once(api, B, V, in_place, dtype):
     got = bf16_bits_to_f32(host_bits(c.ot)) if dtype == "bf16" else host_bits(c.ot)
     assert bool((got[known & own & (x == r[seq][:, None])] == 1).all())
     assert int(c.status.item()) == 0
+
+
+def test_masks_and_tables_without_rows(api):
+    """A mask of no rows has no row that could be named, and a table of no rows no slot."""
+    c = Case(api, [2, 1], 100, seed=16)
+    none = torch.zeros(0, 4, dtype=torch.int32, device="cuda")
+    c.run(mask=none, mask_rows=np.full(3, -1, np.int32))                # nothing masked
+    api.spec_adjust_logits(c.args(mask=none, mask_rows=np.array([-1, -1, 0], np.int32)))
+    torch.cuda.synchronize()
+    assert int(c.status.item()) == oracle.DEV_BAD_PARAM
+    assert torch.isnan(c.ot.float()).all(1).tolist() == [False, False, True]
+    from speculative_decoding_verify_09_gb300._binding import SpecVerifyError
+    with pytest.raises(SpecVerifyError, match="num_masks"):
+        api.spec_adjust_logits(c.args(mask=none))
+    with pytest.raises(ValueError, match="row"):
+        c.args(counts=torch.zeros(0, 100, dtype=torch.int32, device="cuda"), seen=none)
