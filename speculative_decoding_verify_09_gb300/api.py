@@ -356,6 +356,7 @@ def rope_args(q, k, v, q_out, k_out, v_out, turns, *, cu_q=None, kv_len=None, po
         if cu_q is not None or kv_len is not None:
             raise ValueError("positions stand instead of cu_q and kv_len")
         a.positions = c.add(positions, "positions", torch.int64, shape=(R,))
+        a.max_q_rows = 1        # (no rows: an empty tensor's null says by sequences)
     else:
         if cu_q is None or kv_len is None:
             raise ValueError("cu_q and kv_len, or positions, are needed")

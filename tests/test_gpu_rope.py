@@ -454,3 +454,17 @@ def test_cos_and_sin_are_as_exact_as_fp32_has_them(api, layout):
         moved = np.pi * np.abs(rest) * 2.0 ** -24
         for g, w, d in ((sin[:, p], want_s, want_c), (cos[:, p], want_c, want_s)):
             assert np.all(np.abs(g - w) <= 2.0 ** -22 * np.abs(w) + moved * np.abs(d)), p
+
+
+def test_no_rows_from_torch(api):
+    """Calls with nothing to turn do nothing, by positions and by sequences."""
+    turns, _ = api.rope_turns(64)
+    x = torch.zeros(0, 2, 64, device="cuda")
+    cu = torch.zeros(3, dtype=torch.int32, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    for kw in (dict(positions=torch.zeros(0, dtype=torch.int64, device="cuda")),
+               dict(cu_q=cu, kv_len=cu[:2], max_q_rows=4),
+               dict(cu_q=cu[:1], kv_len=cu[:0], max_q_rows=1)):
+        api.spec_rope_rows(api.rope_args(x, x, x, x, x, x, turns, dev_status=status, **kw))
+    torch.cuda.synchronize()
+    assert int(status.item()) == 0
