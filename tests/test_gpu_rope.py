@@ -468,3 +468,76 @@ def test_no_rows_from_torch(api):
         api.spec_rope_rows(api.rope_args(x, x, x, x, x, x, turns, dev_status=status, **kw))
     torch.cuda.synchronize()
     assert int(status.item()) == 0
+
+
+def _prompt_rows(more=37):
+    """More rows than pairs of rows can fill the SMs with, so that a CTA takes several
+    rows side by side: 16, 8 or 4 by the heads and their columns, or still 2."""
+    return 8 * torch.cuda.get_device_properties(0).multi_processor_count + more
+
+
+def _ends_and_middle(n):
+    return np.unique(np.concatenate([np.arange(33), n // 2 + np.arange(33), np.arange(n - 40, n)]))
+
+
+WIDE = [(64, 64, "half"), (80, 80, "half"), (64, 24, "half"), (64, 20, "half"), (64, 22, "half"), (40, 36, "half"), (256, 250, "half"),
+        (64, 64, "interleaved"), (80, 80, "interleaved"), (64, 20, "interleaved"), (72, 50, "interleaved")]
+
+
+@pytest.mark.parametrize("D,rot,layout", WIDE)
+@pytest.mark.parametrize("Hq,Hkv", [(3, 1), (14, 7), (40, 5), (80, 5)])
+@pytest.mark.parametrize("dtype,kv8", [("bf16", False), ("bf16", True), ("f32", False), ("f32", True)])
+def test_rows_side_by_side(api, D, rot, layout, Hq, Hkv, dtype, kv8):
+    """All ways a CTA shares its threads among rows, heads and columns, in even and odd
+    numbers; sequences by slots (all about as long) and searched (a long one among
+    short ones), rows behind the last one untouched."""
+    n = _prompt_rows()
+    for rows in ([n - n // 2, n // 2], [n - 63, 0, 1, 50, 12]):
+        c = Case(api, rows, Hq, Hkv, D, rot, dtype, layout, kv8, seed=D + Hq, extra_rows=3, mscale=1.1)
+        api.spec_rope_rows(c.args())
+        c.check(rows=_ends_and_middle(n))
+        assert int(c.status.item()) == 0
+        for p in "qkv":
+            untouched = 0xAB if kv8 and p != "q" else 123
+            assert bool((c.out[p][n:] == untouched).all())
+            assert bool((c.out[p][:n] != untouched).flatten(1).any(1).all())
+
+
+@pytest.mark.parametrize("D,rot,layout", WIDE)
+@pytest.mark.parametrize("Hq,Hkv", [(3, 1), (14, 7), (40, 5)])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_rows_side_by_side_in_place_and_by_positions(api, D, rot, layout, Hq, Hkv, dtype):
+    n = _prompt_rows(5)
+    c = Case(api, [n], Hq, Hkv, D, rot, dtype, layout, seed=rot)
+    api.spec_rope_rows(c.args())
+    c.check(rows=_ends_and_middle(n))
+    own = {p: c.dx[:, c.heads[p]].contiguous() for p in "qkv"}
+    pos = dev(np.array(oracle.row_positions(c.cu, c.kv_len), dtype=np.int64))
+    api.spec_rope_rows(api.rope_args(own["q"], own["k"], own["v"], own["q"], own["k"], own["v"], c.turns,
+                                     positions=pos, layout=layout))
+    torch.cuda.synchronize()
+    for p in "qkv":
+        assert torch.equal(own[p], c.out[p]), p
+
+
+def test_rows_side_by_side_out_of_range(api):
+    """Among many rows, those of bad positions and of bad sequences stay as they are."""
+    n = _prompt_rows()
+    c = Case(api, [n], 3, 1, 64, 64, seed=1)
+    pos = np.arange(n, dtype=np.int64)
+    bad = np.arange(7, n, 97)
+    pos[bad] = np.where(bad % 2, 2 ** 31, -2 ** 40)
+    api.spec_rope_rows(c.args(positions=dev(pos)))
+    keep = np.setdiff1d(_ends_and_middle(n), bad)
+    c.check(positions=pos, rows=keep)
+    assert int(c.status.item()) == oracle.DEV_BAD_LENGTH
+    assert bool((c.out["q"][torch.from_numpy(bad).cuda()] == 123).all())
+    c = Case(api, [n // 4] * 4, 3, 1, 64, 64, seed=2)
+    kv = c.kv_len.copy()
+    kv[2] = -1
+    api.spec_rope_rows(c.args(kv_len=dev(kv)))
+    m = n // 4
+    c.check(rows=np.concatenate([np.arange(2 * m - 20, 2 * m), np.arange(3 * m, 3 * m + 20)]))
+    assert int(c.status.item()) == oracle.DEV_BAD_LENGTH
+    for p in "qkv":
+        assert bool((c.out[p][2 * m:3 * m] == 123).all())
