@@ -30,7 +30,7 @@ namespace sv {
 namespace {
 
 constexpr int kNT = 256;                   // threads of the table's kernels
-constexpr float kMinRepetition = 0x1p-64f, kMaxRepetition = 0x1p64f;   // (its reciprocal is used)
+constexpr float kMinRepetition = 0x1p-64f, kMaxRepetition = 0x1p64f;   // (see penalized())
 constexpr int64_t kMaxEntries = int64_t{1} << 30;   // tokens, biases: a strided int index stays one
 constexpr int kBatch = 3;                  // (sparse) rows in flight per warp
 constexpr int kAhead = 4;                  // listed tokens in flight per lane and row
@@ -745,16 +745,23 @@ cudaError_t launch_adjust(int sms, AdjustParams &P, cudaStream_t s) {
   };
   // In place, changing single tokens in memory pays where a sequence's few
   // thousand listed tokens are thin in the row and there are CTAs enough to
-  // hide its longer chain of loads (bf16, 9 rows a sequence, 2048 tokens of
-  // history, a quarter of the rows masked; this against streaming the rows
-  // through: V = 128256 at B = 64 45 against 62 us, B = 16 17 against 19 us,
-  // B = 8 13 against 11 us; V = 32000, 11 rows, at B = 64 30 against 22 us, B = 8
-  // 13.5 against 7.3 us).
+  // hide its longer chain of loads.  This against streaming the rows through, in us
+  // (bf16, 9 rows a sequence, 2048 tokens of history, 64 biases, a quarter of the
+  // rows masked): V = 128256 at B = 64 45 / 62, B = 32 30 / 35, B = 16 18 / 20, B = 8
+  // 12.9 / 10.8; V = 65536 at B = 64 36 / 36, B = 16 13.5 / 11.0; V = 32000, 11 rows, at
+  // B = 64 29 / 22, B = 8 13.6 / 6.5.  The rule does not look at how much is listed
+  // and barred: V = 128256, B = 64 without masks 18 / 58 (no history), 54 / 67 (8192
+  // tokens), 75 / 86 (32768), fp32 45 / 110, 69 / 114 and 98 / 129 at 2048, 8192 and
+  // 32768; it loses with every row masked, 67 / 64 (2048) to 108 / 91 (32768; fp32 140 /
+  // 135), and with long histories of smaller batches, 55 / 31 at B = 16 with 32768 and
+  // every row masked, 43 / 27 at V = 70003, B = 32 with 8192.
   if (a.target == a.target_out && a.vocab >= 65536 && big >= 6 * static_cast<int64_t>(sms))
     return launch_adjust<T, 4096, 0>(split(big, 4, 16), P, s);
   // Streaming: 1 KB chunks until the 4 KB ones (fewer repeated starts) give
-  // about two CTAs per SM (bf16, V = 32000, 11 rows a sequence: at B = 8 6.4
-  // against 7.3 us, at B = 16 8.8 both, at B = 32 20.1 against 16.3 us).
+  // about two CTAs per SM (bf16, V = 32000, 11 rows a sequence, half of them masked: at
+  // B = 8 6.5 against 7.4 us, at B = 16 9.0 and 8.9, at B = 32 20.1 against 16.3, at
+  // B = 64 34.8 against 22.3; single rows at B = 8 4.7 against 6.7, at B = 64 20.4
+  // against 8.2).
   if (big < 2 * static_cast<int64_t>(sms)) return launch_adjust<T, 1024, 1024>(split(small, 8, 4), P, s);
   return launch_adjust<T, 4096, 2048>(split(big, 4, 8), P, s);
 }
@@ -856,8 +863,9 @@ SV_API sv_status spec_count_tokens(const sv_count_args *a, void *stream) {
   cudaError_t e;
   if (a->flags & SV_COUNT_RESET) {
     // For a prompt the slices are as large as a CTA can be (64 prompts of 1024 to
-    // 4096 tokens, V = 128256: 9.3 us with 8192 tokens a slice, 7.7 us so); counts
-    // take shared memory.
+    // 4096 tokens, V = 128256: 8.6 us with 8192 tokens a slice, 7.4 us so; prompts of
+    // 100 k tokens 44 us, one alone 29 us, for every slice reads all of its tokens);
+    // counts take shared memory (10.0 us for the same tokens).
     auto slices = [&](int threads) { return static_cast<unsigned>((a->vocab + 32 * threads - 1) / (32 * threads)); };
     if (a->flags & SV_COUNT_PROMPT)
       e = launch_behind(reset_kernel<1024, true>, dim3(a->batch, slices(1024)), 1024, 0, s, P);

@@ -183,7 +183,12 @@ __device__ __forceinline__ bool find_row(const RopeParams &P, int64_t slot, int6
 // As measured (32768 rows of 48 heads of 128): bf16 G = 8 122 us at 4 CTAs, 134 at
 // 3, 131 at 5; fp32 237 us at 3, 253 at 4; with codes 131 us at 3, 165 at 5; one,
 // two, four heads at G = 1 304, 266, 232 us, at G = 2 180, 168, 150 us, one and two
-// at G = 4 162 and 134 us.
+// at G = 4 162 and 134 us.  The caps cost some kernels a little local memory, which stays
+// in L1: 16 and 20 bytes a thread in bf16 with codes, interleaved and at G = 8, 28 and 32
+// in fp32 with codes, 12 to 40 at G = 4 with codes or in fp32.  A CTA per SM less needs
+// none, but takes 167 against 135 us (bf16, codes, G = 8), 169 against 140 (interleaved),
+// 243 against 218 (fp32, codes, G = 8); only at G = 4 with codes it would pay (162 against
+// 187 us in bf16, 225 against 258 in fp32).
 template <int G, bool KV8>
 struct InFlight {
   static constexpr int kHeads = G == 1 || G == 2 ? (KV8 ? 2 : 4) : G == 4 ? 2 : 1;
