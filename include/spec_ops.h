@@ -58,8 +58,8 @@ typedef struct sv_rope_args {
   int32_t dtype;            /* SV_F32 or SV_BF16: q, k, v and q_out */
   int32_t kv_dtype;         /* 0 (k_out, v_out in dtype) or SV_E4M3 codes */
   int64_t num_rows;         /* R rows of q, k and v */
-  int32_t max_q_rows;       /* host bound on the rows of one sequence, >= 1
-                               (ignored with positions) */
+  int32_t max_q_rows;       /* host bound on the rows of one sequence, >= 1;
+                               B * max_q_rows < 2^31 (ignored with positions) */
   float mscale;             /* m, the factor on cos and sin; 0 -> 1 */
   float k_scale;            /* E4M3: code = round(k / k_scale); 0 -> 1 */
   float v_scale;            /* E4M3: code = round(v / v_scale); 0 -> 1 */
@@ -73,8 +73,8 @@ typedef struct sv_rope_args {
   const int32_t *kv_len;    /* [dev] [B] row j of sequence i is at kv_len[i] + j */
   const int64_t *positions; /* [dev] [R] or NULL: the rows' positions themselves,
                                instead of cu_q and kv_len; |position| < 2^31.
-                               A rotation by -t undoes one by t and is its
-                               transpose: gradients of q_out and k_out go back
+                               A rotation by -t undoes one by t (but for m^2) and is
+                               its transpose: gradients of q_out and k_out go back
                                through the same call with negated positions */
   const void *q;            /* [dev] [R, Hq, D] rows q_stride apart */
   const void *k;            /* [dev] [R, Hkv, D]; NULL: v only */

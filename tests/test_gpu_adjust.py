@@ -578,3 +578,13 @@ def test_masks_and_tables_without_rows(api):
         api.spec_adjust_logits(c.args(mask=none))
     with pytest.raises(ValueError, match="row"):
         c.args(counts=torch.zeros(0, 100, dtype=torch.int32, device="cuda"), seen=none)
+
+
+@pytest.mark.parametrize("B,V,in_place", CUTS)
+def test_as_many_ctx_tokens_as_allowed_and_long_bias_lists(api, B, V, in_place):
+    c = Case(api, ([2, 1] * B)[:B], V, seed=41, hist=300, ctx=1024, bias=6000, masked=0.2)
+    near = c.rng.integers(0, V - 200)
+    c.kw["ctx_tokens"][:20] = near + c.rng.integers(0, 100, (20, B))       # some of them often
+    c.run(in_place)
+    c = Case(api, ([3, 1] * B)[:B], V, "f32", seed=42, draft=False, table=False, bias=20000)
+    c.run(in_place)

@@ -285,3 +285,48 @@ def test_inputs_written_by_the_kernel_just_before(api):
     for k in range(40):
         assert torch.equal(got_y[k], want[k % 2]), k
         assert torch.equal(got_c[k], marked[k % 2]), k
+
+
+def test_captured_behind_copies_fills_and_another_stream(api):
+    """In a graph, the operators may follow nodes that are no kernels (fills, copies) and
+    join work of another stream: they wait for it all the same."""
+    V, n = 4000, 64
+    g = torch.Generator(device="cuda").manual_seed(3)
+    x = torch.randn(n, 2, 64, device="cuda", generator=g)
+    xs, y, pos = torch.empty_like(x), torch.empty_like(x), torch.arange(n, device="cuda")
+    turns, _ = api.rope_turns(64)
+    rope = api.rope_args(xs, None, None, y, None, None, turns, positions=pos)
+    logits = torch.randn(n, V, device="cuda", generator=g)
+    ls, out = torch.empty_like(logits), torch.empty_like(logits)
+    cu = torch.arange(n + 1, dtype=torch.int32, device="cuda")
+    tokens = torch.randint(0, V, (n,), device="cuda", generator=g, dtype=torch.int32)
+    ts, table = torch.empty_like(tokens), api.TokenCounts(n, V)
+    count = api.count_args(table.counts, table.seen, ts, cu)
+    adjust = api.adjust_args(ls, out, cu, max_q_rows=1, counts=table.counts, seen=table.seen, presence=0.5)
+    main, side = torch.cuda.Stream(), torch.cuda.Stream()
+    main.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=main):
+        table.counts.zero_()
+        table.seen.zero_()
+        ts.copy_(tokens)
+        api.spec_count_tokens(count)                    # behind fills and a copy
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            ls.copy_(logits)
+            xs.copy_(x)
+            api.spec_rope_rows(rope)                    # behind a copy on the other stream
+        main.wait_stream(side)
+        api.spec_adjust_logits(adjust)                  # behind both streams
+    for k in range(3):
+        x.mul_(1.5)
+        logits.mul_(-1.25)
+        tokens.add_(7).remainder_(V)
+        graph.replay()
+        torch.cuda.synchronize()
+        want = torch.empty_like(y)
+        api.spec_rope_rows(api.rope_args(x, None, None, want, None, None, turns, positions=pos))
+        assert torch.equal(y, want), k
+        want = logits.clone()
+        want[torch.arange(n, device="cuda"), tokens.long()] -= 0.5
+        assert torch.equal(out, want), k
