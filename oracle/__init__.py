@@ -17,6 +17,7 @@ Modules (each cites the passages it follows):
              position (single-row attention, append, draw)
   rope       rotary positions of block rows, E4M3 rounding
   logits     penalties, biases and grammar masks on logits rows; the token table
+  kv4        per-head norms; the paged 4-bit KV cache and attention over it
 """
 from .philox import philox4x32, verify_uniforms, word_to_uniform
 from .sampling import (process_row, accept, residual, sample_index, verify_sequence,
@@ -29,3 +30,5 @@ from .step import verify_step
 from .draft import draft_sample, draft_step
 from .rope import (rope_frequencies, rope_rows, row_positions, e4m3_nearest)
 from .logits import (count_tokens, seen_bits, adjust_logits, adjust_row, allowed_tokens)
+from .kv4 import (e2m1_nearest, e2m1_to_f64, kv4_quantize, kv4_values, kv4_store, kv4_load, head_norm,
+                  kv4_attention)

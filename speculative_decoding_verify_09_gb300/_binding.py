@@ -113,6 +113,54 @@ class AdjustArgs(ctypes.Structure):
     ]
 
 
+class Kv4Cache(ctypes.Structure):
+    """Mirror of sv_kv4_cache."""
+    _fields_ = [
+        ("num_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+        ("page_size", ctypes.c_int32), ("max_pages", ctypes.c_int32),
+        ("num_pages", ctypes.c_int64), ("table_stride", ctypes.c_int64),
+        ("k_scale", ctypes.c_float), ("v_scale", ctypes.c_float), ("pages", _p), ("table", _p),
+    ]
+
+
+class NormArgs(ctypes.Structure):
+    """Mirror of sv_norm_args."""
+    _fields_ = [
+        ("q_weight", _p), ("k_weight", _p), ("eps", ctypes.c_float),
+        ("weight_offset", ctypes.c_float),
+    ]
+
+
+class NormRopeArgs(ctypes.Structure):
+    """Mirror of sv_norm_rope_args."""
+    _fields_ = [("rope", RopeArgs), ("norm", NormArgs)]
+
+
+class Kv4AppendArgs(ctypes.Structure):
+    """Mirror of sv_kv4_append_args."""
+    _fields_ = [("rows", RopeArgs), ("norm", NormArgs), ("cache", Kv4Cache)]
+
+
+class Kv4ReadArgs(ctypes.Structure):
+    """Mirror of sv_kv4_read_args."""
+    _fields_ = [
+        ("cache", Kv4Cache), ("batch", ctypes.c_int32), ("max_q_rows", ctypes.c_int32),
+        ("dtype", ctypes.c_int32), ("reserved", ctypes.c_int32), ("num_rows", ctypes.c_int64),
+        ("k_out_scale", ctypes.c_float), ("v_out_scale", ctypes.c_float), ("cu_q", _p),
+        ("kv_len", _p), ("k_out", _p), ("v_out", _p), ("dev_status", _p),
+    ]
+
+
+class Kv4AttnArgs(ctypes.Structure):
+    """Mirror of sv_kv4_attn_args."""
+    _fields_ = [
+        ("cache", Kv4Cache), ("batch", ctypes.c_int32), ("num_q_heads", ctypes.c_int32),
+        ("max_q_rows", ctypes.c_int32), ("dtype", ctypes.c_int32), ("num_rows", ctypes.c_int64),
+        ("q_stride", ctypes.c_int64), ("scale", ctypes.c_float), ("reserved", ctypes.c_int32),
+        ("cu_q", _p), ("kv_len", _p), ("q", _p), ("out", _p), ("dev_status", _p),
+    ]
+
+
 def _load():
     if not os.path.exists(LIB_PATH):
         raise ImportError(
@@ -156,6 +204,20 @@ def _load():
     lib.spec_count_tokens.restype = ctypes.c_int
     lib.spec_adjust_logits.argtypes = [P(AdjustArgs), _p]
     lib.spec_adjust_logits.restype = ctypes.c_int
+    lib.spec_norm_rope_rows.argtypes = [P(NormRopeArgs), _p]
+    lib.spec_norm_rope_rows.restype = ctypes.c_int
+    lib.spec_kv4_append.argtypes = [P(Kv4AppendArgs), _p]
+    lib.spec_kv4_append.restype = ctypes.c_int
+    lib.spec_kv4_read.argtypes = [P(Kv4ReadArgs), _p]
+    lib.spec_kv4_read.restype = ctypes.c_int
+    lib.sv_kv4_workspace_bytes.argtypes = [P(Kv4AttnArgs)]
+    lib.sv_kv4_workspace_bytes.restype = ctypes.c_size_t
+    lib.spec_kv4_attn.argtypes = [P(Kv4AttnArgs), _p, ctypes.c_size_t, _p]
+    lib.spec_kv4_attn.restype = ctypes.c_int
+    lib.sv_kv4_version.argtypes = []
+    lib.sv_kv4_version.restype = ctypes.c_int32
+    lib.sv_kv4_struct_size.argtypes = [ctypes.c_int32]
+    lib.sv_kv4_struct_size.restype = ctypes.c_size_t
     lib.sv_ops_version.argtypes = []
     lib.sv_ops_version.restype = ctypes.c_int32
     lib.sv_ops_struct_size.argtypes = [ctypes.c_int32]
@@ -173,6 +235,10 @@ def _load():
     if any(lib.sv_ops_struct_size(i) != ctypes.sizeof(c)
            for i, c in enumerate((RopeArgs, RopeScaling, CountArgs, AdjustArgs))):
         raise ImportError("libspecverify.so operator structs do not match this binding")
+    if any(lib.sv_kv4_struct_size(i) != ctypes.sizeof(c)
+           for i, c in enumerate((Kv4Cache, NormArgs, NormRopeArgs, Kv4AppendArgs, Kv4ReadArgs,
+                                  Kv4AttnArgs))):
+        raise ImportError("libspecverify.so 4-bit cache structs do not match this binding")
     return lib
 
 

@@ -9,9 +9,9 @@ import ctypes
 import torch
 
 from ._binding import (AdjustArgs, AttnArgs, COUNT_PROMPT, COUNT_RESET, CountArgs, DraftArgs,
-                       ROPE_BANDED, ROPE_HALF, ROPE_INTERLEAVED, ROPE_LINEAR, ROPE_NTK,
-                       ROPE_PLAIN, ROPE_YARN, RopeArgs, RopeScaling, SampleArgs, SV_BF16, SV_E4M3,
-                       SV_F32, _check, lib)
+                       Kv4AppendArgs, Kv4AttnArgs, Kv4ReadArgs, NormRopeArgs, ROPE_BANDED,
+                       ROPE_HALF, ROPE_INTERLEAVED, ROPE_LINEAR, ROPE_NTK, ROPE_PLAIN, ROPE_YARN,
+                       RopeArgs, RopeScaling, SampleArgs, SV_BF16, SV_E4M3, SV_F32, _check, lib)
 
 
 def _ptr(t):
@@ -267,7 +267,7 @@ def _rows_stride(t, name):
     return t.stride(0)
 
 
-def _launch(fn, args, stream):
+def _launch(fn, args, stream, ws=None):
     """Calls fn on `stream` or the current one; the tensors' device has to be the current one.
     (The raw stream: a torch.cuda.Stream object costs more than the launch.)"""
     device = args._device
@@ -279,7 +279,10 @@ def _launch(fn, args, stream):
         raise ValueError(f"tensors are on cuda:{device}, the stream on cuda:{stream.device_index}")
     else:
         raw = stream.cuda_stream
-    st = fn(ctypes.byref(args), raw)
+    if ws is None:
+        st = fn(ctypes.byref(args), raw)
+    else:
+        st = fn(ctypes.byref(args), ws.ptr, ws.nbytes, raw)
     if st:
         _check(st)
 
@@ -309,16 +312,10 @@ def rope_turns(rot_dim, *, base=10000.0, scaling="plain", factor=1.0, trained_le
     return turns.to(device or "cuda"), m.value
 
 
-def rope_args(q, k, v, q_out, k_out, v_out, turns, *, cu_q=None, kv_len=None, positions=None,
-              max_q_rows=0, layout="half", mscale=1.0, k_scale=0.0, v_scale=0.0, dev_status=None):
-    """sv_rope_args for q [R, Hq, D], k / v [R, Hkv, D] (rows may lie apart, as
-    in a fused projection; any of the three may be None) and their contiguous
-    outputs; turns [rot_dim / 2] int64 from rope_turns.  Positions: row j of
-    sequence i at kv_len[i] + j with cu_q [B+1] and kv_len [B] (int32) and the
-    host bound max_q_rows on a sequence's rows, or `positions` [R] int64.
-    layout "half" (pairs rot_dim / 2 apart) or "interleaved" (neighbours).
-    uint8 k_out / v_out take E4M3 codes of k / k_scale and v / v_scale."""
-    a, c = RopeArgs(), _Args()
+def _fill_rows(a, c, q, k, v, q_out, k_out, v_out, turns, cu_q, kv_len, positions, max_q_rows,
+               layout, mscale, k_scale, v_scale, dev_status, paged=False):
+    """Fills sv_rope_args `a`, its tensors collected in c; turns None: no rotation; paged: k and v
+    have no rows to go to."""
     first = next((t for t in (q, k, v) if t is not None), None)
     if first is None:
         raise ValueError("q, k and v are all None")
@@ -331,27 +328,29 @@ def rope_args(q, k, v, q_out, k_out, v_out, turns, *, cu_q=None, kv_len=None, po
     for name, t, out in (("q", q, q_out), ("k", k, k_out), ("v", v, v_out)):
         if t is None:
             continue
-        if out is None:
+        if out is None and (name == "q" or not paged):
             raise ValueError(f"{name}_out is None")
         if t.shape[0] != R or t.shape[2] != D:
             raise ValueError(f"{name}: shape {tuple(t.shape)}, expected ({R}, heads, {D})")
         setattr(a, name, c.add(t, name, first.dtype, rows=True))
-        setattr(a, name + "_out", c.add(out, name + "_out", (first.dtype,) if name == "q" else
-                                        (first.dtype, torch.uint8), shape=t.shape))
         setattr(a, name + "_stride", _rows_stride(t, name))
-    outs = {t.dtype for t, x in ((k_out, k), (v_out, v)) if x is not None}
+        if out is not None:
+            setattr(a, name + "_out", c.add(out, name + "_out", (first.dtype,) if name == "q" else
+                                            (first.dtype, torch.uint8), shape=t.shape))
+    outs = {t.dtype for t, x in ((k_out, k), (v_out, v)) if x is not None and t is not None}
     if len(outs) > 1 or (k is not None and v is not None and k.shape != v.shape):
         raise ValueError("k and v (and their outputs) must have one shape and dtype")
     if layout not in ("half", "interleaved"):
         raise ValueError(f"layout {layout!r} (half or interleaved)")
     a.num_q_heads = q.shape[1] if q is not None else 0
     a.num_kv_heads = next((t.shape[1] for t in (k, v) if t is not None), 0)
-    a.head_dim, a.rot_dim, a.num_rows = D, 2 * turns.shape[0], R
+    a.head_dim, a.num_rows = D, R
+    if turns is not None:
+        a.rot_dim, a.turns = 2 * turns.shape[0], c.add(turns, "turns", torch.int64)
     a.layout = ROPE_HALF if layout == "half" else ROPE_INTERLEAVED
     a.dtype = _dt(first)
     a.kv_dtype = SV_E4M3 if torch.uint8 in outs else 0
     a.mscale, a.k_scale, a.v_scale = float(mscale), float(k_scale), float(v_scale)
-    a.turns = c.add(turns, "turns", torch.int64)
     if positions is not None:
         if cu_q is not None or kv_len is not None:
             raise ValueError("positions stand instead of cu_q and kv_len")
@@ -364,6 +363,22 @@ def rope_args(q, k, v, q_out, k_out, v_out, turns, *, cu_q=None, kv_len=None, po
         a.cu_q = c.add(cu_q, "cu_q", torch.int32)
         a.kv_len = c.add(kv_len, "kv_len", torch.int32, shape=(a.batch,))
     a.dev_status = c.add(dev_status, "dev_status", _WORDS, at_least=1)
+
+
+def rope_args(q, k, v, q_out, k_out, v_out, turns, *, cu_q=None, kv_len=None, positions=None,
+              max_q_rows=0, layout="half", mscale=1.0, k_scale=0.0, v_scale=0.0, dev_status=None):
+    """sv_rope_args for q [R, Hq, D], k / v [R, Hkv, D] (rows may lie apart, as
+    in a fused projection; any of the three may be None) and their contiguous
+    outputs; turns [rot_dim / 2] int64 from rope_turns.  Positions: row j of
+    sequence i at kv_len[i] + j with cu_q [B+1] and kv_len [B] (int32) and the
+    host bound max_q_rows on a sequence's rows, or `positions` [R] int64.
+    layout "half" (pairs rot_dim / 2 apart) or "interleaved" (neighbours).
+    uint8 k_out / v_out take E4M3 codes of k / k_scale and v / v_scale."""
+    if turns is None:
+        raise ValueError("turns is None")
+    a, c = RopeArgs(), _Args()
+    _fill_rows(a, c, q, k, v, q_out, k_out, v_out, turns, cu_q, kv_len, positions, max_q_rows, layout,
+               mscale, k_scale, v_scale, dev_status)
     return _finish(a, c)
 
 
@@ -483,3 +498,147 @@ def adjust_args(target, target_out, cu_q, *, max_q_rows, draft=None, draft_out=N
 def spec_adjust_logits(adjust, stream=None):
     """Penalties, biases and grammar masks on the target (and draft) rows."""
     _launch(lib.spec_adjust_logits, adjust, stream)
+
+
+# --------------------------------------------- norms and the paged 4-bit KV cache
+class Kv4Cache:
+    """Pages of a 4-bit KV cache: `pages` [num_pages, num_kv_heads, page_size / 16, 18 * head_dim]
+    uint8 (spec_kv4.h has the layout), zeroed, or the caller's own.  page_size is a multiple of 16,
+    head_dim 64 or 128.  An element is E2M1 code * E4M3 scale of its 16 elements * k_scale (v_scale)."""
+
+    def __init__(self, num_pages, num_kv_heads, head_dim, *, page_size=64, k_scale=1.0, v_scale=1.0,
+                 pages=None, device=None):
+        if page_size < 16 or page_size % 16:
+            raise ValueError(f"page_size {page_size} (a multiple of 16)")
+        self.num_pages, self.num_kv_heads, self.head_dim = num_pages, num_kv_heads, head_dim
+        self.page_size, self.k_scale, self.v_scale = page_size, float(k_scale), float(v_scale)
+        shape = (num_pages, num_kv_heads, page_size // 16, 18 * head_dim)
+        if pages is None:
+            pages = torch.zeros(shape, dtype=torch.uint8, device=device or "cuda")
+        if tuple(pages.shape) != shape or pages.dtype != torch.uint8:
+            raise ValueError(f"pages: {pages.dtype} {tuple(pages.shape)}, expected uint8 {shape}")
+        self.pages = pages
+
+
+def _fill_cache(a, c, cache, table, batch):
+    """Fills sv_kv4_cache `a` for `table` [B, max_pages] int32 (rows may lie apart)."""
+    if table.dim() != 2 or table.shape[0] != batch:
+        raise ValueError(f"table: shape {tuple(table.shape)}, expected ({batch}, pages)")
+    if (table.shape[1] > 1 and table.stride(1) != 1) or (batch > 1 and table.stride(0) < table.shape[1]):
+        raise ValueError("table: rows must be contiguous and apart")
+    if not cache.k_scale > 0.0 or not cache.v_scale > 0.0:
+        raise ValueError("k_scale and v_scale must be > 0")
+    a.num_kv_heads, a.head_dim, a.page_size = cache.num_kv_heads, cache.head_dim, cache.page_size
+    a.max_pages, a.num_pages = table.shape[1], cache.num_pages
+    a.table_stride = table.stride(0) if batch > 1 else 0
+    a.k_scale, a.v_scale = cache.k_scale, cache.v_scale
+    a.pages = c.add(cache.pages, "pages", torch.uint8)
+    a.table = c.add(table, "table", torch.int32, rows=True)
+
+
+def _fill_norm(a, c, q_weight, k_weight, eps, weight_offset, D):
+    a.q_weight = c.add(q_weight, "q_weight", torch.float32, shape=(D,))
+    a.k_weight = c.add(k_weight, "k_weight", torch.float32, shape=(D,))
+    a.eps, a.weight_offset = float(eps), float(weight_offset)
+
+
+def norm_rope_args(q, k, v, q_out, k_out, v_out, turns=None, *, q_weight=None, k_weight=None, eps=1e-6,
+                   weight_offset=0.0, cu_q=None, kv_len=None, positions=None, max_q_rows=0,
+                   layout="half", mscale=1.0, k_scale=0.0, v_scale=0.0, dev_status=None):
+    """sv_norm_rope_args: as rope_args, with RMS norms over the heads of q and k in front of the
+    rotation: x / sqrt(mean(x^2) + eps) * (weight + weight_offset), weights [D] float32 (None: not
+    normed).  turns None: norms only."""
+    a, c = NormRopeArgs(), _Args()
+    _fill_rows(a.rope, c, q, k, v, q_out, k_out, v_out, turns, cu_q, kv_len, positions, max_q_rows,
+               layout, mscale, k_scale, v_scale, dev_status)
+    _fill_norm(a.norm, c, q_weight, k_weight, eps, weight_offset, a.rope.head_dim)
+    return _finish(a, c)
+
+
+def spec_norm_rope_rows(args, stream=None):
+    """Norms and rotates the q and k heads of every row (and turns k and v into cache codes)."""
+    _launch(lib.spec_norm_rope_rows, args, stream)
+
+
+def kv4_append_args(cache, table, cu_q, kv_len, k, v, *, max_q_rows, q=None, q_out=None, turns=None,
+                    q_weight=None, k_weight=None, eps=1e-6, weight_offset=0.0, layout="half",
+                    mscale=1.0, dev_status=None):
+    """sv_kv4_append_args: row j of sequence i of k and v [R, Hkv, D] becomes token kv_len[i] + j of
+    its pages table[i] (int32 [B, max_pages]) in `cache` (a Kv4Cache); k normed where k_weight is
+    given and rotated where turns is.  q [R, Hq, D] -> q_out (contiguous) takes the same on the way.
+    Other arguments as in norm_rope_args."""
+    a, c = Kv4AppendArgs(), _Args()
+    if k is None or v is None:
+        raise ValueError("k and v are needed")
+    _fill_rows(a.rows, c, q, k, v, q_out, None, None, turns, cu_q, kv_len, None, max_q_rows, layout,
+               mscale, 0.0, 0.0, dev_status, paged=True)
+    if k.shape[1:] != (cache.num_kv_heads, cache.head_dim):
+        raise ValueError(f"k: shape {tuple(k.shape)} for a cache of {cache.num_kv_heads} heads of "
+                         f"{cache.head_dim}")
+    _fill_norm(a.norm, c, q_weight, k_weight, eps, weight_offset, cache.head_dim)
+    _fill_cache(a.cache, c, cache, table, a.rows.batch)
+    return _finish(a, c)
+
+
+def spec_kv4_append(args, stream=None):
+    """Stores the rows' k and v in their sequences' pages as 4-bit codes, q on the way."""
+    _launch(lib.spec_kv4_append, args, stream)
+
+
+def kv4_read_args(cache, table, cu_q, kv_len, k_out, v_out, *, max_q_rows, k_scale=0.0, v_scale=0.0,
+                  dev_status=None):
+    """sv_kv4_read_args: row j of sequence i of k_out and v_out [R, Hkv, D] (bfloat16, float32 or
+    uint8 E4M3 codes of k / k_scale and v / v_scale; either may be None) is token kv_len[i] + j."""
+    a, c = Kv4ReadArgs(), _Args()
+    outs = [t for t in (k_out, v_out) if t is not None]
+    if not outs:
+        raise ValueError("k_out and v_out are both None")
+    shape = (outs[0].shape[0], cache.num_kv_heads, cache.head_dim)
+    a.k_out = c.add(k_out, "k_out", outs[0].dtype, shape=shape)
+    a.v_out = c.add(v_out, "v_out", outs[0].dtype, shape=shape)
+    a.dtype, a.num_rows = _dt(outs[0]), shape[0]
+    a.batch, a.max_q_rows = cu_q.shape[0] - 1, int(max_q_rows)
+    a.k_out_scale, a.v_out_scale = float(k_scale), float(v_scale)
+    a.cu_q = c.add(cu_q, "cu_q", torch.int32)
+    a.kv_len = c.add(kv_len, "kv_len", torch.int32, shape=(a.batch,))
+    _fill_cache(a.cache, c, cache, table, a.batch)
+    a.dev_status = c.add(dev_status, "dev_status", _WORDS, at_least=1)
+    return _finish(a, c)
+
+
+def spec_kv4_read(args, stream=None):
+    """Reads rows of the pages back as contiguous rows."""
+    _launch(lib.spec_kv4_read, args, stream)
+
+
+def kv4_attn_args(cache, table, cu_q, kv_len, q, out, *, max_q_rows, scale=0.0, dev_status=None):
+    """sv_kv4_attn_args for q [R, Hq, D] bfloat16 (rows may lie apart) -> out (contiguous): row j of
+    sequence i attends to tokens 0 .. kv_len[i] + j of its pages, which hold the block's own rows
+    already (spec_kv4_append).  scale 0: 1 / sqrt(D)."""
+    a, c = Kv4AttnArgs(), _Args()
+    if q.dim() != 3 or q.shape[2] != cache.head_dim:
+        raise ValueError(f"q: shape {tuple(q.shape)}, expected (rows, heads, {cache.head_dim})")
+    a.batch, a.num_q_heads, a.max_q_rows = cu_q.shape[0] - 1, q.shape[1], int(max_q_rows)
+    a.q = c.add(q, "q", torch.bfloat16, rows=True)
+    a.q_stride = _rows_stride(q, "q")
+    a.out = c.add(out, "out", torch.bfloat16, shape=q.shape)
+    a.dtype, a.num_rows, a.scale = SV_BF16, q.shape[0], float(scale)
+    a.cu_q = c.add(cu_q, "cu_q", torch.int32)
+    a.kv_len = c.add(kv_len, "kv_len", torch.int32, shape=(a.batch,))
+    _fill_cache(a.cache, c, cache, table, a.batch)
+    a.dev_status = c.add(dev_status, "dev_status", _WORDS, at_least=1)
+    return _finish(a, c)
+
+
+def kv4_workspace(args, stream=None):
+    """A zeroed Workspace for spec_kv4_attn with these argument shapes; calls that follow one another
+    on a stream may share one that is large enough for each."""
+    n = lib.sv_kv4_workspace_bytes(ctypes.byref(args))
+    if n == 0:
+        _check(1)
+    return Workspace(n, device=torch.device("cuda", args._device), stream=stream)
+
+
+def spec_kv4_attn(args, ws, stream=None):
+    """Attention of the block's rows over the pages."""
+    _launch(lib.spec_kv4_attn, args, stream, ws)

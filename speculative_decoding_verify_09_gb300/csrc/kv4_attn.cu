@@ -1,0 +1,707 @@
+// Attention of ragged block rows over a paged cache in 4 bits (sm_103a).
+// Contract: spec_kv4_attn in include/spec_kv4.h.
+//
+// softmax(scale q K^T) V with K and V as E2M1 codes times a scale per 16 elements.
+// A token takes 18 D / 16 bytes per KV head, read once for all of the block's rows
+// that share the head, so for few rows the kernel is bound by those bytes; what
+// stands against it is the work per byte: every code becomes an f16 operand (one
+// conversion and one product per two codes) that a matrix instruction of 8 rows
+// takes once.  E2M1 times E4M3 has six significant bits, so the operands are
+// exact and only q, the weights and the sums are rounded.
+//
+// Split: the tiles of 32 tokens of all (sequence, KV head, part of the rows) are
+// one list, cut into equal runs, one per CTA, one CTA per SM.  A CTA's tiles go to
+// its warps in turn; each warp streams its own through a ring of bulk copies (a
+// slab of 16 tokens is 18 D contiguous bytes, K and V and their scales), so no
+// warp waits for another until a segment -- the tiles of one (sequence, head,
+// part) in the run -- ends, and copies run ahead across segments.  Then the warps'
+// sums are joined in shared memory; a segment cut by a run's end goes to the
+// workspace, and the last of its pieces to arrive joins them, in order.
+//
+// Operands: S^T = K q^T and O^T = V^T P^T, tokens (then elements) on M, rows on N,
+// so a block of 1 row costs 8 columns, not 16 or more rows.  The order of a head's
+// elements in a product is free: a lane takes 16 bytes in a row of a token's K (32
+// elements) and the same elements of q; of V, 8 bytes in a row of four tokens'
+// elements.  The weights' running maximum is kept within 2^8 of the true one, so
+// the sums are rescaled seldom.
+#include <algorithm>
+#include <cmath>
+
+#include "kv4.inl"
+#include "ops_host.inl"
+
+namespace sv {
+
+namespace {
+
+constexpr int kTile = 32;                            // tokens
+constexpr int kMaxBatch = 2048;
+constexpr int kMaxCtas = 192;                        // (sizes the workspace on any host)
+constexpr int kCounters = 65536;                     // first in the workspace, whatever the shape
+constexpr float kLate = 8.0f;                        // log2 the maximum may grow before sums are rescaled
+
+// Warps and stages of a warp's ring; NB: 8-row columns of a part.
+template <int D, int NB>
+struct Shape {
+  static constexpr int kWarps = NB == 1 ? 16 : NB == 2 ? 12 : 8;
+  static constexpr int kThreads = 32 * kWarps;
+  static constexpr int kStages = (NB == 3 ? 3 : 2) * (128 / D);
+  static constexpr int kRows = 8 * NB;
+  static constexpr int kStride = D + 4;              // floats between a slot's rows
+  static constexpr int kTileBytes = 2 * slab_bytes(D);
+  static constexpr size_t kRing = static_cast<size_t>(kWarps) * kStages * kTileBytes;
+  static constexpr size_t kSlots = static_cast<size_t>(kWarps) * kRows * kStride * 4;
+  static constexpr size_t kSums = static_cast<size_t>(kWarps) * kRows * 8;
+  static constexpr size_t kFixed = kRing + kSlots + kSums;
+};
+
+struct Kv4AttnParams {
+  Kv4View cache;
+  int batch, Hq, g, max_q_rows, parts;               // parts: of max_q_rows * g rows
+  int min_tiles;                                     // of a run
+  int64_t num_rows, q_stride;
+  float scale_log2;                                  // of a score, k_scale and log2 e in it
+  const int32_t *cu_q, *kv_len;
+  const uint16_t *q;
+  uint16_t *out;
+  uint32_t *dev_status;
+  uint32_t *counters;                                // [batch, heads, parts]
+  float *part_o;                                     // [2 CTAs, rows, D]
+  float2 *part_ml;                                   // [2 CTAs, rows] maximum, sum
+  uint32_t spin_limit;
+};
+
+__device__ __forceinline__ void bar_init(uint32_t bar) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;\n" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void bar_expect(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n" ::"r"(bar), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void bulk_copy(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n"
+               ::"r"(dst), "l"(src), "r"(bytes), "r"(bar) : "memory");
+}
+// Whether a phase is over (at once), or is within the time that a wait may sleep.
+__device__ __forceinline__ bool bar_test(uint32_t bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile("{.reg .pred p;\n"
+               "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+               "selp.u32 %0, 1, 0, p;}\n"
+               : "=r"(done) : "r"(bar), "r"(parity) : "memory");
+  return done != 0;
+}
+__device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile("{.reg .pred p;\n"
+               "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+               "selp.u32 %0, 1, 0, p;}\n"
+               : "=r"(done) : "r"(bar), "r"(parity) : "memory");
+  return done != 0;
+}
+// Waits for a phase; false after `limit` polls, of which the first does not sleep.
+__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, uint32_t limit) {
+  bool done = bar_test(bar, parity);
+  for (uint32_t n = 1; !done && n < limit; ++n) done = bar_try(bar, parity);
+  return done;
+}
+
+// Rows and tokens of sequence i; nothing to do: R = 0.
+struct Sequence {
+  int r0, R, L, keys;
+};
+__device__ __forceinline__ Sequence sequence_of(const Kv4AttnParams &P, int i, uint32_t *why) {
+  const int r0 = P.cu_q[i], r1 = P.cu_q[i + 1], L = P.kv_len[i];
+  Sequence s{0, 0, 0, 0};
+  if (r0 < 0 || r1 < r0 || r1 > P.num_rows || r1 - r0 > P.max_q_rows || L < 0) {
+    *why = SV_DEV_BAD_LENGTH;
+  } else if (r1 > r0) {
+    if (static_cast<int64_t>(L) + (r1 - r0) > static_cast<int64_t>(P.cache.max_pages) * P.cache.page_size)
+      *why = SV_DEV_CAPACITY;
+    else
+      s = Sequence{r0, r1 - r0, L, L + (r1 - r0)};
+  }
+  return s;
+}
+
+// Tokens of a slab in the order of the products' rows: neighbours of a pair of lanes
+// in different halves of 128 bytes.
+__device__ __forceinline__ int token_of(int x) { return x ^ ((x >> 1) & 1); }
+
+template <int D, int NB>
+__global__ void __launch_bounds__(Shape<D, NB>::kThreads, 1) kv4_attn_kernel(const Kv4AttnParams P) {
+  using Sh = Shape<D, NB>;
+  constexpr int W = Sh::kWarps, S = Sh::kStages, NT = Sh::kThreads, ROWS = Sh::kRows;
+  constexpr int SLAB = slab_bytes(D), STEPS = D / 16, WORDS = D / 32, MT = D / 16;
+  extern __shared__ __align__(128) uint8_t smem[];
+  float *s_slots = reinterpret_cast<float *>(smem + Sh::kRing);
+  float2 *s_ml = reinterpret_cast<float2 *>(smem + Sh::kRing + Sh::kSlots);
+  int32_t *s_start = reinterpret_cast<int32_t *>(smem + Sh::kFixed);         // [batch + 1]
+  uint8_t *s_parts = reinterpret_cast<uint8_t *>(s_start + P.batch + 1);     // [batch]
+  __shared__ __align__(8) uint64_t s_bar[W * S];
+  __shared__ uint8_t s_bad[W * S];
+  __shared__ int32_t s_scan[W];
+  __shared__ int s_last;
+  const int tid = threadIdx.x, w = tid >> 5, l = tid & 31, r = l >> 2, c = l & 3;
+
+  if (tid < W * S) bar_init(smem_u32(&s_bar[tid]));
+  asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
+  wait_for_previous();
+
+  // tiles before each sequence's first
+  const int heads = P.cache.heads;
+  {
+    const int each = (P.batch + NT - 1) / NT, i0 = min(P.batch, tid * each), i1 = min(P.batch, i0 + each);
+    int mine = 0;
+    for (int i = i0; i < i1; ++i) {
+      uint32_t why = 0;
+      const Sequence s = sequence_of(P, i, &why);
+      if (why && blockIdx.x == 0) set_status(P.dev_status, why);
+      const int parts = (s.R * P.g + ROWS - 1) / ROWS;
+      s_parts[i] = static_cast<uint8_t>(parts);
+      const int n = (s.keys + kTile - 1) / kTile * parts * heads;
+      s_start[i] = n;
+      mine += n;
+    }
+    int inc = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, inc, o);
+      if (l >= o) inc += x;
+    }
+    if (l == 31) s_scan[w] = inc;
+    __syncthreads();
+    int before = inc - mine, total = 0;
+    for (int i = 0; i < W; ++i) {
+      if (i < w) before += s_scan[i];
+      total += s_scan[i];
+    }
+    for (int i = i0; i < i1; ++i) {
+      const int n = s_start[i];
+      s_start[i] = before;
+      before += n;
+    }
+    if (tid == 0) s_start[P.batch] = total;
+    __syncthreads();
+  }
+  const int total = s_start[P.batch];
+  const int ctas = max(1, min(static_cast<int>(gridDim.x), total / P.min_tiles));
+  const int b = blockIdx.x;
+  if (b >= ctas || total == 0) return;
+  auto run_start = [&](int x) { return static_cast<int>(static_cast<int64_t>(total) * x / ctas); };
+  auto cta_of = [&](int t) { return static_cast<int>(((static_cast<int64_t>(t) + 1) * ctas - 1) / total); };
+  const int t0 = run_start(b), t1 = run_start(b + 1);
+
+  // sequence, unit (head * parts + part) and tile in it of list entry t
+  struct Place { int i, unit, tile, tiles; };
+  auto locate = [&](int t) {
+    int lo = 0, hi = P.batch;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (s_start[mid] <= t) lo = mid; else hi = mid;
+    }
+    Place p;
+    p.i = lo;
+    p.tiles = (s_start[lo + 1] - s_start[lo]) / (heads * s_parts[lo]);
+    const int rem = t - s_start[lo];
+    p.unit = rem / p.tiles;
+    p.tile = rem - p.unit * p.tiles;
+    return p;
+  };
+
+  // ---- this warp's copies: a lane finds the slabs of each of the next 32 tiles
+  const uint8_t *from0 = nullptr, *from1 = nullptr;  // slabs of this lane's tile (nullptr: not copied)
+  bool from_bad = false;
+  auto look_up = [&](int k) {
+    const int t = t0 + w + W * (k + l);
+    from0 = from1 = nullptr;
+    from_bad = false;
+    if (t >= t1) return;
+    const Place p = locate(t);
+    uint32_t why = 0;
+    const Sequence s = sequence_of(P, p.i, &why);
+    const int64_t at = static_cast<int64_t>(p.unit / s_parts[p.i]) * head_bytes(P.cache);
+    const uint8_t *x = find_slab(P.cache, p.i, static_cast<int64_t>(p.tile) * kTile, &why);
+    if (x != nullptr) from0 = x + at;
+    if (p.tile * kTile + kSlab < s.keys) {
+      const uint8_t *y = find_slab(P.cache, p.i, static_cast<int64_t>(p.tile) * kTile + kSlab, &why);
+      if (y != nullptr) from1 = y + at;
+    }
+    if (why) {
+      set_status(P.dev_status, why);
+      from0 = from1 = nullptr;
+      from_bad = true;
+    }
+  };
+  uint8_t *ring = smem + static_cast<size_t>(w) * S * Sh::kTileBytes;
+  auto issue = [&](int k) {
+    if ((k & 31) == 0) look_up(k);
+    if (t0 + w + W * k >= t1 || l != (k & 31)) return;
+    const int st = k % S;
+    const uint32_t bar = smem_u32(&s_bar[w * S + st]), to = smem_u32(ring + st * Sh::kTileBytes);
+    s_bad[w * S + st] = from_bad;
+    bar_expect(bar, (from0 != nullptr ? SLAB : 0) + (from1 != nullptr ? SLAB : 0));
+    if (from0 != nullptr && from1 == from0 + SLAB) {
+      bulk_copy(to, from0, 2 * SLAB, bar);
+    } else {
+      if (from0 != nullptr) bulk_copy(to, from0, SLAB, bar);
+      if (from1 != nullptr) bulk_copy(to + SLAB, from1, SLAB, bar);
+    }
+  };
+  int k = 0;                                         // tiles this warp has taken
+  bool dead = false;                                 // a wait ran out, at tile dead_at
+  int dead_at = 0;
+  for (int x = 0; x < S; ++x) issue(x);
+
+  for (int t = t0; t < t1;) {
+    // ---- a segment: the run's tiles of one (sequence, head, part)
+    const Place p = locate(t);
+    const int seg_end = min(t1, t - p.tile + p.tiles), parts = s_parts[p.i];
+    const int h = p.unit / parts, part = p.unit - h * parts;
+    uint32_t why = 0;
+    const Sequence s = sequence_of(P, p.i, &why);
+    const int first_row = part * ROWS;               // of the block's R * g rows
+
+    uint32_t qf[NB][STEPS][2];
+    int lim[NB][2];                                  // the last token that this lane's columns see
+    float m[NB][2], mu[NB][2], sum[NB][2], o[MT][NB][4];
+    const int mine = (t - t0) % W;                   // the warp that takes tile t
+    int tile = t + (w - mine + W) % W;               // this warp's first in the segment
+    if (tile < seg_end) {
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) {
+        const int n = first_row + 8 * nb + r, j = n / P.g, hh = n - j * P.g;
+        uint4 v[WORDS];
+#pragma unroll
+        for (int x = 0; x < WORDS; ++x) v[x] = make_uint4(0, 0, 0, 0);
+        if (j < s.R) {
+          const uint4 *src = reinterpret_cast<const uint4 *>(
+              P.q + (s.r0 + j) * P.q_stride + static_cast<int64_t>(h * P.g + hh) * D + c * (D / 4));
+#pragma unroll
+          for (int x = 0; x < WORDS; ++x) v[x] = src[x];
+        }
+#pragma unroll
+        for (int x = 0; x < WORDS; ++x) {
+          qf[nb][2 * x][0] = bf16x2_to_f16x2(v[x].x);
+          qf[nb][2 * x][1] = bf16x2_to_f16x2(v[x].y);
+          qf[nb][2 * x + 1][0] = bf16x2_to_f16x2(v[x].z);
+          qf[nb][2 * x + 1][1] = bf16x2_to_f16x2(v[x].w);
+        }
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          lim[nb][x] = min(s.L + (first_row + 8 * nb + 2 * c + x) / P.g, s.keys - 1);
+          m[nb][x] = -INFINITY;
+          mu[nb][x] = sum[nb][x] = 0.0f;
+        }
+#pragma unroll
+        for (int x = 0; x < MT; ++x) o[x][nb][0] = o[x][nb][1] = o[x][nb][2] = o[x][nb][3] = 0.0f;
+      }
+    }
+    int nan_from = 0x7fffffff;                       // block token whose V has NaN in this lane's elements
+    for (; tile < seg_end; tile += W, ++k) {
+      const int st = k % S;
+      if (!dead &&
+          !__all_sync(0xffffffffu, bar_wait(smem_u32(&s_bar[w * S + st]), (k / S) & 1, P.spin_limit))) {
+        dead = true;
+        dead_at = k;
+        if (l == 0) set_status(P.dev_status, SV_DEV_TIMEOUT);
+      }
+      if (dead || s_bad[w * S + st]) {
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) sum[nb][0] = sum[nb][1] = NAN;
+        __syncwarp();
+        if (!dead) issue(k + S);
+        continue;
+      }
+      const uint8_t *stage = ring + st * Sh::kTileBytes;
+      const int key0 = (tile - t + p.tile) * kTile;
+      const bool edge = key0 + kTile - 1 > s.L;      // tokens that some row does not see
+
+      // ---- S^T = K q^T
+      float sc[2][NB][4];
+#pragma unroll
+      for (int sl = 0; sl < 2; ++sl) {
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) sc[sl][nb][0] = sc[sl][nb][1] = sc[sl][nb][2] = sc[sl][nb][3] = 0.0f;
+        const uint8_t *slab = stage + sl * SLAB;
+        const int ka = token_of(r), kb = ka + 8;
+        uint32_t wa[WORDS], wb[WORDS], fa[2], fb[2]; // codes of two tokens; scales, twice each
+        if constexpr (D == 128) {
+          const uint4 x = *reinterpret_cast<const uint4 *>(slab + ka * 64 + c * 16);
+          const uint4 y = *reinterpret_cast<const uint4 *>(slab + kb * 64 + c * 16);
+          wa[0] = x.x, wa[1] = x.y, wa[2] = x.z, wa[3] = x.w;
+          wb[0] = y.x, wb[1] = y.y, wb[2] = y.z, wb[3] = y.w;
+          const uint32_t sa = e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t *>(slab + slab_k_scales(D) + ka * 8 + c * 2));
+          const uint32_t sb = e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t *>(slab + slab_k_scales(D) + kb * 8 + c * 2));
+          fa[0] = __byte_perm(sa, sa, 0x1010), fa[1] = __byte_perm(sa, sa, 0x3232);
+          fb[0] = __byte_perm(sb, sb, 0x1010), fb[1] = __byte_perm(sb, sb, 0x3232);
+        } else {
+          const uint2 x = *reinterpret_cast<const uint2 *>(slab + ka * 32 + c * 8);
+          const uint2 y = *reinterpret_cast<const uint2 *>(slab + kb * 32 + c * 8);
+          wa[0] = x.x, wa[1] = x.y;
+          wb[0] = y.x, wb[1] = y.y;
+          const uint32_t sa = slab[slab_k_scales(D) + ka * 4 + c], sb = slab[slab_k_scales(D) + kb * 4 + c];
+          fa[0] = fa[1] = e4m3x2_to_f16x2(sa | sa << 8);
+          fb[0] = fb[1] = e4m3x2_to_f16x2(sb | sb << 8);
+        }
+#pragma unroll
+        for (int x = 0; x < WORDS; ++x) {
+          uint32_t ha[4], hb[4];
+          e2m1x8_to_f16x2(wa[x], ha);
+          e2m1x8_to_f16x2(wb[x], hb);
+          const uint32_t pa = fa[2 * x / WORDS], pb = fb[2 * x / WORDS];
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            const uint32_t a[4] = {mul_f16x2(ha[2 * y], pa), mul_f16x2(hb[2 * y], pb),
+                                   mul_f16x2(ha[2 * y + 1], pa), mul_f16x2(hb[2 * y + 1], pb)};
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb)
+              mma_f16_16816(sc[sl][nb], a, qf[nb][2 * x + y][0], qf[nb][2 * x + y][1]);
+          }
+        }
+      }
+
+      // ---- weights
+      if (edge) {
+#pragma unroll
+        for (int sl = 0; sl < 2; ++sl) {
+          const int key = key0 + sl * kSlab + token_of(r);
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+              if (key + (x >> 1) * 8 > lim[nb][x & 1]) sc[sl][nb][x] = -INFINITY;
+        }
+      }
+      bool grows = false;
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+          grows |= fmaxf(fmaxf(sc[0][nb][x], sc[0][nb][2 + x]), fmaxf(sc[1][nb][x], sc[1][nb][2 + x])) *
+                       P.scale_log2 > m[nb][x] + kLate;
+      if (__any_sync(0xffffffffu, grows)) {
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            float top = fmaxf(fmaxf(sc[0][nb][x], sc[0][nb][2 + x]), fmaxf(sc[1][nb][x], sc[1][nb][2 + x]));
+#pragma unroll
+            for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+            const float now = fmaxf(m[nb][x], top * P.scale_log2);
+            const float f = now == -INFINITY ? 1.0f : fast_exp2(m[nb][x] - now);
+            m[nb][x] = now;
+            mu[nb][x] = now == -INFINITY ? 0.0f : now;
+            sum[nb][x] *= f;
+#pragma unroll
+            for (int y = 0; y < MT; ++y) {
+              o[y][nb][x] *= f;
+              o[y][nb][2 + x] *= f;
+            }
+          }
+      }
+      uint32_t pf[2][NB][2];
+#pragma unroll
+      for (int sl = 0; sl < 2; ++sl)
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+          float e[4];
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            e[x] = fast_exp2(fmaf(sc[sl][nb][x], P.scale_log2, -mu[nb][x & 1]));
+            sum[nb][x & 1] += e[x];
+          }
+          pf[sl][nb][0] = movmatrix_trans(pack_f16x2(e[0], e[1]));
+          pf[sl][nb][1] = movmatrix_trans(pack_f16x2(e[2], e[3]));
+        }
+
+      // ---- O^T += V^T P^T
+#pragma unroll
+      for (int sl = 0; sl < 2; ++sl) {
+        const uint8_t *slab = stage + sl * SLAB + slab_v(D);
+        uint32_t v[4][D / 64], s4[4];                // four tokens' codes and scales
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const int tok = token_of(2 * c + (x & 1)) + (x >> 1) * 8;
+          if constexpr (D == 128) {
+            const uint2 y = *reinterpret_cast<const uint2 *>(slab + tok * 64 + r * 8);
+            v[x][0] = y.x, v[x][1] = y.y;
+            s4[x] = slab[8 * D + tok * 8 + r];
+          } else {
+            v[x][0] = *reinterpret_cast<const uint32_t *>(slab + tok * 32 + r * 4);
+            s4[x] = slab[8 * D + tok * 4 + (r >> 1)];
+          }
+          if (edge) {
+            // tokens behind the last hold anything; a block token's NaN is kept from the rows
+            // before it (a weight of 0 would not do that) and given to the others at the end
+            const int key = key0 + sl * kSlab + tok;
+            const bool nan = key > s.L && (s4[x] & 0x7Fu) == 0x7Fu;
+            if (nan && key < s.keys) nan_from = min(nan_from, key);
+            if (nan || key >= s.keys) s4[x] = 0;
+          }
+        }
+        const uint32_t f01 = e4m3x2_to_f16x2(s4[0] | s4[1] << 8), f23 = e4m3x2_to_f16x2(s4[2] | s4[3] << 8);
+#pragma unroll
+        for (int x = 0; x < D / 64; ++x) {
+          constexpr uint32_t kLow = 0x0F0F0F0Fu;
+          uint32_t a0[4], a1[4], a2[4], a3[4];       // even elements of two tokens, odd ones
+          e2m1x8_to_f16x2((v[0][x] & kLow) | (v[1][x] << 4 & ~kLow), a0);
+          e2m1x8_to_f16x2((v[0][x] >> 4 & kLow) | (v[1][x] & ~kLow), a1);
+          e2m1x8_to_f16x2((v[2][x] & kLow) | (v[3][x] << 4 & ~kLow), a2);
+          e2m1x8_to_f16x2((v[2][x] >> 4 & kLow) | (v[3][x] & ~kLow), a3);
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            const uint32_t a[4] = {mul_f16x2(a0[y], f01), mul_f16x2(a1[y], f01), mul_f16x2(a2[y], f23),
+                                   mul_f16x2(a3[y], f23)};
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) mma_f16_16816(o[4 * x + y][nb], a, pf[sl][nb][0], pf[sl][nb][1]);
+          }
+        }
+      }
+      __syncwarp();
+      issue(k + S);
+    }
+
+    // ---- the warps' sums joined
+    const int count = min(W, seg_end - t);
+    __syncthreads();                                 // (the slots of the segment before are read)
+    if ((w - mine + W) % W < count) {
+      if (__any_sync(0xffffffffu, nan_from != 0x7fffffff)) {
+        nan_from = min(nan_from, __shfl_xor_sync(0xffffffffu, nan_from, 1));
+        nan_from = min(nan_from, __shfl_xor_sync(0xffffffffu, nan_from, 2));
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+          for (int y = 0; y < MT; ++y)
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+              if (lim[nb][x & 1] >= nan_from) o[y][nb][x] = NAN;
+      }
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          float a = sum[nb][x];
+#pragma unroll
+          for (int d = 4; d < 32; d <<= 1) a += __shfl_xor_sync(0xffffffffu, a, d);
+          const int n = 8 * nb + 2 * c + x;
+          if (r == 0) s_ml[w * ROWS + n] = make_float2(m[nb][x], a);
+          float4 *to = reinterpret_cast<float4 *>(s_slots + (w * ROWS + n) * Sh::kStride + r * (D / 8));
+#pragma unroll
+          for (int y = 0; y < MT; y += 2)
+            to[y / 2] = make_float4(o[y][nb][x], o[y][nb][2 + x], o[y + 1][nb][x], o[y + 1][nb][2 + x]);
+        }
+    }
+    __syncthreads();
+    const int seg0 = t - p.tile, seg1 = seg0 + p.tiles;              // the whole segment's tiles
+    const bool whole = t == seg0 && seg_end == seg1;
+    const int slot = 2 * b + (t == t0 ? 0 : 1);
+    auto store_row = [&](int n, int d, float x, float y, float total_sum) {
+      const int j = (first_row + n) / P.g, hh = first_row + n - j * P.g;
+      if (j >= s.R) return;
+      const float f = P.cache.v_scale / total_sum;
+      *reinterpret_cast<uint32_t *>(P.out + (static_cast<int64_t>(s.r0 + j) * P.Hq + h * P.g + hh) * D + d) =
+          pack_bf16x2(x * f, y * f);
+    };
+    for (int e = tid; e < ROWS * (D / 2); e += NT) {
+      const int n = e / (D / 2), d = e % (D / 2) * 2;
+      float top = -INFINITY;
+      for (int x = 0; x < count; ++x) top = fmaxf(top, s_ml[(mine + x) % W * ROWS + n].x);
+      const float base = top == -INFINITY ? 0.0f : top;
+      float a = 0.0f, x0 = 0.0f, x1 = 0.0f;
+      for (int x = 0; x < count; ++x) {
+        const int at = (mine + x) % W * ROWS + n;
+        const float2 ml = s_ml[at], v = *reinterpret_cast<const float2 *>(s_slots + at * Sh::kStride + d);
+        const float f = fast_exp2(ml.x - base);
+        a = fmaf(f, ml.y, a);
+        x0 = fmaf(f, v.x, x0);
+        x1 = fmaf(f, v.y, x1);
+      }
+      if (whole) {
+        store_row(n, d, x0, x1, a);
+      } else {
+        *reinterpret_cast<float2 *>(P.part_o + (static_cast<int64_t>(slot) * ROWS + n) * D + d) = make_float2(x0, x1);
+        if (d == 0) P.part_ml[slot * ROWS + n] = make_float2(top, a);
+      }
+    }
+    if (!whole) {
+      const int c0 = cta_of(seg0), c1 = cta_of(seg1 - 1);
+      __threadfence();
+      __syncthreads();
+      if (tid == 0) {
+        uint32_t *counter = P.counters + (p.i * heads + h) * P.parts + part;
+        s_last = atomicInc(counter, c1 - c0) == static_cast<uint32_t>(c1 - c0);
+      }
+      __syncthreads();
+      if (s_last) {
+        __threadfence();
+        for (int e = tid; e < ROWS * (D / 2); e += NT) {
+          const int n = e / (D / 2), d = e % (D / 2) * 2;
+          auto place_of = [&](int x) { return static_cast<int64_t>(2 * x + (run_start(x) >= seg0 ? 0 : 1)) * ROWS + n; };
+          float top = -INFINITY;
+          for (int x = c0; x <= c1; ++x) top = fmaxf(top, __ldcg(&P.part_ml[place_of(x)]).x);
+          const float base = top == -INFINITY ? 0.0f : top;
+          float a = 0.0f, x0 = 0.0f, x1 = 0.0f;
+          for (int x = c0; x <= c1; ++x) {
+            const int64_t at = place_of(x);
+            const float2 ml = __ldcg(&P.part_ml[at]);
+            const float2 v = __ldcg(reinterpret_cast<const float2 *>(P.part_o + at * D + d));
+            const float f = fast_exp2(ml.x - base);
+            a = fmaf(f, ml.y, a);
+            x0 = fmaf(f, v.x, x0);
+            x1 = fmaf(f, v.y, x1);
+          }
+          store_row(n, d, x0, x1, a);
+        }
+      }
+    }
+    t = seg_end;
+  }
+  if (dead)                                          // its copies in flight write this CTA's memory
+    for (int x = dead_at; x < dead_at + S; ++x)
+      if (t0 + w + W * x < t1) bar_wait(smem_u32(&s_bar[w * S + x % S]), (x / S) & 1, 1u << 22);
+}
+
+size_t align256(size_t x) { return (x + 255) / 256 * 256; }
+
+// Columns of 8 rows that a part has (1 to 4), and parts of the largest block.
+struct Plan {
+  int nb, parts;
+  size_t part_o, part_ml, bytes;                     // offsets in the workspace, and its size
+};
+Plan plan_of(const sv_kv4_attn_args &a) {
+  Plan p;
+  const int rows = a.max_q_rows * (a.num_q_heads / a.cache.num_kv_heads), blocks = (rows + 7) / 8;
+  p.parts = (blocks + 3) / 4;
+  p.nb = (blocks + p.parts - 1) / p.parts;
+  p.parts = (blocks + p.nb - 1) / p.nb;
+  p.part_o = kCounters * sizeof(uint32_t);
+  p.part_ml = p.part_o + align256(size_t{2} * kMaxCtas * 8 * p.nb * a.cache.head_dim * sizeof(float));
+  p.bytes = p.part_ml + align256(size_t{2} * kMaxCtas * 8 * p.nb * sizeof(float2));
+  return p;
+}
+
+template <int D, int NB>
+cudaError_t launch_shape(const Kv4AttnParams &P, int ctas, cudaStream_t s) {
+  using Sh = Shape<D, NB>;
+  const size_t smem = Sh::kFixed + (static_cast<size_t>(P.batch) + 1) * 4 + P.batch;
+  return launch_after_previous(kv4_attn_kernel<D, NB>, dim3(ctas), Sh::kThreads, smem, s, P);
+}
+template <int D>
+cudaError_t launch_rows(int nb, const Kv4AttnParams &P, int ctas, cudaStream_t s) {
+  return nb == 1   ? launch_shape<D, 1>(P, ctas, s)
+         : nb == 2 ? launch_shape<D, 2>(P, ctas, s)
+         : nb == 3 ? launch_shape<D, 3>(P, ctas, s)
+                   : launch_shape<D, 4>(P, ctas, s);
+}
+
+sv_status check_attn4(const sv_kv4_attn_args *a, bool tensors) {
+  const char *who = "kv4_attn";
+  if (!a) return record_error(SV_ERR_INVALID, "%s: null arguments", who);
+  sv_kv4_cache cache = a->cache;
+  alignas(16) static unsigned char none[16];
+  static const int32_t no_table[1] = {0};
+  if (!tensors) cache.pages = none, cache.table = no_table;
+  const sv_status st = check_cache(&cache, who);
+  if (st != SV_OK) return st;
+  if (a->batch < 0 || a->batch > kMaxBatch)
+    return record_error(SV_ERR_UNSUPPORTED, "%s: batch %d outside [0, %d]", who, a->batch, kMaxBatch);
+  const int Hkv = cache.num_kv_heads;
+  if (a->num_q_heads < Hkv || a->num_q_heads % Hkv || a->num_q_heads / Hkv > 256)
+    return record_error(SV_ERR_INVALID, "%s: heads Hq=%d Hkv=%d (need Hq %% Hkv == 0, Hq / Hkv <= 256)",
+                        who, a->num_q_heads, Hkv);
+  if (a->dtype != SV_BF16) return record_error(SV_ERR_UNSUPPORTED, "%s: dtype %d (built: bf16)", who, a->dtype);
+  if (a->reserved != 0) return record_error(SV_ERR_INVALID, "%s: reserved must be 0", who);
+  if (a->max_q_rows < 1 || a->max_q_rows > 1024)
+    return record_error(SV_ERR_INVALID, "%s: max_q_rows %d outside [1, 1024]", who, a->max_q_rows);
+  if (a->num_rows < 0 || a->num_rows >= (int64_t{1} << 31))
+    return record_error(SV_ERR_INVALID, "%s: num_rows %lld", who, static_cast<long long>(a->num_rows));
+  if (!std::isfinite(a->scale) || a->scale < 0.0f)
+    return record_error(SV_ERR_INVALID, "%s: scale must be finite and >= 0", who);
+  const Plan p = plan_of(*a);
+  const int64_t units = static_cast<int64_t>(a->batch) * Hkv * p.parts;
+  if (p.parts > 255 || units > kCounters)
+    return record_error(SV_ERR_UNSUPPORTED, "%s: %d sequences x %d KV heads x %d parts of rows", who,
+                        a->batch, Hkv, p.parts);
+  const int64_t tokens = static_cast<int64_t>(cache.max_pages) * cache.page_size;
+  if (tokens >= (int64_t{1} << 31) || units * ((tokens + kTile - 1) / kTile) >= (int64_t{1} << 31))
+    return record_error(SV_ERR_UNSUPPORTED, "%s: tables of %d pages of %d tokens", who, cache.max_pages,
+                        cache.page_size);
+  const int64_t width = static_cast<int64_t>(a->num_q_heads) * cache.head_dim;
+  if (a->q_stride != 0 && (a->q_stride < width || a->q_stride % 8 || a->q_stride > (int64_t{1} << 40)))
+    return record_error(SV_ERR_INVALID, "%s: q row stride %lld (a multiple of 8, at least %lld)", who,
+                        static_cast<long long>(a->q_stride), static_cast<long long>(width));
+  if (!tensors || a->batch == 0 || a->num_rows == 0) return SV_OK;
+  if (!a->cu_q || !a->kv_len) return record_error(SV_ERR_INVALID, "%s: null cu_q or kv_len", who);
+  if (!a->q || !a->out || !is_aligned16(a->q) || !is_aligned16(a->out))
+    return record_error(SV_ERR_INVALID, "%s: q or out null or not 16-byte aligned", who);
+  if (a->q == a->out) return record_error(SV_ERR_INVALID, "%s: out is q", who);
+  return SV_OK;
+}
+
+}  // namespace
+
+}  // namespace sv
+
+extern "C" {
+
+SV_API size_t sv_kv4_workspace_bytes(const sv_kv4_attn_args *a) {
+  using namespace sv;
+  return check_attn4(a, false) == SV_OK ? plan_of(*a).bytes : 0;
+}
+
+SV_API sv_status spec_kv4_attn(const sv_kv4_attn_args *a, void *ws, size_t ws_bytes, void *stream) {
+  using namespace sv;
+  const char *who = "kv4_attn";
+  const sv_status st = check_attn4(a, true);
+  if (st != SV_OK) return st;
+  const Plan p = plan_of(*a);
+  if (!ws || reinterpret_cast<uintptr_t>(ws) % 256 || ws_bytes < p.bytes)
+    return record_error(SV_ERR_WORKSPACE, "%s: workspace null, not 256-byte aligned or below %zu bytes", who, p.bytes);
+  if (a->batch == 0 || a->num_rows == 0) return SV_OK;
+  const int sms = device_sms();
+  if (sms <= 0) return record_error(SV_ERR_CUDA, "%s: no current CUDA device", who);
+  Kv4AttnParams P{};
+  P.cache = view_of(a->cache);
+  P.batch = a->batch;
+  P.Hq = a->num_q_heads;
+  P.g = a->num_q_heads / a->cache.num_kv_heads;
+  P.max_q_rows = a->max_q_rows;
+  P.parts = p.parts;
+  P.min_tiles = 4;
+  P.num_rows = a->num_rows;
+  P.q_stride = a->q_stride ? a->q_stride : static_cast<int64_t>(P.Hq) * a->cache.head_dim;
+  const double scale = a->scale != 0.0f ? a->scale : 1.0 / std::sqrt(static_cast<double>(a->cache.head_dim));
+  P.scale_log2 = static_cast<float>(scale * P.cache.k_scale * 1.4426950408889634);
+  P.cu_q = a->cu_q;
+  P.kv_len = a->kv_len;
+  P.q = static_cast<const uint16_t *>(a->q);
+  P.out = static_cast<uint16_t *>(a->out);
+  P.dev_status = a->dev_status;
+  P.counters = static_cast<uint32_t *>(ws);
+  P.part_o = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + p.part_o);
+  P.part_ml = reinterpret_cast<float2 *>(static_cast<uint8_t *>(ws) + p.part_ml);
+  const uint32_t limit = attention_wait_limit();
+  P.spin_limit = limit ? limit : 1u << 22;
+  const int ctas = std::min(sms, kMaxCtas);
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = a->cache.head_dim == 128 ? launch_rows<128>(p.nb, P, ctas, s)
+                                                  : launch_rows<64>(p.nb, P, ctas, s);
+  if (e != cudaSuccess) return record_error(SV_ERR_CUDA, "%s launch: %s", who, cudaGetErrorString(e));
+  return SV_OK;
+}
+
+SV_API int32_t sv_kv4_version(void) { return SV_KV4_VERSION; }
+
+SV_API size_t sv_kv4_struct_size(int32_t which) {
+  switch (which) {
+    case 0: return sizeof(sv_kv4_cache);
+    case 1: return sizeof(sv_norm_args);
+    case 2: return sizeof(sv_norm_rope_args);
+    case 3: return sizeof(sv_kv4_append_args);
+    case 4: return sizeof(sv_kv4_read_args);
+    case 5: return sizeof(sv_kv4_attn_args);
+    default: return 0;
+  }
+}
+
+}  // extern "C"

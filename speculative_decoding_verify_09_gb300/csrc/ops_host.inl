@@ -5,12 +5,15 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
-#include "spec_verify.h"
+#include "spec_ops.h"
 
 namespace sv {
 
 // Records the message of a failed call and returns its status.
 sv_status record_error(sv_status st, const char *fmt, ...) __attribute__((format(printf, 2, 3)));
+
+// The checks of spec_rope_rows (rope.cu), in the name of entry point `who`.
+sv_status check_rope(const sv_rope_args *a, const char *who);
 
 // SMs of the current device (0 if it cannot be asked).
 int device_sms();
@@ -41,6 +44,22 @@ inline cudaError_t launch_behind(void (*kernel)(Params), dim3 grid, int threads,
   const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, params);
   if (e != cudaSuccess) cudaGetLastError();     // reported by the caller, not left for another call
   return e;
+}
+
+// The same for a kernel that takes more dynamic shared memory than the default allows.
+template <typename Params>
+inline cudaError_t launch_after_previous(void (*kernel)(Params), dim3 grid, int threads, size_t smem,
+                                         cudaStream_t s, const Params &params) {
+  if (smem > 48 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void *>(kernel),
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               static_cast<int>(smem));
+    if (e != cudaSuccess) {
+      cudaGetLastError();
+      return e;
+    }
+  }
+  return launch_behind(kernel, grid, threads, smem, s, params);
 }
 
 // Waits until the kernel before has completed and its writes are visible.

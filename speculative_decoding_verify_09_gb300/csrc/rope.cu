@@ -19,6 +19,7 @@
 
 #include "common.cuh"
 #include "ops_host.inl"
+#include "rows.inl"
 #include "spec_ops.h"
 
 namespace sv {
@@ -61,122 +62,6 @@ struct RopeParams {
   void *q_out, *k_out, *v_out;
   uint32_t *dev_status;
 };
-
-// N elements as they lie in memory.
-template <int BYTES> struct Raw;
-template <> struct Raw<32> { uint4 a, b; };
-template <> struct Raw<16> { uint4 a; };
-template <> struct Raw<8> { uint2 a; };
-template <> struct Raw<4> { uint32_t a; };
-template <> struct Raw<2> { uint16_t a; };
-
-template <typename T, int N>
-struct Vec {
-  union {
-    Raw<N * static_cast<int>(sizeof(T))> raw;
-    T e[N];
-  };
-  __device__ __forceinline__ void load(const T *p) { raw = *reinterpret_cast<const decltype(raw) *>(p); }
-  __device__ __forceinline__ void store(T *p) const { *reinterpret_cast<decltype(raw) *>(p) = raw; }
-  __device__ __forceinline__ void get(float (&x)[N]) const {
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      if constexpr (sizeof(T) == 2) x[i] = bf16_bits_to_f32(e[i]);
-      else x[i] = e[i];
-    }
-  }
-  __device__ __forceinline__ void set(const float (&x)[N]) {
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      if constexpr (sizeof(T) == 4) {
-        e[i] = x[i];
-      } else if (N % 2) {
-        e[i] = f32_to_bf16_rn(x[i]);
-      } else if (i % 2 == 0) {
-        const uint32_t two = pack_bf16x2(x[i], x[i + 1]);
-        e[i] = static_cast<uint16_t>(two);
-        e[i + 1] = static_cast<uint16_t>(two >> 16);
-      }
-    }
-  }
-  // The pair of elements i (even) and i + 1 turned in place, or left as it is.
-  __device__ __forceinline__ void turn_pair(int i, float cs, float sn, bool on) {
-    if constexpr (sizeof(T) == 2) {
-      const float a = bf16_bits_to_f32(e[i]), b = bf16_bits_to_f32(e[i + 1]);
-      const uint32_t two = pack_bf16x2(a * cs - b * sn, b * cs + a * sn);
-      e[i] = on ? static_cast<uint16_t>(two) : e[i];
-      e[i + 1] = on ? static_cast<uint16_t>(two >> 16) : e[i + 1];
-    } else {
-      const float a = e[i], b = e[i + 1];
-      e[i] = on ? a * cs - b * sn : a;
-      e[i + 1] = on ? b * cs + a * sn : b;
-    }
-  }
-};
-
-// Two floats -> two E4M3 codes (lo in the lower byte), nearest even, saturating.
-__device__ __forceinline__ uint32_t e4m3x2_of(float lo, float hi) {
-  uint16_t r;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;\n" : "=h"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-
-// Codes of x / scale; inverse: 1 / scale where that is exact (scale a power of two), else 0.
-template <int N>
-__device__ __forceinline__ void store_codes(uint8_t *p, const float (&x)[N], float scale, float inverse) {
-  float y[N];
-#pragma unroll
-  for (int i = 0; i < N; ++i) y[i] = inverse != 0.0f ? x[i] * inverse : x[i] / scale;
-  if constexpr (N == 1) {
-    *p = static_cast<uint8_t>(e4m3x2_of(y[0], 0.0f));
-  } else {
-    Vec<uint16_t, N / 2> v;
-#pragma unroll
-    for (int i = 0; i < N / 2; ++i) v.e[i] = static_cast<uint16_t>(e4m3x2_of(y[2 * i], y[2 * i + 1]));
-    v.store(reinterpret_cast<uint16_t *>(p));
-  }
-}
-
-// Whether sequence i's rows agree with the host's bounds.
-__device__ __forceinline__ bool good_sequence(const RopeParams &P, int i) {
-  const int r0 = P.cu_q[i], r1 = P.cu_q[i + 1];
-  return r0 >= 0 && r1 >= r0 && r1 <= P.num_rows && r1 - r0 <= P.max_q_rows && P.kv_len[i] >= 0;
-}
-
-// Row and position of slot `slot`; false if there is no such row (or a bad one).
-__device__ __forceinline__ bool find_row(const RopeParams &P, int64_t slot, int64_t &row,
-                                         int64_t &pos, bool &bad) {
-  bad = false;
-  if (slot >= P.slots) return false;
-  if (P.positions != nullptr) {
-    row = slot;
-    pos = P.positions[slot];
-    bad = pos <= -(int64_t{1} << 31) || pos >= (int64_t{1} << 31);
-    return !bad;
-  }
-  int i, j;
-  if (P.by_row) {                 // the last sequence that starts at or before the row
-    int lo = 0, hi = P.batch;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (P.cu_q[mid] <= slot) lo = mid; else hi = mid;
-    }
-    i = lo;
-    j = static_cast<int>(slot) - P.cu_q[i];
-  } else {
-    i = static_cast<int>(static_cast<uint32_t>(slot) / static_cast<uint32_t>(P.max_q_rows));
-    j = static_cast<int>(slot) - i * P.max_q_rows;
-  }
-  const int r0 = P.cu_q[i], r1 = P.cu_q[i + 1], L = P.kv_len[i];
-  if (!good_sequence(P, i)) {
-    bad = true;
-    return false;
-  }
-  if (j < 0 || j >= r1 - r0) return false;
-  row = r0 + j;
-  pos = static_cast<int64_t>(L) + j;
-  return true;
-}
 
 // Heads that a thread has in flight (and as many that it works on): narrow
 // columns load little at a time.  CTAs per SM that the registers are capped for.
@@ -359,32 +244,34 @@ cudaError_t launch_shape(int g, dim3 grid, const RopeParams &P, cudaStream_t s) 
 
 bool positive(float x) { return std::isfinite(x) && x > 0.0f; }
 
-sv_status check_rope(const sv_rope_args *a) {
-  auto bad = [](const char *what) { return record_error(SV_ERR_INVALID, "rope: %s", what); };
+}  // namespace
+
+sv_status check_rope(const sv_rope_args *a, const char *who) {
+  auto bad = [who](const char *what) { return record_error(SV_ERR_INVALID, "%s: %s", who, what); };
   if (!a) return bad("null arguments");
   if (a->dtype != SV_F32 && a->dtype != SV_BF16)
-    return record_error(SV_ERR_INVALID, "rope: dtype %d", a->dtype);
+    return record_error(SV_ERR_INVALID, "%s: dtype %d", who, a->dtype);
   if (a->kv_dtype != 0 && a->kv_dtype != SV_E4M3)
-    return record_error(SV_ERR_INVALID, "rope: kv_dtype %d (0 or SV_E4M3)", a->kv_dtype);
+    return record_error(SV_ERR_INVALID, "%s: kv_dtype %d (0 or SV_E4M3)", who, a->kv_dtype);
   if (a->num_q_heads < 0 || a->num_q_heads > kMaxHeads || a->num_kv_heads < 0 || a->num_kv_heads > kMaxHeads)
-    return record_error(SV_ERR_INVALID, "rope: heads Hq=%d Hkv=%d outside [0, %d]", a->num_q_heads,
+    return record_error(SV_ERR_INVALID, "%s: heads Hq=%d Hkv=%d outside [0, %d]", who, a->num_q_heads,
                         a->num_kv_heads, kMaxHeads);
   if (a->head_dim < 8 || a->head_dim > kMaxDim || a->head_dim % 8)
-    return record_error(SV_ERR_UNSUPPORTED, "rope: head_dim %d (built: multiples of 8 up to %d)",
+    return record_error(SV_ERR_UNSUPPORTED, "%s: head_dim %d (built: multiples of 8 up to %d)", who,
                         a->head_dim, kMaxDim);
   if (a->rot_dim < 2 || a->rot_dim > a->head_dim || a->rot_dim % 2)
-    return record_error(SV_ERR_INVALID, "rope: rot_dim %d (even, 2..head_dim %d)", a->rot_dim,
+    return record_error(SV_ERR_INVALID, "%s: rot_dim %d (even, 2..head_dim %d)", who, a->rot_dim,
                         a->head_dim);
   if (a->layout != SV_ROPE_HALF && a->layout != SV_ROPE_INTERLEAVED)
-    return record_error(SV_ERR_INVALID, "rope: layout %d", a->layout);
+    return record_error(SV_ERR_INVALID, "%s: layout %d", who, a->layout);
   if (a->num_rows < 0 || a->num_rows >= (int64_t{1} << 31))
-    return record_error(SV_ERR_INVALID, "rope: num_rows %lld", static_cast<long long>(a->num_rows));
+    return record_error(SV_ERR_INVALID, "%s: num_rows %lld", who, static_cast<long long>(a->num_rows));
   if (!(a->mscale == 0.0f || positive(a->mscale))) return bad("mscale must be finite and >= 0");
   if (!(a->k_scale == 0.0f || positive(a->k_scale)) || !(a->v_scale == 0.0f || positive(a->v_scale)))
     return bad("k_scale / v_scale must be finite and >= 0");
   if (!a->positions) {
-    if (a->batch < 0) return record_error(SV_ERR_INVALID, "rope: batch %d", a->batch);
-    if (a->max_q_rows < 1) return record_error(SV_ERR_INVALID, "rope: max_q_rows %d", a->max_q_rows);
+    if (a->batch < 0) return record_error(SV_ERR_INVALID, "%s: batch %d", who, a->batch);
+    if (a->max_q_rows < 1) return record_error(SV_ERR_INVALID, "%s: max_q_rows %d", who, a->max_q_rows);
     const int64_t slots = static_cast<int64_t>(a->batch) * a->max_q_rows;
     if (slots >= (int64_t{1} << 31)) return bad("batch * max_q_rows passes 2^31");
     if (a->batch > 0 && (!a->cu_q || !a->kv_len)) return bad("null cu_q / kv_len without positions");
@@ -398,21 +285,19 @@ sv_status check_rope(const sv_rope_args *a) {
                     {a->v, a->v_out, a->num_kv_heads, a->v_stride, true, "v"}};
   for (const auto &x : tensors) {
     if (x.heads == 0 || (!x.in && x.kv)) continue;
-    if (!x.in || !x.out) return record_error(SV_ERR_INVALID, "rope: null %s or %s_out", x.name, x.name);
+    if (!x.in || !x.out) return record_error(SV_ERR_INVALID, "%s: null %s or %s_out", who, x.name, x.name);
     if (!is_aligned16(x.in) || !is_aligned16(x.out))
-      return record_error(SV_ERR_INVALID, "rope: %s and %s_out must be 16-byte aligned", x.name, x.name);
+      return record_error(SV_ERR_INVALID, "%s: %s and %s_out must be 16-byte aligned", who, x.name, x.name);
     const int64_t width = static_cast<int64_t>(x.heads) * a->head_dim;
     const int64_t stride = x.stride ? x.stride : width;
     if (stride < width || stride * esz % 16 || stride > (int64_t{1} << 40))
-      return record_error(SV_ERR_INVALID, "rope: %s row stride %lld (a multiple of 16 bytes, at least %lld)",
+      return record_error(SV_ERR_INVALID, "%s: %s row stride %lld (a multiple of 16 bytes, at least %lld)", who,
                           x.name, static_cast<long long>(stride), static_cast<long long>(width));
     if (x.in == x.out && (stride != width || (x.kv && a->kv_dtype == SV_E4M3)))
-      return record_error(SV_ERR_INVALID, "rope: %s in place needs contiguous rows of one dtype", x.name);
+      return record_error(SV_ERR_INVALID, "%s: %s in place needs contiguous rows of one dtype", who, x.name);
   }
   return SV_OK;
 }
-
-}  // namespace
 
 }  // namespace sv
 
@@ -420,7 +305,7 @@ extern "C" {
 
 SV_API sv_status spec_rope_rows(const sv_rope_args *a, void *stream) {
   using namespace sv;
-  const sv_status st = check_rope(a);
+  const sv_status st = check_rope(a, "rope");
   if (st != SV_OK) return st;
   RopeParams P{};
   P.batch = a->batch;
