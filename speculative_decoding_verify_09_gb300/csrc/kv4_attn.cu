@@ -9,14 +9,14 @@
 // takes once.  E2M1 times E4M3 has six significant bits, so the operands are
 // exact and only q, the weights and the sums are rounded.
 //
-// Split: the tiles of 32 tokens of all (sequence, KV head, part of the rows) are
-// one list, cut into equal runs, one per CTA, one CTA per SM.  A CTA's tiles go to
-// its warps in turn; each warp streams its own through a ring of bulk copies (a
-// slab of 16 tokens is 18 D contiguous bytes, K and V and their scales), so no
-// warp waits for another until a segment -- the tiles of one (sequence, head,
-// part) in the run -- ends, and copies run ahead across segments.  Then the warps'
-// sums are joined in shared memory; a segment cut by a run's end goes to the
-// workspace, and the last of its pieces to arrive joins them, in order.
+// Split: the tiles of 32 tokens of all (sequence, KV head, part of the rows) --
+// segments -- are one list, cut into equal runs, one per warp of a persistent grid
+// (one CTA per SM).  A warp streams its run through a ring of its own: a slab of 16
+// tokens is 18 D contiguous bytes, K and V and their scales, so a tile is one or two
+// bulk copies, which run ahead across segments; no warp waits for another before its
+// run is done.  A segment that lies in one run is finished by its warp.  The pieces of
+// the others are left in shared memory, joined there by the CTA, and, where a segment
+// passes the CTA's runs, joined in the workspace by the last CTA to arrive, in order.
 //
 // Operands: S^T = K q^T and O^T = V^T P^T, tokens (then elements) on M, rows on N,
 // so a block of 1 row costs 8 columns, not 16 or more rows.  The order of a head's
@@ -38,6 +38,7 @@ constexpr int kTile = 32;                            // tokens
 constexpr int kMaxBatch = 2048;
 constexpr int kMaxCtas = 192;                        // (sizes the workspace on any host)
 constexpr int kCounters = 65536;                     // first in the workspace, whatever the shape
+constexpr int kHead = 2;                             // units that a segment costs beside its tiles
 constexpr float kLate = 8.0f;                        // log2 the maximum may grow before sums are rescaled
 
 // Warps and stages of a warp's ring; NB: 8-row columns of a part.
@@ -49,16 +50,19 @@ struct Shape {
   static constexpr int kRows = 8 * NB;
   static constexpr int kStride = D + 4;              // floats between a slot's rows
   static constexpr int kTileBytes = 2 * slab_bytes(D);
-  static constexpr size_t kRing = static_cast<size_t>(kWarps) * kStages * kTileBytes;
-  static constexpr size_t kSlots = static_cast<size_t>(kWarps) * kRows * kStride * 4;
-  static constexpr size_t kSums = static_cast<size_t>(kWarps) * kRows * 8;
+  static constexpr size_t kRingOne = static_cast<size_t>(kStages) * kTileBytes;
+  static constexpr size_t kSlotOne = static_cast<size_t>(kRows) * kStride * 4;
+  static_assert(kSlotOne <= kRingOne, "a warp's last piece goes into its ring");
+  static_assert(2 * kWarps <= 32, "a lane per piece");
+  static constexpr size_t kRing = kWarps * kRingOne, kSlots = kWarps * kSlotOne;
+  static constexpr size_t kSums = size_t{2} * kWarps * kRows * 8;
   static constexpr size_t kFixed = kRing + kSlots + kSums;
 };
 
 struct Kv4AttnParams {
   Kv4View cache;
   int batch, Hq, g, max_q_rows, parts;               // parts: of max_q_rows * g rows
-  int min_tiles;                                     // of a run
+  int least;                                         // units of a run
   int64_t num_rows, q_stride;
   float scale_log2;                                  // of a score, k_scale and log2 e in it
   const int32_t *cu_q, *kv_len;
@@ -127,27 +131,35 @@ __device__ __forceinline__ Sequence sequence_of(const Kv4AttnParams &P, int i, u
 // in different halves of 128 bytes.
 __device__ __forceinline__ int token_of(int x) { return x ^ ((x >> 1) & 1); }
 
+// A piece of a segment that its warp could not finish: the segment (its first unit in
+// the list), whether it holds the segment's first and last tiles.
+struct Piece {
+  int seg, i, unit;                                  // seg < 0: none
+  int ends;                                          // 1: the first tile, 2: the last one
+};
+
 template <int D, int NB>
 __global__ void __launch_bounds__(Shape<D, NB>::kThreads, 1) kv4_attn_kernel(const Kv4AttnParams P) {
   using Sh = Shape<D, NB>;
   constexpr int W = Sh::kWarps, S = Sh::kStages, NT = Sh::kThreads, ROWS = Sh::kRows;
   constexpr int SLAB = slab_bytes(D), STEPS = D / 16, WORDS = D / 32, MT = D / 16;
   extern __shared__ __align__(128) uint8_t smem[];
-  float *s_slots = reinterpret_cast<float *>(smem + Sh::kRing);
-  float2 *s_ml = reinterpret_cast<float2 *>(smem + Sh::kRing + Sh::kSlots);
+  float2 *s_ml = reinterpret_cast<float2 *>(smem + Sh::kRing + Sh::kSlots);  // [2 W, ROWS] maximum, sum
   int32_t *s_start = reinterpret_cast<int32_t *>(smem + Sh::kFixed);         // [batch + 1]
   uint8_t *s_parts = reinterpret_cast<uint8_t *>(s_start + P.batch + 1);     // [batch]
   __shared__ __align__(8) uint64_t s_bar[W * S];
   __shared__ uint8_t s_bad[W * S];
+  __shared__ Piece s_piece[2 * W];
   __shared__ int32_t s_scan[W];
-  __shared__ int s_last;
+  __shared__ int s_last[2];
   const int tid = threadIdx.x, w = tid >> 5, l = tid & 31, r = l >> 2, c = l & 3;
 
   if (tid < W * S) bar_init(smem_u32(&s_bar[tid]));
+  if (tid < 2 * W) s_piece[tid].seg = -1;
   asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
   wait_for_previous();
 
-  // tiles before each sequence's first
+  // units (tiles, and kHead for each segment) before each sequence's first
   const int heads = P.cache.heads;
   {
     const int each = (P.batch + NT - 1) / NT, i0 = min(P.batch, tid * each), i1 = min(P.batch, i0 + each);
@@ -158,7 +170,7 @@ __global__ void __launch_bounds__(Shape<D, NB>::kThreads, 1) kv4_attn_kernel(con
       if (why && blockIdx.x == 0) set_status(P.dev_status, why);
       const int parts = (s.R * P.g + ROWS - 1) / ROWS;
       s_parts[i] = static_cast<uint8_t>(parts);
-      const int n = (s.keys + kTile - 1) / kTile * parts * heads;
+      const int n = ((s.keys + kTile - 1) / kTile + kHead) * parts * heads;
       s_start[i] = n;
       mine += n;
     }
@@ -184,136 +196,156 @@ __global__ void __launch_bounds__(Shape<D, NB>::kThreads, 1) kv4_attn_kernel(con
     __syncthreads();
   }
   const int total = s_start[P.batch];
-  const int ctas = max(1, min(static_cast<int>(gridDim.x), total / P.min_tiles));
-  const int b = blockIdx.x;
-  if (b >= ctas || total == 0) return;
-  auto run_start = [&](int x) { return static_cast<int>(static_cast<int64_t>(total) * x / ctas); };
-  auto cta_of = [&](int t) { return static_cast<int>(((static_cast<int64_t>(t) + 1) * ctas - 1) / total); };
-  const int t0 = run_start(b), t1 = run_start(b + 1);
+  if (total == 0) return;
+  // runs: at least P.least units each, over all SMs before a second warp of one has any
+  const int wanted = max(1, min(static_cast<int>(gridDim.x) * W, total / P.least));
+  const int ctas = min(static_cast<int>(gridDim.x), wanted), busy = (wanted + ctas - 1) / ctas;
+  const int runs = ctas * busy, b = blockIdx.x;
+  if (b >= ctas) return;
+  auto run_start = [&](int x) { return static_cast<int>(static_cast<int64_t>(total) * x / runs); };
+  auto cta_of = [&](int v) { return static_cast<int>(((static_cast<int64_t>(v) + 1) * runs - 1) / total) / busy; };
+  const int v0 = w < busy ? run_start(b * busy + w) : 0, v1 = w < busy ? run_start(b * busy + w + 1) : 0;
 
-  // sequence, unit (head * parts + part) and tile in it of list entry t
-  struct Place { int i, unit, tile, tiles; };
-  auto locate = [&](int t) {
+  // sequence, unit (head * parts + part) and place in it of list entry v
+  struct Place { int i, unit, at, tiles; };
+  auto locate = [&](int v) {
     int lo = 0, hi = P.batch;
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
-      if (s_start[mid] <= t) lo = mid; else hi = mid;
+      if (s_start[mid] <= v) lo = mid; else hi = mid;
     }
     Place p;
     p.i = lo;
-    p.tiles = (s_start[lo + 1] - s_start[lo]) / (heads * s_parts[lo]);
-    const int rem = t - s_start[lo];
-    p.unit = rem / p.tiles;
-    p.tile = rem - p.unit * p.tiles;
+    const int each = (s_start[lo + 1] - s_start[lo]) / (heads * s_parts[lo]), rem = v - s_start[lo];
+    p.unit = rem / each;
+    p.at = rem - p.unit * each;
+    p.tiles = each - kHead;
     return p;
   };
 
-  // ---- this warp's copies: a lane finds the slabs of each of the next 32 tiles
+  // ---- this warp's copies: a lane finds the slabs of each of the next 32 units
   const uint8_t *from0 = nullptr, *from1 = nullptr;  // slabs of this lane's tile (nullptr: not copied)
   bool from_bad = false;
-  auto look_up = [&](int k) {
-    const int t = t0 + w + W * (k + l);
+  uint32_t open = 0;                                 // of these units: tiles not yet asked for
+  int looked = v0;                                   // units looked at
+  int issued = 0, taken = 0;                         // tiles asked for, and used
+  auto look_up = [&]() {
+    const int v = looked + l;
     from0 = from1 = nullptr;
     from_bad = false;
-    if (t >= t1) return;
-    const Place p = locate(t);
-    uint32_t why = 0;
-    const Sequence s = sequence_of(P, p.i, &why);
-    const int64_t at = static_cast<int64_t>(p.unit / s_parts[p.i]) * head_bytes(P.cache);
-    const uint8_t *x = find_slab(P.cache, p.i, static_cast<int64_t>(p.tile) * kTile, &why);
-    if (x != nullptr) from0 = x + at;
-    if (p.tile * kTile + kSlab < s.keys) {
-      const uint8_t *y = find_slab(P.cache, p.i, static_cast<int64_t>(p.tile) * kTile + kSlab, &why);
-      if (y != nullptr) from1 = y + at;
+    bool real = false;
+    if (v < v1) {
+      const Place p = locate(v);
+      real = p.at >= kHead;
+      if (real) {
+        uint32_t why = 0;
+        const Sequence s = sequence_of(P, p.i, &why);
+        const int64_t at = static_cast<int64_t>(p.unit / s_parts[p.i]) * head_bytes(P.cache);
+        const int first = (p.at - kHead) * kTile;
+        const uint8_t *x = find_slab(P.cache, p.i, first, &why);
+        if (x != nullptr) from0 = x + at;
+        if (first + kSlab < s.keys) {
+          const uint8_t *y = find_slab(P.cache, p.i, first + kSlab, &why);
+          if (y != nullptr) from1 = y + at;
+        }
+        if (why) {
+          set_status(P.dev_status, why);
+          from0 = from1 = nullptr;
+          from_bad = true;
+        }
+      }
     }
-    if (why) {
-      set_status(P.dev_status, why);
-      from0 = from1 = nullptr;
-      from_bad = true;
-    }
+    open = __ballot_sync(0xffffffffu, real);
+    looked += 32;
   };
-  uint8_t *ring = smem + static_cast<size_t>(w) * S * Sh::kTileBytes;
-  auto issue = [&](int k) {
-    if ((k & 31) == 0) look_up(k);
-    if (t0 + w + W * k >= t1 || l != (k & 31)) return;
-    const int st = k % S;
-    const uint32_t bar = smem_u32(&s_bar[w * S + st]), to = smem_u32(ring + st * Sh::kTileBytes);
-    s_bad[w * S + st] = from_bad;
-    bar_expect(bar, (from0 != nullptr ? SLAB : 0) + (from1 != nullptr ? SLAB : 0));
-    if (from0 != nullptr && from1 == from0 + SLAB) {
-      bulk_copy(to, from0, 2 * SLAB, bar);
-    } else {
-      if (from0 != nullptr) bulk_copy(to, from0, SLAB, bar);
-      if (from1 != nullptr) bulk_copy(to + SLAB, from1, SLAB, bar);
+  uint8_t *ring = smem + w * Sh::kRingOne;
+  auto issue = [&]() {
+    while (open == 0) {
+      if (looked >= v1) return;
+      look_up();
     }
+    const int st = issued % S;
+    if (l == __ffs(open) - 1) {
+      const uint32_t bar = smem_u32(&s_bar[w * S + st]), to = smem_u32(ring + st * Sh::kTileBytes);
+      s_bad[w * S + st] = from_bad;
+      bar_expect(bar, (from0 != nullptr ? SLAB : 0) + (from1 != nullptr ? SLAB : 0));
+      if (from0 != nullptr && from1 == from0 + SLAB) {
+        bulk_copy(to, from0, 2 * SLAB, bar);
+      } else {
+        if (from0 != nullptr) bulk_copy(to, from0, SLAB, bar);
+        if (from1 != nullptr) bulk_copy(to + SLAB, from1, SLAB, bar);
+      }
+    }
+    open &= open - 1;
+    ++issued;
   };
-  int k = 0;                                         // tiles this warp has taken
-  bool dead = false;                                 // a wait ran out, at tile dead_at
-  int dead_at = 0;
-  for (int x = 0; x < S; ++x) issue(x);
+  for (int x = 0; x < S; ++x) issue();
+  bool dead = false;                                 // a wait ran out: nothing more is asked for
 
-  for (int t = t0; t < t1;) {
-    // ---- a segment: the run's tiles of one (sequence, head, part)
-    const Place p = locate(t);
-    const int seg_end = min(t1, t - p.tile + p.tiles), parts = s_parts[p.i];
-    const int h = p.unit / parts, part = p.unit - h * parts;
+  for (int v = v0; v < v1;) {
+    // ---- a segment's tiles in this run
+    const Place p = locate(v);
+    const int seg = v - p.at, end = min(v1, seg + kHead + p.tiles);
+    const int tile0 = max(0, p.at - kHead), tile1 = end - seg - kHead;
+    const bool starts = p.at <= kHead, stops = end == seg + kHead + p.tiles;
+    v = end;
+    if (tile1 <= tile0) continue;
+    const int parts = s_parts[p.i], h = p.unit / parts, part = p.unit - h * parts;
     uint32_t why = 0;
     const Sequence s = sequence_of(P, p.i, &why);
     const int first_row = part * ROWS;               // of the block's R * g rows
+    const int rows = min(ROWS, s.R * P.g - first_row);
 
     uint32_t qf[NB][STEPS][2];
     int lim[NB][2];                                  // the last token that this lane's columns see
     float m[NB][2], mu[NB][2], sum[NB][2], o[MT][NB][4];
-    const int mine = (t - t0) % W;                   // the warp that takes tile t
-    int tile = t + (w - mine + W) % W;               // this warp's first in the segment
-    if (tile < seg_end) {
 #pragma unroll
-      for (int nb = 0; nb < NB; ++nb) {
-        const int n = first_row + 8 * nb + r, j = n / P.g, hh = n - j * P.g;
-        uint4 v[WORDS];
+    for (int nb = 0; nb < NB; ++nb) {
+      const int n = 8 * nb + r, j = (first_row + n) / P.g, hh = first_row + n - j * P.g;
+      uint4 q[WORDS];
 #pragma unroll
-        for (int x = 0; x < WORDS; ++x) v[x] = make_uint4(0, 0, 0, 0);
-        if (j < s.R) {
-          const uint4 *src = reinterpret_cast<const uint4 *>(
-              P.q + (s.r0 + j) * P.q_stride + static_cast<int64_t>(h * P.g + hh) * D + c * (D / 4));
+      for (int x = 0; x < WORDS; ++x) q[x] = make_uint4(0, 0, 0, 0);
+      if (n < rows) {
+        const uint4 *src = reinterpret_cast<const uint4 *>(
+            P.q + (s.r0 + j) * P.q_stride + static_cast<int64_t>(h * P.g + hh) * D + c * (D / 4));
 #pragma unroll
-          for (int x = 0; x < WORDS; ++x) v[x] = src[x];
-        }
-#pragma unroll
-        for (int x = 0; x < WORDS; ++x) {
-          qf[nb][2 * x][0] = bf16x2_to_f16x2(v[x].x);
-          qf[nb][2 * x][1] = bf16x2_to_f16x2(v[x].y);
-          qf[nb][2 * x + 1][0] = bf16x2_to_f16x2(v[x].z);
-          qf[nb][2 * x + 1][1] = bf16x2_to_f16x2(v[x].w);
-        }
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          lim[nb][x] = min(s.L + (first_row + 8 * nb + 2 * c + x) / P.g, s.keys - 1);
-          m[nb][x] = -INFINITY;
-          mu[nb][x] = sum[nb][x] = 0.0f;
-        }
-#pragma unroll
-        for (int x = 0; x < MT; ++x) o[x][nb][0] = o[x][nb][1] = o[x][nb][2] = o[x][nb][3] = 0.0f;
+        for (int x = 0; x < WORDS; ++x) q[x] = src[x];
       }
+#pragma unroll
+      for (int x = 0; x < WORDS; ++x) {
+        qf[nb][2 * x][0] = bf16x2_to_f16x2(q[x].x);
+        qf[nb][2 * x][1] = bf16x2_to_f16x2(q[x].y);
+        qf[nb][2 * x + 1][0] = bf16x2_to_f16x2(q[x].z);
+        qf[nb][2 * x + 1][1] = bf16x2_to_f16x2(q[x].w);
+      }
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        lim[nb][x] = min(s.L + (first_row + 8 * nb + 2 * c + x) / P.g, s.keys - 1);
+        m[nb][x] = -INFINITY;
+        mu[nb][x] = sum[nb][x] = 0.0f;
+      }
+#pragma unroll
+      for (int x = 0; x < MT; ++x) o[x][nb][0] = o[x][nb][1] = o[x][nb][2] = o[x][nb][3] = 0.0f;
     }
     int nan_from = 0x7fffffff;                       // block token whose V has NaN in this lane's elements
-    for (; tile < seg_end; tile += W, ++k) {
-      const int st = k % S;
+    for (int tile = tile0; tile < tile1; ++tile, ++taken) {
+      const int st = taken % S;
       if (!dead &&
-          !__all_sync(0xffffffffu, bar_wait(smem_u32(&s_bar[w * S + st]), (k / S) & 1, P.spin_limit))) {
+          !__all_sync(0xffffffffu, bar_wait(smem_u32(&s_bar[w * S + st]), (taken / S) & 1, P.spin_limit))) {
         dead = true;
-        dead_at = k;
         if (l == 0) set_status(P.dev_status, SV_DEV_TIMEOUT);
+        for (int x = taken; x < issued; ++x)         // copies in flight write this CTA's memory
+          bar_wait(smem_u32(&s_bar[w * S + x % S]), (x / S) & 1, 1u << 22);
       }
       if (dead || s_bad[w * S + st]) {
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) sum[nb][0] = sum[nb][1] = NAN;
         __syncwarp();
-        if (!dead) issue(k + S);
+        if (!dead) issue();
         continue;
       }
       const uint8_t *stage = ring + st * Sh::kTileBytes;
-      const int key0 = (tile - t + p.tile) * kTile;
+      const int key0 = tile * kTile;
       const bool edge = key0 + kTile - 1 > s.L;      // tokens that some row does not see
 
       // ---- S^T = K q^T
@@ -458,112 +490,188 @@ __global__ void __launch_bounds__(Shape<D, NB>::kThreads, 1) kv4_attn_kernel(con
         }
       }
       __syncwarp();
-      issue(k + S);
+      issue();
     }
 
-    // ---- the warps' sums joined
-    const int count = min(W, seg_end - t);
-    __syncthreads();                                 // (the slots of the segment before are read)
-    if ((w - mine + W) % W < count) {
-      if (__any_sync(0xffffffffu, nan_from != 0x7fffffff)) {
-        nan_from = min(nan_from, __shfl_xor_sync(0xffffffffu, nan_from, 1));
-        nan_from = min(nan_from, __shfl_xor_sync(0xffffffffu, nan_from, 2));
+    // ---- its sums: rows that this warp has seen whole are done, others a piece
+    if (__any_sync(0xffffffffu, nan_from != 0x7fffffff)) {
+      nan_from = min(nan_from, __shfl_xor_sync(0xffffffffu, nan_from, 1));
+      nan_from = min(nan_from, __shfl_xor_sync(0xffffffffu, nan_from, 2));
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb)
+      for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-          for (int y = 0; y < MT; ++y)
+        for (int y = 0; y < MT; ++y)
 #pragma unroll
-            for (int x = 0; x < 4; ++x)
-              if (lim[nb][x & 1] >= nan_from) o[y][nb][x] = NAN;
-      }
+          for (int x = 0; x < 4; ++x)
+            if (lim[nb][x & 1] >= nan_from) o[y][nb][x] = NAN;
+    }
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+      for (int x = 0; x < 2; ++x)
+#pragma unroll
+        for (int d = 4; d < 32; d <<= 1) sum[nb][x] += __shfl_xor_sync(0xffffffffu, sum[nb][x], d);
+    if (starts && stops) {
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-          float a = sum[nb][x];
-#pragma unroll
-          for (int d = 4; d < 32; d <<= 1) a += __shfl_xor_sync(0xffffffffu, a, d);
           const int n = 8 * nb + 2 * c + x;
-          if (r == 0) s_ml[w * ROWS + n] = make_float2(m[nb][x], a);
-          float4 *to = reinterpret_cast<float4 *>(s_slots + (w * ROWS + n) * Sh::kStride + r * (D / 8));
+          if (n >= rows) continue;
+          const int j = (first_row + n) / P.g, hh = first_row + n - j * P.g;
+          const float f = P.cache.v_scale / sum[nb][x];
+          uint32_t pair[MT];
 #pragma unroll
-          for (int y = 0; y < MT; y += 2)
-            to[y / 2] = make_float4(o[y][nb][x], o[y][nb][2 + x], o[y + 1][nb][x], o[y + 1][nb][2 + x]);
+          for (int y = 0; y < MT; ++y) pair[y] = pack_bf16x2(o[y][nb][x] * f, o[y][nb][2 + x] * f);
+          uint4 *to = reinterpret_cast<uint4 *>(
+              P.out + (static_cast<int64_t>(s.r0 + j) * P.Hq + h * P.g + hh) * D + r * (D / 8));
+#pragma unroll
+          for (int y = 0; y < MT; y += 4) to[y / 4] = make_uint4(pair[y], pair[y + 1], pair[y + 2], pair[y + 3]);
         }
+      continue;
     }
-    __syncthreads();
-    const int seg0 = t - p.tile, seg1 = seg0 + p.tiles;              // the whole segment's tiles
-    const bool whole = t == seg0 && seg_end == seg1;
-    const int slot = 2 * b + (t == t0 ? 0 : 1);
-    auto store_row = [&](int n, int d, float x, float y, float total_sum) {
-      const int j = (first_row + n) / P.g, hh = first_row + n - j * P.g;
-      if (j >= s.R) return;
-      const float f = P.cache.v_scale / total_sum;
-      *reinterpret_cast<uint32_t *>(P.out + (static_cast<int64_t>(s.r0 + j) * P.Hq + h * P.g + hh) * D + d) =
-          pack_bf16x2(x * f, y * f);
-    };
-    for (int e = tid; e < ROWS * (D / 2); e += NT) {
-      const int n = e / (D / 2), d = e % (D / 2) * 2;
-      float top = -INFINITY;
-      for (int x = 0; x < count; ++x) top = fmaxf(top, s_ml[(mine + x) % W * ROWS + n].x);
-      const float base = top == -INFINITY ? 0.0f : top;
-      float a = 0.0f, x0 = 0.0f, x1 = 0.0f;
-      for (int x = 0; x < count; ++x) {
-        const int at = (mine + x) % W * ROWS + n;
-        const float2 ml = s_ml[at], v = *reinterpret_cast<const float2 *>(s_slots + at * Sh::kStride + d);
-        const float f = fast_exp2(ml.x - base);
-        a = fmaf(f, ml.y, a);
-        x0 = fmaf(f, v.x, x0);
-        x1 = fmaf(f, v.y, x1);
+    // (the last piece of a run goes where its ring was)
+    const int e = 2 * w + (end == v1 ? 1 : 0);
+    float *slot = reinterpret_cast<float *>(end == v1 ? ring : smem + Sh::kRing + w * Sh::kSlotOne);
+    __syncwarp();
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const int n = 8 * nb + 2 * c + x;
+        if (n >= rows) continue;
+        if (r == 0) s_ml[e * ROWS + n] = make_float2(m[nb][x], sum[nb][x]);
+        float4 *to = reinterpret_cast<float4 *>(slot + n * Sh::kStride + r * (D / 8));
+#pragma unroll
+        for (int y = 0; y < MT; y += 2)
+          to[y / 2] = make_float4(o[y][nb][x], o[y][nb][2 + x], o[y + 1][nb][x], o[y + 1][nb][2 + x]);
+      }
+    if (l == 0) s_piece[e] = Piece{seg, p.i, p.unit, (starts ? 1 : 0) | (stops ? 2 : 0)};
+  }
+
+  // ---- the pieces joined: those of a segment are neighbours in the list of 2 W
+  __syncthreads();
+  const Piece mine = l < 2 * W ? s_piece[l] : Piece{-1, 0, 0, 0};
+  const uint32_t there = __ballot_sync(0xffffffffu, mine.seg >= 0);
+  if (there == 0) return;
+  const uint32_t below = there & ((1u << l) - 1);
+  const int prev = below ? 31 - __clz(below) : l;
+  const int prev_seg = __shfl_sync(0xffffffffu, mine.seg, prev);
+  uint32_t leaders = __ballot_sync(0xffffffffu, mine.seg >= 0 && (below == 0 || prev_seg != mine.seg));
+  constexpr int E = D / 32;                          // elements of a lane
+  auto store_row = [&](const Sequence &s, int row, int h, const float (&x)[E], float total_sum) {
+    const int j = row / P.g, hh = row - j * P.g;
+    const float f = P.cache.v_scale / total_sum;
+    uint32_t *to = reinterpret_cast<uint32_t *>(
+        P.out + (static_cast<int64_t>(s.r0 + j) * P.Hq + h * P.g + hh) * D + E * l);
+    if constexpr (E == 4)
+      *reinterpret_cast<uint2 *>(to) = make_uint2(pack_bf16x2(x[0] * f, x[1] * f), pack_bf16x2(x[2] * f, x[3] * f));
+    else
+      *to = pack_bf16x2(x[0] * f, x[1] * f);
+  };
+  auto add = [&](float (&x)[E], float f, const float *from) {        // E neighbouring floats
+    if constexpr (E == 4) {
+      const float4 y = *reinterpret_cast<const float4 *>(from);
+      x[0] = fmaf(f, y.x, x[0]), x[1] = fmaf(f, y.y, x[1]), x[2] = fmaf(f, y.z, x[2]), x[3] = fmaf(f, y.w, x[3]);
+    } else {
+      const float2 y = *reinterpret_cast<const float2 *>(from);
+      x[0] = fmaf(f, y.x, x[0]), x[1] = fmaf(f, y.y, x[1]);
+    }
+  };
+  int jobs = 0, passing = 0;                         // rows handed out; segments that pass this CTA
+  Piece open0{-1, 0, 0, 0}, open1{-1, 0, 0, 0};
+  while (leaders) {
+    const int lead = __ffs(leaders) - 1;
+    leaders &= leaders - 1;
+    const uint32_t group = there & ~((1u << lead) - 1) & (leaders ? (1u << (__ffs(leaders) - 1)) - 1 : ~0u);
+    const Piece head = s_piece[lead], tail = s_piece[31 - __clz(group)];
+    const bool whole = (head.ends & 1) && (tail.ends & 2);
+    const int parts = s_parts[head.i], h = head.unit / parts, part = head.unit - h * parts;
+    uint32_t why = 0;
+    const Sequence s = sequence_of(P, head.i, &why);
+    const int rows = min(ROWS, s.R * P.g - part * ROWS);
+    const int slot = 2 * b + (head.ends & 1);
+    for (int n = (w + W - jobs % W) % W; n < rows; n += W) {
+      const bool on = group >> l & 1;
+      const float2 ml = on ? s_ml[l * ROWS + n] : make_float2(-INFINITY, 0.0f);
+      const float top = warp_max(ml.x), base = top == -INFINITY ? 0.0f : top;
+      const float f = fast_exp2(ml.x - base), all = warp_sum(f * ml.y);
+      float x[E] = {};
+      for (uint32_t rest = group; rest; rest &= rest - 1) {
+        const int e = __ffs(rest) - 1;
+        const float *from = reinterpret_cast<const float *>(
+            e & 1 ? smem + (e >> 1) * Sh::kRingOne : smem + Sh::kRing + (e >> 1) * Sh::kSlotOne);
+        add(x, __shfl_sync(0xffffffffu, f, e), from + n * Sh::kStride + E * l);
       }
       if (whole) {
-        store_row(n, d, x0, x1, a);
+        store_row(s, part * ROWS + n, h, x, all);
       } else {
-        *reinterpret_cast<float2 *>(P.part_o + (static_cast<int64_t>(slot) * ROWS + n) * D + d) = make_float2(x0, x1);
-        if (d == 0) P.part_ml[slot * ROWS + n] = make_float2(top, a);
+        float *to = P.part_o + (static_cast<int64_t>(slot) * ROWS + n) * D + E * l;
+#pragma unroll
+        for (int y = 0; y < E; y += 2) *reinterpret_cast<float2 *>(to + y) = make_float2(x[y], x[y + 1]);
+        if (l == 0) P.part_ml[slot * ROWS + n] = make_float2(top, all);
       }
     }
+    jobs += rows;
     if (!whole) {
-      const int c0 = cta_of(seg0), c1 = cta_of(seg1 - 1);
-      __threadfence();
-      __syncthreads();
-      if (tid == 0) {
-        uint32_t *counter = P.counters + (p.i * heads + h) * P.parts + part;
-        s_last = atomicInc(counter, c1 - c0) == static_cast<uint32_t>(c1 - c0);
-      }
-      __syncthreads();
-      if (s_last) {
-        __threadfence();
-        for (int e = tid; e < ROWS * (D / 2); e += NT) {
-          const int n = e / (D / 2), d = e % (D / 2) * 2;
-          auto place_of = [&](int x) { return static_cast<int64_t>(2 * x + (run_start(x) >= seg0 ? 0 : 1)) * ROWS + n; };
-          float top = -INFINITY;
-          for (int x = c0; x <= c1; ++x) top = fmaxf(top, __ldcg(&P.part_ml[place_of(x)]).x);
-          const float base = top == -INFINITY ? 0.0f : top;
-          float a = 0.0f, x0 = 0.0f, x1 = 0.0f;
-          for (int x = c0; x <= c1; ++x) {
-            const int64_t at = place_of(x);
-            const float2 ml = __ldcg(&P.part_ml[at]);
-            const float2 v = __ldcg(reinterpret_cast<const float2 *>(P.part_o + at * D + d));
-            const float f = fast_exp2(ml.x - base);
-            a = fmaf(f, ml.y, a);
-            x0 = fmaf(f, v.x, x0);
-            x1 = fmaf(f, v.y, x1);
+      if (passing == 0) open0 = head; else open1 = head;         // (the first and the last one)
+      ++passing;
+    }
+  }
+  if (passing == 0) return;
+
+  // ---- segments of several CTAs: the last of them joins what all have left
+  __threadfence();
+  __syncthreads();
+  if (tid < passing) {
+    const Piece head = tid == 0 ? open0 : open1;
+    const Place p = locate(head.seg);
+    const int c0 = cta_of(head.seg + kHead), c1 = cta_of(head.seg + kHead + p.tiles - 1);
+    uint32_t *counter = P.counters + static_cast<int64_t>(head.i) * heads * P.parts + head.unit;
+    s_last[tid] = atomicInc(counter, c1 - c0) == static_cast<uint32_t>(c1 - c0);
+  }
+  __syncthreads();
+  for (int which = 0; which < passing; ++which) {
+    if (!s_last[which]) continue;
+    __threadfence();
+    const Piece head = which == 0 ? open0 : open1;
+    const Place p = locate(head.seg);
+    const int c0 = cta_of(head.seg + kHead), c1 = cta_of(head.seg + kHead + p.tiles - 1);
+    const int parts = s_parts[head.i], h = head.unit / parts, part = head.unit - h * parts;
+    uint32_t why = 0;
+    const Sequence s = sequence_of(P, head.i, &why);
+    const int rows = min(ROWS, s.R * P.g - part * ROWS);
+    for (int n = w; n < rows; n += W) {
+      auto place_of = [&](int x) { return static_cast<int64_t>(2 * x + (x == c0 ? 1 : 0)) * ROWS + n; };
+      float top = -INFINITY;
+      for (int x = c0 + l; x <= c1; x += 32) top = fmaxf(top, __ldcg(&P.part_ml[place_of(x)]).x);
+      top = warp_max(top);
+      const float base = top == -INFINITY ? 0.0f : top;
+      float all = 0.0f, x[E] = {};
+      for (int x0 = c0; x0 <= c1; x0 += 32) {
+        const float2 ml = x0 + l <= c1 ? __ldcg(&P.part_ml[place_of(x0 + l)]) : make_float2(-INFINITY, 0.0f);
+        const float f = fast_exp2(ml.x - base);
+        all += warp_sum(f * ml.y);
+        const int count = min(32, c1 - x0 + 1);
+#pragma unroll 4
+        for (int y = 0; y < count; ++y) {
+          float have[E];
+#pragma unroll
+          for (int z = 0; z < E; z += 2) {
+            const float2 two = __ldcg(reinterpret_cast<const float2 *>(P.part_o + place_of(x0 + y) * D + E * l + z));
+            have[z] = two.x, have[z + 1] = two.y;
           }
-          store_row(n, d, x0, x1, a);
+          add(x, __shfl_sync(0xffffffffu, f, y), have);
         }
       }
+      store_row(s, part * ROWS + n, h, x, all);
     }
-    t = seg_end;
   }
-  if (dead)                                          // its copies in flight write this CTA's memory
-    for (int x = dead_at; x < dead_at + S; ++x)
-      if (t0 + w + W * x < t1) bar_wait(smem_u32(&s_bar[w * S + x % S]), (x / S) & 1, 1u << 22);
 }
 
 size_t align256(size_t x) { return (x + 255) / 256 * 256; }
 
-// Columns of 8 rows that a part has (1 to 4), and parts of the largest block.
+// Columns of 8 rows that a part has (1 to 3), and parts of the largest block.
 struct Plan {
   int nb, parts;
   size_t part_o, part_ml, bytes;                     // offsets in the workspace, and its size
@@ -571,7 +679,7 @@ struct Plan {
 Plan plan_of(const sv_kv4_attn_args &a) {
   Plan p;
   const int rows = a.max_q_rows * (a.num_q_heads / a.cache.num_kv_heads), blocks = (rows + 7) / 8;
-  p.parts = (blocks + 3) / 4;
+  p.parts = (blocks + 2) / 3;
   p.nb = (blocks + p.parts - 1) / p.parts;
   p.parts = (blocks + p.nb - 1) / p.nb;
   p.part_o = kCounters * sizeof(uint32_t);
@@ -590,8 +698,7 @@ template <int D>
 cudaError_t launch_rows(int nb, const Kv4AttnParams &P, int ctas, cudaStream_t s) {
   return nb == 1   ? launch_shape<D, 1>(P, ctas, s)
          : nb == 2 ? launch_shape<D, 2>(P, ctas, s)
-         : nb == 3 ? launch_shape<D, 3>(P, ctas, s)
-                   : launch_shape<D, 4>(P, ctas, s);
+                   : launch_shape<D, 3>(P, ctas, s);
 }
 
 sv_status check_attn4(const sv_kv4_attn_args *a, bool tensors) {
@@ -623,7 +730,7 @@ sv_status check_attn4(const sv_kv4_attn_args *a, bool tensors) {
     return record_error(SV_ERR_UNSUPPORTED, "%s: %d sequences x %d KV heads x %d parts of rows", who,
                         a->batch, Hkv, p.parts);
   const int64_t tokens = static_cast<int64_t>(cache.max_pages) * cache.page_size;
-  if (tokens >= (int64_t{1} << 31) || units * ((tokens + kTile - 1) / kTile) >= (int64_t{1} << 31))
+  if (tokens >= (int64_t{1} << 31) || units * ((tokens + kTile - 1) / kTile + kHead) >= (int64_t{1} << 31))
     return record_error(SV_ERR_UNSUPPORTED, "%s: tables of %d pages of %d tokens", who, cache.max_pages,
                         cache.page_size);
   const int64_t width = static_cast<int64_t>(a->num_q_heads) * cache.head_dim;
@@ -667,7 +774,7 @@ SV_API sv_status spec_kv4_attn(const sv_kv4_attn_args *a, void *ws, size_t ws_by
   P.g = a->num_q_heads / a->cache.num_kv_heads;
   P.max_q_rows = a->max_q_rows;
   P.parts = p.parts;
-  P.min_tiles = 4;
+  P.least = 4;
   P.num_rows = a->num_rows;
   P.q_stride = a->q_stride ? a->q_stride : static_cast<int64_t>(P.Hq) * a->cache.head_dim;
   const double scale = a->scale != 0.0f ? a->scale : 1.0 / std::sqrt(static_cast<double>(a->cache.head_dim));
