@@ -39,6 +39,7 @@ constexpr int kMaxBatch = 2048;
 constexpr int kMaxCtas = 192;                        // (sizes the workspace on any host)
 constexpr int kCounters = 65536;                     // first in the workspace, whatever the shape
 constexpr int kHead = 2;                             // units that a segment costs beside its tiles
+constexpr int kSnap = 16;                            // units that a CTA's share may end early or late
 constexpr float kLate = 8.0f;                        // log2 the maximum may grow before sums are rescaled
 
 // Warps and stages of a warp's ring; NB: 8-row columns of a part.
@@ -62,6 +63,8 @@ struct Shape {
 struct Kv4AttnParams {
   Kv4View cache;
   int batch, Hq, g, max_q_rows, parts;               // parts: of max_q_rows * g rows
+  uint32_t g_inverse;                                // 2^32 / g rounded up: exact quotients of rows
+                                                     // below 2^32 / g; 0: g is 1
   int least;                                         // units of a run
   int64_t num_rows, q_stride;
   float scale_log2;                                  // of a score, k_scale and log2 e in it
@@ -131,11 +134,13 @@ __device__ __forceinline__ Sequence sequence_of(const Kv4AttnParams &P, int i, u
 // in different halves of 128 bytes.
 __device__ __forceinline__ int token_of(int x) { return x ^ ((x >> 1) & 1); }
 
-// A piece of a segment that its warp could not finish: the segment (its first unit in
-// the list), whether it holds the segment's first and last tiles.
-struct Piece {
-  int seg, i, unit;                                  // seg < 0: none
-  int ends;                                          // 1: the first tile, 2: the last one
+// A piece of a segment that its warp could not finish.
+struct __align__(16) Piece {
+  int seg;                                           // the segment's first unit; < 0: no piece
+  int ends;                                          // 1: holds the segment's first tile, 2: its last
+  int tiles;                                         // of the segment
+  int counter;                                       // its place among the counters
+  int rows, first_row, r0, h;                        // its rows: packed rows of a block at r0, KV head
 };
 
 template <int D, int NB>
@@ -151,7 +156,7 @@ __global__ void __launch_bounds__(Shape<D, NB>::kThreads, 1) kv4_attn_kernel(con
   __shared__ uint8_t s_bad[W * S];
   __shared__ Piece s_piece[2 * W];
   __shared__ int32_t s_scan[W];
-  __shared__ int s_last[2];
+  __shared__ int s_share[kMaxCtas + 1], s_last[2], s_from[2], s_to[2];
   const int tid = threadIdx.x, w = tid >> 5, l = tid & 31, r = l >> 2, c = l & 3;
 
   if (tid < W * S) bar_init(smem_u32(&s_bar[tid]));
@@ -197,15 +202,6 @@ __global__ void __launch_bounds__(Shape<D, NB>::kThreads, 1) kv4_attn_kernel(con
   }
   const int total = s_start[P.batch];
   if (total == 0) return;
-  // runs: at least P.least units each, over all SMs before a second warp of one has any
-  const int wanted = max(1, min(static_cast<int>(gridDim.x) * W, total / P.least));
-  const int ctas = min(static_cast<int>(gridDim.x), wanted), busy = (wanted + ctas - 1) / ctas;
-  const int runs = ctas * busy, b = blockIdx.x;
-  if (b >= ctas) return;
-  auto run_start = [&](int x) { return static_cast<int>(static_cast<int64_t>(total) * x / runs); };
-  auto cta_of = [&](int v) { return static_cast<int>(((static_cast<int64_t>(v) + 1) * runs - 1) / total) / busy; };
-  const int v0 = w < busy ? run_start(b * busy + w) : 0, v1 = w < busy ? run_start(b * busy + w + 1) : 0;
-
   // sequence, unit (head * parts + part) and place in it of list entry v
   struct Place { int i, unit, at, tiles; };
   auto locate = [&](int v) {
@@ -223,6 +219,33 @@ __global__ void __launch_bounds__(Shape<D, NB>::kThreads, 1) kv4_attn_kernel(con
     return p;
   };
 
+  // The CTAs' shares: equal, but for ends that come within kSnap of a segment's, which are
+  // moved there (a cut there would cost the joining of two CTAs' pieces); a share's
+  // units go to the warps in runs of equal length.
+  const int ctas = max(1, min(static_cast<int>(gridDim.x), total / P.least)), b = blockIdx.x;
+  if (b >= ctas) return;
+  for (int x = tid; x <= ctas; x += NT) {
+    const int each = total / ctas, v = each * x + (total - each * ctas) * x / ctas;
+    int to = v;
+    if (v > 0 && v < total) {
+      const Place p = locate(v);
+      const int after = kHead + p.tiles - p.at;
+      to = p.at <= min(after, kSnap) ? v - p.at : after <= kSnap ? v + after : v;
+    }
+    s_share[x] = to;
+  }
+  __syncthreads();
+  auto cta_of = [&](int v) {                         // the last share that starts at or before v
+    int lo = 0, hi = ctas;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (s_share[mid] <= v) lo = mid; else hi = mid;
+    }
+    return lo;
+  };
+  const int u0 = s_share[b], u1 = s_share[b + 1];
+  const int v0 = u0 + (u1 - u0) * w / W, v1 = u0 + (u1 - u0) * (w + 1) / W;
+
   // ---- this warp's copies: a lane finds the slabs of each of the next 32 units
   const uint8_t *from0 = nullptr, *from1 = nullptr;  // slabs of this lane's tile (nullptr: not copied)
   bool from_bad = false;
@@ -238,20 +261,22 @@ __global__ void __launch_bounds__(Shape<D, NB>::kThreads, 1) kv4_attn_kernel(con
       const Place p = locate(v);
       real = p.at >= kHead;
       if (real) {
-        uint32_t why = 0;
-        const Sequence s = sequence_of(P, p.i, &why);
-        const int64_t at = static_cast<int64_t>(p.unit / s_parts[p.i]) * head_bytes(P.cache);
-        const int first = (p.at - kHead) * kTile;
-        const uint8_t *x = find_slab(P.cache, p.i, first, &why);
-        if (x != nullptr) from0 = x + at;
-        if (first + kSlab < s.keys) {
-          const uint8_t *y = find_slab(P.cache, p.i, first + kSlab, &why);
-          if (y != nullptr) from1 = y + at;
-        }
-        if (why) {
-          set_status(P.dev_status, why);
-          from0 = from1 = nullptr;
+        // the slabs 2 n and 2 n + 1 of the sequence, of one page or of two neighbours
+        const uint32_t n = 2u * static_cast<uint32_t>(p.at - kHead), per = P.cache.slabs;
+        const uint32_t at0 = n / per, in0 = n - at0 * per;
+        const bool same = in0 + 1 < per;
+        const int32_t *row = P.cache.table + p.i * P.cache.table_stride;
+        const int keys = P.kv_len[p.i] + P.cu_q[p.i + 1] - P.cu_q[p.i];
+        const bool second = static_cast<int>(n + 1) * kSlab < keys;
+        const int32_t page0 = row[at0], page1 = same || !second ? page0 : row[at0 + 1];
+        const int64_t head = static_cast<int64_t>(p.unit / s_parts[p.i]) * head_bytes(P.cache);
+        const int64_t page_bytes = P.cache.heads * head_bytes(P.cache);
+        if (page0 < 0 || page0 >= P.cache.num_pages || page1 < 0 || page1 >= P.cache.num_pages) {
+          set_status(P.dev_status, SV_DEV_BAD_PARAM);
           from_bad = true;
+        } else {
+          from0 = P.cache.pages + page0 * page_bytes + head + static_cast<int64_t>(in0) * SLAB;
+          if (second) from1 = same ? from0 + SLAB : P.cache.pages + page1 * page_bytes + head;
         }
       }
     }
@@ -279,48 +304,69 @@ __global__ void __launch_bounds__(Shape<D, NB>::kThreads, 1) kv4_attn_kernel(con
     open &= open - 1;
     ++issued;
   };
-  for (int x = 0; x < S; ++x) issue();
+  // the segment of list entry v, and this lane's part of its rows of q
+  struct Segment { Place p; Sequence s; int h, part, rows; };
+  auto segment_of = [&](int v) {
+    Segment x;
+    x.p = locate(v);
+    const int parts = s_parts[x.p.i];
+    x.h = x.p.unit / parts;
+    x.part = x.p.unit - x.h * parts;
+    uint32_t why = 0;
+    x.s = sequence_of(P, x.p.i, &why);
+    x.rows = min(ROWS, x.s.R * P.g - x.part * ROWS);
+    return x;
+  };
+  auto token_row = [&](int row) {                    // of the block, of packed row `row`
+    return P.g_inverse ? static_cast<int>(__umulhi(static_cast<uint32_t>(row), P.g_inverse)) : row;
+  };
+  auto q_row = [&](const Segment &x, int n) {
+    const int row = x.part * ROWS + n, j = token_row(row), hh = row - j * P.g;
+    return P.q + (x.s.r0 + j) * P.q_stride + static_cast<int64_t>(x.h * P.g + hh) * D + c * (D / 4);
+  };
+  issue();
   bool dead = false;                                 // a wait ran out: nothing more is asked for
 
   for (int v = v0; v < v1;) {
     // ---- a segment's tiles in this run
-    const Place p = locate(v);
+    const Segment here = segment_of(v);
+    const Place p = here.p;
+    const Sequence s = here.s;
+    const int h = here.h, rows = here.rows, first_row = here.part * ROWS;   // of the block's R * g rows
     const int seg = v - p.at, end = min(v1, seg + kHead + p.tiles);
     const int tile0 = max(0, p.at - kHead), tile1 = end - seg - kHead;
     const bool starts = p.at <= kHead, stops = end == seg + kHead + p.tiles;
     v = end;
     if (tile1 <= tile0) continue;
-    const int parts = s_parts[p.i], h = p.unit / parts, part = p.unit - h * parts;
-    uint32_t why = 0;
-    const Sequence s = sequence_of(P, p.i, &why);
-    const int first_row = part * ROWS;               // of the block's R * g rows
-    const int rows = min(ROWS, s.R * P.g - first_row);
 
+    // (the run's first rows of q are asked for behind one tile, not behind all of the ring)
     uint32_t qf[NB][STEPS][2];
+    {
+      uint4 q[NB][WORDS];
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) {
+        const uint4 *src = reinterpret_cast<const uint4 *>(q_row(here, 8 * nb + r));
+#pragma unroll
+        for (int x = 0; x < WORDS; ++x) q[nb][x] = 8 * nb + r < rows ? src[x] : make_uint4(0, 0, 0, 0);
+      }
+      for (int x = issued - taken; x < S; ++x) issue();
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int x = 0; x < WORDS; ++x) {
+          qf[nb][2 * x][0] = bf16x2_to_f16x2(q[nb][x].x);
+          qf[nb][2 * x][1] = bf16x2_to_f16x2(q[nb][x].y);
+          qf[nb][2 * x + 1][0] = bf16x2_to_f16x2(q[nb][x].z);
+          qf[nb][2 * x + 1][1] = bf16x2_to_f16x2(q[nb][x].w);
+        }
+    }
     int lim[NB][2];                                  // the last token that this lane's columns see
     float m[NB][2], mu[NB][2], sum[NB][2], o[MT][NB][4];
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
-      const int n = 8 * nb + r, j = (first_row + n) / P.g, hh = first_row + n - j * P.g;
-      uint4 q[WORDS];
-#pragma unroll
-      for (int x = 0; x < WORDS; ++x) q[x] = make_uint4(0, 0, 0, 0);
-      if (n < rows) {
-        const uint4 *src = reinterpret_cast<const uint4 *>(
-            P.q + (s.r0 + j) * P.q_stride + static_cast<int64_t>(h * P.g + hh) * D + c * (D / 4));
-#pragma unroll
-        for (int x = 0; x < WORDS; ++x) q[x] = src[x];
-      }
-#pragma unroll
-      for (int x = 0; x < WORDS; ++x) {
-        qf[nb][2 * x][0] = bf16x2_to_f16x2(q[x].x);
-        qf[nb][2 * x][1] = bf16x2_to_f16x2(q[x].y);
-        qf[nb][2 * x + 1][0] = bf16x2_to_f16x2(q[x].z);
-        qf[nb][2 * x + 1][1] = bf16x2_to_f16x2(q[x].w);
-      }
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
-        lim[nb][x] = min(s.L + (first_row + 8 * nb + 2 * c + x) / P.g, s.keys - 1);
+        lim[nb][x] = min(s.L + token_row(first_row + 8 * nb + 2 * c + x), s.keys - 1);
         m[nb][x] = -INFINITY;
         mu[nb][x] = sum[nb][x] = 0.0f;
       }
@@ -462,10 +508,13 @@ __global__ void __launch_bounds__(Shape<D, NB>::kThreads, 1) kv4_attn_kernel(con
             v[x][0] = *reinterpret_cast<const uint32_t *>(slab + tok * 32 + r * 4);
             s4[x] = slab[8 * D + tok * 4 + (r >> 1)];
           }
-          if (edge) {
-            // tokens behind the last hold anything; a block token's NaN is kept from the rows
-            // before it (a weight of 0 would not do that) and given to the others at the end
-            const int key = key0 + sl * kSlab + tok;
+        }
+        if (edge) {
+          // tokens behind the last hold anything; a block token's NaN is kept from the rows before
+          // it (a weight of 0 would not do that) and given to the others at the end
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const int key = key0 + sl * kSlab + token_of(2 * c + (x & 1)) + (x >> 1) * 8;
             const bool nan = key > s.L && (s4[x] & 0x7Fu) == 0x7Fu;
             if (nan && key < s.keys) nan_from = min(nan_from, key);
             if (nan || key >= s.keys) s4[x] = 0;
@@ -518,7 +567,7 @@ __global__ void __launch_bounds__(Shape<D, NB>::kThreads, 1) kv4_attn_kernel(con
         for (int x = 0; x < 2; ++x) {
           const int n = 8 * nb + 2 * c + x;
           if (n >= rows) continue;
-          const int j = (first_row + n) / P.g, hh = first_row + n - j * P.g;
+          const int j = token_row(first_row + n), hh = first_row + n - j * P.g;
           const float f = P.cache.v_scale / sum[nb][x];
           uint32_t pair[MT];
 #pragma unroll
@@ -546,24 +595,25 @@ __global__ void __launch_bounds__(Shape<D, NB>::kThreads, 1) kv4_attn_kernel(con
         for (int y = 0; y < MT; y += 2)
           to[y / 2] = make_float4(o[y][nb][x], o[y][nb][2 + x], o[y + 1][nb][x], o[y + 1][nb][2 + x]);
       }
-    if (l == 0) s_piece[e] = Piece{seg, p.i, p.unit, (starts ? 1 : 0) | (stops ? 2 : 0)};
+    if (l == 0)
+      s_piece[e] = Piece{seg, (starts ? 1 : 0) | (stops ? 2 : 0), p.tiles, p.i * heads * P.parts + p.unit,
+                         rows, first_row, s.r0, h};
   }
 
   // ---- the pieces joined: those of a segment are neighbours in the list of 2 W
   __syncthreads();
-  const Piece mine = l < 2 * W ? s_piece[l] : Piece{-1, 0, 0, 0};
-  const uint32_t there = __ballot_sync(0xffffffffu, mine.seg >= 0);
+  const int my_seg = l < 2 * W ? s_piece[l].seg : -1;
+  const uint32_t there = __ballot_sync(0xffffffffu, my_seg >= 0);
   if (there == 0) return;
   const uint32_t below = there & ((1u << l) - 1);
-  const int prev = below ? 31 - __clz(below) : l;
-  const int prev_seg = __shfl_sync(0xffffffffu, mine.seg, prev);
-  uint32_t leaders = __ballot_sync(0xffffffffu, mine.seg >= 0 && (below == 0 || prev_seg != mine.seg));
+  const int prev_seg = __shfl_sync(0xffffffffu, my_seg, below ? 31 - __clz(below) : l);
+  uint32_t leaders = __ballot_sync(0xffffffffu, my_seg >= 0 && (below == 0 || prev_seg != my_seg));
   constexpr int E = D / 32;                          // elements of a lane
-  auto store_row = [&](const Sequence &s, int row, int h, const float (&x)[E], float total_sum) {
-    const int j = row / P.g, hh = row - j * P.g;
+  auto store_row = [&](const Piece &of, int n, const float (&x)[E], float total_sum) {
+    const int row = of.first_row + n, j = token_row(row), hh = row - j * P.g;
     const float f = P.cache.v_scale / total_sum;
     uint32_t *to = reinterpret_cast<uint32_t *>(
-        P.out + (static_cast<int64_t>(s.r0 + j) * P.Hq + h * P.g + hh) * D + E * l);
+        P.out + (static_cast<int64_t>(of.r0 + j) * P.Hq + of.h * P.g + hh) * D + E * l);
     if constexpr (E == 4)
       *reinterpret_cast<uint2 *>(to) = make_uint2(pack_bf16x2(x[0] * f, x[1] * f), pack_bf16x2(x[2] * f, x[3] * f));
     else
@@ -579,19 +629,15 @@ __global__ void __launch_bounds__(Shape<D, NB>::kThreads, 1) kv4_attn_kernel(con
     }
   };
   int jobs = 0, passing = 0;                         // rows handed out; segments that pass this CTA
-  Piece open0{-1, 0, 0, 0}, open1{-1, 0, 0, 0};
+  int open0 = 0, open1 = 0;                          // (their first pieces)
   while (leaders) {
     const int lead = __ffs(leaders) - 1;
     leaders &= leaders - 1;
     const uint32_t group = there & ~((1u << lead) - 1) & (leaders ? (1u << (__ffs(leaders) - 1)) - 1 : ~0u);
-    const Piece head = s_piece[lead], tail = s_piece[31 - __clz(group)];
-    const bool whole = (head.ends & 1) && (tail.ends & 2);
-    const int parts = s_parts[head.i], h = head.unit / parts, part = head.unit - h * parts;
-    uint32_t why = 0;
-    const Sequence s = sequence_of(P, head.i, &why);
-    const int rows = min(ROWS, s.R * P.g - part * ROWS);
+    const Piece head = s_piece[lead];
+    const bool whole = (head.ends & 1) && (s_piece[31 - __clz(group)].ends & 2);
     const int slot = 2 * b + (head.ends & 1);
-    for (int n = (w + W - jobs % W) % W; n < rows; n += W) {
+    for (int n = (w + W - jobs % W) % W; n < head.rows; n += W) {
       const bool on = group >> l & 1;
       const float2 ml = on ? s_ml[l * ROWS + n] : make_float2(-INFINITY, 0.0f);
       const float top = warp_max(ml.x), base = top == -INFINITY ? 0.0f : top;
@@ -604,7 +650,7 @@ __global__ void __launch_bounds__(Shape<D, NB>::kThreads, 1) kv4_attn_kernel(con
         add(x, __shfl_sync(0xffffffffu, f, e), from + n * Sh::kStride + E * l);
       }
       if (whole) {
-        store_row(s, part * ROWS + n, h, x, all);
+        store_row(head, n, x, all);
       } else {
         float *to = P.part_o + (static_cast<int64_t>(slot) * ROWS + n) * D + E * l;
 #pragma unroll
@@ -612,36 +658,33 @@ __global__ void __launch_bounds__(Shape<D, NB>::kThreads, 1) kv4_attn_kernel(con
         if (l == 0) P.part_ml[slot * ROWS + n] = make_float2(top, all);
       }
     }
-    jobs += rows;
+    jobs += head.rows;
     if (!whole) {
-      if (passing == 0) open0 = head; else open1 = head;         // (the first and the last one)
+      if (passing == 0) open0 = lead; else open1 = lead;         // (the first and the last one)
       ++passing;
     }
   }
   if (passing == 0) return;
 
   // ---- segments of several CTAs: the last of them joins what all have left
+  const Piece &mine = s_piece[tid == 1 ? open1 : open0];
+  const int from_cta = tid < passing ? cta_of(mine.seg + kHead) : 0;
+  const int to_cta = tid < passing ? cta_of(mine.seg + kHead + mine.tiles - 1) : 0;
   __threadfence();
   __syncthreads();
   if (tid < passing) {
-    const Piece head = tid == 0 ? open0 : open1;
-    const Place p = locate(head.seg);
-    const int c0 = cta_of(head.seg + kHead), c1 = cta_of(head.seg + kHead + p.tiles - 1);
-    uint32_t *counter = P.counters + static_cast<int64_t>(head.i) * heads * P.parts + head.unit;
-    s_last[tid] = atomicInc(counter, c1 - c0) == static_cast<uint32_t>(c1 - c0);
+    const uint32_t others = to_cta - from_cta;
+    s_last[tid] = atomicInc(P.counters + mine.counter, others) == others;
+    s_from[tid] = from_cta;
+    s_to[tid] = to_cta;
   }
   __syncthreads();
   for (int which = 0; which < passing; ++which) {
     if (!s_last[which]) continue;
     __threadfence();
-    const Piece head = which == 0 ? open0 : open1;
-    const Place p = locate(head.seg);
-    const int c0 = cta_of(head.seg + kHead), c1 = cta_of(head.seg + kHead + p.tiles - 1);
-    const int parts = s_parts[head.i], h = head.unit / parts, part = head.unit - h * parts;
-    uint32_t why = 0;
-    const Sequence s = sequence_of(P, head.i, &why);
-    const int rows = min(ROWS, s.R * P.g - part * ROWS);
-    for (int n = w; n < rows; n += W) {
+    const Piece head = s_piece[which == 0 ? open0 : open1];
+    const int c0 = s_from[which], c1 = s_to[which];
+    for (int n = w; n < head.rows; n += W) {
       auto place_of = [&](int x) { return static_cast<int64_t>(2 * x + (x == c0 ? 1 : 0)) * ROWS + n; };
       float top = -INFINITY;
       for (int x = c0 + l; x <= c1; x += 32) top = fmaxf(top, __ldcg(&P.part_ml[place_of(x)]).x);
@@ -664,7 +707,7 @@ __global__ void __launch_bounds__(Shape<D, NB>::kThreads, 1) kv4_attn_kernel(con
           add(x, __shfl_sync(0xffffffffu, f, y), have);
         }
       }
-      store_row(s, part * ROWS + n, h, x, all);
+      store_row(head, n, x, all);
     }
   }
 }
@@ -772,6 +815,7 @@ SV_API sv_status spec_kv4_attn(const sv_kv4_attn_args *a, void *ws, size_t ws_by
   P.batch = a->batch;
   P.Hq = a->num_q_heads;
   P.g = a->num_q_heads / a->cache.num_kv_heads;
+  P.g_inverse = P.g == 1 ? 0 : static_cast<uint32_t>(((uint64_t{1} << 32) + P.g - 1) / P.g);
   P.max_q_rows = a->max_q_rows;
   P.parts = p.parts;
   P.least = 4;
