@@ -248,7 +248,7 @@ __global__ void __launch_bounds__(Shape<D, NB>::kThreads, 1) kv4_attn_kernel(con
 
   // ---- this warp's copies: a lane finds the slabs of each of the next 32 units
   const uint8_t *from0 = nullptr, *from1 = nullptr;  // slabs of this lane's tile (nullptr: not copied)
-  bool from_bad = false;
+  bool from_bad = false, any_bad = false;            // pages outside the pool; any so far
   uint32_t open = 0;                                 // of these units: tiles not yet asked for
   int looked = v0;                                   // units looked at
   int issued = 0, taken = 0;                         // tiles asked for, and used
@@ -281,6 +281,7 @@ __global__ void __launch_bounds__(Shape<D, NB>::kThreads, 1) kv4_attn_kernel(con
       }
     }
     open = __ballot_sync(0xffffffffu, real);
+    any_bad |= __any_sync(0xffffffffu, from_bad);
     looked += 32;
   };
   uint8_t *ring = smem + w * Sh::kRingOne;
@@ -383,7 +384,7 @@ __global__ void __launch_bounds__(Shape<D, NB>::kThreads, 1) kv4_attn_kernel(con
         for (int x = taken; x < issued; ++x)         // copies in flight write this CTA's memory
           bar_wait(smem_u32(&s_bar[w * S + x % S]), (x / S) & 1, 1u << 22);
       }
-      if (dead || s_bad[w * S + st]) {
+      if (dead || (any_bad && s_bad[w * S + st])) {
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) sum[nb][0] = sum[nb][1] = NAN;
         __syncwarp();
@@ -393,6 +394,22 @@ __global__ void __launch_bounds__(Shape<D, NB>::kThreads, 1) kv4_attn_kernel(con
       const uint8_t *stage = ring + st * Sh::kTileBytes;
       const int key0 = tile * kTile;
       const bool edge = key0 + kTile - 1 > s.L;      // tokens that some row does not see
+      if (edge) {
+        // Tokens behind the last hold anything: V's scales there become 0.  So do a block token's
+        // that are NaN, to keep them from the rows before it (a weight of 0 would not do that);
+        // the rows that see it get their NaN at the end.  A lane takes a token.
+        const int key = key0 + l;
+        uint8_t *scales = ring + st * Sh::kTileBytes + (l >> 4) * SLAB + slab_v(D) + 8 * D + (l & 15) * (D / 16);
+#pragma unroll
+        for (int x = 0; x < D / 16; ++x) {
+          const bool nan = key > s.L && key < s.keys && (scales[x] & 0x7Fu) == 0x7Fu;
+          if (nan || key >= s.keys) scales[x] = 0;
+          const uint32_t who = __ballot_sync(0xffffffffu, nan);
+          if (who != 0 && x == (D == 128 ? r : r >> 1)) nan_from = min(nan_from, key0 + __ffs(who) - 1);
+        }
+        asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
+        __syncwarp();
+      }
 
       // ---- S^T = K q^T
       float sc[2][NB][4];
@@ -433,7 +450,7 @@ __global__ void __launch_bounds__(Shape<D, NB>::kThreads, 1) kv4_attn_kernel(con
                                    mul_f16x2(ha[2 * y + 1], pa), mul_f16x2(hb[2 * y + 1], pb)};
 #pragma unroll
             for (int nb = 0; nb < NB; ++nb)
-              mma_f16_16816(sc[sl][nb], a, qf[nb][2 * x + y][0], qf[nb][2 * x + y][1]);
+              mma_f16(sc[sl][nb], a, qf[nb][2 * x + y][0], qf[nb][2 * x + y][1]);
           }
         }
       }
@@ -509,17 +526,6 @@ __global__ void __launch_bounds__(Shape<D, NB>::kThreads, 1) kv4_attn_kernel(con
             s4[x] = slab[8 * D + tok * 4 + (r >> 1)];
           }
         }
-        if (edge) {
-          // tokens behind the last hold anything; a block token's NaN is kept from the rows before
-          // it (a weight of 0 would not do that) and given to the others at the end
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            const int key = key0 + sl * kSlab + token_of(2 * c + (x & 1)) + (x >> 1) * 8;
-            const bool nan = key > s.L && (s4[x] & 0x7Fu) == 0x7Fu;
-            if (nan && key < s.keys) nan_from = min(nan_from, key);
-            if (nan || key >= s.keys) s4[x] = 0;
-          }
-        }
         const uint32_t f01 = e4m3x2_to_f16x2(s4[0] | s4[1] << 8), f23 = e4m3x2_to_f16x2(s4[2] | s4[3] << 8);
 #pragma unroll
         for (int x = 0; x < D / 64; ++x) {
@@ -534,7 +540,7 @@ __global__ void __launch_bounds__(Shape<D, NB>::kThreads, 1) kv4_attn_kernel(con
             const uint32_t a[4] = {mul_f16x2(a0[y], f01), mul_f16x2(a1[y], f01), mul_f16x2(a2[y], f23),
                                    mul_f16x2(a3[y], f23)};
 #pragma unroll
-            for (int nb = 0; nb < NB; ++nb) mma_f16_16816(o[4 * x + y][nb], a, pf[sl][nb][0], pf[sl][nb][1]);
+            for (int nb = 0; nb < NB; ++nb) mma_f16(o[4 * x + y][nb], a, pf[sl][nb][0], pf[sl][nb][1]);
           }
         }
       }
@@ -544,8 +550,6 @@ __global__ void __launch_bounds__(Shape<D, NB>::kThreads, 1) kv4_attn_kernel(con
 
     // ---- its sums: rows that this warp has seen whole are done, others a piece
     if (__any_sync(0xffffffffu, nan_from != 0x7fffffff)) {
-      nan_from = min(nan_from, __shfl_xor_sync(0xffffffffu, nan_from, 1));
-      nan_from = min(nan_from, __shfl_xor_sync(0xffffffffu, nan_from, 2));
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
