@@ -674,45 +674,86 @@ __global__ void __launch_bounds__(Shape<D, NB>::kThreads, 1) kv4_attn_kernel(con
   const Piece &mine = s_piece[tid == 1 ? open1 : open0];
   const int from_cta = tid < passing ? cta_of(mine.seg + kHead) : 0;
   const int to_cta = tid < passing ? cta_of(mine.seg + kHead + mine.tiles - 1) : 0;
-  __threadfence();
   __syncthreads();
   if (tid < passing) {
     const uint32_t others = to_cta - from_cta;
+    __threadfence();                                 // (the CTA's writes, seen by this thread at the barrier)
     s_last[tid] = atomicInc(P.counters + mine.counter, others) == others;
+    __threadfence();
     s_from[tid] = from_cta;
     s_to[tid] = to_cta;
   }
   __syncthreads();
+  struct __align__(8) Some { float x[E]; };
+  float *s_weight = reinterpret_cast<float *>(smem);                 // [ROWS, CTAs of the segment]
+  float *s_sum = s_weight + ROWS * kMaxCtas;                         // [W, D]
   for (int which = 0; which < passing; ++which) {
     if (!s_last[which]) continue;
-    __threadfence();
     const Piece head = s_piece[which == 0 ? open0 : open1];
-    const int c0 = s_from[which], c1 = s_to[which];
+    const int c0 = s_from[which], count = s_to[which] - c0 + 1;
+    auto place_of = [&](int x, int n) { return static_cast<int64_t>(2 * (c0 + x) + (x == 0 ? 1 : 0)) * ROWS + n; };
+    auto part = [&](int x, int n) {
+      const float *from = P.part_o + place_of(x, n) * D + E * l;
+      Some v;
+#pragma unroll
+      for (int z = 0; z < E; z += 2) {
+        const float2 two = __ldcg(reinterpret_cast<const float2 *>(from + z));
+        v.x[z] = two.x, v.x[z + 1] = two.y;
+      }
+      return v;
+    };
+    // weights of the pieces: a warp per row, a lane per piece
     for (int n = w; n < head.rows; n += W) {
-      auto place_of = [&](int x) { return static_cast<int64_t>(2 * x + (x == c0 ? 1 : 0)) * ROWS + n; };
-      float top = -INFINITY;
-      for (int x = c0 + l; x <= c1; x += 32) top = fmaxf(top, __ldcg(&P.part_ml[place_of(x)]).x);
+      float top = -INFINITY, all = 0.0f;
+      for (int x = l; x < count; x += 32) top = fmaxf(top, __ldcg(&P.part_ml[place_of(x, n)]).x);
       top = warp_max(top);
       const float base = top == -INFINITY ? 0.0f : top;
-      float all = 0.0f, x[E] = {};
-      for (int x0 = c0; x0 <= c1; x0 += 32) {
-        const float2 ml = x0 + l <= c1 ? __ldcg(&P.part_ml[place_of(x0 + l)]) : make_float2(-INFINITY, 0.0f);
+      for (int x = l; x < count; x += 32) {
+        const float2 ml = __ldcg(&P.part_ml[place_of(x, n)]);
         const float f = fast_exp2(ml.x - base);
-        all += warp_sum(f * ml.y);
-        const int count = min(32, c1 - x0 + 1);
-#pragma unroll 4
-        for (int y = 0; y < count; ++y) {
-          float have[E];
-#pragma unroll
-          for (int z = 0; z < E; z += 2) {
-            const float2 two = __ldcg(reinterpret_cast<const float2 *>(P.part_o + place_of(x0 + y) * D + E * l + z));
-            have[z] = two.x, have[z + 1] = two.y;
-          }
-          add(x, __shfl_sync(0xffffffffu, f, y), have);
-        }
+        s_weight[n * kMaxCtas + x] = f;
+        all = fmaf(f, ml.y, all);
       }
-      store_row(head, n, x, all);
+      const float f = P.cache.v_scale / warp_sum(all);
+      for (int x = l; x < count; x += 32) s_weight[n * kMaxCtas + x] *= f;
     }
+    // Sums: few rows of many pieces by several warps each, which take the pieces in turn; else
+    // a warp's (up to three) rows side by side.
+    const int share = count > 16 ? max(1, W / head.rows) : 1;
+    if (share > 1) {
+      __syncthreads();
+      const int n = w / share, sub = w % share;
+      float x[E] = {};
+      if (n < head.rows) {
+#pragma unroll 4
+        for (int y = sub; y < count; y += share) add(x, s_weight[n * kMaxCtas + y], part(y, n).x);
+      }
+#pragma unroll
+      for (int z = 0; z < E; ++z) s_sum[w * D + E * l + z] = x[z];
+      __syncthreads();
+      if (n < head.rows && sub == 0) {
+        for (int y = 1; y < share; ++y) add(x, 1.0f, s_sum + (w + y) * D + E * l);
+        store_row(head, n, x, P.cache.v_scale);      // (the weights hold the scale)
+      }
+    } else {
+      __syncwarp();
+      constexpr int kSide = (ROWS + W - 1) / W;
+      float x[kSide][E] = {};
+#pragma unroll 2
+      for (int y = 0; y < count; ++y) {
+        Some v[kSide];
+#pragma unroll
+        for (int z = 0; z < kSide; ++z)
+          if (w + z * W < head.rows) v[z] = part(y, w + z * W);
+#pragma unroll
+        for (int z = 0; z < kSide; ++z)
+          if (w + z * W < head.rows) add(x[z], s_weight[(w + z * W) * kMaxCtas + y], v[z].x);
+      }
+#pragma unroll
+      for (int z = 0; z < kSide; ++z)
+        if (w + z * W < head.rows) store_row(head, w + z * W, x[z], P.cache.v_scale);
+    }
+    __syncthreads();                                 // (the weights of the next segment)
   }
 }
 
