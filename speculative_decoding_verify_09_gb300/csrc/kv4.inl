@@ -28,21 +28,20 @@ __device__ __forceinline__ int64_t head_bytes(const Kv4View &c) {
   return static_cast<int64_t>(c.slabs) * slab_bytes(c.D);
 }
 
-// The slab of token `pos` (>= 0) of sequence i for KV head 0, or nullptr with the
+// The slab of token `pos` (0 .. 2^32 - 1) of sequence i for KV head 0, or nullptr with the
 // problem's bit in *why.
 __device__ __forceinline__ uint8_t *find_slab(const Kv4View &c, int i, int64_t pos, uint32_t *why) {
-  const int64_t at = pos / c.page_size;
-  if (at >= c.max_pages) {
+  const uint32_t slab = static_cast<uint32_t>(pos) / kSlab, at = slab / static_cast<uint32_t>(c.slabs);
+  if (at >= static_cast<uint32_t>(c.max_pages)) {
     *why = SV_DEV_CAPACITY;
     return nullptr;
   }
-  const int64_t page = c.table[i * c.table_stride + at];
+  const int32_t page = c.table[i * c.table_stride + at];
   if (page < 0 || page >= c.num_pages) {
     *why = SV_DEV_BAD_PARAM;
     return nullptr;
   }
-  const int64_t slab = (pos - at * c.page_size) / kSlab;
-  return c.pages + page * c.heads * head_bytes(c) + slab * slab_bytes(c.D);
+  return c.pages + page * (c.heads * head_bytes(c)) + static_cast<int64_t>(slab - at * c.slabs) * slab_bytes(c.D);
 }
 
 // Four bytes of code pairs -> four f16x2 (a byte's lower code in the lower half).
@@ -94,7 +93,12 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], u
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// The larger one; NaN if either is.
+// The largest of three; NaN if any is.
+__device__ __forceinline__ float max_nan(float a, float b, float c) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2, %3;\n" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
 __device__ __forceinline__ float max_nan(float a, float b) {
   float r;
   asm("max.NaN.f32 %0, %1, %2;\n" : "=f"(r) : "f"(a), "f"(b));

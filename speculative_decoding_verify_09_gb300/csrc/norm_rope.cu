@@ -4,13 +4,13 @@
 // spec_kv4_append and spec_kv4_read in include/spec_kv4.h.
 //
 // A head's D elements lie with D / 16 neighbouring lanes (rounded up to a power of
-// two), 16 each, so that its sum of squares and the largest magnitude of 16
-// elements are a few shuffles away and nothing is read twice.  Where the two
-// halves of a pair are a multiple of 8 apart a lane holds 8 elements and the 8
-// partners of these; neighbouring pairs lie with one lane anyway; for other
-// distances the partner is fetched through shared memory.  Angles as in rope.cu:
-// the position times the turn fraction modulo 2^64, a quarter turn taken off,
-// the rest rounded once.
+// two), 16 each as 8 pairs (a, b), so that its sum of squares and the largest
+// magnitude of 16 elements are a few shuffles away and nothing is read twice.  Where
+// the members of a pair are a multiple of 8 apart a lane holds 8 elements and the 8
+// partners of these; neighbours lie with one lane anyway; for other distances the
+// partner is fetched through shared memory.  Arithmetic is done on two floats at a
+// time.  Angles as in rope.cu: the position times the turn fraction modulo 2^64, a
+// quarter turn taken off, the rest rounded once.
 #include <algorithm>
 #include <cmath>
 
@@ -26,17 +26,21 @@ constexpr int kNT = 256;
 constexpr int kPad = 20;                             // floats between lanes in the exchange
 
 enum Output { kRows, kCodes8, kPages };              // k and v: as they came, E4M3, E2M1 in pages
+// How pairs lie with a lane: a = 8 elements, b = the 8 that are half further on; a and b
+// neighbours among 16 elements in a row; 16 elements in a row, partners elsewhere.
+enum Layout { kPaired, kNeighbours, kFar };
 
 struct NormRopeParams {
   int batch, max_q_rows, Hq, Hkv, D, half;           // half: pairs that are turned
   int nq, nk, heads;                                 // q heads, k heads, all heads of a row
   int lane_shift, row_shift, pairs;                  // log2 lanes of a head, threads of a row
   int heads_per_cta;
-  int by_row, interleaved;
+  int by_row;
   int64_t num_rows, slots;
   int64_t q_stride, k_stride, v_stride;
   float mscale, k_scale, v_scale, k_inverse, v_inverse;
-  float eps, weight_offset;
+  float k_sixth, v_sixth;                            // 1 / (6 scale)
+  float eps, weight_offset, inverse_D;
   const float *q_weight, *k_weight;
   const uint64_t *turns;
   const int32_t *cu_q, *kv_len;
@@ -47,32 +51,142 @@ struct NormRopeParams {
   uint32_t *dev_status;
 };
 
-// Codes and scale of 16 elements whose largest magnitude is m, of which this lane
-// holds N (eight, or all): unit = scale * factor is what a code of 1 stands for.
-__device__ __forceinline__ uint32_t scale_code(float m, float factor, float &unit) {
-  const uint32_t s = e4m3x2_of(__fdiv_rn(m, __fmul_rn(6.0f, factor)), 0.0f) & 0xFFu;
+// Two floats in a register pair, worked on at once.
+typedef unsigned long long F2;
+__device__ __forceinline__ F2 f2(float lo, float hi) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};\n" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void f2_get(F2 x, float &lo, float &hi) {
+  asm("mov.b64 {%0, %1}, %2;\n" : "=f"(lo), "=f"(hi) : "l"(x));
+}
+__device__ __forceinline__ F2 f2_mul(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ F2 f2_fma(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;\n" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
+// Scale of 16 elements whose largest magnitude is m, times_sixth being 1 / (6 factor);
+// unit = scale * factor is what a code of 1 stands for.  (With a factor that is a power
+// of two the product meets the ties of two scales: 1 / 3 in fp32 is off by 2^-25, less
+// than half a step of any tie, which has five significant bits.)
+__device__ __forceinline__ uint32_t scale_code(float m, float times_sixth, float factor, float &unit) {
+  const uint32_t s = e4m3x2_of(__fmul_rn(m, times_sixth), 0.0f) & 0xFFu;
   unit = __fmul_rn(e4m3_to_f32(s), factor);
   return s;
 }
-__device__ __forceinline__ uint32_t codes_of(const float (&x)[8], float unit) {
+// Codes of x / unit.  The quotient by the reciprocal and one correction with the exact
+// remainder: where it is a tie of two codes (x = t unit) the remainder is exact too, so
+// it is met exactly.  A saturated scale (or NaN) may come with quotients that overflow:
+// these are divided.
+__device__ __forceinline__ uint32_t codes_of(const F2 (&x)[4], float unit, uint32_t scale) {
   float y[8];
+  if (scale - 1u < 0x7Du) {
+    float inv;
+    asm("rcp.approx.ftz.f32 %0, %1;\n" : "=f"(inv) : "f"(unit));
+    inv = fmaf(fmaf(-unit, inv, 1.0f), inv, inv);
+    const F2 inv2 = f2(inv, inv), neg = f2(-unit, -unit);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) y[i] = unit == 0.0f ? 0.0f : __fdiv_rn(x[i], unit);
+    for (int i = 0; i < 4; ++i) {
+      const F2 q = f2_mul(x[i], inv2);
+      f2_get(f2_fma(f2_fma(q, neg, x[i]), inv2, q), y[2 * i], y[2 * i + 1]);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float lo, hi;
+      f2_get(x[i], lo, hi);
+      y[2 * i] = scale == 0 ? 0.0f : __fdiv_rn(lo, unit);
+      y[2 * i + 1] = scale == 0 ? 0.0f : __fdiv_rn(hi, unit);
+    }
+  }
   return e2m1x8_of(y);
 }
-__device__ __forceinline__ float largest(const float (&x)[8]) {
-  float m = fabsf(x[0]);
+__device__ __forceinline__ float largest(const F2 (&x)[4]) {
+  float m = 0.0f;
 #pragma unroll
-  for (int i = 1; i < 8; ++i) m = max_nan(m, fabsf(x[i]));
+  for (int i = 0; i < 4; ++i) {
+    float lo, hi;
+    f2_get(x[i], lo, hi);
+    m = max_nan(fabsf(lo), fabsf(hi), m);
+  }
   return m;
 }
 
-// PAIRED: the half layout with half a multiple of 8 (16 for pages), or no pairs;
-// else 16 elements in a row lie with a lane.
-template <typename T, Output OUT, bool PAIRED>
-__global__ void __launch_bounds__(kNT, 3) norm_rope_kernel(const NormRopeParams P) {
-  extern __shared__ __align__(16) float s_turn[];    // [rows][cos, sin][pairs]
-  __shared__ float s_swap[PAIRED ? 1 : kNT * kPad];
+// 16 elements as they lie in memory (two runs of 8) and as pairs: a[i], b[i] hold members
+// 2 i and 2 i + 1 of the runs, or (neighbours) the even and the odd elements.
+template <bool NEIGHBOURS>
+__device__ __forceinline__ void split(const Vec<uint16_t, 8> (&v)[2], F2 (&a)[4], F2 (&b)[4]) {
+  const uint32_t x[4] = {v[0].raw.a.x, v[0].raw.a.y, v[0].raw.a.z, v[0].raw.a.w};
+  const uint32_t y[4] = {v[1].raw.a.x, v[1].raw.a.y, v[1].raw.a.z, v[1].raw.a.w};
+  auto low = [](uint32_t z) { return __uint_as_float(z << 16); };
+  auto high = [](uint32_t z) { return __uint_as_float(z & 0xFFFF0000u); };
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (NEIGHBOURS) {
+      const uint32_t z0 = i < 2 ? x[2 * i] : y[2 * i - 4], z1 = i < 2 ? x[2 * i + 1] : y[2 * i - 3];
+      a[i] = f2(low(z0), low(z1));
+      b[i] = f2(high(z0), high(z1));
+    } else {
+      a[i] = f2(low(x[i]), high(x[i]));
+      b[i] = f2(low(y[i]), high(y[i]));
+    }
+  }
+}
+template <bool NEIGHBOURS>
+__device__ __forceinline__ void split(const Vec<float, 8> (&v)[2], F2 (&a)[4], F2 (&b)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (NEIGHBOURS) {
+      const float *from = i < 2 ? v[0].e + 4 * i : v[1].e + 4 * i - 8;
+      a[i] = f2(from[0], from[2]);
+      b[i] = f2(from[1], from[3]);
+    } else {
+      a[i] = f2(v[0].e[2 * i], v[0].e[2 * i + 1]);
+      b[i] = f2(v[1].e[2 * i], v[1].e[2 * i + 1]);
+    }
+  }
+}
+// The other way: runs x and y of 8 elements.
+template <bool NEIGHBOURS>
+__device__ __forceinline__ void runs(const F2 (&a)[4], const F2 (&b)[4], float (&x)[8], float (&y)[8]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float a0, a1, b0, b1;
+    f2_get(a[i], a0, a1);
+    f2_get(b[i], b0, b1);
+    if constexpr (NEIGHBOURS) {
+      float *to = i < 2 ? x + 4 * i : y + 4 * i - 8;
+      to[0] = a0, to[1] = b0, to[2] = a1, to[3] = b1;
+    } else {
+      x[2 * i] = a0, x[2 * i + 1] = a1;
+      y[2 * i] = b0, y[2 * i + 1] = b1;
+    }
+  }
+}
+
+// Back into a vector of the rows' type.
+__device__ __forceinline__ void join(Vec<uint16_t, 8> &v, const float (&x)[8]) {
+  v.raw.a = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
+                       pack_bf16x2(x[6], x[7]));
+}
+__device__ __forceinline__ void join(Vec<float, 8> &v, const float (&x)[8]) { v.set(x); }
+
+// CTAs per SM that the registers are capped for.
+template <typename T, Output OUT, Layout LAYOUT>
+constexpr int kCtas = LAYOUT != kFar && sizeof(T) == 2 ? 3 : 2;
+
+template <typename T, Output OUT, Layout LAYOUT>
+__global__ void __launch_bounds__(kNT, kCtas<T, OUT, LAYOUT>) norm_rope_kernel(const NormRopeParams P) {
+  constexpr bool kSide = LAYOUT == kNeighbours;
+  extern __shared__ __align__(16) float s_turn[];    // [rows][cos, sin][pairs], [q, k][16 lanes] weights
+  __shared__ float s_swap[LAYOUT == kFar ? kNT * kPad : 1];
   const int row_threads = 1 << P.row_shift, lanes = 1 << P.lane_shift;
   const int rl = threadIdx.x >> P.row_shift, t = threadIdx.x & (row_threads - 1);
   const int hl = t >> P.lane_shift, c = t & (lanes - 1), hstep = row_threads >> P.lane_shift;
@@ -91,27 +205,38 @@ __global__ void __launch_bounds__(kNT, 3) norm_rope_kernel(const NormRopeParams 
          i += static_cast<int64_t>(gridDim.x) * kNT)
       if (!good_sequence(P, static_cast<int>(i))) set_status(P.dev_status, SV_DEV_BAD_LENGTH);
 
-  // this lane's column: two vectors of 8 elements of a head
-  const bool turn = PAIRED && 8 * c < P.half;
-  const int o0 = !PAIRED ? 16 * c : turn ? 8 * c : 2 * P.half + 16 * (c - P.half / 8);
-  const int o1 = turn ? o0 + P.half : o0 + 8;
+  // this lane's column: two runs of 8 elements of a head, and how many of its pairs turn
+  const bool apart = LAYOUT == kPaired && 8 * c < P.half;            // the runs are a pair's members
+  const int o0 = LAYOUT != kPaired ? 16 * c : apart ? 8 * c : 2 * P.half + 16 * (c - P.half / 8);
+  const int o1 = apart ? o0 + P.half : o0 + 8;
   const bool column = live && o0 < P.D, both = column && o1 < P.D;
+  const int turning = LAYOUT == kPaired ? (apart ? 8 : 0) : min(8, max(0, P.half - 8 * c));
 
-  Vec<T, 8> cur[2], nxt[2];
-  const int k0 = P.nq * P.D, v0 = (P.nq + P.nk) * P.D;
-  const T *in_q = static_cast<const T *>(P.q) + row * P.q_stride;
-  const T *in_k = static_cast<const T *>(P.k) + row * P.k_stride - k0;
-  const T *in_v = static_cast<const T *>(P.v) + row * P.v_stride - v0;
-  auto fetch = [&](Vec<T, 8> (&v)[2], int h) {
-    if (!column || h >= h_end) return;
-    const T *p = (h < P.nq ? in_q : h < P.nq + P.nk ? in_k : in_v) + h * P.D;
+  auto fetch = [&](Vec<T, 8> (&v)[2], const T *p, bool on) {
+    if (!on) return;
     v[0].load(p + o0);
     if (both) v[1].load(p + o1);
   };
-  fetch(cur, h_begin + hl);
+  // the kinds' first heads and their tensors: q, k, v
+  auto first_of = [&](int kind) { return kind == 0 ? 0 : kind == 1 ? P.nq : P.nq + P.nk; };
+  auto source = [&](int kind) {
+    return kind == 0   ? static_cast<const T *>(P.q) + row * P.q_stride
+           : kind == 1 ? static_cast<const T *>(P.k) + row * P.k_stride
+                       : static_cast<const T *>(P.v) + row * P.v_stride;
+  };
+  int kind = h_begin < P.nq ? 0 : h_begin < P.nq + P.nk ? 1 : 2;
+  Vec<T, 8> cur[2], nxt[2];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) cur[0].e[i] = cur[1].e[i] = nxt[0].e[i] = nxt[1].e[i] = T(0);
+  {
+    const int h = h_begin - first_of(kind) + hl;
+    fetch(cur, source(kind) + h * P.D, column && h_begin + hl < min(h_end, kind == 2 ? P.heads : first_of(kind + 1)));
+  }
 
-  // cos and sin of the row's pairs, by the threads that share the row
+  // cos and sin of the row's pairs, by the threads that share the row; the weights in the order
+  // of the columns' a and b
   float *s_cos = s_turn + rl * 2 * P.pairs, *s_sin = s_cos + P.pairs;
+  float *s_weight = s_turn + (kNT >> P.row_shift) * 2 * P.pairs;
   const bool any_turn = P.half > 0 && h_begin < P.nq + P.nk;
   if (live && any_turn) {
     for (int p = t; p < P.half; p += row_threads) {
@@ -125,6 +250,19 @@ __global__ void __launch_bounds__(kNT, 3) norm_rope_kernel(const NormRopeParams 
       s_sin[p] = (quarter & 2 ? -sn : sn) * P.mscale;
     }
   }
+  const bool norms = P.q_weight != nullptr || P.k_weight != nullptr;
+  if (norms) {
+    for (int x = threadIdx.x; x < 32 * lanes; x += kNT) {          // [kind][a, b][lanes][8]
+      const float *weight = x < 16 * lanes ? P.q_weight : P.k_weight;
+      const int y = x & (16 * lanes - 1), second = y >= 8 * lanes, col = (y & (8 * lanes - 1)) >> 3, i = y & 7;
+      const bool far = LAYOUT == kPaired && 8 * col < P.half;
+      const int at = kSide              ? 16 * col + 2 * i + second
+                     : LAYOUT != kPaired ? 16 * col + 8 * second + i
+                     : far               ? 8 * col + i + second * P.half
+                                         : 2 * P.half + 16 * (col - P.half / 8) + 8 * second + i;
+      s_weight[x] = weight != nullptr && at < P.D ? weight[at] + P.weight_offset : 1.0f;
+    }
+  }
   uint8_t *slab = nullptr;                           // of the row's token, KV head 0
   if (OUT == kPages && live) {
     uint32_t why = 0;
@@ -134,81 +272,72 @@ __global__ void __launch_bounds__(kNT, 3) norm_rope_kernel(const NormRopeParams 
   __syncthreads();
   if (!live) return;                                 // (all threads of a warp share a row)
 
-  // the pairs of this column, and its weights, fetched again where q's end and k's begin
-  float cs[8], sn[8], w0[8], w1[8];
-  if (any_turn) {
+  // the pairs of this column
+  F2 cs[4], sn[4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int p = 8 * c + i;
-      const bool on = (PAIRED || P.interleaved) && p < P.half;
-      cs[i] = on ? s_cos[p] : 1.0f;
-      sn[i] = on ? s_sin[p] : 0.0f;
-    }
+  for (int i = 0; i < 4; ++i) {
+    float x[2] = {1.0f, 1.0f}, y[2] = {0.0f, 0.0f};
+#pragma unroll
+    for (int n = 0; n < 2; ++n)
+      if (LAYOUT != kFar && any_turn && 2 * i + n < turning) {
+        x[n] = s_cos[8 * c + 2 * i + n];
+        y[n] = s_sin[8 * c + 2 * i + n];
+      }
+    cs[i] = f2(x[0], x[1]);
+    sn[i] = f2(y[0], y[1]);
   }
-  const bool norms = P.q_weight != nullptr || P.k_weight != nullptr;
-  const float *have = nullptr;                       // whose weights w0 and w1 hold
-  const int64_t kv_row = row * P.Hkv * P.D;
+  const bool all_turn = __all_sync(0xffffffffu, turning == 8 || !column);
   const int token = static_cast<int>(pos) & (kSlab - 1);
 
-  for (int hb = h_begin; hb < h_end; hb += hstep) {
-    const int h = hb + hl;
-    const bool on = column && h < h_end;
-    const bool is_q = h < P.nq, is_k = !is_q && h < P.nq + P.nk;
-    fetch(nxt, h + hstep);
-    float x[8], y[8];
+  for (; kind < 3; ++kind) {
+    const int k0 = first_of(kind), kend = min(h_end, kind == 2 ? P.heads : first_of(kind + 1));
+    if (k0 >= h_end) break;
+    const int begin = max(h_begin, k0) - k0, end = kend - k0;        // heads of this kind
+    if (begin >= end) continue;
+    const bool is_q = kind == 0, turns = kind < 2 && any_turn;
+    const bool normed = kind == 0 ? P.q_weight != nullptr : kind == 1 && P.k_weight != nullptr;
+    const bool changed = turns || normed;
+    const T *in = source(kind) + (begin + hl) * P.D;
+    if (max(h_begin, k0) != h_begin) fetch(cur, in, column && begin + hl < end);
+    const float factor = kind == 1 ? P.k_scale : P.v_scale, inverse = kind == 1 ? P.k_inverse : P.v_inverse;
+    const float sixth = kind == 1 ? P.k_sixth : P.v_sixth;
+    const float4 *w4 = reinterpret_cast<const float4 *>(s_weight + (is_q ? 0 : 16 * lanes)) + 2 * c;
+    const int64_t out = is_q ? row * P.Hq * P.D : row * P.Hkv * P.D;
+    T *to = static_cast<T *>(is_q ? P.q_out : kind == 1 ? P.k_out : P.v_out) + out + (begin + hl) * P.D;
+    uint8_t *to8 = static_cast<uint8_t *>(kind == 1 ? P.k_out : P.v_out) + out + (begin + hl) * P.D;
+    uint8_t *page = slab == nullptr ? nullptr
+                                    : slab + (begin + hl) * head_bytes(P.cache) + (kind == 1 ? 0 : slab_v(P.D));
+#pragma unroll 2
+    for (int hb = begin; hb < end; hb += hstep) {
+      const bool on = column && hb + hl < end;
+      in += hstep * P.D;
+      fetch(nxt, in, column && hb + hstep + hl < end);
+      F2 a[4], b[4];
+      if (changed || OUT == kCodes8 || OUT == kPages) split<kSide>(cur, a, b);
+      if (normed) {
+        F2 s = f2_mul(a[0], a[0]);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = y[i] = 0.0f;
-    if (on) cur[0].get(x);
-    if (on && both) cur[1].get(y);
-    if (norms) {
-      float ss = 0.0f;
+        for (int i = 1; i < 4; ++i) s = f2_fma(a[i], a[i], s);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], fmaf(y[i], y[i], ss));
-      for (int o = lanes >> 1; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-      const float *w = is_q ? P.q_weight : is_k ? P.k_weight : nullptr;
-      if (on && w != nullptr) {
-        if (w != have) {
-          have = w;
+        for (int i = 0; i < 4; ++i) s = f2_fma(b[i], b[i], s);
+        float s0, s1;
+        f2_get(s, s0, s1);
+        s0 = on ? s0 + s1 : 0.0f;
+        for (int o = lanes >> 1; o > 0; o >>= 1) s0 += __shfl_xor_sync(0xffffffffu, s0, o);
+        const float r = rsqrtf(fmaf(s0, P.inverse_D, P.eps));
+        const F2 r2 = f2(r, r);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            w0[i] = w[o0 + i] + P.weight_offset;
-            w1[i] = both ? w[o1 + i] + P.weight_offset : 0.0f;
-          }
-        }
-        const float r = 1.0f / sqrtf(ss / static_cast<float>(P.D) + P.eps);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          x[i] = x[i] * r * w0[i];
-          y[i] = y[i] * r * w1[i];
+        for (int x = 0; x < 2; ++x) {
+          const float4 wa = w4[x], wb = w4[2 * lanes + x];
+          a[2 * x] = f2_mul(f2_mul(a[2 * x], r2), f2(wa.x, wa.y));
+          a[2 * x + 1] = f2_mul(f2_mul(a[2 * x + 1], r2), f2(wa.z, wa.w));
+          b[2 * x] = f2_mul(f2_mul(b[2 * x], r2), f2(wb.x, wb.y));
+          b[2 * x + 1] = f2_mul(f2_mul(b[2 * x + 1], r2), f2(wb.z, wb.w));
         }
       }
-    }
-    if constexpr (PAIRED) {
-      if (turn && any_turn && (is_q || is_k)) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float a = x[i], b = y[i];
-          x[i] = a * cs[i] - b * sn[i];
-          y[i] = b * cs[i] + a * sn[i];
-        }
-      }
-    } else if (any_turn) {
-      if (P.interleaved) {
-        if (is_q || is_k) {
-          auto turn4 = [&](float (&z)[8], int first) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float a = z[2 * i], b = z[2 * i + 1];
-              if (8 * c + first + i < P.half) {
-                z[2 * i] = a * cs[first + i] - b * sn[first + i];
-                z[2 * i + 1] = b * cs[first + i] + a * sn[first + i];
-              }
-            }
-          };
-          turn4(x, 0);
-          turn4(y, 4);
-        }
-      } else {                                       // partners through shared memory
+      if (turns && LAYOUT == kFar) {                 // partners through shared memory
+        float x[8], y[8];
+        runs<false>(a, b, x, y);
         float *mine = s_swap + threadIdx.x * kPad, *head = s_swap + (threadIdx.x - c) * kPad;
         __syncwarp();
 #pragma unroll
@@ -217,62 +346,103 @@ __global__ void __launch_bounds__(kNT, 3) norm_rope_kernel(const NormRopeParams 
           mine[8 + i] = y[i];
         }
         __syncwarp();
-        if (is_q || is_k) {
-          auto turned = [&](float own, int e) {
-            if (e >= 2 * P.half) return own;
-            const bool first = e < P.half;
-            const int p = first ? e : e - P.half, o = first ? e + P.half : p;
-            const float other = head[(o >> 4) * kPad + (o & 15)];
-            return first ? own * s_cos[p] - other * s_sin[p] : own * s_cos[p] + other * s_sin[p];
-          };
+        auto turned = [&](float own, int e) {
+          if (e >= 2 * P.half) return own;
+          const bool first = e < P.half;
+          const int p = first ? e : e - P.half, o = first ? e + P.half : p;
+          const float other = head[(o >> 4) * kPad + (o & 15)];
+          return first ? own * s_cos[p] - other * s_sin[p] : own * s_cos[p] + other * s_sin[p];
+        };
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            x[i] = turned(x[i], o0 + i);
-            y[i] = turned(y[i], o1 + i);
+        for (int i = 0; i < 8; ++i) {
+          x[i] = turned(x[i], o0 + i);
+          y[i] = turned(y[i], o1 + i);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          a[i] = f2(x[2 * i], x[2 * i + 1]);
+          b[i] = f2(y[2 * i], y[2 * i + 1]);
+        }
+      } else if (turns) {
+        const F2 minus = f2(-1.0f, -1.0f);
+        if (all_turn) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const F2 x = f2_fma(a[i], cs[i], f2_mul(f2_mul(b[i], minus), sn[i]));
+            b[i] = f2_fma(b[i], cs[i], f2_mul(a[i], sn[i]));
+            a[i] = x;
+          }
+        } else {                                     // (a partner that does not turn is not touched)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            float a0, a1, b0, b1, x0, x1, y0, y1;
+            f2_get(a[i], a0, a1);
+            f2_get(b[i], b0, b1);
+            f2_get(f2_fma(a[i], cs[i], f2_mul(f2_mul(b[i], minus), sn[i])), x0, x1);
+            f2_get(f2_fma(b[i], cs[i], f2_mul(a[i], sn[i])), y0, y1);
+            const bool on0 = 2 * i < turning, on1 = 2 * i + 1 < turning;
+            a[i] = f2(on0 ? x0 : a0, on1 ? x1 : a1);
+            b[i] = f2(on0 ? y0 : b0, on1 ? y1 : b1);
           }
         }
       }
-    }
-    if (OUT == kPages) {                             // (all lanes: shuffles)
-      float m0 = largest(x), m1 = largest(y);
-      const float n0 = __shfl_xor_sync(0xffffffffu, m0, 1), n1 = __shfl_xor_sync(0xffffffffu, m1, 1);
-      const float all = max_nan(m0, m1);
-      m0 = turn ? max_nan(m0, n0) : all;
-      m1 = turn ? max_nan(m1, n1) : all;
-      if (on && !is_q && slab != nullptr) {
-        const int hk = is_k ? h - P.nq : h - P.nq - P.nk;
-        uint8_t *at = slab + hk * head_bytes(P.cache) + (is_k ? 0 : slab_v(P.D));
-        const float factor = is_k ? P.k_scale : P.v_scale;
-        float u0, u1;
-        const uint32_t s0 = scale_code(m0, factor, u0), s1 = scale_code(m1, factor, u1);
-        uint8_t *codes = at + token * (P.D / 2), *scales = at + slab_k_scales(P.D) + token * (P.D / 16);
-        *reinterpret_cast<uint32_t *>(codes + o0 / 2) = codes_of(x, u0);
-        *reinterpret_cast<uint32_t *>(codes + o1 / 2) = codes_of(y, u1);
-        if (!turn || c % 2 == 0) {                   // one lane of those that share 16 elements
-          scales[o0 / 16] = static_cast<uint8_t>(s0);
-          if (turn) scales[o1 / 16] = static_cast<uint8_t>(s1);
+      if (OUT == kPages && !is_q) {                  // (all lanes: shuffles)
+        float m0 = largest(a), m1 = largest(b);
+        const float n0 = __shfl_xor_sync(0xffffffffu, m0, 1), n1 = __shfl_xor_sync(0xffffffffu, m1, 1);
+        const float all = max_nan(m0, m1);
+        m0 = apart ? max_nan(m0, n0) : all;
+        m1 = apart ? max_nan(m1, n1) : all;
+        if (on && page != nullptr) {
+          float u0, u1;
+          const uint32_t s0 = scale_code(m0, sixth, factor, u0);
+          uint8_t *codes = page + token * (P.D / 2), *scales = page + slab_k_scales(P.D) + token * (P.D / 16);
+          if constexpr (kSide) {
+            float x[8], y[8];
+            runs<true>(a, b, x, y);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              a[i] = f2(x[2 * i], x[2 * i + 1]);
+              b[i] = f2(y[2 * i], y[2 * i + 1]);
+            }
+          }
+          if (apart) {
+            const uint32_t s1 = scale_code(m1, sixth, factor, u1);
+            *reinterpret_cast<uint32_t *>(codes + o0 / 2) = codes_of(a, u0, s0);
+            *reinterpret_cast<uint32_t *>(codes + o1 / 2) = codes_of(b, u1, s1);
+            if (c % 2 == 0) {                        // one lane of those that share 16 elements
+              scales[o0 / 16] = static_cast<uint8_t>(s0);
+              scales[o1 / 16] = static_cast<uint8_t>(s1);
+            }
+          } else {
+            *reinterpret_cast<uint2 *>(codes + o0 / 2) = make_uint2(codes_of(a, u0, s0), codes_of(b, u0, s0));
+            scales[o0 / 16] = static_cast<uint8_t>(s0);
+          }
         }
-      }
-    }
-    if (on && (OUT != kPages || is_q)) {
-      if (OUT == kCodes8 && !is_q) {
-        uint8_t *o = static_cast<uint8_t *>(is_k ? P.k_out : P.v_out) + kv_row + (h * P.D - (is_k ? k0 : v0));
-        const float scale = is_k ? P.k_scale : P.v_scale, inverse = is_k ? P.k_inverse : P.v_inverse;
-        store_codes(o + o0, x, scale, inverse);
-        if (both) store_codes(o + o1, y, scale, inverse);
+        page += hstep * head_bytes(P.cache);
+      } else if (OUT == kCodes8 && !is_q) {
+        if (on) {
+          float x[8], y[8];
+          runs<kSide>(a, b, x, y);
+          store_codes(to8 + o0, x, factor, inverse);
+          if (both) store_codes(to8 + o1, y, factor, inverse);
+        }
+        to8 += hstep * P.D;
       } else {
-        T *o = is_q ? static_cast<T *>(P.q_out) + row * P.Hq * P.D + h * P.D
-                    : static_cast<T *>(is_k ? P.k_out : P.v_out) + kv_row + (h * P.D - (is_k ? k0 : v0));
-        if (is_q || is_k) {                          // (v keeps its bits)
-          cur[0].set(x);
-          cur[1].set(y);
+        if (on) {
+          if (changed) {                             // (else the bits stay)
+            float x[8], y[8];
+            runs<kSide>(a, b, x, y);
+            join(cur[0], x);
+            join(cur[1], y);
+          }
+          cur[0].store(to + o0);
+          if (both) cur[1].store(to + o1);
         }
-        cur[0].store(o + o0);
-        if (both) cur[1].store(o + o1);
+        to += hstep * P.D;
       }
+      cur[0] = nxt[0];
+      cur[1] = nxt[1];
     }
-    cur[0] = nxt[0];
-    cur[1] = nxt[1];
   }
 }
 
@@ -289,8 +459,9 @@ struct ReadParams {
   uint32_t *dev_status;
 };
 
-// The threads of a row take 16 elements (8 bytes of codes, one scale) at a time
-// from its K and V heads in turn.
+// A thread takes 8 elements (4 bytes of codes, a scale that two share) at a time from the
+// row's K and V heads, so that a warp writes whole lines, kReads of them under way.
+constexpr int kReads = 4;
 template <typename T>
 __global__ void __launch_bounds__(kNT) kv4_read_kernel(const ReadParams P) {
   const int row_threads = 1 << P.row_shift;
@@ -312,35 +483,51 @@ __global__ void __launch_bounds__(kNT) kv4_read_kernel(const ReadParams P) {
   if (why && t == 0 && blockIdx.y == 0) set_status(P.dev_status, why);
   if (slab == nullptr) return;
   const int token = static_cast<int>(pos) & (kSlab - 1);
-  const int groups = P.D / 16, items = 2 * P.cache.heads * groups;
-  for (int it = blockIdx.y * row_threads + t; it < items; it += gridDim.y * row_threads) {
-    const int part = it / groups, g = it - part * groups;
-    const bool is_v = part >= P.cache.heads;
-    void *out = is_v ? P.v_out : P.k_out;
+  const int shift = P.D == 128 ? 4 : 3;              // log2 of the items of a head
+  const int heads = P.cache.heads, g = t & ((1 << shift) - 1);
+  const int each = row_threads >> shift, step = each * gridDim.y;    // heads at once: of a slice, of all
+  const int64_t head = head_bytes(P.cache);
+  const int scale_at = slab_k_scales(P.D) + token * (P.D / 16) + (g >> 1), code_at = token * (P.D / 2) + 4 * g;
+#pragma unroll
+  for (int is_v = 0; is_v < 2; ++is_v) {
+    T *out = static_cast<T *>(is_v ? P.v_out : P.k_out);
     if (out == nullptr) continue;
-    const int h = is_v ? part - P.cache.heads : part;
-    const uint8_t *at = slab + h * head_bytes(P.cache) + (is_v ? slab_v(P.D) : 0);
-    const uint2 codes = *reinterpret_cast<const uint2 *>(at + token * (P.D / 2) + 8 * g);
-    const float s = e4m3_to_f32(at[slab_k_scales(P.D) + token * groups + g]);
+    const int h0 = blockIdx.y * each + (t >> shift);
     const float factor = is_v ? P.cache.v_scale : P.cache.k_scale;
-    T *o = static_cast<T *>(out) + (row * P.cache.heads + h) * P.D + 16 * g;
+    const float to_scale = is_v ? P.v_scale : P.k_scale, inverse = is_v ? P.v_inverse : P.k_inverse;
+    const uint8_t *at = slab + (is_v ? slab_v(P.D) : 0) + h0 * head;
+    out += (row * heads + h0) * P.D + 8 * g;
+    for (int h = h0; h < heads; h += kReads * step) {
+      uint32_t codes[kReads], scale[kReads];
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      uint32_t pair[4];
-      e2m1x8_to_f16x2(half ? codes.y : codes.x, pair);
-      float x[8];
+      for (int u = 0; u < kReads; ++u)
+        if (h + u * step < heads) {
+          codes[u] = *reinterpret_cast<const uint32_t *>(at + u * step * head + code_at);
+          scale[u] = at[u * step * head + scale_at];
+        }
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float c = f16_bits_to_f32(i % 2 ? pair[i / 2] >> 16 : pair[i / 2] & 0xFFFFu);
-        x[i] = __fmul_rn(__fmul_rn(c, s), factor);   // the first product is exact
+      for (int u = 0; u < kReads; ++u) {
+        if (h + u * step >= heads) continue;
+        uint32_t pair[4];
+        e2m1x8_to_f16x2(codes[u], pair);
+        const uint32_t s = e4m3x2_to_f16x2(scale[u] | scale[u] << 8);
+        float x[8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t y = mul_f16x2(pair[i], s);  // exact
+          x[2 * i] = __fmul_rn(f16_bits_to_f32(y & 0xFFFFu), factor);
+          x[2 * i + 1] = __fmul_rn(f16_bits_to_f32(y >> 16), factor);
+        }
+        if constexpr (sizeof(T) == 1) {
+          store_codes(out + u * step * P.D, x, to_scale, inverse);
+        } else {
+          Vec<T, 8> v;
+          v.set(x);
+          v.store(out + u * step * P.D);
+        }
       }
-      if constexpr (sizeof(T) == 1) {
-        store_codes(o + 8 * half, x, is_v ? P.v_scale : P.k_scale, is_v ? P.v_inverse : P.k_inverse);
-      } else {
-        Vec<T, 8> v;
-        v.set(x);
-        v.store(o + 8 * half);
-      }
+      at += kReads * step * head;
+      out += kReads * step * P.D;
     }
   }
 }
@@ -352,9 +539,10 @@ float exact_inverse(float x) {                       // 1 / x where x is a power
 }
 
 template <typename T, Output OUT>
-cudaError_t launch_layout(bool paired, dim3 grid, size_t smem, cudaStream_t s, const NormRopeParams &P) {
-  return paired ? launch_after_previous(norm_rope_kernel<T, OUT, true>, grid, kNT, smem, s, P)
-                : launch_after_previous(norm_rope_kernel<T, OUT, false>, grid, kNT, smem, s, P);
+cudaError_t launch_layout(Layout layout, dim3 grid, size_t smem, cudaStream_t s, const NormRopeParams &P) {
+  return layout == kPaired       ? launch_after_previous(norm_rope_kernel<T, OUT, kPaired>, grid, kNT, smem, s, P)
+         : layout == kNeighbours ? launch_after_previous(norm_rope_kernel<T, OUT, kNeighbours>, grid, kNT, smem, s, P)
+                                 : launch_after_previous(norm_rope_kernel<T, OUT, kFar>, grid, kNT, smem, s, P);
 }
 
 sv_status check_norm(const sv_norm_args &n, const char *who) {
@@ -386,7 +574,6 @@ sv_status run_rows(const sv_rope_args &a, const sv_norm_args &n, const sv_kv4_ca
   P.Hkv = a.num_kv_heads;
   P.D = a.head_dim;
   P.half = a.turns ? a.rot_dim / 2 : 0;
-  P.interleaved = a.layout == SV_ROPE_INTERLEAVED;
   P.num_rows = a.num_rows;
   P.cu_q = a.cu_q;
   P.kv_len = a.kv_len;
@@ -400,6 +587,7 @@ sv_status run_rows(const sv_rope_args &a, const sv_norm_args &n, const sv_kv4_ca
   P.v_scale = a.v_scale == 0.0f ? 1.0f : a.v_scale;
   P.eps = n.eps;
   P.weight_offset = n.weight_offset;
+  P.inverse_D = 1.0f / static_cast<float>(P.D);
   P.q_weight = n.q_weight;
   P.k_weight = n.k_weight;
   P.turns = a.turns;
@@ -421,16 +609,19 @@ sv_status run_rows(const sv_rope_args &a, const sv_norm_args &n, const sv_kv4_ca
   }
   P.k_inverse = exact_inverse(P.k_scale);
   P.v_inverse = exact_inverse(P.v_scale);
+  P.k_sixth = static_cast<float>(1.0 / (6.0 * P.k_scale));
+  P.v_sixth = static_cast<float>(1.0 / (6.0 * P.v_scale));
   if (P.num_rows == 0 || P.slots == 0 || P.heads == 0) return SV_OK;
   const int sms = device_sms();
   if (sms <= 0) return record_error(SV_ERR_CUDA, "%s: no current CUDA device", who);
 
   while ((16 << P.lane_shift) < P.D) ++P.lane_shift;
-  const bool paired = !P.half || (!P.interleaved && P.half % (cache ? 16 : 8) == 0);
+  const Layout layout = !P.half ? kPaired : a.layout == SV_ROPE_INTERLEAVED ? kNeighbours
+                        : P.half % (cache ? 16 : 8) == 0 ? kPaired : kFar;
   const int64_t threads = (P.slots * P.heads) << P.lane_shift, room = 512 * static_cast<int64_t>(sms);
   P.row_shift = 7;
   if (P.slots > 6 * static_cast<int64_t>(sms))
-    for (P.row_shift = 5; P.row_shift < 7 && (6 << P.row_shift) < (P.heads << P.lane_shift);) ++P.row_shift;
+    for (P.row_shift = 5; P.row_shift < 7 && (12 << P.row_shift) < (P.heads << P.lane_shift);) ++P.row_shift;
   P.pairs = (P.half + 7) / 4 * 4;
   const int at_once = 1 << (P.row_shift - P.lane_shift);
   P.heads_per_cta = static_cast<int>(
@@ -438,17 +629,17 @@ sv_status run_rows(const sv_rope_args &a, const sv_norm_args &n, const sv_kv4_ca
   const int rows_per_cta = kNT >> P.row_shift;
   const dim3 grid(static_cast<unsigned>((P.slots + rows_per_cta - 1) / rows_per_cta),
                   static_cast<unsigned>((P.heads + P.heads_per_cta - 1) / P.heads_per_cta));
-  const size_t smem = static_cast<size_t>(rows_per_cta) * 2 * P.pairs * sizeof(float);
+  const size_t smem = (static_cast<size_t>(rows_per_cta) * 2 * P.pairs + (32u << P.lane_shift)) * sizeof(float);
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e;
   if (a.dtype == SV_BF16)
-    e = cache                     ? launch_layout<uint16_t, kPages>(paired, grid, smem, s, P)
-        : a.kv_dtype == SV_E4M3 ? launch_layout<uint16_t, kCodes8>(paired, grid, smem, s, P)
-                                  : launch_layout<uint16_t, kRows>(paired, grid, smem, s, P);
+    e = cache                     ? launch_layout<uint16_t, kPages>(layout, grid, smem, s, P)
+        : a.kv_dtype == SV_E4M3 ? launch_layout<uint16_t, kCodes8>(layout, grid, smem, s, P)
+                                  : launch_layout<uint16_t, kRows>(layout, grid, smem, s, P);
   else
-    e = cache                     ? launch_layout<float, kPages>(paired, grid, smem, s, P)
-        : a.kv_dtype == SV_E4M3 ? launch_layout<float, kCodes8>(paired, grid, smem, s, P)
-                                  : launch_layout<float, kRows>(paired, grid, smem, s, P);
+    e = cache                     ? launch_layout<float, kPages>(layout, grid, smem, s, P)
+        : a.kv_dtype == SV_E4M3 ? launch_layout<float, kCodes8>(layout, grid, smem, s, P)
+                                  : launch_layout<float, kRows>(layout, grid, smem, s, P);
   if (e != cudaSuccess) return record_error(SV_ERR_CUDA, "%s launch: %s", who, cudaGetErrorString(e));
   return SV_OK;
 }
@@ -575,10 +766,20 @@ SV_API sv_status spec_kv4_read(const sv_kv4_read_args *a, void *stream) {
   P.dev_status = a->dev_status;
   set_slots(P);
   if (P.num_rows == 0 || P.slots == 0 || (!P.k_out && !P.v_out)) return SV_OK;
-  const int items = 2 * P.cache.heads * (P.D / 16);
-  for (P.row_shift = 5; P.row_shift < 8 && (1 << P.row_shift) < items;) ++P.row_shift;
+  // Threads of a row: a warp, which looks the row up once for all heads, where rows are
+  // many; else as many as a pass over K and V takes, in slices of a head per thread.
+  const int sms = device_sms();
+  if (sms <= 0) return record_error(SV_ERR_CUDA, "%s: no current CUDA device", who);
+  const int threads = P.cache.heads * (P.D / 8);     // for one head each
+  P.row_shift = 5;
+  int slices = 1;
+  if (P.slots * threads < int64_t{1024} * sms * kReads) {
+    while (P.row_shift < 7 && (1 << P.row_shift) < threads) ++P.row_shift;
+    slices = (threads + (1 << P.row_shift) - 1) >> P.row_shift;
+  }
   const int rows_per_cta = kNT >> P.row_shift;
-  const dim3 grid(static_cast<unsigned>((P.slots + rows_per_cta - 1) / rows_per_cta));
+  const dim3 grid(static_cast<unsigned>((P.slots + rows_per_cta - 1) / rows_per_cta),
+                  static_cast<unsigned>(slices));
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   const cudaError_t e =
       a->dtype == SV_BF16  ? launch_after_previous(kv4_read_kernel<uint16_t>, grid, kNT, size_t{0}, s, P)
