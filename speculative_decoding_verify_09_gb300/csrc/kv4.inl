@@ -28,20 +28,31 @@ __device__ __forceinline__ int64_t head_bytes(const Kv4View &c) {
   return static_cast<int64_t>(c.slabs) * slab_bytes(c.D);
 }
 
-// The slab of token `pos` (0 .. 2^32 - 1) of sequence i for KV head 0, or nullptr with the
-// problem's bit in *why.
-__device__ __forceinline__ uint8_t *find_slab(const Kv4View &c, int i, int64_t pos, uint32_t *why) {
+// Where token `pos` (0 .. 2^32 - 1) of sequence i is, in two steps: its page is asked for,
+// then its slab (of KV head 0) found: nullptr with the problem's bit in *why.
+struct Kv4Spot {
+  uint32_t slab;                                     // of the page
+  int32_t page;
+  bool in_table;
+};
+__device__ __forceinline__ Kv4Spot find_page(const Kv4View &c, int i, int64_t pos) {
   const uint32_t slab = static_cast<uint32_t>(pos) / kSlab, at = slab / static_cast<uint32_t>(c.slabs);
-  if (at >= static_cast<uint32_t>(c.max_pages)) {
+  Kv4Spot s;
+  s.slab = slab - at * c.slabs;
+  s.in_table = at < static_cast<uint32_t>(c.max_pages);
+  s.page = s.in_table ? c.table[i * c.table_stride + at] : 0;
+  return s;
+}
+__device__ __forceinline__ uint8_t *find_slab(const Kv4View &c, const Kv4Spot &s, uint32_t *why) {
+  if (!s.in_table) {
     *why = SV_DEV_CAPACITY;
     return nullptr;
   }
-  const int32_t page = c.table[i * c.table_stride + at];
-  if (page < 0 || page >= c.num_pages) {
+  if (s.page < 0 || s.page >= c.num_pages) {
     *why = SV_DEV_BAD_PARAM;
     return nullptr;
   }
-  return c.pages + page * (c.heads * head_bytes(c)) + static_cast<int64_t>(slab - at * c.slabs) * slab_bytes(c.D);
+  return c.pages + s.page * (c.heads * head_bytes(c)) + static_cast<int64_t>(s.slab) * slab_bytes(c.D);
 }
 
 // Four bytes of code pairs -> four f16x2 (a byte's lower code in the lower half).

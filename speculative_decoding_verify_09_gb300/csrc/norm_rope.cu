@@ -51,6 +51,39 @@ struct NormRopeParams {
   uint32_t *dev_status;
 };
 
+// The last of the batch's sequences that begins at or before row `slot`, found by a warp
+// in two loads one after the other (a binary search takes one for each bit of the batch).
+__device__ __forceinline__ int search_sequence(const int32_t *cu_q, int batch, int64_t slot) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0, step = (batch + 31) / 32;
+  while (true) {
+    const int at = lo + lane * step;
+    const uint32_t not_behind = __ballot_sync(0xffffffffu, at < batch && cu_q[at] <= slot);
+    lo += not_behind ? (31 - __clz(not_behind)) * step : 0;
+    if (step == 1) return lo;
+    step = (step + 31) / 32;
+  }
+}
+
+// find_row (rows.inl) for a warp whose lanes ask for the same slot.
+template <typename Params>
+__device__ __forceinline__ bool find_row_by_warp(const Params &P, int64_t slot, int64_t &row, int64_t &pos,
+                                                 bool &bad, int &seq) {
+  if (!P.by_row) return find_row(P, slot, row, pos, bad, &seq);
+  bad = false;
+  if (slot >= P.slots) return false;
+  seq = search_sequence(P.cu_q, P.batch, slot);
+  const int r0 = P.cu_q[seq], r1 = P.cu_q[seq + 1], L = P.kv_len[seq], j = static_cast<int>(slot) - r0;
+  if (!good_sequence(P, seq)) {
+    bad = true;
+    return false;
+  }
+  if (j < 0 || j >= r1 - r0) return false;
+  row = slot;
+  pos = static_cast<int64_t>(L) + j;
+  return true;
+}
+
 // Two floats in a register pair, worked on at once.
 typedef unsigned long long F2;
 __device__ __forceinline__ F2 f2(float lo, float hi) {
@@ -185,6 +218,7 @@ constexpr int kCtas = LAYOUT != kFar && sizeof(T) == 2 ? 3 : 2;
 template <typename T, Output OUT, Layout LAYOUT>
 __global__ void __launch_bounds__(kNT, kCtas<T, OUT, LAYOUT>) norm_rope_kernel(const NormRopeParams P) {
   constexpr bool kSide = LAYOUT == kNeighbours;
+  constexpr int kUnroll = OUT == kPages ? 1 : 2;     // (two: nothing is moved from nxt to cur)
   extern __shared__ __align__(16) float s_turn[];    // [rows][cos, sin][pairs], [q, k][16 lanes] weights
   __shared__ float s_swap[LAYOUT == kFar ? kNT * kPad : 1];
   const int row_threads = 1 << P.row_shift, lanes = 1 << P.lane_shift;
@@ -197,8 +231,8 @@ __global__ void __launch_bounds__(kNT, kCtas<T, OUT, LAYOUT>) norm_rope_kernel(c
   int64_t row = 0, pos = 0;
   int seq = 0;
   bool bad;
-  const bool live = find_row(P, static_cast<int64_t>(blockIdx.x) * (kNT >> P.row_shift) + rl, row, pos,
-                             bad, &seq);
+  const bool live = find_row_by_warp(P, static_cast<int64_t>(blockIdx.x) * (kNT >> P.row_shift) + rl, row,
+                                     pos, bad, seq);
   if (bad && t == 0 && blockIdx.y == 0) set_status(P.dev_status, SV_DEV_BAD_LENGTH);
   if (P.by_row && blockIdx.y == 0)                   // (a bad sequence need not be found by a row)
     for (int64_t i = static_cast<int64_t>(blockIdx.x) * kNT + threadIdx.x; i < P.batch;
@@ -211,6 +245,9 @@ __global__ void __launch_bounds__(kNT, kCtas<T, OUT, LAYOUT>) norm_rope_kernel(c
   const int o1 = apart ? o0 + P.half : o0 + 8;
   const bool column = live && o0 < P.D, both = column && o1 < P.D;
   const int turning = LAYOUT == kPaired ? (apart ? 8 : 0) : min(8, max(0, P.half - 8 * c));
+
+  Kv4Spot spot{};
+  if (OUT == kPages && live) spot = find_page(P.cache, seq, pos);
 
   auto fetch = [&](Vec<T, 8> (&v)[2], const T *p, bool on) {
     if (!on) return;
@@ -266,7 +303,7 @@ __global__ void __launch_bounds__(kNT, kCtas<T, OUT, LAYOUT>) norm_rope_kernel(c
   uint8_t *slab = nullptr;                           // of the row's token, KV head 0
   if (OUT == kPages && live) {
     uint32_t why = 0;
-    slab = find_slab(P.cache, seq, pos, &why);
+    slab = find_slab(P.cache, spot, &why);
     if (why && t == 0 && blockIdx.y == 0) set_status(P.dev_status, why);
   }
   __syncthreads();
@@ -305,9 +342,14 @@ __global__ void __launch_bounds__(kNT, kCtas<T, OUT, LAYOUT>) norm_rope_kernel(c
     const int64_t out = is_q ? row * P.Hq * P.D : row * P.Hkv * P.D;
     T *to = static_cast<T *>(is_q ? P.q_out : kind == 1 ? P.k_out : P.v_out) + out + (begin + hl) * P.D;
     uint8_t *to8 = static_cast<uint8_t *>(kind == 1 ? P.k_out : P.v_out) + out + (begin + hl) * P.D;
-    uint8_t *page = slab == nullptr ? nullptr
-                                    : slab + (begin + hl) * head_bytes(P.cache) + (kind == 1 ? 0 : slab_v(P.D));
-#pragma unroll 2
+    const int64_t next_head = OUT == kPages ? hstep * head_bytes(P.cache) : 0;
+    uint8_t *codes = nullptr, *scales = nullptr;     // of this lane's elements from o0 on
+    if (OUT == kPages && !is_q && slab != nullptr) {
+      uint8_t *page = slab + (begin + hl) * head_bytes(P.cache) + (kind == 1 ? 0 : slab_v(P.D));
+      codes = page + token * (P.D / 2) + o0 / 2;
+      scales = page + slab_k_scales(P.D) + token * (P.D / 16) + o0 / 16;
+    }
+#pragma unroll kUnroll
     for (int hb = begin; hb < end; hb += hstep) {
       const bool on = column && hb + hl < end;
       in += hstep * P.D;
@@ -392,10 +434,9 @@ __global__ void __launch_bounds__(kNT, kCtas<T, OUT, LAYOUT>) norm_rope_kernel(c
         const float all = max_nan(m0, m1);
         m0 = apart ? max_nan(m0, n0) : all;
         m1 = apart ? max_nan(m1, n1) : all;
-        if (on && page != nullptr) {
-          float u0, u1;
+        if (on && slab != nullptr) {
+          float u0;
           const uint32_t s0 = scale_code(m0, sixth, factor, u0);
-          uint8_t *codes = page + token * (P.D / 2), *scales = page + slab_k_scales(P.D) + token * (P.D / 16);
           if constexpr (kSide) {
             float x[8], y[8];
             runs<true>(a, b, x, y);
@@ -406,19 +447,21 @@ __global__ void __launch_bounds__(kNT, kCtas<T, OUT, LAYOUT>) norm_rope_kernel(c
             }
           }
           if (apart) {
+            float u1;
             const uint32_t s1 = scale_code(m1, sixth, factor, u1);
-            *reinterpret_cast<uint32_t *>(codes + o0 / 2) = codes_of(a, u0, s0);
-            *reinterpret_cast<uint32_t *>(codes + o1 / 2) = codes_of(b, u1, s1);
+            *reinterpret_cast<uint32_t *>(codes) = codes_of(a, u0, s0);
+            *reinterpret_cast<uint32_t *>(codes + P.half / 2) = codes_of(b, u1, s1);
             if (c % 2 == 0) {                        // one lane of those that share 16 elements
-              scales[o0 / 16] = static_cast<uint8_t>(s0);
-              scales[o1 / 16] = static_cast<uint8_t>(s1);
+              *scales = static_cast<uint8_t>(s0);
+              scales[P.half / 16] = static_cast<uint8_t>(s1);
             }
           } else {
-            *reinterpret_cast<uint2 *>(codes + o0 / 2) = make_uint2(codes_of(a, u0, s0), codes_of(b, u0, s0));
-            scales[o0 / 16] = static_cast<uint8_t>(s0);
+            *reinterpret_cast<uint2 *>(codes) = make_uint2(codes_of(a, u0, s0), codes_of(b, u0, s0));
+            *scales = static_cast<uint8_t>(s0);
           }
         }
-        page += hstep * head_bytes(P.cache);
+        codes += next_head;
+        scales += next_head;
       } else if (OUT == kCodes8 && !is_q) {
         if (on) {
           float x[8], y[8];
@@ -470,8 +513,8 @@ __global__ void __launch_bounds__(kNT) kv4_read_kernel(const ReadParams P) {
   int64_t row = 0, pos = 0;
   int seq = 0;
   bool bad;
-  const bool live = find_row(P, static_cast<int64_t>(blockIdx.x) * (kNT >> P.row_shift) + rl, row, pos,
-                             bad, &seq);
+  const bool live = find_row_by_warp(P, static_cast<int64_t>(blockIdx.x) * (kNT >> P.row_shift) + rl, row,
+                                     pos, bad, seq);
   if (bad && t == 0 && blockIdx.y == 0) set_status(P.dev_status, SV_DEV_BAD_LENGTH);
   if (P.by_row && blockIdx.y == 0)
     for (int64_t i = static_cast<int64_t>(blockIdx.x) * kNT + threadIdx.x; i < P.batch;
@@ -479,7 +522,7 @@ __global__ void __launch_bounds__(kNT) kv4_read_kernel(const ReadParams P) {
       if (!good_sequence(P, static_cast<int>(i))) set_status(P.dev_status, SV_DEV_BAD_LENGTH);
   if (!live) return;
   uint32_t why = 0;
-  const uint8_t *slab = find_slab(P.cache, seq, pos, &why);
+  const uint8_t *slab = find_slab(P.cache, find_page(P.cache, seq, pos), &why);
   if (why && t == 0 && blockIdx.y == 0) set_status(P.dev_status, why);
   if (slab == nullptr) return;
   const int token = static_cast<int>(pos) & (kSlab - 1);
@@ -620,7 +663,7 @@ sv_status run_rows(const sv_rope_args &a, const sv_norm_args &n, const sv_kv4_ca
                         : P.half % (cache ? 16 : 8) == 0 ? kPaired : kFar;
   const int64_t threads = (P.slots * P.heads) << P.lane_shift, room = 512 * static_cast<int64_t>(sms);
   P.row_shift = 7;
-  if (P.slots > 6 * static_cast<int64_t>(sms))
+  if (P.slots > 2 * static_cast<int64_t>(sms))
     for (P.row_shift = 5; P.row_shift < 7 && (12 << P.row_shift) < (P.heads << P.lane_shift);) ++P.row_shift;
   P.pairs = (P.half + 7) / 4 * 4;
   const int at_once = 1 << (P.row_shift - P.lane_shift);
