@@ -224,7 +224,10 @@ __global__ void __launch_bounds__(Shape<D, NB>::kThreads, 1) kv4_attn_kernel(con
   // units go to the warps in runs of equal length.
   const int ctas = max(1, min(static_cast<int>(gridDim.x), total / P.least)), b = blockIdx.x;
   if (b >= ctas) return;
-  for (int x = tid; x <= ctas; x += NT) {
+  // (a warp's lanes 0 and 1 find its own share's ends, the others part of the table for later)
+  int u0, u1;
+  {
+    const int x = min(ctas, l < 2 ? b + l : 30 * w + l - 2);
     const int each = total / ctas, v = each * x + (total - each * ctas) * x / ctas;
     int to = v;
     if (v > 0 && v < total) {
@@ -232,9 +235,11 @@ __global__ void __launch_bounds__(Shape<D, NB>::kThreads, 1) kv4_attn_kernel(con
       const int after = kHead + p.tiles - p.at;
       to = p.at <= min(after, kSnap) ? v - p.at : after <= kSnap ? v + after : v;
     }
-    s_share[x] = to;
+    if (l >= 2) s_share[x] = to;
+    u0 = __shfl_sync(0xffffffffu, to, 0);
+    u1 = __shfl_sync(0xffffffffu, to, 1);
   }
-  __syncthreads();
+  static_assert(30 * W > kMaxCtas, "a table entry per lane");
   auto cta_of = [&](int v) {                         // the last share that starts at or before v
     int lo = 0, hi = ctas;
     while (hi - lo > 1) {
@@ -243,41 +248,56 @@ __global__ void __launch_bounds__(Shape<D, NB>::kThreads, 1) kv4_attn_kernel(con
     }
     return lo;
   };
-  const int u0 = s_share[b], u1 = s_share[b + 1];
   const int v0 = u0 + (u1 - u0) * w / W, v1 = u0 + (u1 - u0) * (w + 1) / W;
 
-  // ---- this warp's copies: a lane finds the slabs of each of the next 32 units
+  // ---- this warp's copies: a lane finds the slabs of each of the next 32 units, in two steps
+  // (their pages asked for, their addresses)
   const uint8_t *from0 = nullptr, *from1 = nullptr;  // slabs of this lane's tile (nullptr: not copied)
   bool from_bad = false, any_bad = false;            // pages outside the pool; any so far
   uint32_t open = 0;                                 // of these units: tiles not yet asked for
   int looked = v0;                                   // units looked at
   int issued = 0, taken = 0;                         // tiles asked for, and used
+  Place ahead{0, 0, 0, 0};                           // this lane's unit, and the sequence it is of
+  Sequence ahead_s{0, 0, 0, 0};
+  int32_t page0 = 0, page1 = 0;                      // pages of the tile's slabs 2 n and 2 n + 1
+  uint32_t slab0 = 0;                                // the first one's place in its page
+  bool second = false;
   auto look_up = [&]() {
     const int v = looked + l;
+    ahead = Place{0, 0, 0, 0};
+    ahead_s = Sequence{0, 0, 0, 0};
+    page0 = page1 = 0;
+    slab0 = 0;
+    second = false;
+    if (v < v1) {
+      ahead = locate(v);
+      uint32_t why = 0;
+      ahead_s = sequence_of(P, ahead.i, &why);
+      if (ahead.at >= kHead) {
+        const uint32_t n = 2u * static_cast<uint32_t>(ahead.at - kHead), per = P.cache.slabs, at0 = n / per;
+        slab0 = n - at0 * per;
+        second = static_cast<int>(n + 1) * kSlab < ahead_s.keys;
+        const int32_t *row = P.cache.table + ahead.i * P.cache.table_stride + at0;
+        page0 = row[0];
+        page1 = slab0 + 1 == per && second ? row[1] : page0;
+      }
+    }
+  };
+  auto look_up_done = [&]() {
+    const bool real = looked + l < v1 && ahead.at >= kHead;
     from0 = from1 = nullptr;
     from_bad = false;
-    bool real = false;
-    if (v < v1) {
-      const Place p = locate(v);
-      real = p.at >= kHead;
-      if (real) {
-        // the slabs 2 n and 2 n + 1 of the sequence, of one page or of two neighbours
-        const uint32_t n = 2u * static_cast<uint32_t>(p.at - kHead), per = P.cache.slabs;
-        const uint32_t at0 = n / per, in0 = n - at0 * per;
-        const bool same = in0 + 1 < per;
-        const int32_t *row = P.cache.table + p.i * P.cache.table_stride;
-        const int keys = P.kv_len[p.i] + P.cu_q[p.i + 1] - P.cu_q[p.i];
-        const bool second = static_cast<int>(n + 1) * kSlab < keys;
-        const int32_t page0 = row[at0], page1 = same || !second ? page0 : row[at0 + 1];
-        const int64_t head = static_cast<int64_t>(p.unit / s_parts[p.i]) * head_bytes(P.cache);
-        const int64_t page_bytes = P.cache.heads * head_bytes(P.cache);
-        if (page0 < 0 || page0 >= P.cache.num_pages || page1 < 0 || page1 >= P.cache.num_pages) {
-          set_status(P.dev_status, SV_DEV_BAD_PARAM);
-          from_bad = true;
-        } else {
-          from0 = P.cache.pages + page0 * page_bytes + head + static_cast<int64_t>(in0) * SLAB;
-          if (second) from1 = same ? from0 + SLAB : P.cache.pages + page1 * page_bytes + head;
-        }
+    if (real) {
+      const int64_t head = static_cast<int64_t>(ahead.unit / s_parts[ahead.i]) * head_bytes(P.cache);
+      const int64_t page_bytes = P.cache.heads * head_bytes(P.cache);
+      if (page0 < 0 || page0 >= P.cache.num_pages || page1 < 0 || page1 >= P.cache.num_pages) {
+        set_status(P.dev_status, SV_DEV_BAD_PARAM);
+        from_bad = true;
+      } else {
+        from0 = P.cache.pages + page0 * page_bytes + head + static_cast<int64_t>(slab0) * SLAB;
+        if (second)
+          from1 = slab0 + 1 < static_cast<uint32_t>(P.cache.slabs) ? from0 + SLAB
+                                                                   : P.cache.pages + page1 * page_bytes + head;
       }
     }
     open = __ballot_sync(0xffffffffu, real);
@@ -289,6 +309,7 @@ __global__ void __launch_bounds__(Shape<D, NB>::kThreads, 1) kv4_attn_kernel(con
     while (open == 0) {
       if (looked >= v1) return;
       look_up();
+      look_up_done();
     }
     const int st = issued % S;
     if (l == __ffs(open) - 1) {
@@ -307,16 +328,11 @@ __global__ void __launch_bounds__(Shape<D, NB>::kThreads, 1) kv4_attn_kernel(con
   };
   // the segment of list entry v, and this lane's part of its rows of q
   struct Segment { Place p; Sequence s; int h, part, rows; };
-  auto segment_of = [&](int v) {
-    Segment x;
-    x.p = locate(v);
+  auto complete = [&](Segment &x) {
     const int parts = s_parts[x.p.i];
     x.h = x.p.unit / parts;
     x.part = x.p.unit - x.h * parts;
-    uint32_t why = 0;
-    x.s = sequence_of(P, x.p.i, &why);
     x.rows = min(ROWS, x.s.R * P.g - x.part * ROWS);
-    return x;
   };
   auto token_row = [&](int row) {                    // of the block, of packed row `row`
     return P.g_inverse ? static_cast<int>(__umulhi(static_cast<uint32_t>(row), P.g_inverse)) : row;
@@ -325,12 +341,37 @@ __global__ void __launch_bounds__(Shape<D, NB>::kThreads, 1) kv4_attn_kernel(con
     const int row = x.part * ROWS + n, j = token_row(row), hh = row - j * P.g;
     return P.q + (x.s.r0 + j) * P.q_stride + static_cast<int64_t>(x.h * P.g + hh) * D + c * (D / 4);
   };
-  issue();
+  uint4 q[NB][WORDS];
+  auto fetch_q = [&](const Segment &x) {
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
+      const uint4 *src = reinterpret_cast<const uint4 *>(q_row(x, 8 * nb + r));
+#pragma unroll
+      for (int y = 0; y < WORDS; ++y) q[nb][y] = 8 * nb + r < x.rows ? src[y] : make_uint4(0, 0, 0, 0);
+    }
+  };
   bool dead = false;                                 // a wait ran out: nothing more is asked for
 
   for (int v = v0; v < v1;) {
     // ---- a segment's tiles in this run
-    const Segment here = segment_of(v);
+    Segment here;
+    if (v == v0) {                                   // the first unit is lane 0's; q before the copies
+      look_up();
+      here.p = Place{__shfl_sync(0xffffffffu, ahead.i, 0), __shfl_sync(0xffffffffu, ahead.unit, 0),
+                     __shfl_sync(0xffffffffu, ahead.at, 0), __shfl_sync(0xffffffffu, ahead.tiles, 0)};
+      here.s = Sequence{__shfl_sync(0xffffffffu, ahead_s.r0, 0), __shfl_sync(0xffffffffu, ahead_s.R, 0),
+                        __shfl_sync(0xffffffffu, ahead_s.L, 0), __shfl_sync(0xffffffffu, ahead_s.keys, 0)};
+      complete(here);
+      fetch_q(here);
+      look_up_done();
+      for (int x = 0; x < S; ++x) issue();
+    } else {
+      here.p = locate(v);
+      uint32_t why = 0;
+      here.s = sequence_of(P, here.p.i, &why);
+      complete(here);
+      fetch_q(here);
+    }
     const Place p = here.p;
     const Sequence s = here.s;
     const int h = here.h, rows = here.rows, first_row = here.part * ROWS;   // of the block's R * g rows
@@ -340,27 +381,16 @@ __global__ void __launch_bounds__(Shape<D, NB>::kThreads, 1) kv4_attn_kernel(con
     v = end;
     if (tile1 <= tile0) continue;
 
-    // (the run's first rows of q are asked for behind one tile, not behind all of the ring)
     uint32_t qf[NB][STEPS][2];
-    {
-      uint4 q[NB][WORDS];
 #pragma unroll
-      for (int nb = 0; nb < NB; ++nb) {
-        const uint4 *src = reinterpret_cast<const uint4 *>(q_row(here, 8 * nb + r));
+    for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-        for (int x = 0; x < WORDS; ++x) q[nb][x] = 8 * nb + r < rows ? src[x] : make_uint4(0, 0, 0, 0);
+      for (int x = 0; x < WORDS; ++x) {
+        qf[nb][2 * x][0] = bf16x2_to_f16x2(q[nb][x].x);
+        qf[nb][2 * x][1] = bf16x2_to_f16x2(q[nb][x].y);
+        qf[nb][2 * x + 1][0] = bf16x2_to_f16x2(q[nb][x].z);
+        qf[nb][2 * x + 1][1] = bf16x2_to_f16x2(q[nb][x].w);
       }
-      for (int x = issued - taken; x < S; ++x) issue();
-#pragma unroll
-      for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-        for (int x = 0; x < WORDS; ++x) {
-          qf[nb][2 * x][0] = bf16x2_to_f16x2(q[nb][x].x);
-          qf[nb][2 * x][1] = bf16x2_to_f16x2(q[nb][x].y);
-          qf[nb][2 * x + 1][0] = bf16x2_to_f16x2(q[nb][x].z);
-          qf[nb][2 * x + 1][1] = bf16x2_to_f16x2(q[nb][x].w);
-        }
-    }
     int lim[NB][2];                                  // the last token that this lane's columns see
     float m[NB][2], mu[NB][2], sum[NB][2], o[MT][NB][4];
 #pragma unroll
@@ -685,8 +715,6 @@ __global__ void __launch_bounds__(Shape<D, NB>::kThreads, 1) kv4_attn_kernel(con
   }
   __syncthreads();
   struct __align__(8) Some { float x[E]; };
-  float *s_weight = reinterpret_cast<float *>(smem);                 // [ROWS, CTAs of the segment]
-  float *s_sum = s_weight + ROWS * kMaxCtas;                         // [W, D]
   for (int which = 0; which < passing; ++which) {
     if (!s_last[which]) continue;
     const Piece head = s_piece[which == 0 ? open0 : open1];
@@ -702,7 +730,41 @@ __global__ void __launch_bounds__(Shape<D, NB>::kThreads, 1) kv4_attn_kernel(con
       }
       return v;
     };
-    // weights of the pieces: a warp per row, a lane per piece
+    if (count <= 32) {
+      // A warp per row, (up to three) side by side, a lane per piece for the weights; the first
+      // pieces' sums are under way meanwhile.
+      constexpr int kSide = (ROWS + W - 1) / W, kFirst = kSide == 1 ? 4 : 2;
+      float2 ml[kSide];
+      Some v[kSide][kFirst];
+#pragma unroll
+      for (int z = 0; z < kSide; ++z) {
+        const int n = w + z * W;
+        ml[z] = n < head.rows && l < count ? __ldcg(&P.part_ml[place_of(l, n)]) : make_float2(-INFINITY, 0.0f);
+#pragma unroll
+        for (int y = 0; y < kFirst; ++y)
+          if (n < head.rows && y < count) v[z][y] = part(y, n);
+      }
+#pragma unroll
+      for (int z = 0; z < kSide; ++z) {
+        const int n = w + z * W;
+        if (n >= head.rows) continue;
+        const float top = warp_max(ml[z].x), base = top == -INFINITY ? 0.0f : top;
+        float f = fast_exp2(ml[z].x - base);
+        f *= P.cache.v_scale / warp_sum(f * ml[z].y);
+        float x[E] = {};
+#pragma unroll
+        for (int y = 0; y < kFirst; ++y)
+          if (y < count) add(x, __shfl_sync(0xffffffffu, f, y), v[z][y].x);
+#pragma unroll 4
+        for (int y = kFirst; y < count; ++y) add(x, __shfl_sync(0xffffffffu, f, y), part(y, n).x);
+        store_row(head, n, x, P.cache.v_scale);      // (the weights hold the scale)
+      }
+      continue;
+    }
+    // Pieces of many CTAs: weights in shared memory, a warp per row, then sums by several warps
+    // for each row, which take the pieces in turn.
+    float *s_weight = reinterpret_cast<float *>(smem);               // [ROWS, CTAs of the segment]
+    float *s_sum = s_weight + ROWS * kMaxCtas;                       // [W, D]
     for (int n = w; n < head.rows; n += W) {
       float top = -INFINITY, all = 0.0f;
       for (int x = l; x < count; x += 32) top = fmaxf(top, __ldcg(&P.part_ml[place_of(x, n)]).x);
@@ -717,43 +779,25 @@ __global__ void __launch_bounds__(Shape<D, NB>::kThreads, 1) kv4_attn_kernel(con
       const float f = P.cache.v_scale / warp_sum(all);
       for (int x = l; x < count; x += 32) s_weight[n * kMaxCtas + x] *= f;
     }
-    // Sums: few rows of many pieces by several warps each, which take the pieces in turn; else
-    // a warp's (up to three) rows side by side.
-    const int share = count > 16 ? max(1, W / head.rows) : 1;
-    if (share > 1) {
-      __syncthreads();
-      const int n = w / share, sub = w % share;
+    __syncthreads();
+    const int share = max(1, W / head.rows), sub = w % share;
+    for (int n0 = 0; n0 < head.rows; n0 += W / share) {
+      const int n = n0 + w / share;
+      const bool on = n < head.rows && w / share < W / share;
       float x[E] = {};
-      if (n < head.rows) {
+      if (on) {
 #pragma unroll 4
         for (int y = sub; y < count; y += share) add(x, s_weight[n * kMaxCtas + y], part(y, n).x);
       }
 #pragma unroll
       for (int z = 0; z < E; ++z) s_sum[w * D + E * l + z] = x[z];
       __syncthreads();
-      if (n < head.rows && sub == 0) {
+      if (on && sub == 0) {
         for (int y = 1; y < share; ++y) add(x, 1.0f, s_sum + (w + y) * D + E * l);
-        store_row(head, n, x, P.cache.v_scale);      // (the weights hold the scale)
+        store_row(head, n, x, P.cache.v_scale);
       }
-    } else {
-      __syncwarp();
-      constexpr int kSide = (ROWS + W - 1) / W;
-      float x[kSide][E] = {};
-#pragma unroll 2
-      for (int y = 0; y < count; ++y) {
-        Some v[kSide];
-#pragma unroll
-        for (int z = 0; z < kSide; ++z)
-          if (w + z * W < head.rows) v[z] = part(y, w + z * W);
-#pragma unroll
-        for (int z = 0; z < kSide; ++z)
-          if (w + z * W < head.rows) add(x[z], s_weight[(w + z * W) * kMaxCtas + y], v[z].x);
-      }
-#pragma unroll
-      for (int z = 0; z < kSide; ++z)
-        if (w + z * W < head.rows) store_row(head, w + z * W, x[z], P.cache.v_scale);
+      __syncthreads();
     }
-    __syncthreads();                                 // (the weights of the next segment)
   }
 }
 
