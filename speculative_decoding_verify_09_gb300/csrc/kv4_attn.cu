@@ -26,6 +26,7 @@
 // the sums are rescaled seldom.
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "kv4.inl"
 #include "ops_host.inl"
@@ -35,11 +36,12 @@ namespace sv {
 namespace {
 
 constexpr int kTile = 32;                            // tokens
-constexpr int kMaxBatch = 2048;
+constexpr int kMaxBatch = 1024;
 constexpr int kMaxCtas = 192;                        // (sizes the workspace on any host)
 constexpr int kCounters = 65536;                     // first in the workspace, whatever the shape
 constexpr int kHead = 2;                             // units that a segment costs beside its tiles
-constexpr int kSnap = 16;                            // units that a CTA's share may end early or late
+constexpr int kLeast = 4;                            // units of a CTA's share
+constexpr int kSnap = 8;                             // units that a CTA's share may end early or late
 constexpr float kLate = 8.0f;                        // log2 the maximum may grow before sums are rescaled
 
 // Warps and stages of a warp's ring; NB: 8-row columns of a part.
@@ -63,9 +65,9 @@ struct Shape {
 struct Kv4AttnParams {
   Kv4View cache;
   int batch, Hq, g, max_q_rows, parts;               // parts: of max_q_rows * g rows
+  int slab_shift;                                    // log2 of a page's slabs, or -1
   uint32_t g_inverse;                                // 2^32 / g rounded up: exact quotients of rows
                                                      // below 2^32 / g; 0: g is 1
-  int least;                                         // units of a run
   int64_t num_rows, q_stride;
   float scale_log2;                                  // of a score, k_scale and log2 e in it
   const int32_t *cu_q, *kv_len;
@@ -151,7 +153,8 @@ __global__ void __launch_bounds__(Shape<D, NB>::kThreads, 1) kv4_attn_kernel(con
   extern __shared__ __align__(128) uint8_t smem[];
   float2 *s_ml = reinterpret_cast<float2 *>(smem + Sh::kRing + Sh::kSlots);  // [2 W, ROWS] maximum, sum
   int32_t *s_start = reinterpret_cast<int32_t *>(smem + Sh::kFixed);         // [batch + 1]
-  uint8_t *s_parts = reinterpret_cast<uint8_t *>(s_start + P.batch + 1);     // [batch]
+  int32_t *s_each = s_start + P.batch + 1;           // [batch] units of one of its segments
+  uint8_t *s_parts = reinterpret_cast<uint8_t *>(s_each + P.batch);          // [batch]
   __shared__ __align__(8) uint64_t s_bar[W * S];
   __shared__ uint8_t s_bad[W * S];
   __shared__ Piece s_piece[2 * W];
@@ -175,7 +178,8 @@ __global__ void __launch_bounds__(Shape<D, NB>::kThreads, 1) kv4_attn_kernel(con
       if (why && blockIdx.x == 0) set_status(P.dev_status, why);
       const int parts = (s.R * P.g + ROWS - 1) / ROWS;
       s_parts[i] = static_cast<uint8_t>(parts);
-      const int n = ((s.keys + kTile - 1) / kTile + kHead) * parts * heads;
+      const int one = (s.keys + kTile - 1) / kTile + kHead, n = one * parts * heads;
+      s_each[i] = one;
       s_start[i] = n;
       mine += n;
     }
@@ -212,9 +216,12 @@ __global__ void __launch_bounds__(Shape<D, NB>::kThreads, 1) kv4_attn_kernel(con
     }
     Place p;
     p.i = lo;
-    const int each = (s_start[lo + 1] - s_start[lo]) / (heads * s_parts[lo]), rem = v - s_start[lo];
-    p.unit = rem / each;
+    const int each = s_each[lo], rem = v - s_start[lo];
+    // (a quotient below 2^17: by floats it is off by one at most)
+    p.unit = static_cast<int>(__fdividef(static_cast<float>(rem), static_cast<float>(each)));
     p.at = rem - p.unit * each;
+    if (p.at < 0) --p.unit, p.at += each;
+    if (p.at >= each) ++p.unit, p.at -= each;
     p.tiles = each - kHead;
     return p;
   };
@@ -222,13 +229,13 @@ __global__ void __launch_bounds__(Shape<D, NB>::kThreads, 1) kv4_attn_kernel(con
   // The CTAs' shares: equal, but for ends that come within kSnap of a segment's, which are
   // moved there (a cut there would cost the joining of two CTAs' pieces); a share's
   // units go to the warps in runs of equal length.
-  const int ctas = max(1, min(static_cast<int>(gridDim.x), total / P.least)), b = blockIdx.x;
+  const int ctas = max(1, min(static_cast<int>(gridDim.x), total / kLeast)), b = blockIdx.x;
   if (b >= ctas) return;
   // (a warp's lanes 0 and 1 find its own share's ends, the others part of the table for later)
   int u0, u1;
   {
     const int x = min(ctas, l < 2 ? b + l : 30 * w + l - 2);
-    const int each = total / ctas, v = each * x + (total - each * ctas) * x / ctas;
+    const int each = total / ctas, v = each * x + min(x, total - each * ctas);
     int to = v;
     if (v > 0 && v < total) {
       const Place p = locate(v);
@@ -274,7 +281,8 @@ __global__ void __launch_bounds__(Shape<D, NB>::kThreads, 1) kv4_attn_kernel(con
       uint32_t why = 0;
       ahead_s = sequence_of(P, ahead.i, &why);
       if (ahead.at >= kHead) {
-        const uint32_t n = 2u * static_cast<uint32_t>(ahead.at - kHead), per = P.cache.slabs, at0 = n / per;
+        const uint32_t n = 2u * static_cast<uint32_t>(ahead.at - kHead), per = P.cache.slabs;
+        const uint32_t at0 = P.slab_shift >= 0 ? n >> P.slab_shift : n / per;
         slab0 = n - at0 * per;
         second = static_cast<int>(n + 1) * kSlab < ahead_s.keys;
         const int32_t *row = P.cache.table + ahead.i * P.cache.table_stride + at0;
@@ -288,7 +296,8 @@ __global__ void __launch_bounds__(Shape<D, NB>::kThreads, 1) kv4_attn_kernel(con
     from0 = from1 = nullptr;
     from_bad = false;
     if (real) {
-      const int64_t head = static_cast<int64_t>(ahead.unit / s_parts[ahead.i]) * head_bytes(P.cache);
+      const int parts = s_parts[ahead.i];
+      const int64_t head = (parts == 1 ? ahead.unit : ahead.unit / parts) * head_bytes(P.cache);
       const int64_t page_bytes = P.cache.heads * head_bytes(P.cache);
       if (page0 < 0 || page0 >= P.cache.num_pages || page1 < 0 || page1 >= P.cache.num_pages) {
         set_status(P.dev_status, SV_DEV_BAD_PARAM);
@@ -330,7 +339,7 @@ __global__ void __launch_bounds__(Shape<D, NB>::kThreads, 1) kv4_attn_kernel(con
   struct Segment { Place p; Sequence s; int h, part, rows; };
   auto complete = [&](Segment &x) {
     const int parts = s_parts[x.p.i];
-    x.h = x.p.unit / parts;
+    x.h = parts == 1 ? x.p.unit : x.p.unit / parts;
     x.part = x.p.unit - x.h * parts;
     x.rows = min(ROWS, x.s.R * P.g - x.part * ROWS);
   };
@@ -405,178 +414,189 @@ __global__ void __launch_bounds__(Shape<D, NB>::kThreads, 1) kv4_attn_kernel(con
       for (int x = 0; x < MT; ++x) o[x][nb][0] = o[x][nb][1] = o[x][nb][2] = o[x][nb][3] = 0.0f;
     }
     int nan_from = 0x7fffffff;                       // block token whose V has NaN in this lane's elements
-    for (int tile = tile0; tile < tile1; ++tile, ++taken) {
-      const int st = taken % S;
-      if (!dead &&
-          !__all_sync(0xffffffffu, bar_wait(smem_u32(&s_bar[w * S + st]), (taken / S) & 1, P.spin_limit))) {
-        dead = true;
-        if (l == 0) set_status(P.dev_status, SV_DEV_TIMEOUT);
-        for (int x = taken; x < issued; ++x)         // copies in flight write this CTA's memory
-          bar_wait(smem_u32(&s_bar[w * S + x % S]), (x / S) & 1, 1u << 22);
-      }
-      if (dead || (any_bad && s_bad[w * S + st])) {
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb) sum[nb][0] = sum[nb][1] = NAN;
-        __syncwarp();
-        if (!dead) issue();
-        continue;
-      }
-      const uint8_t *stage = ring + st * Sh::kTileBytes;
-      const int key0 = tile * kTile;
-      const bool edge = key0 + kTile - 1 > s.L;      // tokens that some row does not see
-      if (edge) {
-        // Tokens behind the last hold anything: V's scales there become 0.  So do a block token's
-        // that are NaN, to keep them from the rows before it (a weight of 0 would not do that);
-        // the rows that see it get their NaN at the end.  A lane takes a token.
-        const int key = key0 + l;
-        uint8_t *scales = ring + st * Sh::kTileBytes + (l >> 4) * SLAB + slab_v(D) + 8 * D + (l & 15) * (D / 16);
-#pragma unroll
-        for (int x = 0; x < D / 16; ++x) {
-          const bool nan = key > s.L && key < s.keys && (scales[x] & 0x7Fu) == 0x7Fu;
-          if (nan || key >= s.keys) scales[x] = 0;
-          const uint32_t who = __ballot_sync(0xffffffffu, nan);
-          if (who != 0 && x == (D == 128 ? r : r >> 1)) nan_from = min(nan_from, key0 + __ffs(who) - 1);
+    // (columns that have no rows are not computed)
+    auto run_tiles = [&](auto columns) {
+      constexpr int NC = decltype(columns)::value;
+      for (int tile = tile0; tile < tile1; ++tile, ++taken) {
+        const int st = taken % S;
+        if (!dead &&
+            !__all_sync(0xffffffffu, bar_wait(smem_u32(&s_bar[w * S + st]), (taken / S) & 1, P.spin_limit))) {
+          dead = true;
+          if (l == 0) set_status(P.dev_status, SV_DEV_TIMEOUT);
+          for (int x = taken; x < issued; ++x)         // copies in flight write this CTA's memory
+            bar_wait(smem_u32(&s_bar[w * S + x % S]), (x / S) & 1, 1u << 22);
         }
-        asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
-        __syncwarp();
-      }
-
-      // ---- S^T = K q^T
-      float sc[2][NB][4];
+        if (dead || (any_bad && s_bad[w * S + st])) {
 #pragma unroll
-      for (int sl = 0; sl < 2; ++sl) {
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb) sc[sl][nb][0] = sc[sl][nb][1] = sc[sl][nb][2] = sc[sl][nb][3] = 0.0f;
-        const uint8_t *slab = stage + sl * SLAB;
-        const int ka = token_of(r), kb = ka + 8;
-        uint32_t wa[WORDS], wb[WORDS], fa[2], fb[2]; // codes of two tokens; scales, twice each
-        if constexpr (D == 128) {
-          const uint4 x = *reinterpret_cast<const uint4 *>(slab + ka * 64 + c * 16);
-          const uint4 y = *reinterpret_cast<const uint4 *>(slab + kb * 64 + c * 16);
-          wa[0] = x.x, wa[1] = x.y, wa[2] = x.z, wa[3] = x.w;
-          wb[0] = y.x, wb[1] = y.y, wb[2] = y.z, wb[3] = y.w;
-          const uint32_t sa = e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t *>(slab + slab_k_scales(D) + ka * 8 + c * 2));
-          const uint32_t sb = e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t *>(slab + slab_k_scales(D) + kb * 8 + c * 2));
-          fa[0] = __byte_perm(sa, sa, 0x1010), fa[1] = __byte_perm(sa, sa, 0x3232);
-          fb[0] = __byte_perm(sb, sb, 0x1010), fb[1] = __byte_perm(sb, sb, 0x3232);
-        } else {
-          const uint2 x = *reinterpret_cast<const uint2 *>(slab + ka * 32 + c * 8);
-          const uint2 y = *reinterpret_cast<const uint2 *>(slab + kb * 32 + c * 8);
-          wa[0] = x.x, wa[1] = x.y;
-          wb[0] = y.x, wb[1] = y.y;
-          const uint32_t sa = slab[slab_k_scales(D) + ka * 4 + c], sb = slab[slab_k_scales(D) + kb * 4 + c];
-          fa[0] = fa[1] = e4m3x2_to_f16x2(sa | sa << 8);
-          fb[0] = fb[1] = e4m3x2_to_f16x2(sb | sb << 8);
+          for (int nb = 0; nb < NC; ++nb) sum[nb][0] = sum[nb][1] = NAN;
+          __syncwarp();
+          if (!dead) issue();
+          continue;
         }
+        const uint8_t *stage = ring + st * Sh::kTileBytes;
+        const int key0 = tile * kTile;
+        const bool edge = key0 + kTile - 1 > s.L;      // tokens that some row does not see
+        if (edge) {
+          // Tokens behind the last hold anything: V's scales there become 0.  So do a block token's
+          // that are NaN, to keep them from the rows before it (a weight of 0 would not do that);
+          // the rows that see it get their NaN at the end.  A lane takes a token.
+          const int key = key0 + l;
+          uint8_t *scales = ring + st * Sh::kTileBytes + (l >> 4) * SLAB + slab_v(D) + 8 * D + (l & 15) * (D / 16);
 #pragma unroll
-        for (int x = 0; x < WORDS; ++x) {
-          uint32_t ha[4], hb[4];
-          e2m1x8_to_f16x2(wa[x], ha);
-          e2m1x8_to_f16x2(wb[x], hb);
-          const uint32_t pa = fa[2 * x / WORDS], pb = fb[2 * x / WORDS];
-#pragma unroll
-          for (int y = 0; y < 2; ++y) {
-            const uint32_t a[4] = {mul_f16x2(ha[2 * y], pa), mul_f16x2(hb[2 * y], pb),
-                                   mul_f16x2(ha[2 * y + 1], pa), mul_f16x2(hb[2 * y + 1], pb)};
-#pragma unroll
-            for (int nb = 0; nb < NB; ++nb)
-              mma_f16(sc[sl][nb], a, qf[nb][2 * x + y][0], qf[nb][2 * x + y][1]);
+          for (int x = 0; x < D / 16; ++x) {
+            const bool nan = key > s.L && key < s.keys && (scales[x] & 0x7Fu) == 0x7Fu;
+            if (nan || key >= s.keys) scales[x] = 0;
+            const uint32_t who = __ballot_sync(0xffffffffu, nan);
+            if (who != 0 && x == (D == 128 ? r : r >> 1)) nan_from = min(nan_from, key0 + __ffs(who) - 1);
           }
+          asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
+          __syncwarp();
         }
-      }
 
-      // ---- weights
-      if (edge) {
+        // ---- S^T = K q^T
+        float sc[2][NC][4];
 #pragma unroll
         for (int sl = 0; sl < 2; ++sl) {
-          const int key = key0 + sl * kSlab + token_of(r);
 #pragma unroll
-          for (int nb = 0; nb < NB; ++nb)
+          for (int nb = 0; nb < NC; ++nb) sc[sl][nb][0] = sc[sl][nb][1] = sc[sl][nb][2] = sc[sl][nb][3] = 0.0f;
+          const uint8_t *slab = stage + sl * SLAB;
+          const int ka = token_of(r), kb = ka + 8;
+          uint32_t wa[WORDS], wb[WORDS], fa[2], fb[2]; // codes of two tokens; scales, twice each
+          if constexpr (D == 128) {
+            const uint4 x = *reinterpret_cast<const uint4 *>(slab + ka * 64 + c * 16);
+            const uint4 y = *reinterpret_cast<const uint4 *>(slab + kb * 64 + c * 16);
+            wa[0] = x.x, wa[1] = x.y, wa[2] = x.z, wa[3] = x.w;
+            wb[0] = y.x, wb[1] = y.y, wb[2] = y.z, wb[3] = y.w;
+            const uint32_t sa = e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t *>(slab + slab_k_scales(D) + ka * 8 + c * 2));
+            const uint32_t sb = e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t *>(slab + slab_k_scales(D) + kb * 8 + c * 2));
+            fa[0] = __byte_perm(sa, sa, 0x1010), fa[1] = __byte_perm(sa, sa, 0x3232);
+            fb[0] = __byte_perm(sb, sb, 0x1010), fb[1] = __byte_perm(sb, sb, 0x3232);
+          } else {
+            const uint2 x = *reinterpret_cast<const uint2 *>(slab + ka * 32 + c * 8);
+            const uint2 y = *reinterpret_cast<const uint2 *>(slab + kb * 32 + c * 8);
+            wa[0] = x.x, wa[1] = x.y;
+            wb[0] = y.x, wb[1] = y.y;
+            const uint32_t sa = slab[slab_k_scales(D) + ka * 4 + c], sb = slab[slab_k_scales(D) + kb * 4 + c];
+            fa[0] = fa[1] = e4m3x2_to_f16x2(sa | sa << 8);
+            fb[0] = fb[1] = e4m3x2_to_f16x2(sb | sb << 8);
+          }
 #pragma unroll
-            for (int x = 0; x < 4; ++x)
-              if (key + (x >> 1) * 8 > lim[nb][x & 1]) sc[sl][nb][x] = -INFINITY;
-        }
-      }
-      bool grows = false;
+          for (int x = 0; x < WORDS; ++x) {
+            uint32_t ha[4], hb[4];
+            e2m1x8_to_f16x2(wa[x], ha);
+            e2m1x8_to_f16x2(wb[x], hb);
+            const uint32_t pa = fa[2 * x / WORDS], pb = fb[2 * x / WORDS];
 #pragma unroll
-      for (int nb = 0; nb < NB; ++nb)
+            for (int y = 0; y < 2; ++y) {
+              const uint32_t a[4] = {mul_f16x2(ha[2 * y], pa), mul_f16x2(hb[2 * y], pb),
+                                     mul_f16x2(ha[2 * y + 1], pa), mul_f16x2(hb[2 * y + 1], pb)};
 #pragma unroll
-        for (int x = 0; x < 2; ++x)
-          grows |= fmaxf(fmaxf(sc[0][nb][x], sc[0][nb][2 + x]), fmaxf(sc[1][nb][x], sc[1][nb][2 + x])) *
-                       P.scale_log2 > m[nb][x] + kLate;
-      if (__any_sync(0xffffffffu, grows)) {
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            float top = fmaxf(fmaxf(sc[0][nb][x], sc[0][nb][2 + x]), fmaxf(sc[1][nb][x], sc[1][nb][2 + x]));
-#pragma unroll
-            for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-            const float now = fmaxf(m[nb][x], top * P.scale_log2);
-            const float f = now == -INFINITY ? 1.0f : fast_exp2(m[nb][x] - now);
-            m[nb][x] = now;
-            mu[nb][x] = now == -INFINITY ? 0.0f : now;
-            sum[nb][x] *= f;
-#pragma unroll
-            for (int y = 0; y < MT; ++y) {
-              o[y][nb][x] *= f;
-              o[y][nb][2 + x] *= f;
+              for (int nb = 0; nb < NC; ++nb)
+                mma_f16(sc[sl][nb], a, qf[nb][2 * x + y][0], qf[nb][2 * x + y][1]);
             }
           }
-      }
-      uint32_t pf[2][NB][2];
-#pragma unroll
-      for (int sl = 0; sl < 2; ++sl)
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb) {
-          float e[4];
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            e[x] = fast_exp2(fmaf(sc[sl][nb][x], P.scale_log2, -mu[nb][x & 1]));
-            sum[nb][x & 1] += e[x];
-          }
-          pf[sl][nb][0] = movmatrix_trans(pack_f16x2(e[0], e[1]));
-          pf[sl][nb][1] = movmatrix_trans(pack_f16x2(e[2], e[3]));
         }
 
-      // ---- O^T += V^T P^T
+        // ---- weights
+        if (edge) {
 #pragma unroll
-      for (int sl = 0; sl < 2; ++sl) {
-        const uint8_t *slab = stage + sl * SLAB + slab_v(D);
-        uint32_t v[4][D / 64], s4[4];                // four tokens' codes and scales
+          for (int sl = 0; sl < 2; ++sl) {
+            const int key = key0 + sl * kSlab + token_of(r);
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          const int tok = token_of(2 * c + (x & 1)) + (x >> 1) * 8;
-          if constexpr (D == 128) {
-            const uint2 y = *reinterpret_cast<const uint2 *>(slab + tok * 64 + r * 8);
-            v[x][0] = y.x, v[x][1] = y.y;
-            s4[x] = slab[8 * D + tok * 8 + r];
-          } else {
-            v[x][0] = *reinterpret_cast<const uint32_t *>(slab + tok * 32 + r * 4);
-            s4[x] = slab[8 * D + tok * 4 + (r >> 1)];
+            for (int nb = 0; nb < NC; ++nb)
+#pragma unroll
+              for (int x = 0; x < 4; ++x)
+                if (key + (x >> 1) * 8 > lim[nb][x & 1]) sc[sl][nb][x] = -INFINITY;
           }
         }
-        const uint32_t f01 = e4m3x2_to_f16x2(s4[0] | s4[1] << 8), f23 = e4m3x2_to_f16x2(s4[2] | s4[3] << 8);
+        bool grows = false;
 #pragma unroll
-        for (int x = 0; x < D / 64; ++x) {
-          constexpr uint32_t kLow = 0x0F0F0F0Fu;
-          uint32_t a0[4], a1[4], a2[4], a3[4];       // even elements of two tokens, odd ones
-          e2m1x8_to_f16x2((v[0][x] & kLow) | (v[1][x] << 4 & ~kLow), a0);
-          e2m1x8_to_f16x2((v[0][x] >> 4 & kLow) | (v[1][x] & ~kLow), a1);
-          e2m1x8_to_f16x2((v[2][x] & kLow) | (v[3][x] << 4 & ~kLow), a2);
-          e2m1x8_to_f16x2((v[2][x] >> 4 & kLow) | (v[3][x] & ~kLow), a3);
+        for (int nb = 0; nb < NC; ++nb)
 #pragma unroll
-          for (int y = 0; y < 4; ++y) {
-            const uint32_t a[4] = {mul_f16x2(a0[y], f01), mul_f16x2(a1[y], f01), mul_f16x2(a2[y], f23),
-                                   mul_f16x2(a3[y], f23)};
+          for (int x = 0; x < 2; ++x)
+            grows |= fmaxf(fmaxf(sc[0][nb][x], sc[0][nb][2 + x]), fmaxf(sc[1][nb][x], sc[1][nb][2 + x])) *
+                         P.scale_log2 > m[nb][x] + kLate;
+        if (__any_sync(0xffffffffu, grows)) {
 #pragma unroll
-            for (int nb = 0; nb < NB; ++nb) mma_f16(o[4 * x + y][nb], a, pf[sl][nb][0], pf[sl][nb][1]);
+          for (int nb = 0; nb < NC; ++nb)
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              float top = fmaxf(fmaxf(sc[0][nb][x], sc[0][nb][2 + x]), fmaxf(sc[1][nb][x], sc[1][nb][2 + x]));
+#pragma unroll
+              for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+              const float now = fmaxf(m[nb][x], top * P.scale_log2);
+              const float f = now == -INFINITY ? 1.0f : fast_exp2(m[nb][x] - now);
+              m[nb][x] = now;
+              mu[nb][x] = now == -INFINITY ? 0.0f : now;
+              sum[nb][x] *= f;
+#pragma unroll
+              for (int y = 0; y < MT; ++y) {
+                o[y][nb][x] *= f;
+                o[y][nb][2 + x] *= f;
+              }
+            }
+        }
+        uint32_t pf[2][NC][2];
+#pragma unroll
+        for (int sl = 0; sl < 2; ++sl)
+#pragma unroll
+          for (int nb = 0; nb < NC; ++nb) {
+            float e[4];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              e[x] = fast_exp2(fmaf(sc[sl][nb][x], P.scale_log2, -mu[nb][x & 1]));
+              sum[nb][x & 1] += e[x];
+            }
+            pf[sl][nb][0] = movmatrix_trans(pack_f16x2(e[0], e[1]));
+            pf[sl][nb][1] = movmatrix_trans(pack_f16x2(e[2], e[3]));
+          }
+
+        // ---- O^T += V^T P^T
+#pragma unroll
+        for (int sl = 0; sl < 2; ++sl) {
+          const uint8_t *slab = stage + sl * SLAB + slab_v(D);
+          uint32_t v[4][D / 64], s4[4];                // four tokens' codes and scales
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const int tok = token_of(2 * c + (x & 1)) + (x >> 1) * 8;
+            if constexpr (D == 128) {
+              const uint2 y = *reinterpret_cast<const uint2 *>(slab + tok * 64 + r * 8);
+              v[x][0] = y.x, v[x][1] = y.y;
+              s4[x] = slab[8 * D + tok * 8 + r];
+            } else {
+              v[x][0] = *reinterpret_cast<const uint32_t *>(slab + tok * 32 + r * 4);
+              s4[x] = slab[8 * D + tok * 4 + (r >> 1)];
+            }
+          }
+          const uint32_t f01 = e4m3x2_to_f16x2(s4[0] | s4[1] << 8), f23 = e4m3x2_to_f16x2(s4[2] | s4[3] << 8);
+#pragma unroll
+          for (int x = 0; x < D / 64; ++x) {
+            constexpr uint32_t kLow = 0x0F0F0F0Fu;
+            uint32_t a0[4], a1[4], a2[4], a3[4];       // even elements of two tokens, odd ones
+            e2m1x8_to_f16x2((v[0][x] & kLow) | (v[1][x] << 4 & ~kLow), a0);
+            e2m1x8_to_f16x2((v[0][x] >> 4 & kLow) | (v[1][x] & ~kLow), a1);
+            e2m1x8_to_f16x2((v[2][x] & kLow) | (v[3][x] << 4 & ~kLow), a2);
+            e2m1x8_to_f16x2((v[2][x] >> 4 & kLow) | (v[3][x] & ~kLow), a3);
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+              const uint32_t a[4] = {mul_f16x2(a0[y], f01), mul_f16x2(a1[y], f01), mul_f16x2(a2[y], f23),
+                                     mul_f16x2(a3[y], f23)};
+#pragma unroll
+              for (int nb = 0; nb < NC; ++nb) mma_f16(o[4 * x + y][nb], a, pf[sl][nb][0], pf[sl][nb][1]);
+            }
           }
         }
+        __syncwarp();
+        issue();
       }
-      __syncwarp();
-      issue();
-    }
+    };
+    const int columns = (rows + 7) / 8;
+    if (NB >= 2 && columns == 1)
+      run_tiles(std::integral_constant<int, 1>());
+    else if (NB >= 3 && columns == 2)
+      run_tiles(std::integral_constant<int, 2>());
+    else
+      run_tiles(std::integral_constant<int, NB>());
 
     // ---- its sums: rows that this warp has seen whole are done, others a piece
     if (__any_sync(0xffffffffu, nan_from != 0x7fffffff)) {
@@ -811,7 +831,10 @@ struct Plan {
 Plan plan_of(const sv_kv4_attn_args &a) {
   Plan p;
   const int rows = a.max_q_rows * (a.num_q_heads / a.cache.num_kv_heads), blocks = (rows + 7) / 8;
-  p.parts = (blocks + 2) / 3;
+  // Two columns a part, or three in one: a third costs a third of the warps (128k keys of 8
+  // heads: 16 rows 161 us, 24 rows 220 us, but 36 rows or fewer, ragged, 59 us in parts of two
+  // and 65 us in parts of three).
+  p.parts = blocks <= 3 ? 1 : (blocks + 1) / 2;
   p.nb = (blocks + p.parts - 1) / p.parts;
   p.parts = (blocks + p.nb - 1) / p.nb;
   p.part_o = kCounters * sizeof(uint32_t);
@@ -823,7 +846,7 @@ Plan plan_of(const sv_kv4_attn_args &a) {
 template <int D, int NB>
 cudaError_t launch_shape(const Kv4AttnParams &P, int ctas, cudaStream_t s) {
   using Sh = Shape<D, NB>;
-  const size_t smem = Sh::kFixed + (static_cast<size_t>(P.batch) + 1) * 4 + P.batch;
+  const size_t smem = Sh::kFixed + (static_cast<size_t>(P.batch) + 1) * 4 + P.batch * size_t{5};
   return launch_after_previous(kv4_attn_kernel<D, NB>, dim3(ctas), Sh::kThreads, smem, s, P);
 }
 template <int D>
@@ -904,10 +927,12 @@ SV_API sv_status spec_kv4_attn(const sv_kv4_attn_args *a, void *ws, size_t ws_by
   P.batch = a->batch;
   P.Hq = a->num_q_heads;
   P.g = a->num_q_heads / a->cache.num_kv_heads;
+  P.slab_shift = -1;
+  for (int x = 0; x <= 8; ++x)
+    if (P.cache.slabs == 1 << x) P.slab_shift = x;
   P.g_inverse = P.g == 1 ? 0 : static_cast<uint32_t>(((uint64_t{1} << 32) + P.g - 1) / P.g);
   P.max_q_rows = a->max_q_rows;
   P.parts = p.parts;
-  P.least = 4;
   P.num_rows = a->num_rows;
   P.q_stride = a->q_stride ? a->q_stride : static_cast<int64_t>(P.Hq) * a->cache.head_dim;
   const double scale = a->scale != 0.0f ? a->scale : 1.0 / std::sqrt(static_cast<double>(a->cache.head_dim));
