@@ -495,6 +495,9 @@ struct ReadParams {
   int by_row;
   int64_t num_rows, slots;
   float k_scale, v_scale, k_inverse, v_inverse;      // E4M3 outputs
+  uint32_t k_short, v_short;                         // f16x2 of what a product of code and scale is to be
+                                                     // multiplied by, where that may be done to the scale
+                                                     // in f16 (below), else 0
   const int32_t *cu_q, *kv_len;
   const int64_t *positions;                          // nullptr
   void *k_out, *v_out;
@@ -538,6 +541,7 @@ __global__ void __launch_bounds__(kNT) kv4_read_kernel(const ReadParams P) {
     const int h0 = blockIdx.y * each + (t >> shift);
     const float factor = is_v ? P.cache.v_scale : P.cache.k_scale;
     const float to_scale = is_v ? P.v_scale : P.k_scale, inverse = is_v ? P.v_inverse : P.k_inverse;
+    const uint32_t brief = is_v ? P.v_short : P.k_short;
     const uint8_t *at = slab + (is_v ? slab_v(P.D) : 0) + h0 * head;
     out += (row * heads + h0) * P.D + 8 * g;
     for (int h = h0; h < heads; h += kReads * step) {
@@ -553,13 +557,28 @@ __global__ void __launch_bounds__(kNT) kv4_read_kernel(const ReadParams P) {
         if (h + u * step >= heads) continue;
         uint32_t pair[4];
         e2m1x8_to_f16x2(codes[u], pair);
-        const uint32_t s = e4m3x2_to_f16x2(scale[u] | scale[u] << 8);
+        uint32_t s = e4m3x2_to_f16x2(scale[u] | scale[u] << 8);
+        if (brief != 0) s = mul_f16x2(s, brief);
+        uint32_t y[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) y[i] = mul_f16x2(pair[i], s);    // exact
+        if constexpr (sizeof(T) == 1) {
+          if (brief != 0) {
+            *reinterpret_cast<uint2 *>(out + u * step * P.D) =
+                make_uint2(f16x2_to_e4m3x2(y[0]) | f16x2_to_e4m3x2(y[1]) << 16,
+                           f16x2_to_e4m3x2(y[2]) | f16x2_to_e4m3x2(y[3]) << 16);
+            continue;
+          }
+        }
         float x[8];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const uint32_t y = mul_f16x2(pair[i], s);  // exact
-          x[2 * i] = __fmul_rn(f16_bits_to_f32(y & 0xFFFFu), factor);
-          x[2 * i + 1] = __fmul_rn(f16_bits_to_f32(y >> 16), factor);
+          x[2 * i] = f16_bits_to_f32(y[i] & 0xFFFFu);
+          x[2 * i + 1] = f16_bits_to_f32(y[i] >> 16);
+        }
+        if (brief == 0) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) x[i] = __fmul_rn(x[i], factor);
         }
         if constexpr (sizeof(T) == 1) {
           store_codes(out + u * step * P.D, x, to_scale, inverse);
@@ -579,6 +598,16 @@ float exact_inverse(float x) {                       // 1 / x where x is a power
   int e;
   const float inv = 1.0f / x;
   return std::frexp(x, &e) == 0.5f && std::isnormal(inv) ? inv : 0.0f;
+}
+
+// f16x2 of `x` if it is a power of two in [2^-5, 2^5], else 0.  A scale (2^-9 .. 448, four
+// significant bits) times such an x is exact in f16, and so is that times a code: six bits
+// from 2^-15 on, or beyond f16's range where E4M3 saturates all the same.
+uint32_t short_factor(float x) {
+  int e;
+  if (std::frexp(x, &e) != 0.5f || e < -4 || e > 6) return 0;
+  const uint32_t h = static_cast<uint32_t>(e - 1 + 15) << 10;
+  return h | h << 16;
 }
 
 template <typename T, Output OUT>
@@ -806,6 +835,12 @@ SV_API sv_status spec_kv4_read(const sv_kv4_read_args *a, void *stream) {
   P.k_out = a->k_out;
   P.v_out = a->v_out;
   P.cache = view_of(a->cache);
+  // (bf16 and fp32 rows keep what f16 would overflow at: factors above 2^4 are not brief there)
+  const bool codes = a->dtype == SV_E4M3;
+  const float k_all = codes ? P.cache.k_scale / P.k_scale : P.cache.k_scale;
+  const float v_all = codes ? P.cache.v_scale / P.v_scale : P.cache.v_scale;
+  P.k_short = codes || k_all <= 16.0f ? short_factor(k_all) : 0;
+  P.v_short = codes || v_all <= 16.0f ? short_factor(v_all) : 0;
   P.dev_status = a->dev_status;
   set_slots(P);
   if (P.num_rows == 0 || P.slots == 0 || (!P.k_out && !P.v_out)) return SV_OK;
