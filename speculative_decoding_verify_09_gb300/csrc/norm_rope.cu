@@ -509,7 +509,7 @@ struct ReadParams {
 // row's K and V heads, so that a warp writes whole lines, kReads of them under way.
 constexpr int kReads = 4;
 template <typename T>
-__global__ void __launch_bounds__(kNT) kv4_read_kernel(const ReadParams P) {
+__global__ void __launch_bounds__(kNT, sizeof(T) == 1 ? 6 : 4) kv4_read_kernel(const ReadParams P) {
   const int row_threads = 1 << P.row_shift;
   const int rl = threadIdx.x >> P.row_shift, t = threadIdx.x & (row_threads - 1);
   wait_for_previous();
