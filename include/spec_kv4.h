@@ -146,7 +146,7 @@ SV_API sv_status spec_kv4_read(const sv_kv4_read_args *args, void *stream);
  * case of one row per sequence. */
 typedef struct sv_kv4_attn_args {
   sv_kv4_cache cache;
-  int32_t batch;            /* B, 0..1024 */
+  int32_t batch;            /* B, 0..768 */
   int32_t num_q_heads;      /* Hq, a multiple of Hkv; Hq / Hkv <= 256 */
   int32_t max_q_rows;       /* host bound on R_i, 1..1024 */
   int32_t dtype;            /* SV_BF16: q and out */

@@ -36,7 +36,7 @@ namespace sv {
 namespace {
 
 constexpr int kTile = 32;                            // tokens
-constexpr int kMaxBatch = 1024;
+constexpr int kMaxBatch = 768;                       // (16 bytes each in shared memory)
 constexpr int kMaxCtas = 192;                        // (sizes the workspace on any host)
 constexpr int kCounters = 65536;                     // first in the workspace, whatever the shape
 constexpr int kHead = 2;                             // units that a segment costs beside its tiles
@@ -114,12 +114,11 @@ __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, uint32_t
   return done;
 }
 
-// Rows and tokens of sequence i; nothing to do: R = 0.
+// Rows and tokens of a sequence; nothing to do: R = 0.
 struct Sequence {
   int r0, R, L, keys;
 };
-__device__ __forceinline__ Sequence sequence_of(const Kv4AttnParams &P, int i, uint32_t *why) {
-  const int r0 = P.cu_q[i], r1 = P.cu_q[i + 1], L = P.kv_len[i];
+__device__ __forceinline__ Sequence sequence_of(const Kv4AttnParams &P, int r0, int r1, int L, uint32_t *why) {
   Sequence s{0, 0, 0, 0};
   if (r0 < 0 || r1 < r0 || r1 > P.num_rows || r1 - r0 > P.max_q_rows || L < 0) {
     *why = SV_DEV_BAD_LENGTH;
@@ -152,9 +151,9 @@ __global__ void __launch_bounds__(Shape<D, NB>::kThreads, 1) kv4_attn_kernel(con
   constexpr int SLAB = slab_bytes(D), STEPS = D / 16, WORDS = D / 32, MT = D / 16;
   extern __shared__ __align__(128) uint8_t smem[];
   float2 *s_ml = reinterpret_cast<float2 *>(smem + Sh::kRing + Sh::kSlots);  // [2 W, ROWS] maximum, sum
-  int32_t *s_start = reinterpret_cast<int32_t *>(smem + Sh::kFixed);         // [batch + 1]
-  int32_t *s_each = s_start + P.batch + 1;           // [batch] units of one of its segments
-  uint8_t *s_parts = reinterpret_cast<uint8_t *>(s_each + P.batch);          // [batch]
+  int32_t *s_start = reinterpret_cast<int32_t *>(smem + Sh::kFixed);         // [batch + 1] units before
+  int32_t *s_r0 = s_start + P.batch + 1, *s_rows = s_r0 + P.batch;           // [batch] of sequences with
+  int32_t *s_len = reinterpret_cast<int32_t *>(s_rows + P.batch);            // units: first row, rows, tokens
   __shared__ __align__(8) uint64_t s_bar[W * S];
   __shared__ uint8_t s_bad[W * S];
   __shared__ Piece s_piece[2 * W];
@@ -162,33 +161,45 @@ __global__ void __launch_bounds__(Shape<D, NB>::kThreads, 1) kv4_attn_kernel(con
   __shared__ int s_share[kMaxCtas + 1], s_last[2], s_from[2], s_to[2];
   const int tid = threadIdx.x, w = tid >> 5, l = tid & 31, r = l >> 2, c = l & 3;
 
-  if (tid < W * S) bar_init(smem_u32(&s_bar[tid]));
-  if (tid < 2 * W) s_piece[tid].seg = -1;
+  if (l < S) bar_init(smem_u32(&s_bar[w * S + l]));  // (a warp's barriers and pieces are its own)
+  if (l < 2) s_piece[2 * w + l].seg = -1;
   asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
+  __syncwarp();
   wait_for_previous();
 
   // units (tiles, and kHead for each segment) before each sequence's first
   const int heads = P.cache.heads;
-  {
+  auto parts_of = [&](int rows) { return (rows * P.g + ROWS - 1) / ROWS; };
+  auto each_of = [&](int keys) { return (keys + kTile - 1) / kTile + kHead; };
+  auto enter = [&](int i) {                          // the sequence's data; its units
+    uint32_t why = 0;
+    const Sequence s = sequence_of(P, P.cu_q[i], P.cu_q[i + 1], P.kv_len[i], &why);
+    if (why && blockIdx.x == 0) set_status(P.dev_status, why);
+    s_r0[i] = s.r0, s_rows[i] = s.R, s_len[i] = s.L;
+    return s.R == 0 ? 0 : each_of(s.keys) * parts_of(s.R) * heads;
+  };
+  auto inclusive = [&](int x) {                      // sums over a warp's lanes up to this one
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, x, o);
+      if (l >= o) x += y;
+    }
+    return x;
+  };
+  if (P.batch <= 32) {                               // every warp for itself: the same values, no barrier
+    const int n = l < P.batch ? enter(l) : 0, inc = inclusive(n);
+    if (l < P.batch) s_start[l] = inc - n;
+    if (l == 31) s_start[P.batch] = inc;
+    __syncwarp();
+  } else {
     const int each = (P.batch + NT - 1) / NT, i0 = min(P.batch, tid * each), i1 = min(P.batch, i0 + each);
     int mine = 0;
     for (int i = i0; i < i1; ++i) {
-      uint32_t why = 0;
-      const Sequence s = sequence_of(P, i, &why);
-      if (why && blockIdx.x == 0) set_status(P.dev_status, why);
-      const int parts = (s.R * P.g + ROWS - 1) / ROWS;
-      s_parts[i] = static_cast<uint8_t>(parts);
-      const int one = (s.keys + kTile - 1) / kTile + kHead, n = one * parts * heads;
-      s_each[i] = one;
+      const int n = enter(i);
       s_start[i] = n;
       mine += n;
     }
-    int inc = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int x = __shfl_up_sync(0xffffffffu, inc, o);
-      if (l >= o) inc += x;
-    }
+    const int inc = inclusive(mine);
     if (l == 31) s_scan[w] = inc;
     __syncthreads();
     int before = inc - mine, total = 0;
@@ -208,6 +219,10 @@ __global__ void __launch_bounds__(Shape<D, NB>::kThreads, 1) kv4_attn_kernel(con
   if (total == 0) return;
   // sequence, unit (head * parts + part) and place in it of list entry v
   struct Place { int i, unit, at, tiles; };
+  auto data_of = [&](int i) {
+    const int R = s_rows[i], L = s_len[i];
+    return Sequence{s_r0[i], R, L, L + R};
+  };
   auto locate = [&](int v) {
     int lo = 0, hi = P.batch;
     while (hi - lo > 1) {
@@ -216,7 +231,7 @@ __global__ void __launch_bounds__(Shape<D, NB>::kThreads, 1) kv4_attn_kernel(con
     }
     Place p;
     p.i = lo;
-    const int each = s_each[lo], rem = v - s_start[lo];
+    const int each = each_of(s_rows[lo] + s_len[lo]), rem = v - s_start[lo];
     // (a quotient below 2^17: by floats it is off by one at most)
     p.unit = static_cast<int>(__fdividef(static_cast<float>(rem), static_cast<float>(each)));
     p.at = rem - p.unit * each;
@@ -278,8 +293,7 @@ __global__ void __launch_bounds__(Shape<D, NB>::kThreads, 1) kv4_attn_kernel(con
     second = false;
     if (v < v1) {
       ahead = locate(v);
-      uint32_t why = 0;
-      ahead_s = sequence_of(P, ahead.i, &why);
+      ahead_s = data_of(ahead.i);
       if (ahead.at >= kHead) {
         const uint32_t n = 2u * static_cast<uint32_t>(ahead.at - kHead), per = P.cache.slabs;
         const uint32_t at0 = P.slab_shift >= 0 ? n >> P.slab_shift : n / per;
@@ -296,7 +310,7 @@ __global__ void __launch_bounds__(Shape<D, NB>::kThreads, 1) kv4_attn_kernel(con
     from0 = from1 = nullptr;
     from_bad = false;
     if (real) {
-      const int parts = s_parts[ahead.i];
+      const int parts = parts_of(ahead_s.R);
       const int64_t head = (parts == 1 ? ahead.unit : ahead.unit / parts) * head_bytes(P.cache);
       const int64_t page_bytes = P.cache.heads * head_bytes(P.cache);
       if (page0 < 0 || page0 >= P.cache.num_pages || page1 < 0 || page1 >= P.cache.num_pages) {
@@ -338,7 +352,7 @@ __global__ void __launch_bounds__(Shape<D, NB>::kThreads, 1) kv4_attn_kernel(con
   // the segment of list entry v, and this lane's part of its rows of q
   struct Segment { Place p; Sequence s; int h, part, rows; };
   auto complete = [&](Segment &x) {
-    const int parts = s_parts[x.p.i];
+    const int parts = parts_of(x.s.R);
     x.h = parts == 1 ? x.p.unit : x.p.unit / parts;
     x.part = x.p.unit - x.h * parts;
     x.rows = min(ROWS, x.s.R * P.g - x.part * ROWS);
@@ -376,8 +390,7 @@ __global__ void __launch_bounds__(Shape<D, NB>::kThreads, 1) kv4_attn_kernel(con
       for (int x = 0; x < S; ++x) issue();
     } else {
       here.p = locate(v);
-      uint32_t why = 0;
-      here.s = sequence_of(P, here.p.i, &why);
+      here.s = data_of(here.p.i);
       complete(here);
       fetch_q(here);
     }
@@ -846,7 +859,7 @@ Plan plan_of(const sv_kv4_attn_args &a) {
 template <int D, int NB>
 cudaError_t launch_shape(const Kv4AttnParams &P, int ctas, cudaStream_t s) {
   using Sh = Shape<D, NB>;
-  const size_t smem = Sh::kFixed + (static_cast<size_t>(P.batch) + 1) * 4 + P.batch * size_t{5};
+  const size_t smem = Sh::kFixed + (static_cast<size_t>(P.batch) * 4 + 1) * 4;
   return launch_after_previous(kv4_attn_kernel<D, NB>, dim3(ctas), Sh::kThreads, smem, s, P);
 }
 template <int D>
