@@ -211,9 +211,11 @@ __device__ __forceinline__ void join(Vec<uint16_t, 8> &v, const float (&x)[8]) {
 }
 __device__ __forceinline__ void join(Vec<float, 8> &v, const float (&x)[8]) { v.set(x); }
 
-// CTAs per SM that the registers are capped for.
+// CTAs per SM that the registers are capped for.  Loads under way are what prompts need: 32768
+// bf16 rows of 48 heads of 128 take 134 us at 4 CTAs, 144 at 3.  With pages 4 would cost local
+// memory: 17936 rows 77 us against 79, but 576 rows 6.7 against 6.3.
 template <typename T, Output OUT, Layout LAYOUT>
-constexpr int kCtas = LAYOUT != kFar && sizeof(T) == 2 ? 3 : 2;
+constexpr int kCtas = LAYOUT == kFar || sizeof(T) == 4 ? 2 : OUT == kPages ? 3 : 4;
 
 template <typename T, Output OUT, Layout LAYOUT>
 __global__ void __launch_bounds__(kNT, kCtas<T, OUT, LAYOUT>) norm_rope_kernel(const NormRopeParams P) {
@@ -309,20 +311,8 @@ __global__ void __launch_bounds__(kNT, kCtas<T, OUT, LAYOUT>) norm_rope_kernel(c
   __syncthreads();
   if (!live) return;                                 // (all threads of a warp share a row)
 
-  // the pairs of this column
-  F2 cs[4], sn[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    float x[2] = {1.0f, 1.0f}, y[2] = {0.0f, 0.0f};
-#pragma unroll
-    for (int n = 0; n < 2; ++n)
-      if (LAYOUT != kFar && any_turn && 2 * i + n < turning) {
-        x[n] = s_cos[8 * c + 2 * i + n];
-        y[n] = s_sin[8 * c + 2 * i + n];
-      }
-    cs[i] = f2(x[0], x[1]);
-    sn[i] = f2(y[0], y[1]);
-  }
+  // the pairs of this column (those that do not turn read others' and are not touched)
+  const float4 *cos4 = reinterpret_cast<const float4 *>(s_cos + 8 * c), *sin4 = reinterpret_cast<const float4 *>(s_sin + 8 * c);
   const bool all_turn = __all_sync(0xffffffffu, turning == 8 || !column);
   const int token = static_cast<int>(pos) & (kSlab - 1);
 
@@ -406,25 +396,31 @@ __global__ void __launch_bounds__(kNT, kCtas<T, OUT, LAYOUT>) norm_rope_kernel(c
           b[i] = f2(y[2 * i], y[2 * i + 1]);
         }
       } else if (turns) {
-        const F2 minus = f2(-1.0f, -1.0f);
-        if (all_turn) {
+        if (all_turn || turning > 0) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const F2 x = f2_fma(a[i], cs[i], f2_mul(f2_mul(b[i], minus), sn[i]));
-            b[i] = f2_fma(b[i], cs[i], f2_mul(a[i], sn[i]));
-            a[i] = x;
-          }
-        } else {                                     // (a partner that does not turn is not touched)
+          for (int n = 0; n < 2; ++n) {
+            const float4 cx = cos4[n], sx = sin4[n];
+            const F2 cs[2] = {f2(cx.x, cx.y), f2(cx.z, cx.w)}, sn[2] = {f2(sx.x, sx.y), f2(sx.z, sx.w)};
+            const F2 minus[2] = {f2(-sx.x, -sx.y), f2(-sx.z, -sx.w)};
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            float a0, a1, b0, b1, x0, x1, y0, y1;
-            f2_get(a[i], a0, a1);
-            f2_get(b[i], b0, b1);
-            f2_get(f2_fma(a[i], cs[i], f2_mul(f2_mul(b[i], minus), sn[i])), x0, x1);
-            f2_get(f2_fma(b[i], cs[i], f2_mul(a[i], sn[i])), y0, y1);
-            const bool on0 = 2 * i < turning, on1 = 2 * i + 1 < turning;
-            a[i] = f2(on0 ? x0 : a0, on1 ? x1 : a1);
-            b[i] = f2(on0 ? y0 : b0, on1 ? y1 : b1);
+            for (int m = 0; m < 2; ++m) {
+              const int i = 2 * n + m;
+              const F2 x = f2_fma(a[i], cs[m], f2_mul(b[i], minus[m]));
+              const F2 y = f2_fma(b[i], cs[m], f2_mul(a[i], sn[m]));
+              if (all_turn) {
+                a[i] = x;
+                b[i] = y;
+              } else {
+                float a0, a1, b0, b1, x0, x1, y0, y1;
+                f2_get(a[i], a0, a1);
+                f2_get(b[i], b0, b1);
+                f2_get(x, x0, x1);
+                f2_get(y, y0, y1);
+                const bool on0 = 2 * i < turning, on1 = 2 * i + 1 < turning;
+                a[i] = f2(on0 ? x0 : a0, on1 ? x1 : a1);
+                b[i] = f2(on0 ? y0 : b0, on1 ? y1 : b1);
+              }
+            }
           }
         }
       }
