@@ -3,11 +3,12 @@
 //
 // softmax(scale q K^T) V with K and V as E2M1 codes times a scale per 16 elements.
 // A token takes 18 D / 16 bytes per KV head, read once for all of the block's rows
-// that share the head, so for few rows the kernel is bound by those bytes; what
-// stands against it is the work per byte: every code becomes an f16 operand (one
-// conversion and one product per two codes) that a matrix instruction of 8 rows
-// takes once.  E2M1 times E4M3 has six significant bits, so the operands are
-// exact and only q, the weights and the sums are rounded.
+// that share the head.  What stands against those bytes is the work per byte: every
+// code becomes an f16 operand (one conversion and one product per two codes, and a
+// byte moved down for three of four conversions) that a matrix instruction of 8 rows
+// takes once.  E2M1 times E4M3 has six significant bits, so the operands are exact and
+// only q (to f16, exact for bf16 in its range), the weights (to f16: 2^-11, below the
+// output's 2^-8) and the fp32 sums are rounded.
 //
 // Split: the tiles of 32 tokens of all (sequence, KV head, part of the rows) --
 // segments -- are one list, cut into equal runs, one per warp of a persistent grid
@@ -16,14 +17,28 @@
 // bulk copies, which run ahead across segments; no warp waits for another before its
 // run is done.  A segment that lies in one run is finished by its warp.  The pieces of
 // the others are left in shared memory, joined there by the CTA, and, where a segment
-// passes the CTA's runs, joined in the workspace by the last CTA to arrive, in order.
+// passes the CTA's runs, joined in the workspace by the last CTA to arrive, in order
+// (runs per CTA instead, its warps taking tiles in turn and meeting at every segment's
+// end: 160 us against 76 at 32 ragged GQA sequences).
 //
 // Operands: S^T = K q^T and O^T = V^T P^T, tokens (then elements) on M, rows on N,
 // so a block of 1 row costs 8 columns, not 16 or more rows.  The order of a head's
 // elements in a product is free: a lane takes 16 bytes in a row of a token's K (32
 // elements) and the same elements of q; of V, 8 bytes in a row of four tokens'
 // elements.  The weights' running maximum is kept within 2^8 of the true one, so
-// the sums are rescaled seldom.
+// the sums are rescaled seldom.  The 5th-generation tensor path would want the
+// operands in shared memory, i.e. 2 x 512 bytes written and read per token and head
+// next to 144 from memory: as long as the register-fed products of 40 rows take.
+//
+// Bounds, D = 128, 8 KV heads, device time per call: 4 sequences of 128k tokens,
+// single rows, 105 us = 5.7 TB/s (0.84 of the measured copy rate), 614 instructions a
+// tile of 32 tokens issued at 2.6 of 4 per clock, the ALU pipe (conversions, byte
+// moves) at 0.46; 16 and 24 rows take 161 and 220 us, 67 instructions more a tile for
+// each 8 rows but 12 and 8 warps, and fewer registers free to overlap in.  Short
+// lists are bound by latency: 8 sequences of 32 heads over 512 to 2048 tokens 20 us,
+// of which 4 us pass before the first copies (bounds, places, pages: one dependent
+// load after the other), 2 until the first tile is there, 7 in tiles, the rest in the
+// slowest warps and the joining.
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
@@ -39,12 +54,22 @@ constexpr int kTile = 32;                            // tokens
 constexpr int kMaxBatch = 768;                       // (16 bytes each in shared memory)
 constexpr int kMaxCtas = 192;                        // (sizes the workspace on any host)
 constexpr int kCounters = 65536;                     // first in the workspace, whatever the shape
-constexpr int kHead = 2;                             // units that a segment costs beside its tiles
-constexpr int kLeast = 4;                            // units of a CTA's share
-constexpr int kSnap = 8;                             // units that a CTA's share may end early or late
-constexpr float kLate = 8.0f;                        // log2 the maximum may grow before sums are rescaled
+// Units that a segment costs beside its tiles (1: 61.4 us, 2: 59.1, 4: 59.9 at the ragged
+// verify rows above).
+constexpr int kHead = 2;
+// Units of a CTA's share at least (13 small ragged sequences 6.8 us, with 16 7.7), and by how many
+// it may end early or late to end with a segment (0: the same small sequences 9.0 us, 8: 6.8;
+// 16: shares so unequal that 8 sequences of 32 heads take 20.8 us instead of 20.0).
+constexpr int kLeast = 4;
+constexpr int kSnap = 8;
+// log2 the maximum may grow before sums are rescaled (0: 63.2 us, 8: 59.1; weights up to 2^8 lose
+// nothing in f16).
+constexpr float kLate = 8.0f;
 
-// Warps and stages of a warp's ring; NB: 8-row columns of a part.
+// Warps and stages of a warp's ring; NB: 8-row columns of a part.  As many warps as registers
+// allow (128, 168, 255 a thread; 12 instead of 16 warps with three stages: 116 us against 105
+// at 128k tokens, 8 with four: 128), and two stages each, which keep 147 KB under way; a
+// third one fits only where there are 8 warps.
 template <int D, int NB>
 struct Shape {
   static constexpr int kWarps = NB == 1 ? 16 : NB == 2 ? 12 : 8;

@@ -289,6 +289,44 @@ def test_read(api, dtype, D, page, Hkv, rows):
                     assert np.array_equal(oracle.to_f64(x), want, equal_nan=True)
 
 
+@pytest.mark.parametrize("f,to", [((0.3, 1.7), (0.3, 0.1)), ((64.0, 2.0 ** -9), (1.0, 1.0)),
+                                  ((2.0 ** -30, 2.0 ** 30), (2.0 ** -33, 2.0 ** 27)),
+                                  ((0.5, 0.5), (2.0 ** -6, 2.0 ** 5))])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32, torch.uint8])
+def test_read_scales(api, f, to, dtype):
+    """Factors that do and do not fit f16, and quotients of them that are no powers of two.  Values:
+    one rounding of fp32 (and one of bf16); codes: the quotient of a value so rounded, rounded."""
+    rng = np.random.default_rng(5)
+    D, Hkv, page, n = 64, 3, 16, 40
+    pages = rng.integers(0, 256, (3, Hkv, 1, 18 * D)).astype(np.uint8)
+    cache = api.Kv4Cache(3, Hkv, D, page_size=page, k_scale=f[0], v_scale=f[1], pages=dev(pages))
+    table = np.array([[2, 0, 1]], np.int32)
+    out = [torch.zeros(n, Hkv, D, dtype=dtype, device="cuda") for _ in range(2)]
+    api.spec_kv4_read(api.kv4_read_args(cache, dev(table), dev(np.array([0, n], np.int32)),
+                                        dev(np.array([5], np.int32)), *out, max_q_rows=n, k_scale=to[0],
+                                        v_scale=to[1]))
+    torch.cuda.synchronize()
+    e4 = oracle.sampling.e4m3_to_f64
+    for which in range(2):
+        got = host_bits(out[which])
+        for h in range(Hkv):
+            codes, scales = oracle.kv4_load(pages, table, page, 0, 5 + n, h, which)
+            want = oracle.kv4_values(codes[5:], scales[5:], float(np.float32(f[which])))
+            nan = np.isnan(want)
+            if dtype == torch.uint8:
+                y = np.clip(want / float(np.float32(to[which])), -448, 448)[~nan]
+                assert ((got[:, h][nan] & 0x7F) == 0x7F).all()
+                best = np.abs(e4(oracle.e4m3_nearest(y)) - y)
+                assert np.all(np.abs(e4(got[:, h][~nan]) - y) <= best + 2 * 3 * 2.0 ** -24 * np.abs(y))
+                continue
+            got_h = oracle.to_f64(got[:, h])
+            assert np.isnan(got_h[nan]).all()
+            eps = 2.0 ** -24 + (2.0 ** -8 if dtype == torch.bfloat16 else 0)
+            assert np.all(np.abs(got_h - want)[~nan] <= eps * (1 + 2.0 ** -20) * np.abs(want)[~nan])
+            if np.log2(f[which]) % 1 == 0:
+                assert np.array_equal(got_h, want, equal_nan=True)
+
+
 def test_read_parts_and_problems(api):
     rng = np.random.default_rng(2)
     D, Hkv, page = 64, 2, 16
@@ -402,7 +440,8 @@ def test_attention_lengths(api, D, page):
 
 
 @pytest.mark.parametrize("Hq,Hkv,lens,rows", [
-    (1, 1, [20000], [1]), (4, 1, [9000, 1], [4, 2]), (8, 1, [5000], [3]), (32, 32, [600, 1500], [1, 6]),
+    (1, 1, [20000], [1]), (24, 1, [17000], [1]), (5, 1, [14000], [1]), (16, 1, [13000, 0], [2, 1]),
+    (4, 1, [9000, 1], [4, 2]), (8, 1, [5000], [3]), (32, 32, [600, 1500], [1, 6]),
     (8, 8, [3001, 10, 0, 700], [2, 5, 1, 3])])
 def test_attention_cut_segments(api, Hq, Hkv, lens, rows):
     """Long segments over many CTAs, several segments in one."""
@@ -415,6 +454,17 @@ def test_attention_cut_segments(api, Hq, Hkv, lens, rows):
         c.out.fill_(0)
         c.run(ws)
         assert torch.equal(c.out, first)
+
+
+def test_attention_of_the_largest_batch(api):
+    """768 sequences, most of a few tokens, some without rows."""
+    rng = np.random.default_rng(8)
+    lens = rng.integers(0, 40, 768)
+    lens[100], rows = 900, rng.integers(0, 3, 768)
+    c = Attn(api, lens, rows, 2, 1, 64, 16, garbage=None)
+    c.run()
+    c.check()
+    assert int(c.status.item()) == 0
 
 
 @pytest.mark.parametrize("g", [64, 256])

@@ -156,16 +156,16 @@ def test_read_refusals(binding, kw, status):
 
 
 BAD_SHAPES = [
-    (dict(batch=-1), UNSUPPORTED), (dict(batch=2049), UNSUPPORTED), (dict(num_q_heads=0), INVALID),
+    (dict(batch=-1), UNSUPPORTED), (dict(batch=769), UNSUPPORTED), (dict(num_q_heads=0), INVALID),
     (dict(num_q_heads=7), INVALID), (dict(num_q_heads=1026), INVALID), (dict(dtype=0), UNSUPPORTED),
     (dict(dtype=2), UNSUPPORTED), (dict(reserved=1), INVALID), (dict(max_q_rows=0), INVALID),
     (dict(max_q_rows=1025), INVALID), (dict(num_rows=-1), INVALID), (dict(scale=-1.0), INVALID),
     (dict(scale=NAN), INVALID), (dict(scale=INF), INVALID), (dict(q_stride=1023), INVALID),
     (dict(q_stride=1028), INVALID), (dict(q_stride=-1024), INVALID),
-    (dict(batch=2048, cache__num_kv_heads=64, num_q_heads=64), UNSUPPORTED),
+    (dict(batch=768, cache__num_kv_heads=128, num_q_heads=128), UNSUPPORTED),
     (dict(max_q_rows=1024, num_q_heads=512), UNSUPPORTED),
     (dict(cache__max_pages=1 << 27), UNSUPPORTED),
-    (dict(batch=2048, cache__max_pages=1 << 18), UNSUPPORTED),
+    (dict(batch=768, cache__max_pages=1 << 20), UNSUPPORTED),
 ]
 
 
