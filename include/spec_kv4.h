@@ -133,8 +133,9 @@ typedef struct sv_kv4_read_args {
   uint32_t *dev_status;     /* [dev] one word or NULL */
 } sv_kv4_read_args;
 
-/* Values are exact in fp32 and (with scales that are powers of two) in bf16, else
- * rounded once; E4M3 codes as in spec_rope_rows.  Rows that spec_kv4_append would
+/* fp32 rows are the values' products rounded to fp32, bf16 rows and E4M3 codes (as
+ * in spec_rope_rows) are those rounded; with factors that are powers of two the
+ * first are exact, and in bf16 too.  Rows that spec_kv4_append would
  * not store (bad lengths, behind the table, bad pages) are left unwritten with the
  * same bits. */
 SV_API sv_status spec_kv4_read(const sv_kv4_read_args *args, void *stream);
@@ -148,7 +149,7 @@ typedef struct sv_kv4_attn_args {
   sv_kv4_cache cache;
   int32_t batch;            /* B, 0..768 */
   int32_t num_q_heads;      /* Hq, a multiple of Hkv; Hq / Hkv <= 256 */
-  int32_t max_q_rows;       /* host bound on R_i, 1..1024 */
+  int32_t max_q_rows;       /* host bound on R_i, 1..1024; times Hq / Hkv <= 16384 */
   int32_t dtype;            /* SV_BF16: q and out */
   int64_t num_rows;         /* R */
   int64_t q_stride;         /* elements from one q row to the next; 0 -> Hq * D */
@@ -175,8 +176,10 @@ SV_API size_t sv_kv4_workspace_bytes(const sv_kv4_attn_args *args);
  * NaN, does not reach it.  Sequences whose cu_q / kv_len disagree with the host
  * bounds (SV_DEV_BAD_LENGTH) or whose tokens pass the table (SV_DEV_CAPACITY) are
  * left unwritten; one with a page outside [0, num_pages) gets NaN in the rows of
- * the parts it was needed for, with SV_DEV_BAD_PARAM.  B * Hkv times the 32-row
- * parts of a block (max_q_rows * Hq / Hkv rows) may not pass 65536. */
+ * the parts it was needed for, with SV_DEV_BAD_PARAM.  A score that passes fp32's
+ * range makes its row and head non-finite.  The max_q_rows * Hq / Hkv rows that a
+ * block has per KV head go in parts of 16 (up to 24: one part), each with its own
+ * pass over the tokens; B * Hkv times the parts may not pass 65536. */
 SV_API sv_status spec_kv4_attn(const sv_kv4_attn_args *args, void *ws, size_t ws_bytes, void *stream);
 
 /* SV_KV4_VERSION of the loaded library. */

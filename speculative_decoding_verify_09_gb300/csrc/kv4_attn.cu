@@ -52,6 +52,7 @@ namespace {
 
 constexpr int kTile = 32;                            // tokens
 constexpr int kMaxBatch = 768;                       // (16 bytes each in shared memory)
+constexpr int kMaxParts = 1024;
 constexpr int kMaxCtas = 192;                        // (sizes the workspace on any host)
 constexpr int kCounters = 65536;                     // first in the workspace, whatever the shape
 // Units that a segment costs beside its tiles (1: 61.4 us, 2: 59.1, 4: 59.9 at the ragged
@@ -919,7 +920,7 @@ sv_status check_attn4(const sv_kv4_attn_args *a, bool tensors) {
     return record_error(SV_ERR_INVALID, "%s: scale must be finite and >= 0", who);
   const Plan p = plan_of(*a);
   const int64_t units = static_cast<int64_t>(a->batch) * Hkv * p.parts;
-  if (p.parts > 255 || units > kCounters)
+  if (p.parts > kMaxParts || units > kCounters)
     return record_error(SV_ERR_UNSUPPORTED, "%s: %d sequences x %d KV heads x %d parts of rows", who,
                         a->batch, Hkv, p.parts);
   const int64_t tokens = static_cast<int64_t>(cache.max_pages) * cache.page_size;
@@ -974,7 +975,8 @@ SV_API sv_status spec_kv4_attn(const sv_kv4_attn_args *a, void *ws, size_t ws_by
   P.num_rows = a->num_rows;
   P.q_stride = a->q_stride ? a->q_stride : static_cast<int64_t>(P.Hq) * a->cache.head_dim;
   const double scale = a->scale != 0.0f ? a->scale : 1.0 / std::sqrt(static_cast<double>(a->cache.head_dim));
-  P.scale_log2 = static_cast<float>(scale * P.cache.k_scale * 1.4426950408889634);
+  // (kept a normal number: 0 or infinity times a masked score of -inf or a score of 0 were NaN)
+  P.scale_log2 = static_cast<float>(std::min(std::max(scale * P.cache.k_scale * 1.4426950408889634, 0x1p-126), 0x1p127));
   P.cu_q = a->cu_q;
   P.kv_len = a->kv_len;
   P.q = static_cast<const uint16_t *>(a->q);

@@ -474,6 +474,24 @@ def test_attention_many_query_heads(api, g):
     c.check()
 
 
+@pytest.mark.parametrize("Hq,rows,bound", [(8, [600, 3], 1024), (2, [1024, 0], 1024)])
+def test_attention_of_long_blocks(api, Hq, rows, bound):
+    """Hundreds of parts (of which the host's bound allows more than there are)."""
+    c = Attn(api, [40, 70], rows, Hq, 1, 64, 16)
+    c.run(max_q_rows=bound)
+    c.check()
+    assert int(c.status.item()) == 0
+
+
+def test_attention_scales_at_fp32s_ends(api):
+    """A scale that underflows with the factor weighs all tokens alike, and masks hold."""
+    c = Attn(api, [37], [3], 2, 1, 128, 16)
+    c.cache.k_scale = 2.0 ** -64
+    c.run(scale=2.0 ** -126)
+    close(c.out, c.q.contiguous(), c.pages, c.table, 16, c.cu, c.kv_len, scale=2.0 ** -126,
+          f=(2.0 ** -64, 0.25))
+
+
 def test_attention_large_scores(api):
     """Scores that grow along the sequence and overflow exp without a maximum."""
     c = Attn(api, [500, 90], [2, 3], 4, 2, 128, 64)
