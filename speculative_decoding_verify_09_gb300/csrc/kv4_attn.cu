@@ -354,12 +354,7 @@ __global__ void __launch_bounds__(Shape<D, NB>::kThreads, 1) kv4_attn_kernel(con
     looked += 32;
   };
   uint8_t *ring = smem + w * Sh::kRingOne;
-  auto issue = [&]() {
-    while (open == 0) {
-      if (looked >= v1) return;
-      look_up();
-      look_up_done();
-    }
+  auto issue_open = [&]() {
     const int st = issued % S;
     if (l == __ffs(open) - 1) {
       const uint32_t bar = smem_u32(&s_bar[w * S + st]), to = smem_u32(ring + st * Sh::kTileBytes);
@@ -374,6 +369,14 @@ __global__ void __launch_bounds__(Shape<D, NB>::kThreads, 1) kv4_attn_kernel(con
     }
     open &= open - 1;
     ++issued;
+  };
+  auto issue = [&]() {
+    while (open == 0) {
+      if (looked >= v1) return;
+      look_up();
+      look_up_done();
+    }
+    issue_open();
   };
   // the segment of list entry v, and this lane's part of its rows of q
   struct Segment { Place p; Sequence s; int h, part, rows; };
@@ -413,7 +416,9 @@ __global__ void __launch_bounds__(Shape<D, NB>::kThreads, 1) kv4_attn_kernel(con
       complete(here);
       fetch_q(here);
       look_up_done();
-      for (int x = 0; x < S; ++x) issue();
+      static_assert(32 / (kHead + 1) >= S, "32 units hold the first stages' tiles");
+#pragma unroll 1
+      for (int x = 0; x < S && open != 0; ++x) issue_open();
     } else {
       here.p = locate(v);
       here.s = data_of(here.p.i);
