@@ -92,6 +92,7 @@ struct Kv4AttnParams {
   Kv4View cache;
   int batch, Hq, g, max_q_rows, parts;               // parts: of max_q_rows * g rows
   int slab_shift;                                    // log2 of a page's slabs, or -1
+  int weighted;                                      // costs of tiles by their columns (NB > 1)
   uint32_t g_inverse;                                // 2^32 / g rounded up: exact quotients of rows
                                                      // below 2^32 / g; 0: g is 1
   int64_t num_rows, q_stride;
@@ -140,6 +141,12 @@ __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, uint32_t
   return done;
 }
 
+// Units of the list, and what they cost.
+struct Amount {
+  int units;
+  uint32_t cost;
+};
+
 // Rows and tokens of a sequence; nothing to do: R = 0.
 struct Sequence {
   int r0, R, L, keys;
@@ -180,10 +187,10 @@ __global__ void __launch_bounds__(Shape<D, NB>::kThreads, 1) kv4_attn_kernel(con
   int32_t *s_start = reinterpret_cast<int32_t *>(smem + Sh::kFixed);         // [batch + 1] units before
   int32_t *s_r0 = s_start + P.batch + 1, *s_rows = s_r0 + P.batch;           // [batch] of sequences with
   int32_t *s_len = reinterpret_cast<int32_t *>(s_rows + P.batch);            // units: first row, rows, tokens
+  uint32_t *s_cost = reinterpret_cast<uint32_t *>(s_len + P.batch);          // [batch + 1] costs before (NB > 1)
   __shared__ __align__(8) uint64_t s_bar[W * S];
   __shared__ uint8_t s_bad[W * S];
   __shared__ Piece s_piece[2 * W];
-  __shared__ int32_t s_scan[W];
   __shared__ int s_share[kMaxCtas + 1], s_last[2], s_from[2], s_to[2];
   const int tid = threadIdx.x, w = tid >> 5, l = tid & 31, r = l >> 2, c = l & 3;
 
@@ -197,12 +204,27 @@ __global__ void __launch_bounds__(Shape<D, NB>::kThreads, 1) kv4_attn_kernel(con
   const int heads = P.cache.heads;
   auto parts_of = [&](int rows) { return (rows * P.g + ROWS - 1) / ROWS; };
   auto each_of = [&](int keys) { return (keys + kTile - 1) / kTile + kHead; };
+  // (costs of a tile with so many columns, of a segment beside its tiles, of one segment of a sequence)
+  auto tile_cost = [&](int columns) { return P.weighted ? 3u + 2u * columns : 1u; };
+  const uint32_t head_cost = P.weighted ? 6 * kHead : kHead;
+  struct Costs { int tiles, parts; uint32_t last_tile, full, head; };        // a full part, all parts of a KV head
+  auto costs_of = [&](int rows, int keys) {
+    Costs c;
+    c.tiles = (keys + kTile - 1) / kTile;
+    c.parts = parts_of(rows);
+    c.last_tile = tile_cost((rows * P.g + 7) / 8 - (c.parts - 1) * NB);
+    c.full = head_cost + c.tiles * tile_cost(NB);
+    c.head = (c.parts - 1) * c.full + head_cost + c.tiles * c.last_tile;
+    return c;
+  };
+  __shared__ Amount s_scan[W];
   auto enter = [&](int i) {                          // the sequence's data; its units
     uint32_t why = 0;
     const Sequence s = sequence_of(P, P.cu_q[i], P.cu_q[i + 1], P.kv_len[i], &why);
     if (why && blockIdx.x == 0) set_status(P.dev_status, why);
     s_r0[i] = s.r0, s_rows[i] = s.R, s_len[i] = s.L;
-    return s.R == 0 ? 0 : each_of(s.keys) * parts_of(s.R) * heads;
+    return Amount{s.R == 0 ? 0 : each_of(s.keys) * parts_of(s.R) * heads,
+                  s.R == 0 || NB == 1 ? 0 : costs_of(s.R, s.keys).head * heads};
   };
   auto inclusive = [&](int x) {                      // sums over a warp's lanes up to this one
 #pragma unroll
@@ -213,32 +235,52 @@ __global__ void __launch_bounds__(Shape<D, NB>::kThreads, 1) kv4_attn_kernel(con
     return x;
   };
   if (P.batch <= 32) {                               // every warp for itself: the same values, no barrier
-    const int n = l < P.batch ? enter(l) : 0, inc = inclusive(n);
-    if (l < P.batch) s_start[l] = inc - n;
+    const Amount n = l < P.batch ? enter(l) : Amount{0, 0};
+    const int inc = inclusive(n.units);
+    if (l < P.batch) s_start[l] = inc - n.units;
     if (l == 31) s_start[P.batch] = inc;
+    if constexpr (NB > 1) {
+      const uint32_t cost = inclusive(n.cost);
+      if (l < P.batch) s_cost[l] = cost - n.cost;
+      if (l == 31) s_cost[P.batch] = cost;
+    }
     __syncwarp();
   } else {
     const int each = (P.batch + NT - 1) / NT, i0 = min(P.batch, tid * each), i1 = min(P.batch, i0 + each);
-    int mine = 0;
+    Amount mine{0, 0};
     for (int i = i0; i < i1; ++i) {
-      const int n = enter(i);
-      s_start[i] = n;
-      mine += n;
+      const Amount n = enter(i);
+      s_start[i] = n.units;
+      mine.units += n.units;
+      if constexpr (NB > 1) {
+        s_cost[i] = n.cost;
+        mine.cost += n.cost;
+      }
     }
-    const int inc = inclusive(mine);
-    if (l == 31) s_scan[w] = inc;
+    const int inc = inclusive(mine.units);
+    const uint32_t cost = NB > 1 ? inclusive(mine.cost) : 0;
+    if (l == 31) s_scan[w] = Amount{inc, cost};
     __syncthreads();
-    int before = inc - mine, total = 0;
+    Amount before{inc - mine.units, cost - mine.cost}, all{0, 0};
     for (int i = 0; i < W; ++i) {
-      if (i < w) before += s_scan[i];
-      total += s_scan[i];
+      const Amount x = s_scan[i];
+      if (i < w) before.units += x.units, before.cost += x.cost;
+      all.units += x.units, all.cost += x.cost;
     }
     for (int i = i0; i < i1; ++i) {
       const int n = s_start[i];
-      s_start[i] = before;
-      before += n;
+      s_start[i] = before.units;
+      before.units += n;
+      if constexpr (NB > 1) {
+        const uint32_t x = s_cost[i];
+        s_cost[i] = before.cost;
+        before.cost += x;
+      }
     }
-    if (tid == 0) s_start[P.batch] = total;
+    if (tid == 0) {
+      s_start[P.batch] = all.units;
+      if constexpr (NB > 1) s_cost[P.batch] = all.cost;
+    }
     __syncthreads();
   }
   const int total = s_start[P.batch];
@@ -273,8 +315,8 @@ __global__ void __launch_bounds__(Shape<D, NB>::kThreads, 1) kv4_attn_kernel(con
   const int ctas = max(1, min(static_cast<int>(gridDim.x), total / kLeast)), b = blockIdx.x;
   if (b >= ctas) return;
   // (a warp's lanes 0 and 1 find its own share's ends, the others part of the table for later)
-  int u0, u1;
-  {
+  int u0, u1, v0, v1;
+  if constexpr (NB == 1) {
     const int x = min(ctas, l < 2 ? b + l : 30 * w + l - 2);
     const int each = total / ctas, v = each * x + min(x, total - each * ctas);
     int to = v;
@@ -286,6 +328,49 @@ __global__ void __launch_bounds__(Shape<D, NB>::kThreads, 1) kv4_attn_kernel(con
     if (l >= 2) s_share[x] = to;
     u0 = __shfl_sync(0xffffffffu, to, 0);
     u1 = __shfl_sync(0xffffffffu, to, 1);
+    v0 = u0 + (u1 - u0) * w / W, v1 = u0 + (u1 - u0) * (w + 1) / W;
+  } else {
+    // (the unit that a cost falls in, and its segment)
+    struct Cut { int unit, at, left; uint32_t into, rest; };           // units, costs of the segment before and after
+    auto cut_at = [&](uint32_t x) {
+      int lo = 0, hi = P.batch;
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (s_cost[mid] <= x) lo = mid; else hi = mid;
+      }
+      const Costs k = costs_of(s_rows[lo], s_rows[lo] + s_len[lo]);
+      Cut c;
+      c.into = x - s_cost[lo];
+      const int h = c.into / k.head;
+      c.into -= h * k.head;
+      const int part = min(k.parts - 1, static_cast<int>(c.into / k.full));
+      c.into -= part * k.full;
+      const uint32_t one = part == k.parts - 1 ? k.last_tile : tile_cost(NB);
+      c.rest = head_cost + k.tiles * one - c.into;
+      c.at = c.into < head_cost ? c.into * kHead / head_cost : kHead + (c.into - head_cost) / one;
+      c.left = kHead + k.tiles - c.at;
+      c.unit = s_start[lo] + (h * k.parts + part) * (kHead + k.tiles) + c.at;
+      return c;
+    };
+    const uint32_t sum = s_cost[P.batch], each = sum / ctas;
+    const int x = min(ctas, l < 2 ? b + l : 30 * w + l - 2);
+    uint32_t from = each * x + min(static_cast<uint32_t>(x), sum - each * ctas);
+    int to = x == 0 ? 0 : total;
+    if (x > 0 && x < ctas) {
+      const Cut c = cut_at(from);
+      to = c.unit;
+      if (c.at <= min(c.left, kSnap)) to -= c.at, from -= c.into;
+      else if (c.left <= kSnap) to += c.left, from += c.rest;
+    }
+    if (l >= 2) s_share[x] = to;
+    u0 = __shfl_sync(0xffffffffu, to, 0);
+    u1 = __shfl_sync(0xffffffffu, to, 1);
+    const uint32_t x0 = __shfl_sync(0xffffffffu, from, 0), x1 = __shfl_sync(0xffffffffu, from, 1);
+    // (lanes 0 and 1 find the run's ends)
+    const int y = w + (l & 1);
+    const int end = y == 0 ? u0 : y == W || x1 <= x0 ? u1 : min(u1, max(u0, cut_at(x0 + (x1 - x0) * y / W).unit));
+    v0 = __shfl_sync(0xffffffffu, end, 0);
+    v1 = __shfl_sync(0xffffffffu, end, 1);
   }
   static_assert(30 * W > kMaxCtas, "a table entry per lane");
   auto cta_of = [&](int v) {                         // the last share that starts at or before v
@@ -296,7 +381,6 @@ __global__ void __launch_bounds__(Shape<D, NB>::kThreads, 1) kv4_attn_kernel(con
     }
     return lo;
   };
-  const int v0 = u0 + (u1 - u0) * w / W, v1 = u0 + (u1 - u0) * (w + 1) / W;
 
   // ---- this warp's copies: a lane finds the slabs of each of the next 32 units, in two steps
   // (their pages asked for, their addresses)
@@ -890,7 +974,7 @@ Plan plan_of(const sv_kv4_attn_args &a) {
 template <int D, int NB>
 cudaError_t launch_shape(const Kv4AttnParams &P, int ctas, cudaStream_t s) {
   using Sh = Shape<D, NB>;
-  const size_t smem = Sh::kFixed + (static_cast<size_t>(P.batch) * 4 + 1) * 4;
+  const size_t smem = Sh::kFixed + (static_cast<size_t>(P.batch) * 5 + 2) * 4;
   return launch_after_previous(kv4_attn_kernel<D, NB>, dim3(ctas), Sh::kThreads, smem, s, P);
 }
 template <int D>
@@ -977,6 +1061,9 @@ SV_API sv_status spec_kv4_attn(const sv_kv4_attn_args *a, void *ws, size_t ws_by
   P.g_inverse = P.g == 1 ? 0 : static_cast<uint32_t>(((uint64_t{1} << 32) + P.g - 1) / P.g);
   P.max_q_rows = a->max_q_rows;
   P.parts = p.parts;
+  const int64_t units = static_cast<int64_t>(P.batch) * P.cache.heads * p.parts,
+                tiles = (static_cast<int64_t>(P.cache.max_pages) * P.cache.page_size + kTile - 1) / kTile;
+  P.weighted = units * ((3 + 2 * p.nb) * tiles + 6 * kHead) < (int64_t{1} << 32);
   P.num_rows = a->num_rows;
   P.q_stride = a->q_stride ? a->q_stride : static_cast<int64_t>(P.Hq) * a->cache.head_dim;
   const double scale = a->scale != 0.0f ? a->scale : 1.0 / std::sqrt(static_cast<double>(a->cache.head_dim));
