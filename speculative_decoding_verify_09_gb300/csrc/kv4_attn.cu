@@ -17,7 +17,7 @@
 // bulk copies, which run ahead across segments; no warp waits for another before its
 // run is done.  A segment that lies in one run is finished by its warp.  The pieces of
 // the others are left in shared memory, joined there by the CTA, and, where a segment
-// passes the CTA's runs, joined in the workspace by the last CTA to arrive, in order
+// passes the CTA's runs, joined in the workspace, in order, by the last warp to leave a row's
 // (runs per CTA instead, its warps taking tiles in turn and meeting at every segment's
 // end: 160 us against 76 at 32 ragged GQA sequences).
 //
@@ -51,10 +51,11 @@ namespace sv {
 namespace {
 
 constexpr int kTile = 32;                            // tokens
-constexpr int kMaxBatch = 768;                       // (16 bytes each in shared memory)
+constexpr int kMaxBatch = 768;                       // (16 or 20 bytes each in shared memory)
 constexpr int kMaxParts = 1024;
 constexpr int kMaxCtas = 192;                        // (sizes the workspace on any host)
-constexpr int kCounters = 65536;                     // first in the workspace, whatever the shape
+constexpr int kCounters = 24 * kMaxCtas;             // first in the workspace, whatever the shape
+constexpr int kMaxUnits = 65536;                     // sequences times KV heads times parts
 // Units that a segment costs beside its tiles (1: 61.4 us, 2: 59.1, 4: 59.9 at the ragged
 // verify rows above).
 constexpr int kHead = 2;
@@ -101,7 +102,7 @@ struct Kv4AttnParams {
   const uint16_t *q;
   uint16_t *out;
   uint32_t *dev_status;
-  uint32_t *counters;                                // [batch, heads, parts]
+  uint32_t *counters;                                // [CTAs, rows] of the segment that a CTA begins and passes on
   float *part_o;                                     // [2 CTAs, rows, D]
   float2 *part_ml;                                   // [2 CTAs, rows] maximum, sum
   uint32_t spin_limit;
@@ -173,7 +174,6 @@ struct __align__(16) Piece {
   int seg;                                           // the segment's first unit; < 0: no piece
   int ends;                                          // 1: holds the segment's first tile, 2: its last
   int tiles;                                         // of the segment
-  int counter;                                       // its place among the counters
   int rows, first_row, r0, h;                        // its rows: packed rows of a block at r0, KV head
 };
 
@@ -191,7 +191,7 @@ __global__ void __launch_bounds__(Shape<D, NB>::kThreads, 1) kv4_attn_kernel(con
   __shared__ __align__(8) uint64_t s_bar[W * S];
   __shared__ uint8_t s_bad[W * S];
   __shared__ Piece s_piece[2 * W];
-  __shared__ int s_share[kMaxCtas + 1], s_last[2], s_from[2], s_to[2];
+  __shared__ int s_share[kMaxCtas + 1];
   const int tid = threadIdx.x, w = tid >> 5, l = tid & 31, r = l >> 2, c = l & 3;
 
   if (l < S) bar_init(smem_u32(&s_bar[w * S + l]));  // (a warp's barriers and pieces are its own)
@@ -202,6 +202,9 @@ __global__ void __launch_bounds__(Shape<D, NB>::kThreads, 1) kv4_attn_kernel(con
 
   // units (tiles, and kHead for each segment) before each sequence's first
   const int heads = P.cache.heads;
+  auto head_of = [&](int unit, int parts) {          // unit / parts, exact: unit below 2^16
+    return parts == 1 ? unit : static_cast<int>(__fdividef(static_cast<float>(unit) + 0.5f, static_cast<float>(parts)));
+  };
   auto parts_of = [&](int rows) { return (rows * P.g + ROWS - 1) / ROWS; };
   auto each_of = [&](int keys) { return (keys + kTile - 1) / kTile + kHead; };
   // (costs of a tile with so many columns, of a segment beside its tiles, of one segment of a sequence)
@@ -332,6 +335,12 @@ __global__ void __launch_bounds__(Shape<D, NB>::kThreads, 1) kv4_attn_kernel(con
   } else {
     // (the unit that a cost falls in, and its segment)
     struct Cut { int unit, at, left; uint32_t into, rest; };           // units, costs of the segment before and after
+    auto quotient = [&](uint32_t a, uint32_t d) {    // below 2^16: by floats it is off by one at most
+      uint32_t q = static_cast<uint32_t>(__fdividef(static_cast<float>(a), static_cast<float>(d)));
+      const int32_t rem = static_cast<int32_t>(a - q * d);
+      q += rem < 0 ? -1 : static_cast<uint32_t>(rem) >= d ? 1 : 0;
+      return static_cast<int>(q);
+    };
     auto cut_at = [&](uint32_t x) {
       int lo = 0, hi = P.batch;
       while (hi - lo > 1) {
@@ -341,13 +350,15 @@ __global__ void __launch_bounds__(Shape<D, NB>::kThreads, 1) kv4_attn_kernel(con
       const Costs k = costs_of(s_rows[lo], s_rows[lo] + s_len[lo]);
       Cut c;
       c.into = x - s_cost[lo];
-      const int h = c.into / k.head;
+      const int h = quotient(c.into, k.head);
       c.into -= h * k.head;
-      const int part = min(k.parts - 1, static_cast<int>(c.into / k.full));
+      const int part = k.parts == 1 ? 0 : min(k.parts - 1, quotient(c.into, k.full));
       c.into -= part * k.full;
       const uint32_t one = part == k.parts - 1 ? k.last_tile : tile_cost(NB);
       c.rest = head_cost + k.tiles * one - c.into;
-      c.at = c.into < head_cost ? c.into * kHead / head_cost : kHead + (c.into - head_cost) / one;
+      const uint32_t x_tiles = c.into - head_cost;
+      c.at = c.into < head_cost ? (P.weighted ? c.into / 6 : c.into)
+                                : kHead + (one == 1 ? x_tiles : one == 5 ? x_tiles / 5 : one == 7 ? x_tiles / 7 : x_tiles / 9);
       c.left = kHead + k.tiles - c.at;
       c.unit = s_start[lo] + (h * k.parts + part) * (kHead + k.tiles) + c.at;
       return c;
@@ -421,7 +432,7 @@ __global__ void __launch_bounds__(Shape<D, NB>::kThreads, 1) kv4_attn_kernel(con
     from_bad = false;
     if (real) {
       const int parts = parts_of(ahead_s.R);
-      const int64_t head = (parts == 1 ? ahead.unit : ahead.unit / parts) * head_bytes(P.cache);
+      const int64_t head = head_of(ahead.unit, parts) * head_bytes(P.cache);
       const int64_t page_bytes = P.cache.heads * head_bytes(P.cache);
       if (page0 < 0 || page0 >= P.cache.num_pages || page1 < 0 || page1 >= P.cache.num_pages) {
         set_status(P.dev_status, SV_DEV_BAD_PARAM);
@@ -466,7 +477,7 @@ __global__ void __launch_bounds__(Shape<D, NB>::kThreads, 1) kv4_attn_kernel(con
   struct Segment { Place p; Sequence s; int h, part, rows; };
   auto complete = [&](Segment &x) {
     const int parts = parts_of(x.s.R);
-    x.h = parts == 1 ? x.p.unit : x.p.unit / parts;
+    x.h = head_of(x.p.unit, parts);
     x.part = x.p.unit - x.h * parts;
     x.rows = min(ROWS, x.s.R * P.g - x.part * ROWS);
   };
@@ -778,8 +789,7 @@ __global__ void __launch_bounds__(Shape<D, NB>::kThreads, 1) kv4_attn_kernel(con
           to[y / 2] = make_float4(o[y][nb][x], o[y][nb][2 + x], o[y + 1][nb][x], o[y + 1][nb][2 + x]);
       }
     if (l == 0)
-      s_piece[e] = Piece{seg, (starts ? 1 : 0) | (stops ? 2 : 0), p.tiles, p.i * heads * P.parts + p.unit,
-                         rows, first_row, s.r0, h};
+      s_piece[e] = Piece{seg, (starts ? 1 : 0) | (stops ? 2 : 0), p.tiles, rows, first_row, s.r0, h};
   }
 
   // ---- the pieces joined: those of a segment are neighbours in the list of 2 W
@@ -812,6 +822,7 @@ __global__ void __launch_bounds__(Shape<D, NB>::kThreads, 1) kv4_attn_kernel(con
   };
   int jobs = 0, passing = 0;                         // rows handed out; segments that pass this CTA
   int open0 = 0, open1 = 0;                          // (their first pieces)
+  int left = 0, left_which = 0, left_row = 0;        // rows left in the workspace by this warp; lane n has the n-th
   while (leaders) {
     const int lead = __ffs(leaders) - 1;
     leaders &= leaders - 1;
@@ -838,6 +849,8 @@ __global__ void __launch_bounds__(Shape<D, NB>::kThreads, 1) kv4_attn_kernel(con
 #pragma unroll
         for (int y = 0; y < E; y += 2) *reinterpret_cast<float2 *>(to + y) = make_float2(x[y], x[y + 1]);
         if (l == 0) P.part_ml[slot * ROWS + n] = make_float2(top, all);
+        if (l == left) left_which = passing, left_row = n;
+        ++left;
       }
     }
     jobs += head.rows;
@@ -848,104 +861,68 @@ __global__ void __launch_bounds__(Shape<D, NB>::kThreads, 1) kv4_attn_kernel(con
   }
   if (passing == 0) return;
 
-  // ---- segments of several CTAs: the last of them joins what all have left
-  const Piece &mine = s_piece[tid == 1 ? open1 : open0];
-  const int from_cta = tid < passing ? cta_of(mine.seg + kHead) : 0;
-  const int to_cta = tid < passing ? cta_of(mine.seg + kHead + mine.tiles - 1) : 0;
-  __syncthreads();
-  if (tid < passing) {
-    const uint32_t others = to_cta - from_cta;
-    __threadfence();                                 // (the CTA's writes, seen by this thread at the barrier)
-    s_last[tid] = atomicInc(P.counters + mine.counter, others) == others;
-    __threadfence();
-    s_from[tid] = from_cta;
-    s_to[tid] = to_cta;
-  }
-  __syncthreads();
+  // ---- segments of several CTAs.  Each is known by the CTA that its first tile is in, and goes no
+  // further back than that.  A row's pieces are joined, in order, by the last warp to leave one,
+  // a lane per piece for the weights.
+  const Piece &lane_piece = s_piece[(l & 1) == 0 ? open0 : open1];
+  const int lane_cta = cta_of(lane_piece.seg + kHead + (l & 2 ? lane_piece.tiles - 1 : 0));
+  const int from_a = __shfl_sync(0xffffffffu, lane_cta, 0), from_b = __shfl_sync(0xffffffffu, lane_cta, 1);
+  const int pass_a = __shfl_sync(0xffffffffu, lane_cta, 2) - from_a,         // CTAs after the first
+            pass_b = __shfl_sync(0xffffffffu, lane_cta, 3) - from_b;
   struct __align__(8) Some { float x[E]; };
-  for (int which = 0; which < passing; ++which) {
-    if (!s_last[which]) continue;
-    const Piece head = s_piece[which == 0 ? open0 : open1];
-    const int c0 = s_from[which], count = s_to[which] - c0 + 1;
-    auto place_of = [&](int x, int n) { return static_cast<int64_t>(2 * (c0 + x) + (x == 0 ? 1 : 0)) * ROWS + n; };
-    auto part = [&](int x, int n) {
-      const float *from = P.part_o + place_of(x, n) * D + E * l;
-      Some v;
+  auto place_of = [&](int c0, int x, int n) { return static_cast<int64_t>(2 * (c0 + x) + (x == 0 ? 1 : 0)) * ROWS + n; };
+  auto part = [&](int c0, int x, int n) {
+    const float *from = P.part_o + place_of(c0, x, n) * D + E * l;
+    Some v;
 #pragma unroll
-      for (int z = 0; z < E; z += 2) {
-        const float2 two = __ldcg(reinterpret_cast<const float2 *>(from + z));
-        v.x[z] = two.x, v.x[z + 1] = two.y;
-      }
-      return v;
-    };
-    if (count <= 32) {
-      // A warp per row, (up to three) side by side, a lane per piece for the weights; the first
-      // pieces' sums are under way meanwhile.
-      constexpr int kSide = (ROWS + W - 1) / W, kFirst = kSide == 1 ? 4 : 2;
-      float2 ml[kSide];
-      Some v[kSide][kFirst];
-#pragma unroll
-      for (int z = 0; z < kSide; ++z) {
-        const int n = w + z * W;
-        ml[z] = n < head.rows && l < count ? __ldcg(&P.part_ml[place_of(l, n)]) : make_float2(-INFINITY, 0.0f);
-#pragma unroll
-        for (int y = 0; y < kFirst; ++y)
-          if (n < head.rows && y < count) v[z][y] = part(y, n);
-      }
-#pragma unroll
-      for (int z = 0; z < kSide; ++z) {
-        const int n = w + z * W;
-        if (n >= head.rows) continue;
-        const float top = warp_max(ml[z].x), base = top == -INFINITY ? 0.0f : top;
-        float f = fast_exp2(ml[z].x - base);
-        f *= P.cache.v_scale / warp_sum(f * ml[z].y);
-        float x[E] = {};
-#pragma unroll
-        for (int y = 0; y < kFirst; ++y)
-          if (y < count) add(x, __shfl_sync(0xffffffffu, f, y), v[z][y].x);
-#pragma unroll 4
-        for (int y = kFirst; y < count; ++y) add(x, __shfl_sync(0xffffffffu, f, y), part(y, n).x);
-        store_row(head, n, x, P.cache.v_scale);      // (the weights hold the scale)
-      }
-      continue;
+    for (int z = 0; z < E; z += 2) {
+      const float2 two = __ldcg(reinterpret_cast<const float2 *>(from + z));
+      v.x[z] = two.x, v.x[z + 1] = two.y;
     }
-    // Pieces of many CTAs: weights in shared memory, a warp per row, then sums by several warps
-    // for each row, which take the pieces in turn.
-    float *s_weight = reinterpret_cast<float *>(smem);               // [ROWS, CTAs of the segment]
-    float *s_sum = s_weight + ROWS * kMaxCtas;                       // [W, D]
-    for (int n = w; n < head.rows; n += W) {
-      float top = -INFINITY, all = 0.0f;
-      for (int x = l; x < count; x += 32) top = fmaxf(top, __ldcg(&P.part_ml[place_of(x, n)]).x);
-      top = warp_max(top);
-      const float base = top == -INFINITY ? 0.0f : top;
-      for (int x = l; x < count; x += 32) {
-        const float2 ml = __ldcg(&P.part_ml[place_of(x, n)]);
-        const float f = fast_exp2(ml.x - base);
-        s_weight[n * kMaxCtas + x] = f;
+    return v;
+  };
+  __threadfence();                                   // (each lane's writes, before the warp's counts)
+  __syncwarp();
+  bool last = false;
+  if (l < left) {
+    const uint32_t others = left_which ? pass_b : pass_a;
+    last = atomicInc(P.counters + (left_which ? from_b : from_a) * ROWS + left_row, others) == others;
+    __threadfence();
+  }
+  __syncwarp();
+  for (uint32_t todo = __ballot_sync(0xffffffffu, last); todo; todo &= todo - 1) {
+    const int who = __ffs(todo) - 1, which = __shfl_sync(0xffffffffu, left_which, who),
+              n = __shfl_sync(0xffffffffu, left_row, who);
+    const int c0 = which ? from_b : from_a, count = (which ? pass_b : pass_a) + 1;
+    constexpr int kFirst = 3;                        // sums under way together with the weights
+    auto weight = [&](int y) {                       // maximum and sum of piece y + lane
+      return y + l < count ? __ldcg(&P.part_ml[place_of(c0, y + l, n)]) : make_float2(-INFINITY, 0.0f);
+    };
+    float2 ml = weight(0);
+    Some v[kFirst];
+#pragma unroll
+    for (int y = 0; y < kFirst; ++y)
+      if (y < count) v[y] = part(c0, y, n);
+    float top = ml.x;
+    for (int y = 32; y < count; y += 32) top = fmaxf(top, weight(y).x);
+    top = warp_max(top);
+    const float base = top == -INFINITY ? 0.0f : top;
+    float f = fast_exp2(ml.x - base), all = f * ml.y;
+    float x[E] = {};
+#pragma unroll
+    for (int y = 0; y < kFirst; ++y)
+      if (y < count) add(x, __shfl_sync(0xffffffffu, f, y), v[y].x);
+    for (int y0 = 0; y0 < count; y0 += 32) {
+      if (y0 > 0) {
+        ml = weight(y0);
+        f = fast_exp2(ml.x - base);
         all = fmaf(f, ml.y, all);
       }
-      const float f = P.cache.v_scale / warp_sum(all);
-      for (int x = l; x < count; x += 32) s_weight[n * kMaxCtas + x] *= f;
+#pragma unroll 8
+      for (int y = y0 == 0 ? kFirst : 0; y < min(32, count - y0); ++y)
+        add(x, __shfl_sync(0xffffffffu, f, y), part(c0, y0 + y, n).x);
     }
-    __syncthreads();
-    const int share = max(1, W / head.rows), sub = w % share;
-    for (int n0 = 0; n0 < head.rows; n0 += W / share) {
-      const int n = n0 + w / share;
-      const bool on = n < head.rows && w / share < W / share;
-      float x[E] = {};
-      if (on) {
-#pragma unroll 4
-        for (int y = sub; y < count; y += share) add(x, s_weight[n * kMaxCtas + y], part(y, n).x);
-      }
-#pragma unroll
-      for (int z = 0; z < E; ++z) s_sum[w * D + E * l + z] = x[z];
-      __syncthreads();
-      if (on && sub == 0) {
-        for (int y = 1; y < share; ++y) add(x, 1.0f, s_sum + (w + y) * D + E * l);
-        store_row(head, n, x, P.cache.v_scale);
-      }
-      __syncthreads();
-    }
+    store_row(s_piece[which ? open1 : open0], n, x, warp_sum(all));
   }
 }
 
@@ -974,7 +951,7 @@ Plan plan_of(const sv_kv4_attn_args &a) {
 template <int D, int NB>
 cudaError_t launch_shape(const Kv4AttnParams &P, int ctas, cudaStream_t s) {
   using Sh = Shape<D, NB>;
-  const size_t smem = Sh::kFixed + (static_cast<size_t>(P.batch) * 5 + 2) * 4;
+  const size_t smem = Sh::kFixed + (static_cast<size_t>(P.batch) * (NB == 1 ? 4 : 5) + 2) * 4;
   return launch_after_previous(kv4_attn_kernel<D, NB>, dim3(ctas), Sh::kThreads, smem, s, P);
 }
 template <int D>
@@ -1009,7 +986,7 @@ sv_status check_attn4(const sv_kv4_attn_args *a, bool tensors) {
     return record_error(SV_ERR_INVALID, "%s: scale must be finite and >= 0", who);
   const Plan p = plan_of(*a);
   const int64_t units = static_cast<int64_t>(a->batch) * Hkv * p.parts;
-  if (p.parts > kMaxParts || units > kCounters)
+  if (p.parts > kMaxParts || units > kMaxUnits)
     return record_error(SV_ERR_UNSUPPORTED, "%s: %d sequences x %d KV heads x %d parts of rows", who,
                         a->batch, Hkv, p.parts);
   const int64_t tokens = static_cast<int64_t>(cache.max_pages) * cache.page_size;
