@@ -501,11 +501,17 @@ struct ReadParams {
   uint32_t *dev_status;
 };
 
-// A thread takes 8 elements (4 bytes of codes, a scale that two share) at a time from the
-// row's K and V heads, so that a warp writes whole lines, kReads of them under way.
-constexpr int kReads = 4;
+// A thread takes 16 bytes of a row of the output at a time (of fp32 32), 8 elements (4 bytes of
+// codes, a scale that two threads share) or 16, so that a warp writes whole lines, of kReads K and
+// V heads each, all asked for before the first is written (17936 rows of 8 heads as E4M3 14.8 us;
+// K before V 15.6, and 8 elements at a time 16.6; kReads 4 with E4M3 20.3, but 8192 rows of 32 as
+// bf16 31.9 us against 33.2 with 2).
 template <typename T>
-__global__ void __launch_bounds__(kNT, sizeof(T) == 1 ? 6 : 4) kv4_read_kernel(const ReadParams P) {
+constexpr int kItem = sizeof(T) == 1 ? 16 : 8;
+template <typename T>
+constexpr int kReadsOf = sizeof(T) == 2 ? 4 : 2;
+template <typename T>
+__global__ void __launch_bounds__(kNT, sizeof(T) == 1 ? 5 : 4) kv4_read_kernel(const ReadParams P) {
   const int row_threads = 1 << P.row_shift;
   const int rl = threadIdx.x >> P.row_shift, t = threadIdx.x & (row_threads - 1);
   wait_for_previous();
@@ -525,67 +531,78 @@ __global__ void __launch_bounds__(kNT, sizeof(T) == 1 ? 6 : 4) kv4_read_kernel(c
   if (why && t == 0 && blockIdx.y == 0) set_status(P.dev_status, why);
   if (slab == nullptr) return;
   const int token = static_cast<int>(pos) & (kSlab - 1);
-  const int shift = P.D == 128 ? 4 : 3;              // log2 of the items of a head
+  constexpr int N = kItem<T>, WORDS = N / 8, kReads = kReadsOf<T>;
+  const int shift = (P.D == 128 ? 4 : 3) - (N == 16);                // log2 of the items of a head
   const int heads = P.cache.heads, g = t & ((1 << shift) - 1);
   const int each = row_threads >> shift, step = each * gridDim.y;    // heads at once: of a slice, of all
   const int64_t head = head_bytes(P.cache);
-  const int scale_at = slab_k_scales(P.D) + token * (P.D / 16) + (g >> 1), code_at = token * (P.D / 2) + 4 * g;
+  const int scale_at = slab_k_scales(P.D) + token * (P.D / 16) + (N == 16 ? g : g >> 1), code_at = token * (P.D / 2) + N / 2 * g;
+  const int h0 = blockIdx.y * each + (t >> shift);
+  const uint8_t *at = slab + h0 * head;
+  const int64_t to = (row * heads + h0) * P.D + N * g;
+  const bool both[2] = {P.k_out != nullptr, P.v_out != nullptr};
+  for (int h = h0, done = 0; h < heads; h += kReads * step, done += kReads * step) {
+    uint32_t codes[2][kReads][WORDS], scale[2][kReads];
 #pragma unroll
-  for (int is_v = 0; is_v < 2; ++is_v) {
-    T *out = static_cast<T *>(is_v ? P.v_out : P.k_out);
-    if (out == nullptr) continue;
-    const int h0 = blockIdx.y * each + (t >> shift);
-    const float factor = is_v ? P.cache.v_scale : P.cache.k_scale;
-    const float to_scale = is_v ? P.v_scale : P.k_scale, inverse = is_v ? P.v_inverse : P.k_inverse;
-    const uint32_t brief = is_v ? P.v_short : P.k_short;
-    const uint8_t *at = slab + (is_v ? slab_v(P.D) : 0) + h0 * head;
-    out += (row * heads + h0) * P.D + 8 * g;
-    for (int h = h0; h < heads; h += kReads * step) {
-      uint32_t codes[kReads], scale[kReads];
+    for (int is_v = 0; is_v < 2; ++is_v)
 #pragma unroll
       for (int u = 0; u < kReads; ++u)
-        if (h + u * step < heads) {
-          codes[u] = *reinterpret_cast<const uint32_t *>(at + u * step * head + code_at);
-          scale[u] = at[u * step * head + scale_at];
+        if (both[is_v] && h + u * step < heads) {
+          const uint8_t *from = at + (done + u * step) * head + (is_v ? slab_v(P.D) : 0);
+          if constexpr (WORDS == 2) {
+            const uint2 two = *reinterpret_cast<const uint2 *>(from + code_at);
+            codes[is_v][u][0] = two.x, codes[is_v][u][1] = two.y;
+          } else {
+            codes[is_v][u][0] = *reinterpret_cast<const uint32_t *>(from + code_at);
+          }
+          scale[is_v][u] = from[scale_at];
         }
 #pragma unroll
-      for (int u = 0; u < kReads; ++u) {
-        if (h + u * step >= heads) continue;
-        uint32_t pair[4];
-        e2m1x8_to_f16x2(codes[u], pair);
-        uint32_t s = e4m3x2_to_f16x2(scale[u] | scale[u] << 8);
-        if (brief != 0) s = mul_f16x2(s, brief);
-        uint32_t y[4];
+    for (int is_v = 0; is_v < 2; ++is_v) {
+      const float factor = is_v ? P.cache.v_scale : P.cache.k_scale;
+      const float to_scale = is_v ? P.v_scale : P.k_scale, inverse = is_v ? P.v_inverse : P.k_inverse;
+      const uint32_t brief = is_v ? P.v_short : P.k_short;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) y[i] = mul_f16x2(pair[i], s);    // exact
+      for (int u = 0; u < kReads; ++u) {
+        if (!both[is_v] || h + u * step >= heads) continue;
+        T *out = static_cast<T *>(is_v ? P.v_out : P.k_out) + to + (done + u * step) * P.D;
+        uint32_t s = e4m3x2_to_f16x2(scale[is_v][u] | scale[is_v][u] << 8);
+        if (brief != 0) s = mul_f16x2(s, brief);
+        uint32_t y[4 * WORDS];
+#pragma unroll
+        for (int n = 0; n < WORDS; ++n) {
+          uint32_t pair[4];
+          e2m1x8_to_f16x2(codes[is_v][u][n], pair);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) y[4 * n + i] = mul_f16x2(pair[i], s);    // exact
+        }
         if constexpr (sizeof(T) == 1) {
           if (brief != 0) {
-            *reinterpret_cast<uint2 *>(out + u * step * P.D) =
-                make_uint2(f16x2_to_e4m3x2(y[0]) | f16x2_to_e4m3x2(y[1]) << 16,
-                           f16x2_to_e4m3x2(y[2]) | f16x2_to_e4m3x2(y[3]) << 16);
+            uint32_t z[2 * WORDS];
+#pragma unroll
+            for (int i = 0; i < 2 * WORDS; ++i) z[i] = f16x2_to_e4m3x2(y[2 * i]) | f16x2_to_e4m3x2(y[2 * i + 1]) << 16;
+            *reinterpret_cast<uint4 *>(out) = make_uint4(z[0], z[1], z[2], z[3]);
             continue;
           }
         }
-        float x[8];
+        float x[N];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < N / 2; ++i) {
           x[2 * i] = f16_bits_to_f32(y[i] & 0xFFFFu);
           x[2 * i + 1] = f16_bits_to_f32(y[i] >> 16);
         }
         if (brief == 0) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) x[i] = __fmul_rn(x[i], factor);
+          for (int i = 0; i < N; ++i) x[i] = __fmul_rn(x[i], factor);
         }
         if constexpr (sizeof(T) == 1) {
-          store_codes(out + u * step * P.D, x, to_scale, inverse);
+          store_codes(out, x, to_scale, inverse);
         } else {
           Vec<T, 8> v;
           v.set(x);
-          v.store(out + u * step * P.D);
+          v.store(out);
         }
       }
-      at += kReads * step * head;
-      out += kReads * step * P.D;
     }
   }
 }
@@ -844,10 +861,10 @@ SV_API sv_status spec_kv4_read(const sv_kv4_read_args *a, void *stream) {
   // many; else as many as a pass over K and V takes, in slices of a head per thread.
   const int sms = device_sms();
   if (sms <= 0) return record_error(SV_ERR_CUDA, "%s: no current CUDA device", who);
-  const int threads = P.cache.heads * (P.D / 8);     // for one head each
+  const int threads = P.cache.heads * (P.D / (codes ? kItem<uint8_t> : kItem<float>));          // an item each
   P.row_shift = 5;
   int slices = 1;
-  if (P.slots * threads < int64_t{1024} * sms * kReads) {
+  if (P.slots * threads < int64_t{2048} * sms) {
     while (P.row_shift < 7 && (1 << P.row_shift) < threads) ++P.row_shift;
     slices = (threads + (1 << P.row_shift) - 1) >> P.row_shift;
   }
