@@ -31,11 +31,13 @@
 // next to 144 from memory: as long as the register-fed products of 40 rows take.
 //
 // Bounds, D = 128, 8 KV heads, device time per call: 4 sequences of 128k tokens,
-// single rows, 105 us = 5.7 TB/s (0.84 of the measured copy rate), 614 instructions a
+// single rows, 104 us = 5.8 TB/s (0.86 of the measured copy rate), 614 instructions a
 // tile of 32 tokens issued at 2.6 of 4 per clock, the ALU pipe (conversions, byte
-// moves) at 0.46; 16 and 24 rows take 161 and 220 us, 67 instructions more a tile for
-// each 8 rows but 12 and 8 warps, and fewer registers free to overlap in.  Short
-// lists are bound by latency: 8 sequences of 32 heads over 512 to 2048 tokens 20 us,
+// moves) at 0.46; 16 and 24 rows take 151 and 208 us, 67 instructions more a tile for
+// each 8 rows but 12 and 8 warps, and fewer registers free to overlap in.  Blocks of
+// more rows go in parts, each of which converts the tokens anew: 32 ragged sequences
+// of 2 to 9 rows of 4 heads take 59 us, 5 times the time of their bytes.  Short
+// lists are bound by latency: 8 sequences of 32 heads over 512 to 2048 tokens 18.6 us,
 // of which 4 us pass before the first copies (bounds, places, pages: one dependent
 // load after the other), 2 until the first tile is there, 7 in tiles, the rest in the
 // slowest warps and the joining.
@@ -56,21 +58,21 @@ constexpr int kMaxParts = 1024;
 constexpr int kMaxCtas = 192;                        // (sizes the workspace on any host)
 constexpr int kCounters = 24 * kMaxCtas;             // first in the workspace, whatever the shape
 constexpr int kMaxUnits = 65536;                     // sequences times KV heads times parts
-// Units that a segment costs beside its tiles (1: 61.4 us, 2: 59.1, 4: 59.9 at the ragged
-// verify rows above).
+// Units that a segment costs beside its tiles (at the ragged verify rows above and 13 small ragged
+// sequences 1: 62.3 and 6.7 us, 2: 58.6 and 6.7, 4: 57.9 and 7.0).
 constexpr int kHead = 2;
-// Units of a CTA's share at least (13 small ragged sequences 6.8 us, with 16 7.7), and by how many
-// it may end early or late to end with a segment (0: the same small sequences 9.0 us, 8: 6.8;
-// 16: shares so unequal that 8 sequences of 32 heads take 20.8 us instead of 20.0).
+// Units of a CTA's share at least (the small sequences 6.7 us, with 16 7.5), and by how many it may
+// end early or late to end with a segment (0: the same small sequences 8.3 us, 8: 6.7; 16: shares
+// so unequal that 8 sequences of 32 heads take 19.2 us instead of 18.5).
 constexpr int kLeast = 4;
 constexpr int kSnap = 8;
-// log2 the maximum may grow before sums are rescaled (0: 63.2 us, 8: 59.1; weights up to 2^8 lose
+// log2 the maximum may grow before sums are rescaled (0: 61.3 us, 8: 58.6; weights up to 2^8 lose
 // nothing in f16).
 constexpr float kLate = 8.0f;
 
 // Warps and stages of a warp's ring; NB: 8-row columns of a part.  As many warps as registers
 // allow (128, 168, 255 a thread; 12 instead of 16 warps with three stages: 116 us against 105
-// at 128k tokens, 8 with four: 128), and two stages each, which keep 147 KB under way; a
+// at 128k tokens before other steps, 8 with four: 128), and two stages each, which keep 147 KB under way; a
 // third one fits only where there are 8 warps.
 template <int D, int NB>
 struct Shape {
@@ -207,10 +209,12 @@ __global__ void __launch_bounds__(Shape<D, NB>::kThreads, 1) kv4_attn_kernel(con
   };
   auto parts_of = [&](int rows) { return (rows * P.g + ROWS - 1) / ROWS; };
   auto each_of = [&](int keys) { return (keys + kTile - 1) / kTile + kHead; };
-  // (costs of a tile with so many columns, of a segment beside its tiles, of one segment of a sequence)
+  // Costs of a tile with so many columns (two take 1.4 times as long as one; with equal costs the
+  // ragged verify rows take 59.6 us instead of 58.6), of a segment beside its tiles, and of a
+  // sequence's parts.
   auto tile_cost = [&](int columns) { return P.weighted ? 3u + 2u * columns : 1u; };
   const uint32_t head_cost = P.weighted ? 6 * kHead : kHead;
-  struct Costs { int tiles, parts; uint32_t last_tile, full, head; };        // a full part, all parts of a KV head
+  struct Costs { int tiles, parts; uint32_t last_tile, full, head; };        // (full: a full part; head: all of a KV head)
   auto costs_of = [&](int rows, int keys) {
     Costs c;
     c.tiles = (keys + kTile - 1) / kTile;
@@ -936,9 +940,9 @@ struct Plan {
 Plan plan_of(const sv_kv4_attn_args &a) {
   Plan p;
   const int rows = a.max_q_rows * (a.num_q_heads / a.cache.num_kv_heads), blocks = (rows + 7) / 8;
-  // Two columns a part, or three in one: a third costs a third of the warps (128k keys of 8
-  // heads: 16 rows 161 us, 24 rows 220 us, but 36 rows or fewer, ragged, 59 us in parts of two
-  // and 65 us in parts of three).
+  // Two columns a part, or three in one: a third costs a third of the warps (128k tokens of 8
+  // heads: 16 rows 151 us, 24 rows 208 us, but 36 rows or fewer, ragged, 59 us in parts of two
+  // and 73 us in parts of three).
   p.parts = blocks <= 3 ? 1 : (blocks + 1) / 2;
   p.nb = (blocks + p.parts - 1) / p.parts;
   p.parts = (blocks + p.nb - 1) / p.nb;
