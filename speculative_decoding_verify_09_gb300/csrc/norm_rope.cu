@@ -15,7 +15,7 @@
 // Bounds: prompts are bound by DRAM and, into the pages, by instructions too: 32768 bf16
 // rows of 48 heads of 128 (q and k normed and rotated) 134 us, 6.0 TB/s, 0.89 of the
 // measured copy rate; 17936 rows of 32 + 2 x 8 heads into pages 79 us, 0.72, at 2.1
-// instructions of 4 per clock; read back as bf16 0.79 of that rate, as E4M3 0.58 (with
+// instructions of 4 per clock; read back as bf16 0.80 of that rate, as E4M3 0.58 (with
 // 38 bytes moved per 16 elements instructions and latency weigh more).  Blocks of a few
 // rows take 2.3 to 6.3 us: the launch and one chain of dependent loads.
 #include <algorithm>
