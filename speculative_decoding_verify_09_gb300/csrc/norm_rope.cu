@@ -12,12 +12,11 @@
 // time.  Angles as in rope.cu: the position times the turn fraction modulo 2^64, a
 // quarter turn taken off, the rest rounded once.
 //
-// Bounds: prompts are bound by DRAM and, into the pages, by instructions too: 32768 bf16
-// rows of 48 heads of 128 (q and k normed and rotated) 134 us, 6.0 TB/s, 0.89 of the
-// measured copy rate; 17936 rows of 32 + 2 x 8 heads into pages 79 us, 0.72, at 2.1
-// instructions of 4 per clock; read back as bf16 0.80 of that rate, as E4M3 0.58 (with
-// 38 bytes moved per 16 elements instructions and latency weigh more).  Blocks of a few
-// rows take 2.3 to 6.3 us: the launch and one chain of dependent loads.
+// Bounds: prompts are bound by DRAM: 32768 bf16 rows of 48 heads of 128 (q and k normed and
+// rotated) 121 us, 6.6 TB/s, 0.98 of the measured copy rate; 17936 rows of 32 + 2 x 8 heads
+// into pages 66 us, 0.87, with instructions next; read back as bf16 0.80 of that rate, as
+// E4M3 0.58 (with 38 bytes moved per 16 elements instructions and latency weigh more).
+// Blocks of a few rows take 2.3 to 6.7 us: the launch and one chain of dependent loads.
 #include <algorithm>
 #include <cmath>
 
@@ -218,18 +217,39 @@ __device__ __forceinline__ void join(Vec<uint16_t, 8> &v, const float (&x)[8]) {
 }
 __device__ __forceinline__ void join(Vec<float, 8> &v, const float (&x)[8]) { v.set(x); }
 
-// CTAs per SM that the registers are capped for.  Loads under way are what prompts need: 32768
-// bf16 rows of 48 heads of 128 take 134 us at 4 CTAs, 144 at 3.  With pages 4 would cost local
-// memory: 17936 rows 77 us against 79, but 576 rows 6.7 against 6.3.
+// CTAs per SM that the registers are capped for: copies under way are what prompts need (32768 bf16
+// rows of 48 heads of 128 take 123 us at 4 CTAs, 126 at 3), but with pages 4 cost local memory:
+// 17936 rows 69 us against 66, 576 rows 7.0 against 6.7.
 template <typename T, Output OUT, Layout LAYOUT>
 constexpr int kCtas = LAYOUT == kFar || sizeof(T) == 4 ? 2 : OUT == kPages ? 3 : 4;
+
+// A lane asks for its 16 elements of kStages - 1 heads ahead, into places of its own in shared memory
+// (32768 rows of 48 heads with 3 stages 121 us, 4 123, 6 129; 17936 rows into pages 67, 66, 69; with
+// one head ahead in registers, and none from one kind of heads to the next, 134 and 79).
+template <typename T, Output OUT>
+constexpr int kStages = OUT == kPages && sizeof(T) == 2 ? 4 : 3;
+template <typename T, Output OUT>
+constexpr size_t kRing = kStages<T, OUT> * sizeof(T) * kNT * 16;     // bytes
+// Past L1, where neighbouring lanes take neighbouring 16 bytes; else what is left of a sector is
+// found there by the next copy (16384 rows of 48 heads: half, past it or not 66 and 72 us;
+// interleaved 90 and 82, fp32 172 and 130).
+template <bool PAST_L1>
+__device__ __forceinline__ void copy16(uint32_t to, const void *from) {
+  if constexpr (PAST_L1)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(to), "l"(from) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 16;\n" ::"r"(to), "l"(from) : "memory");
+}
+__device__ __forceinline__ void copies_end() { asm volatile("cp.async.commit_group;\n" ::: "memory"); }
 
 template <typename T, Output OUT, Layout LAYOUT>
 __global__ void __launch_bounds__(kNT, kCtas<T, OUT, LAYOUT>) norm_rope_kernel(const NormRopeParams P) {
   constexpr bool kSide = LAYOUT == kNeighbours;
-  constexpr int kUnroll = OUT == kPages ? 1 : 2;     // (two: nothing is moved from nxt to cur)
-  extern __shared__ __align__(16) float s_turn[];    // [rows][cos, sin][pairs], [q, k][16 lanes] weights
-  __shared__ float s_swap[LAYOUT == kFar ? kNT * kPad : 1];
+  constexpr bool kPastL1 = LAYOUT == kPaired && sizeof(T) == 2;
+  constexpr int S = kStages<T, OUT>, CHUNKS = static_cast<int>(sizeof(T));        // 16 bytes of a stage that a lane has
+  extern __shared__ __align__(16) uint8_t s_ring[];  // [stages][chunks][threads] of 16 bytes
+  float *s_swap = reinterpret_cast<float *>(s_ring + kRing<T, OUT>);                   // (kFar) the exchange
+  float *s_turn = s_swap + (LAYOUT == kFar ? kNT * kPad : 0);        // [rows][cos, sin][pairs], [q, k][16 lanes] weights
   const int row_threads = 1 << P.row_shift, lanes = 1 << P.lane_shift;
   const int rl = threadIdx.x >> P.row_shift, t = threadIdx.x & (row_threads - 1);
   const int hl = t >> P.lane_shift, c = t & (lanes - 1), hstep = row_threads >> P.lane_shift;
@@ -258,11 +278,6 @@ __global__ void __launch_bounds__(kNT, kCtas<T, OUT, LAYOUT>) norm_rope_kernel(c
   Kv4Spot spot{};
   if (OUT == kPages && live) spot = find_page(P.cache, seq, pos);
 
-  auto fetch = [&](Vec<T, 8> (&v)[2], const T *p, bool on) {
-    if (!on) return;
-    v[0].load(p + o0);
-    if (both) v[1].load(p + o1);
-  };
   // the kinds' first heads and their tensors: q, k, v
   auto first_of = [&](int kind) { return kind == 0 ? 0 : kind == 1 ? P.nq : P.nq + P.nk; };
   auto source = [&](int kind) {
@@ -270,14 +285,34 @@ __global__ void __launch_bounds__(kNT, kCtas<T, OUT, LAYOUT>) norm_rope_kernel(c
            : kind == 1 ? static_cast<const T *>(P.k) + row * P.k_stride
                        : static_cast<const T *>(P.v) + row * P.v_stride;
   };
-  int kind = h_begin < P.nq ? 0 : h_begin < P.nq + P.nk ? 1 : 2;
-  Vec<T, 8> cur[2], nxt[2];
+  auto range = [&](int kind, int &begin, int &end) {  // heads of a kind that this CTA has
+    const int k0 = first_of(kind);
+    begin = max(h_begin, k0) - k0, end = min(h_end, kind == 2 ? P.heads : first_of(kind + 1)) - k0;
+  };
+  // This lane's elements of the next heads in order: into its own places of a stage
+  int f_kind = h_begin < P.nq ? 0 : h_begin < P.nq + P.nk ? 1 : 2, f_hb, f_end;
+  range(f_kind, f_hb, f_end);
+  const T *f_in = source(f_kind) + (f_hb + hl) * P.D;
+  auto fetch = [&](int stage) {
+    if (f_hb >= f_end && first_of(f_kind) + f_end < h_end) {         // the next kind that has heads here
+      do range(++f_kind, f_hb, f_end);
+      while (f_hb >= f_end);
+      f_in = source(f_kind) + (f_hb + hl) * P.D;
+    }
+    if (column && f_hb + hl < f_end) {
+      const uint32_t to = smem_u32(s_ring) + (stage * CHUNKS * kNT + threadIdx.x) * 16;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) cur[0].e[i] = cur[1].e[i] = nxt[0].e[i] = nxt[1].e[i] = T(0);
-  {
-    const int h = h_begin - first_of(kind) + hl;
-    fetch(cur, source(kind) + h * P.D, column && h_begin + hl < min(h_end, kind == 2 ? P.heads : first_of(kind + 1)));
-  }
+      for (int x = 0; x < CHUNKS / 2; ++x) {
+        copy16<kPastL1>(to + x * kNT * 16, f_in + o0 + x * 4);
+        if (both) copy16<kPastL1>(to + (CHUNKS / 2 + x) * kNT * 16, f_in + o1 + x * 4);
+      }
+    }
+    f_hb += hstep;
+    f_in += hstep * P.D;
+    copies_end();
+  };
+  fetch(0);
+  int stage = 0;
 
   // cos and sin of the row's pairs, by the threads that share the row; the weights in the order
   // of the columns' a and b
@@ -315,6 +350,13 @@ __global__ void __launch_bounds__(kNT, kCtas<T, OUT, LAYOUT>) norm_rope_kernel(c
     slab = find_slab(P.cache, spot, &why);
     if (why && t == 0 && blockIdx.y == 0) set_status(P.dev_status, why);
   }
+  if (f_hb < f_end || first_of(f_kind) + f_end < h_end) {            // (else there is nothing more)
+#pragma unroll
+    for (int x = 1; x < S - 1; ++x) fetch(x);
+  } else {
+#pragma unroll
+    for (int x = 1; x < S - 1; ++x) copies_end();
+  }
   __syncthreads();
   if (!live) return;                                 // (all threads of a warp share a row)
 
@@ -323,16 +365,13 @@ __global__ void __launch_bounds__(kNT, kCtas<T, OUT, LAYOUT>) norm_rope_kernel(c
   const bool all_turn = __all_sync(0xffffffffu, turning == 8 || !column);
   const int token = static_cast<int>(pos) & (kSlab - 1);
 
-  for (; kind < 3; ++kind) {
-    const int k0 = first_of(kind), kend = min(h_end, kind == 2 ? P.heads : first_of(kind + 1));
-    if (k0 >= h_end) break;
-    const int begin = max(h_begin, k0) - k0, end = kend - k0;        // heads of this kind
+  for (int kind = 0; kind < 3; ++kind) {
+    int begin, end;
+    range(kind, begin, end);
     if (begin >= end) continue;
     const bool is_q = kind == 0, turns = kind < 2 && any_turn;
     const bool normed = kind == 0 ? P.q_weight != nullptr : kind == 1 && P.k_weight != nullptr;
     const bool changed = turns || normed;
-    const T *in = source(kind) + (begin + hl) * P.D;
-    if (max(h_begin, k0) != h_begin) fetch(cur, in, column && begin + hl < end);
     const float factor = kind == 1 ? P.k_scale : P.v_scale, inverse = kind == 1 ? P.k_inverse : P.v_inverse;
     const float sixth = kind == 1 ? P.k_sixth : P.v_sixth;
     const float4 *w4 = reinterpret_cast<const float4 *>(s_weight + (is_q ? 0 : 16 * lanes)) + 2 * c;
@@ -346,11 +385,22 @@ __global__ void __launch_bounds__(kNT, kCtas<T, OUT, LAYOUT>) norm_rope_kernel(c
       codes = page + token * (P.D / 2) + o0 / 2;
       scales = page + slab_k_scales(P.D) + token * (P.D / 16) + o0 / 16;
     }
-#pragma unroll kUnroll
+#pragma unroll 1
     for (int hb = begin; hb < end; hb += hstep) {
       const bool on = column && hb + hl < end;
-      in += hstep * P.D;
-      fetch(nxt, in, column && hb + hstep + hl < end);
+      fetch((stage + S - 1) % S);
+      asm volatile("cp.async.wait_group %0;\n" ::"n"(S - 1) : "memory");
+      Vec<T, 8> cur[2];
+      {
+        const uint8_t *at = s_ring + (stage * CHUNKS * kNT + threadIdx.x) * 16;
+#pragma unroll
+        for (int x = 0; x < CHUNKS / 2; ++x) {
+          reinterpret_cast<uint4 *>(&cur[0])[x] = *reinterpret_cast<const uint4 *>(at + x * kNT * 16);
+          const uint4 second = *reinterpret_cast<const uint4 *>(at + (CHUNKS / 2 + x) * kNT * 16);
+          reinterpret_cast<uint4 *>(&cur[1])[x] = both ? second : make_uint4(0, 0, 0, 0);
+        }
+      }
+      stage = (stage + 1) % S;
       F2 a[4], b[4];
       if (changed || OUT == kCodes8 || OUT == kPages) split<kSide>(cur, a, b);
       if (normed) {
@@ -486,8 +536,6 @@ __global__ void __launch_bounds__(kNT, kCtas<T, OUT, LAYOUT>) norm_rope_kernel(c
         }
         to += hstep * P.D;
       }
-      cur[0] = nxt[0];
-      cur[1] = nxt[1];
     }
   }
 }
@@ -631,7 +679,8 @@ uint32_t short_factor(float x) {
 }
 
 template <typename T, Output OUT>
-cudaError_t launch_layout(Layout layout, dim3 grid, size_t smem, cudaStream_t s, const NormRopeParams &P) {
+cudaError_t launch_layout(Layout layout, dim3 grid, size_t turns, cudaStream_t s, const NormRopeParams &P) {
+  const size_t smem = kRing<T, OUT> + (layout == kFar ? kNT * kPad * sizeof(float) : 0) + turns;
   return layout == kPaired       ? launch_after_previous(norm_rope_kernel<T, OUT, kPaired>, grid, kNT, smem, s, P)
          : layout == kNeighbours ? launch_after_previous(norm_rope_kernel<T, OUT, kNeighbours>, grid, kNT, smem, s, P)
                                  : launch_after_previous(norm_rope_kernel<T, OUT, kFar>, grid, kNT, smem, s, P);
@@ -710,10 +759,10 @@ sv_status run_rows(const sv_rope_args &a, const sv_norm_args &n, const sv_kv4_ca
   while ((16 << P.lane_shift) < P.D) ++P.lane_shift;
   const Layout layout = !P.half ? kPaired : a.layout == SV_ROPE_INTERLEAVED ? kNeighbours
                         : P.half % (cache ? 16 : 8) == 0 ? kPaired : kFar;
-  // Threads of a row: 128 where rows are few (576 rows with pages, 6.3 us by the second rule, 7.1 by
-  // this one; 175 rows 4.8 by this one, 5.0 by the second), else as many as leave a lane up to 12
-  // heads (32768 rows of 48 heads 134 us; with up to 6, two warps a row, 146).  A row's heads are
-  // shared by CTAs until each SM has 512 threads of them (175 rows 4.8 us; with 256 5.7, 1024 4.9).
+  // Threads of a row: 128 where rows are few (both ways 4.6 us for 288 slots; 576 rows with pages 7.6
+  // by this rule, 6.7 by the next), else as many as leave a lane up to 12 heads (32768 rows of 48
+  // heads 123 us; with up to 6, two warps a row, 137).  A row's heads are shared by CTAs until each
+  // SM has 512 threads of them (288 slots 4.6 us; with 256 5.5, 1024 4.7).
   const int64_t threads = (P.slots * P.heads) << P.lane_shift, room = 512 * static_cast<int64_t>(sms);
   P.row_shift = 7;
   if (P.slots > 2 * static_cast<int64_t>(sms))
@@ -725,17 +774,17 @@ sv_status run_rows(const sv_rope_args &a, const sv_norm_args &n, const sv_kv4_ca
   const int rows_per_cta = kNT >> P.row_shift;
   const dim3 grid(static_cast<unsigned>((P.slots + rows_per_cta - 1) / rows_per_cta),
                   static_cast<unsigned>((P.heads + P.heads_per_cta - 1) / P.heads_per_cta));
-  const size_t smem = (static_cast<size_t>(rows_per_cta) * 2 * P.pairs + (32u << P.lane_shift)) * sizeof(float);
+  const size_t turns = (static_cast<size_t>(rows_per_cta) * 2 * P.pairs + (32u << P.lane_shift)) * sizeof(float);
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e;
   if (a.dtype == SV_BF16)
-    e = cache                     ? launch_layout<uint16_t, kPages>(layout, grid, smem, s, P)
-        : a.kv_dtype == SV_E4M3 ? launch_layout<uint16_t, kCodes8>(layout, grid, smem, s, P)
-                                  : launch_layout<uint16_t, kRows>(layout, grid, smem, s, P);
+    e = cache                     ? launch_layout<uint16_t, kPages>(layout, grid, turns, s, P)
+        : a.kv_dtype == SV_E4M3 ? launch_layout<uint16_t, kCodes8>(layout, grid, turns, s, P)
+                                  : launch_layout<uint16_t, kRows>(layout, grid, turns, s, P);
   else
-    e = cache                     ? launch_layout<float, kPages>(layout, grid, smem, s, P)
-        : a.kv_dtype == SV_E4M3 ? launch_layout<float, kCodes8>(layout, grid, smem, s, P)
-                                  : launch_layout<float, kRows>(layout, grid, smem, s, P);
+    e = cache                     ? launch_layout<float, kPages>(layout, grid, turns, s, P)
+        : a.kv_dtype == SV_E4M3 ? launch_layout<float, kCodes8>(layout, grid, turns, s, P)
+                                  : launch_layout<float, kRows>(layout, grid, turns, s, P);
   if (e != cudaSuccess) return record_error(SV_ERR_CUDA, "%s launch: %s", who, cudaGetErrorString(e));
   return SV_OK;
 }
