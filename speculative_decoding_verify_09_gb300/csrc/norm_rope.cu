@@ -7,8 +7,10 @@
 // two), 16 each as 8 pairs (a, b), so that its sum of squares and the largest
 // magnitude of 16 elements are a few shuffles away and nothing is read twice.  Where
 // the members of a pair are a multiple of 8 apart a lane holds 8 elements and the 8
-// partners of these; neighbours lie with one lane anyway; for other distances the
-// partner is fetched through shared memory.  Arithmetic is done on two floats at a
+// partners of these; where they are neighbours, 8 elements of each half of the head (so
+// that neighbouring lanes have neighbouring 16 bytes: 16384 rows of 48 heads 64 us, with
+// 16 elements in a row 81); for other distances the partner is fetched through shared
+// memory.  Arithmetic is done on two floats at a
 // time.  Angles as in rope.cu: the position times the turn fraction modulo 2^64, a
 // quarter turn taken off, the rest rounded once.
 //
@@ -33,7 +35,7 @@ constexpr int kPad = 20;                             // floats between lanes in 
 
 enum Output { kRows, kCodes8, kPages };              // k and v: as they came, E4M3, E2M1 in pages
 // How pairs lie with a lane: a = 8 elements, b = the 8 that are half further on; a and b
-// neighbours among 16 elements in a row; 16 elements in a row, partners elsewhere.
+// neighbours in two runs of 8 elements; 16 elements in a row, partners elsewhere.
 enum Layout { kPaired, kNeighbours, kFar };
 
 struct NormRopeParams {
@@ -231,8 +233,8 @@ constexpr int kStages = OUT == kPages && sizeof(T) == 2 ? 4 : 3;
 template <typename T, Output OUT>
 constexpr size_t kRing = kStages<T, OUT> * sizeof(T) * kNT * 16;     // bytes
 // Past L1, where neighbouring lanes take neighbouring 16 bytes; else what is left of a sector is
-// found there by the next copy (16384 rows of 48 heads: half, past it or not 66 and 72 us;
-// interleaved 90 and 82, fp32 172 and 130).
+// found there by the next copy (16384 rows of 48 heads, past it or not: 66 and 72 us; fp32 172
+// and 130).
 template <bool PAST_L1>
 __device__ __forceinline__ void copy16(uint32_t to, const void *from) {
   if constexpr (PAST_L1)
@@ -245,7 +247,7 @@ __device__ __forceinline__ void copies_end() { asm volatile("cp.async.commit_gro
 template <typename T, Output OUT, Layout LAYOUT>
 __global__ void __launch_bounds__(kNT, kCtas<T, OUT, LAYOUT>) norm_rope_kernel(const NormRopeParams P) {
   constexpr bool kSide = LAYOUT == kNeighbours;
-  constexpr bool kPastL1 = LAYOUT == kPaired && sizeof(T) == 2;
+  constexpr bool kPastL1 = LAYOUT != kFar && sizeof(T) == 2;
   constexpr int S = kStages<T, OUT>, CHUNKS = static_cast<int>(sizeof(T));        // 16 bytes of a stage that a lane has
   extern __shared__ __align__(16) uint8_t s_ring[];  // [stages][chunks][threads] of 16 bytes
   float *s_swap = reinterpret_cast<float *>(s_ring + kRing<T, OUT>);                   // (kFar) the exchange
@@ -269,11 +271,19 @@ __global__ void __launch_bounds__(kNT, kCtas<T, OUT, LAYOUT>) norm_rope_kernel(c
       if (!good_sequence(P, static_cast<int>(i))) set_status(P.dev_status, SV_DEV_BAD_LENGTH);
 
   // this lane's column: two runs of 8 elements of a head, and how many of its pairs turn
-  const bool apart = LAYOUT == kPaired && 8 * c < P.half;            // the runs are a pair's members
-  const int o0 = LAYOUT != kPaired ? 16 * c : apart ? 8 * c : 2 * P.half + 16 * (c - P.half / 8);
-  const int o1 = apart ? o0 + P.half : o0 + 8;
-  const bool column = live && o0 < P.D, both = column && o1 < P.D;
-  const int turning = LAYOUT == kPaired ? (apart ? 8 : 0) : min(8, max(0, P.half - 8 * c));
+  const bool wide = kSide && P.D % 16 == 0;          // (neighbours, in runs of both halves of a head)
+  auto run_of = [&](int c, int second) {
+    if (LAYOUT == kPaired && 8 * c < P.half) return 8 * c + second * P.half;         // the runs are a pair's members
+    if (LAYOUT == kPaired) return 2 * P.half + 16 * (c - P.half / 8) + 8 * second;
+    return wide ? 8 * c + second * (P.D / 2) : 16 * c + 8 * second;
+  };
+  const int o0 = run_of(c, 0), o1 = run_of(c, 1);
+  const bool column = live && o0 < (wide ? P.D / 2 : P.D), both = column && o1 < P.D;
+  const bool apart = (LAYOUT == kPaired && 8 * c < P.half) || wide;  // runs of two times 16 elements
+  auto turning_of = [&](int run) {                   // how many of 4 pairs do
+    return LAYOUT == kPaired ? (8 * c < P.half ? 4 : 0) : min(4, max(0, P.half - run / 2));
+  };
+  const int turning[2] = {turning_of(o0), turning_of(o1)};
 
   Kv4Spot spot{};
   if (OUT == kPages && live) spot = find_page(P.cache, seq, pos);
@@ -336,11 +346,7 @@ __global__ void __launch_bounds__(kNT, kCtas<T, OUT, LAYOUT>) norm_rope_kernel(c
     for (int x = threadIdx.x; x < 32 * lanes; x += kNT) {          // [kind][a, b][lanes][8]
       const float *weight = x < 16 * lanes ? P.q_weight : P.k_weight;
       const int y = x & (16 * lanes - 1), second = y >= 8 * lanes, col = (y & (8 * lanes - 1)) >> 3, i = y & 7;
-      const bool far = LAYOUT == kPaired && 8 * col < P.half;
-      const int at = kSide              ? 16 * col + 2 * i + second
-                     : LAYOUT != kPaired ? 16 * col + 8 * second + i
-                     : far               ? 8 * col + i + second * P.half
-                                         : 2 * P.half + 16 * (col - P.half / 8) + 8 * second + i;
+      const int at = kSide ? run_of(col, i >> 2) + 2 * (i & 3) + second : run_of(col, second) + i;
       s_weight[x] = weight != nullptr && at < P.D ? weight[at] + P.weight_offset : 1.0f;
     }
   }
@@ -361,8 +367,8 @@ __global__ void __launch_bounds__(kNT, kCtas<T, OUT, LAYOUT>) norm_rope_kernel(c
   if (!live) return;                                 // (all threads of a warp share a row)
 
   // the pairs of this column (those that do not turn read others' and are not touched)
-  const float4 *cos4 = reinterpret_cast<const float4 *>(s_cos + 8 * c), *sin4 = reinterpret_cast<const float4 *>(s_sin + 8 * c);
-  const bool all_turn = __all_sync(0xffffffffu, turning == 8 || !column);
+  const int p0 = kSide ? o0 / 2 : 8 * c, p1 = kSide ? o1 / 2 : 8 * c + 4;
+  const bool all_turn = __all_sync(0xffffffffu, turning[0] + turning[1] == 8 || !column);
   const int token = static_cast<int>(pos) & (kSlab - 1);
 
   for (int kind = 0; kind < 3; ++kind) {
@@ -453,10 +459,11 @@ __global__ void __launch_bounds__(kNT, kCtas<T, OUT, LAYOUT>) norm_rope_kernel(c
           b[i] = f2(y[2 * i], y[2 * i + 1]);
         }
       } else if (turns) {
-        if (all_turn || turning > 0) {
+        if (all_turn || turning[0] + turning[1] > 0) {
 #pragma unroll
           for (int n = 0; n < 2; ++n) {
-            const float4 cx = cos4[n], sx = sin4[n];
+            const float4 cx = *reinterpret_cast<const float4 *>(s_cos + (n ? p1 : p0));
+            const float4 sx = *reinterpret_cast<const float4 *>(s_sin + (n ? p1 : p0));
             const F2 cs[2] = {f2(cx.x, cx.y), f2(cx.z, cx.w)}, sn[2] = {f2(sx.x, sx.y), f2(sx.z, sx.w)};
             const F2 minus[2] = {f2(-sx.x, -sx.y), f2(-sx.z, -sx.w)};
 #pragma unroll
@@ -473,7 +480,7 @@ __global__ void __launch_bounds__(kNT, kCtas<T, OUT, LAYOUT>) norm_rope_kernel(c
                 f2_get(b[i], b0, b1);
                 f2_get(x, x0, x1);
                 f2_get(y, y0, y1);
-                const bool on0 = 2 * i < turning, on1 = 2 * i + 1 < turning;
+                const bool on0 = 2 * m < turning[n], on1 = 2 * m + 1 < turning[n];
                 a[i] = f2(on0 ? x0 : a0, on1 ? x1 : a1);
                 b[i] = f2(on0 ? y0 : b0, on1 ? y1 : b1);
               }
@@ -482,6 +489,15 @@ __global__ void __launch_bounds__(kNT, kCtas<T, OUT, LAYOUT>) norm_rope_kernel(c
         }
       }
       if (OUT == kPages && !is_q) {                  // (all lanes: shuffles)
+        if constexpr (kSide) {
+          float x[8], y[8];
+          runs<true>(a, b, x, y);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            a[i] = f2(x[2 * i], x[2 * i + 1]);
+            b[i] = f2(y[2 * i], y[2 * i + 1]);
+          }
+        }
         float m0 = largest(a), m1 = largest(b);
         const float n0 = __shfl_xor_sync(0xffffffffu, m0, 1), n1 = __shfl_xor_sync(0xffffffffu, m1, 1);
         const float all = max_nan(m0, m1);
@@ -490,23 +506,14 @@ __global__ void __launch_bounds__(kNT, kCtas<T, OUT, LAYOUT>) norm_rope_kernel(c
         if (on && slab != nullptr) {
           float u0;
           const uint32_t s0 = scale_code(m0, sixth, factor, u0);
-          if constexpr (kSide) {
-            float x[8], y[8];
-            runs<true>(a, b, x, y);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              a[i] = f2(x[2 * i], x[2 * i + 1]);
-              b[i] = f2(y[2 * i], y[2 * i + 1]);
-            }
-          }
           if (apart) {
             float u1;
             const uint32_t s1 = scale_code(m1, sixth, factor, u1);
             *reinterpret_cast<uint32_t *>(codes) = codes_of(a, u0, s0);
-            *reinterpret_cast<uint32_t *>(codes + P.half / 2) = codes_of(b, u1, s1);
+            *reinterpret_cast<uint32_t *>(codes + (o1 - o0) / 2) = codes_of(b, u1, s1);
             if (c % 2 == 0) {                        // one lane of those that share 16 elements
               *scales = static_cast<uint8_t>(s0);
-              scales[P.half / 16] = static_cast<uint8_t>(s1);
+              scales[(o1 - o0) / 16] = static_cast<uint8_t>(s1);
             }
           } else {
             *reinterpret_cast<uint2 *>(codes) = make_uint2(codes_of(a, u0, s0), codes_of(b, u0, s0));
@@ -767,7 +774,7 @@ sv_status run_rows(const sv_rope_args &a, const sv_norm_args &n, const sv_kv4_ca
   P.row_shift = 7;
   if (P.slots > 2 * static_cast<int64_t>(sms))
     for (P.row_shift = 5; P.row_shift < 7 && (12 << P.row_shift) < (P.heads << P.lane_shift);) ++P.row_shift;
-  P.pairs = (P.half + 7) / 4 * 4;
+  P.pairs = (layout == kNeighbours ? P.D / 2 + 3 : P.half + 7) / 4 * 4;
   const int at_once = 1 << (P.row_shift - P.lane_shift);
   P.heads_per_cta = static_cast<int>(
       std::min<int64_t>(P.heads, std::max<int64_t>(1, (threads + room - 1) / room) * at_once));
