@@ -17,7 +17,7 @@
 // Bounds: prompts are bound by DRAM: 32768 bf16 rows of 48 heads of 128 (q and k normed and
 // rotated) 121 us, 6.6 TB/s, 0.98 of the measured copy rate; 17936 rows of 32 + 2 x 8 heads
 // into pages 66 us, 0.87, with instructions next; read back as bf16 0.80 of that rate, as
-// E4M3 0.58 (with 38 bytes moved per 16 elements instructions and latency weigh more).
+// E4M3 0.58 (25 bytes moved per 16 elements: instructions and latency weigh more).
 // Blocks of a few rows take 2.3 to 6.7 us: the launch and one chain of dependent loads.
 #include <algorithm>
 #include <cmath>

@@ -173,6 +173,30 @@ def test_without_norms_it_is_the_rotary_operator(api):
             assert same > 0.999, (layout, p, same)
 
 
+@pytest.mark.parametrize("Hq,Hkv,parts", [(5, 3, "qv"), (0, 20, "v"), (37, 11, "qkv"), (2, 1, "qv"), (3, 30, "kv")])
+@pytest.mark.parametrize("rows", [[3], [900], [400, 0, 211]])
+@pytest.mark.parametrize("D,dtype,kv8", [(128, "bf16", False), (64, "f32", True), (136, "bf16", True)])
+def test_some_kinds_of_heads(api, Hq, Hkv, parts, rows, D, dtype, kv8):
+    """Tensors left out, and heads of several kinds with one CTA, the last ones fewer than it has places."""
+    c = Case(api, rows, Hq if "q" in parts else 0, Hkv, D, D, dtype, "interleaved" if D == 128 else "half", kv8,
+             seed=Hq, parts=parts)
+    api.spec_norm_rope_rows(c.args())
+    c.check()
+    assert int(c.status.item()) == 0
+
+
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+def test_many_heads_in_place(api, layout):
+    c = Case(api, [700], 32, 8, 128, 128, "bf16", layout)
+    t = {p: c.dx[:, c.heads[p]].contiguous() for p in "qkv"}
+    c.out = t
+    w = {p: dev(x) for p, x in c.weight.items()}
+    api.spec_norm_rope_rows(api.norm_rope_args(
+        t["q"], t["k"], t["v"], t["q"], t["k"], t["v"], c.turns, q_weight=w["q"], k_weight=w["k"],
+        cu_q=dev(c.cu), kv_len=dev(c.kv_len), max_q_rows=c.max_rows, layout=layout))
+    c.check()
+
+
 def test_in_place(api):
     for layout, rot in (("half", 64), ("half", 20), ("interleaved", 64)):
         c = Case(api, [4, 2], 2, 2, 64, rot, "f32", layout)
