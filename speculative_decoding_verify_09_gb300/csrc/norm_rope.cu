@@ -768,18 +768,22 @@ sv_status run_rows(const sv_rope_args &a, const sv_norm_args &n, const sv_kv4_ca
                         : P.half % (cache ? 16 : 8) == 0 ? kPaired : kFar;
   // Threads of a row: 128 where rows are few (both ways 4.6 us for 288 slots; 576 rows with pages 7.6
   // by this rule, 6.7 by the next), else as many as leave a lane up to 12 heads (32768 rows of 48
-  // heads 123 us; with up to 6, two warps a row, 137).  A row's heads are shared by CTAs until each
-  // SM has 512 threads of them (288 slots 4.6 us; with 256 5.5, 1024 4.7).
-  const int64_t threads = (P.slots * P.heads) << P.lane_shift, room = 512 * static_cast<int64_t>(sms);
-  P.row_shift = 7;
-  if (P.slots > 2 * static_cast<int64_t>(sms))
-    for (P.row_shift = 5; P.row_shift < 7 && (12 << P.row_shift) < (P.heads << P.lane_shift);) ++P.row_shift;
+  // heads 123 us; with up to 6, two warps a row, 137).  A few rows' heads are shared by CTAs until
+  // each SM has 512 threads of them (288 slots 4.6 us; with 256 5.5, 1024 4.7), more rows' as long as
+  // all CTAs run at once (864 and 1440 rows of 48 heads 6.9 and 10.1 us, by the other rule 7.7 and
+  // 11.8; 720 rows into pages 7.7, by the other rule 7.5).
+  const bool few = P.slots <= 2 * static_cast<int64_t>(sms);
+  P.row_shift = few ? 7 : 5;
+  while (P.row_shift < 7 && (12 << P.row_shift) < (P.heads << P.lane_shift)) ++P.row_shift;
   P.pairs = (layout == kNeighbours ? P.D / 2 + 3 : P.half + 7) / 4 * 4;
-  const int at_once = 1 << (P.row_shift - P.lane_shift);
-  P.heads_per_cta = static_cast<int>(
-      std::min<int64_t>(P.heads, std::max<int64_t>(1, (threads + room - 1) / room) * at_once));
-  const int rows_per_cta = kNT >> P.row_shift;
-  const dim3 grid(static_cast<unsigned>((P.slots + rows_per_cta - 1) / rows_per_cta),
+  const int at_once = 1 << (P.row_shift - P.lane_shift), rows_per_cta = kNT >> P.row_shift;
+  const int64_t row_ctas = (P.slots + rows_per_cta - 1) / rows_per_cta;
+  const int64_t threads = (P.slots * P.heads) << P.lane_shift, room = 512 * static_cast<int64_t>(sms);
+  const int64_t resident = static_cast<int64_t>(sms) * (layout == kFar || a.dtype == SV_F32 ? 2 : cache ? 3 : 4);
+  const int64_t shares = std::max<int64_t>(1, resident / row_ctas);
+  const int64_t heads = few ? (threads + room - 1) / room * at_once : (P.heads + shares - 1) / shares;
+  P.heads_per_cta = static_cast<int>(std::min<int64_t>(P.heads, (heads + at_once - 1) / at_once * at_once));
+  const dim3 grid(static_cast<unsigned>(row_ctas),
                   static_cast<unsigned>((P.heads + P.heads_per_cta - 1) / P.heads_per_cta));
   const size_t turns = (static_cast<size_t>(rows_per_cta) * 2 * P.pairs + (32u << P.lane_shift)) * sizeof(float);
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
