@@ -277,3 +277,28 @@ def test_streams_and_graphs(api):
     c.dx.copy_(dev(x).view(torch.bfloat16))
     g.replay()
     c.check()
+
+
+@pytest.mark.parametrize("D,rot,dtype", [(128, 20, "bf16"), (256, 250, "f32")])
+def test_a_first_call_may_be_a_captured_one(api, D, rot, dtype):
+    """Partners far apart, which take more shared memory than a kernel has by default; two calls in one
+    graph, the second on the first one's rows."""
+    c = Case(api, [70, 3, 40], 8, 2, D, rot, dtype, norms="")
+    t = {p: c.dx[:, c.heads[p]].contiguous() for p in "qk"}
+    back = {p: torch.zeros_like(x) for p, x in t.items()}
+    where = torch.tensor(oracle.row_positions(c.cu, c.kv_len), dtype=torch.int64, device="cuda")
+    there = api.norm_rope_args(t["q"], t["k"], None, c.out["q"], c.out["k"], None, c.turns, positions=where)
+    again = api.norm_rope_args(c.out["q"], c.out["k"], None, back["q"], back["k"], None, c.turns,
+                               positions=-where)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        api.spec_norm_rope_rows(there)
+        api.spec_norm_rope_rows(again)
+    for _ in range(2):
+        g.replay()
+    torch.cuda.synchronize()
+    for p in "qk":                     # turned and turned back: two roundings of each of a pair
+        x = t[p].double()
+        size = torch.sqrt(2 * (x ** 2).amax()).item()
+        assert (back[p].double() - x).abs().max().item() <= 4 * size * {"bf16": 2.0 ** -8, "f32": 2.0 ** -22}[dtype]
+        assert not torch.equal(c.out[p][:, :, :rot], t[p][:, :, :rot])
