@@ -599,6 +599,16 @@ def test_strided_table_and_shared_pages(api):
     c.check()
 
 
+def test_tables_far_wider_than_the_lengths(api):
+    """Bounds at which the list of tiles could hold hundreds of millions of units."""
+    c = Attn(api, [70 * i for i in range(20)], [3, 1, 2, 0] * 5, 8, 1, 64, 4096, garbage=None)
+    wide = torch.full((20, 1 << 18), -1, dtype=torch.int32, device="cuda")
+    wide[:, :c.table.shape[1]] = dev(c.table)
+    c.run(table=wide)
+    c.check()
+    assert int(c.status.item()) == 0
+
+
 def test_one_workspace_for_many_shapes(api):
     """Larger and smaller calls in turn, counters at zero in between."""
     cases = [Attn(api, [700, 20], [2, 5], 8, 2, 128, garbage=None), Attn(api, [3000], [1], 1, 1, 64, garbage=None),
