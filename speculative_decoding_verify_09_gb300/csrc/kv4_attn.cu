@@ -46,26 +46,18 @@
 #include <type_traits>
 
 #include "kv4.inl"
+#include "kv4_cuts.inl"
 #include "ops_host.inl"
 
 namespace sv {
 
 namespace {
 
-constexpr int kTile = 32;                            // tokens
 constexpr int kMaxBatch = 768;                       // (16 or 20 bytes each in shared memory)
 constexpr int kMaxParts = 1024;
 constexpr int kMaxCtas = 192;                        // (sizes the workspace on any host)
 constexpr int kCounters = 24 * kMaxCtas;             // first in the workspace, whatever the shape
 constexpr int kMaxUnits = 65536;                     // sequences times KV heads times parts
-// Units that a segment costs beside its tiles (at the ragged verify rows above and 13 small ragged
-// sequences 1: 62.3 and 6.7 us, 2: 58.6 and 6.7, 4: 57.9 and 7.0).
-constexpr int kHead = 2;
-// Units of a CTA's share at least (the small sequences 6.7 us, with 16 7.5), and by how many it may
-// end early or late to end with a segment (0: the same small sequences 8.3 us, 8: 6.7; 16: shares
-// so unequal that 8 sequences of 32 heads take 19.2 us instead of 18.5).
-constexpr int kLeast = 4;
-constexpr int kSnap = 8;
 // log2 the maximum may grow before sums are rescaled (0: 61.3 us, 8: 58.6; weights up to 2^8 lose
 // nothing in f16).
 constexpr float kLate = 8.0f;
@@ -144,12 +136,6 @@ __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, uint32_t
   return done;
 }
 
-// Units of the list, and what they cost.
-struct Amount {
-  int units;
-  uint32_t cost;
-};
-
 // Rows and tokens of a sequence; nothing to do: R = 0.
 struct Sequence {
   int r0, R, L, keys;
@@ -204,25 +190,9 @@ __global__ void __launch_bounds__(Shape<D, NB>::kThreads, 1) kv4_attn_kernel(con
 
   // units (tiles, and kHead for each segment) before each sequence's first
   const int heads = P.cache.heads;
+  const TileList<NB, Kv4AttnParams> list{P, s_start, s_rows, s_len, s_cost};
   auto head_of = [&](int unit, int parts) {          // unit / parts, exact: unit below 2^16
     return parts == 1 ? unit : static_cast<int>(__fdividef(static_cast<float>(unit) + 0.5f, static_cast<float>(parts)));
-  };
-  auto parts_of = [&](int rows) { return (rows * P.g + ROWS - 1) / ROWS; };
-  auto each_of = [&](int keys) { return (keys + kTile - 1) / kTile + kHead; };
-  // Costs of a tile with so many columns (two take 1.4 times as long as one; with equal costs the
-  // ragged verify rows take 59.6 us instead of 58.6), of a segment beside its tiles, and of a
-  // sequence's parts.
-  auto tile_cost = [&](int columns) { return P.weighted ? 3u + 2u * columns : 1u; };
-  const uint32_t head_cost = P.weighted ? 6 * kHead : kHead;
-  struct Costs { int tiles, parts; uint32_t last_tile, full, head; };        // (full: a full part; head: all of a KV head)
-  auto costs_of = [&](int rows, int keys) {
-    Costs c;
-    c.tiles = (keys + kTile - 1) / kTile;
-    c.parts = parts_of(rows);
-    c.last_tile = tile_cost((rows * P.g + 7) / 8 - (c.parts - 1) * NB);
-    c.full = head_cost + c.tiles * tile_cost(NB);
-    c.head = (c.parts - 1) * c.full + head_cost + c.tiles * c.last_tile;
-    return c;
   };
   __shared__ Amount s_scan[W];
   auto enter = [&](int i) {                          // the sequence's data; its units
@@ -230,8 +200,7 @@ __global__ void __launch_bounds__(Shape<D, NB>::kThreads, 1) kv4_attn_kernel(con
     const Sequence s = sequence_of(P, P.cu_q[i], P.cu_q[i + 1], P.kv_len[i], &why);
     if (why && blockIdx.x == 0) set_status(P.dev_status, why);
     s_r0[i] = s.r0, s_rows[i] = s.R, s_len[i] = s.L;
-    return Amount{s.R == 0 ? 0 : each_of(s.keys) * parts_of(s.R) * heads,
-                  s.R == 0 || NB == 1 ? 0 : costs_of(s.R, s.keys).head * heads};
+    return s.R == 0 ? Amount{0, 0} : list.amount_of(s.R, s.keys, heads);
   };
   auto inclusive = [&](int x) {                      // sums over a warp's lanes up to this one
 #pragma unroll
@@ -292,98 +261,25 @@ __global__ void __launch_bounds__(Shape<D, NB>::kThreads, 1) kv4_attn_kernel(con
   }
   const int total = s_start[P.batch];
   if (total == 0) return;
-  // sequence, unit (head * parts + part) and place in it of list entry v
-  struct Place { int i, unit, at, tiles; };
   auto data_of = [&](int i) {
     const int R = s_rows[i], L = s_len[i];
     return Sequence{s_r0[i], R, L, L + R};
   };
-  auto locate = [&](int v) {
-    int lo = 0, hi = P.batch;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (s_start[mid] <= v) lo = mid; else hi = mid;
-    }
-    Place p;
-    p.i = lo;
-    const int each = each_of(s_rows[lo] + s_len[lo]), rem = v - s_start[lo];
-    // (a quotient below 2^17: by floats it is off by one at most)
-    p.unit = static_cast<int>(__fdividef(static_cast<float>(rem), static_cast<float>(each)));
-    p.at = rem - p.unit * each;
-    if (p.at < 0) --p.unit, p.at += each;
-    if (p.at >= each) ++p.unit, p.at -= each;
-    p.tiles = each - kHead;
-    return p;
-  };
 
-  // The CTAs' shares: equal, but for ends that come within kSnap of a segment's, which are
-  // moved there (a cut there would cost the joining of two CTAs' pieces); a share's
-  // units go to the warps in runs of equal length.
-  const int ctas = max(1, min(static_cast<int>(gridDim.x), total / kLeast)), b = blockIdx.x;
+  // A share's units go to the warps in runs of equal length (or cost).
+  const int ctas = list.ctas_of(total, static_cast<int>(gridDim.x)), b = blockIdx.x;
   if (b >= ctas) return;
   // (a warp's lanes 0 and 1 find its own share's ends, the others part of the table for later)
-  int u0, u1, v0, v1;
+  const int share = min(ctas, l < 2 ? b + l : 30 * w + l - 2);
+  const Cut cut = list.share_from(share, ctas);
+  if (l >= 2) s_share[share] = cut.unit;
+  const Cut from{__shfl_sync(0xffffffffu, cut.unit, 0), __shfl_sync(0xffffffffu, cut.cost, 0)};
+  const Cut to{__shfl_sync(0xffffffffu, cut.unit, 1), __shfl_sync(0xffffffffu, cut.cost, 1)};
+  int v0, v1;
   if constexpr (NB == 1) {
-    const int x = min(ctas, l < 2 ? b + l : 30 * w + l - 2);
-    const int each = total / ctas, v = each * x + min(x, total - each * ctas);
-    int to = v;
-    if (v > 0 && v < total) {
-      const Place p = locate(v);
-      const int after = kHead + p.tiles - p.at;
-      to = p.at <= min(after, kSnap) ? v - p.at : after <= kSnap ? v + after : v;
-    }
-    if (l >= 2) s_share[x] = to;
-    u0 = __shfl_sync(0xffffffffu, to, 0);
-    u1 = __shfl_sync(0xffffffffu, to, 1);
-    v0 = u0 + (u1 - u0) * w / W, v1 = u0 + (u1 - u0) * (w + 1) / W;
-  } else {
-    // (the unit that a cost falls in, and its segment)
-    struct Cut { int unit, at, left; uint32_t into, rest; };           // units, costs of the segment before and after
-    auto quotient = [&](uint32_t a, uint32_t d) {    // below 2^16: by floats it is off by one at most
-      uint32_t q = static_cast<uint32_t>(__fdividef(static_cast<float>(a), static_cast<float>(d)));
-      const int32_t rem = static_cast<int32_t>(a - q * d);
-      q += rem < 0 ? -1 : static_cast<uint32_t>(rem) >= d ? 1 : 0;
-      return static_cast<int>(q);
-    };
-    auto cut_at = [&](uint32_t x) {
-      int lo = 0, hi = P.batch;
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (s_cost[mid] <= x) lo = mid; else hi = mid;
-      }
-      const Costs k = costs_of(s_rows[lo], s_rows[lo] + s_len[lo]);
-      Cut c;
-      c.into = x - s_cost[lo];
-      const int h = quotient(c.into, k.head);
-      c.into -= h * k.head;
-      const int part = k.parts == 1 ? 0 : min(k.parts - 1, quotient(c.into, k.full));
-      c.into -= part * k.full;
-      const uint32_t one = part == k.parts - 1 ? k.last_tile : tile_cost(NB);
-      c.rest = head_cost + k.tiles * one - c.into;
-      const uint32_t x_tiles = c.into - head_cost;
-      c.at = c.into < head_cost ? (P.weighted ? c.into / 6 : c.into)
-                                : kHead + (one == 1 ? x_tiles : one == 5 ? x_tiles / 5 : one == 7 ? x_tiles / 7 : x_tiles / 9);
-      c.left = kHead + k.tiles - c.at;
-      c.unit = s_start[lo] + (h * k.parts + part) * (kHead + k.tiles) + c.at;
-      return c;
-    };
-    const uint32_t sum = s_cost[P.batch], each = sum / ctas;
-    const int x = min(ctas, l < 2 ? b + l : 30 * w + l - 2);
-    uint32_t from = each * x + min(static_cast<uint32_t>(x), sum - each * ctas);
-    int to = x == 0 ? 0 : total;
-    if (x > 0 && x < ctas) {
-      const Cut c = cut_at(from);
-      to = c.unit;
-      if (c.at <= min(c.left, kSnap)) to -= c.at, from -= c.into;
-      else if (c.left <= kSnap) to += c.left, from += c.rest;
-    }
-    if (l >= 2) s_share[x] = to;
-    u0 = __shfl_sync(0xffffffffu, to, 0);
-    u1 = __shfl_sync(0xffffffffu, to, 1);
-    const uint32_t x0 = __shfl_sync(0xffffffffu, from, 0), x1 = __shfl_sync(0xffffffffu, from, 1);
-    // (lanes 0 and 1 find the run's ends)
-    const int y = w + (l & 1);
-    const int end = y == 0 ? u0 : y == W || x1 <= x0 ? u1 : min(u1, max(u0, cut_at(x0 + (x1 - x0) * y / W).unit));
+    v0 = list.run_from(from, to, w, W), v1 = list.run_from(from, to, w + 1, W);
+  } else {                                           // (lanes 0 and 1 find the run's ends)
+    const int end = list.run_from(from, to, w + (l & 1), W);
     v0 = __shfl_sync(0xffffffffu, end, 0);
     v1 = __shfl_sync(0xffffffffu, end, 1);
   }
@@ -417,7 +313,7 @@ __global__ void __launch_bounds__(Shape<D, NB>::kThreads, 1) kv4_attn_kernel(con
     slab0 = 0;
     second = false;
     if (v < v1) {
-      ahead = locate(v);
+      ahead = list.locate(v);
       ahead_s = data_of(ahead.i);
       if (ahead.at >= kHead) {
         const uint32_t n = 2u * static_cast<uint32_t>(ahead.at - kHead), per = P.cache.slabs;
@@ -435,7 +331,7 @@ __global__ void __launch_bounds__(Shape<D, NB>::kThreads, 1) kv4_attn_kernel(con
     from0 = from1 = nullptr;
     from_bad = false;
     if (real) {
-      const int parts = parts_of(ahead_s.R);
+      const int parts = list.parts_of(ahead_s.R);
       const int64_t head = head_of(ahead.unit, parts) * head_bytes(P.cache);
       const int64_t page_bytes = P.cache.heads * head_bytes(P.cache);
       if (page0 < 0 || page0 >= P.cache.num_pages || page1 < 0 || page1 >= P.cache.num_pages) {
@@ -480,7 +376,7 @@ __global__ void __launch_bounds__(Shape<D, NB>::kThreads, 1) kv4_attn_kernel(con
   // the segment of list entry v, and this lane's part of its rows of q
   struct Segment { Place p; Sequence s; int h, part, rows; };
   auto complete = [&](Segment &x) {
-    const int parts = parts_of(x.s.R);
+    const int parts = list.parts_of(x.s.R);
     x.h = head_of(x.p.unit, parts);
     x.part = x.p.unit - x.h * parts;
     x.rows = min(ROWS, x.s.R * P.g - x.part * ROWS);
@@ -519,7 +415,7 @@ __global__ void __launch_bounds__(Shape<D, NB>::kThreads, 1) kv4_attn_kernel(con
 #pragma unroll 1
       for (int x = 0; x < S && open != 0; ++x) issue_open();
     } else {
-      here.p = locate(v);
+      here.p = list.locate(v);
       here.s = data_of(here.p.i);
       complete(here);
       fetch_q(here);
