@@ -445,7 +445,7 @@ __global__ void __launch_bounds__(Shape<D, NB>::kThreads, 1) kv4_attn_kernel(con
     for (int nb = 0; nb < NB; ++nb) {
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
-        lim[nb][x] = min(s.L + token_row(first_row + 8 * nb + 2 * c + x), s.keys - 1);
+        lim[nb][x] = s.L + min(token_row(first_row + 8 * nb + 2 * c + x), s.R - 1);
         m[nb][x] = -INFINITY;
         mu[nb][x] = sum[nb][x] = 0.0f;
       }

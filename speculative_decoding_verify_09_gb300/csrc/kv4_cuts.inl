@@ -77,7 +77,8 @@ struct TileList {
   const int32_t *rows, *len;                         // [batch] block rows, and tokens before them
   const uint32_t *cost;                              // [batch + 1] costs before a sequence (NB > 1)
 
-  SV_BOTH int tiles_of(int keys) const { return (keys + kTile - 1) / kTile; }
+  // (unsigned: the longest sequences, rounded up, pass 2^31)
+  SV_BOTH int tiles_of(int keys) const { return (static_cast<uint32_t>(keys) + (kTile - 1)) / kTile; }
   SV_BOTH int parts_of(int block_rows) const { return (block_rows * P.g + 8 * NB - 1) / (8 * NB); }
 
   // Costs of a tile with so many columns (two take 1.4 times as long as one; with equal costs the

@@ -209,6 +209,13 @@ def test_one_long_head(host, rows, g, tokens, grid):
     List([rows], [tokens], 1, g).check(host, grid)
 
 
+@pytest.mark.parametrize("rows,g", [(1, 1), (3, 6), (1, 16), (10, 8), (17, 1)])
+@pytest.mark.parametrize("keys", range(TOKENS - 18, TOKENS + 1, 3))
+def test_the_longest_sequences(host, rows, g, keys):
+    """Lengths that, rounded up to tiles, pass 2^31."""
+    List([rows], [keys - rows], 1, g).check(host)
+
+
 @pytest.mark.parametrize("rows,lens,heads,g", [
     ([1024, 3, 0, 1024], [9_000_000, 5, 0, 9_100_000], 1, 16), ([1, 1024], [0, 19_000_000], 1, 16),
     ([1024, 1], [19_000_000, 0], 1, 16), ([24] * 7, [9_000_000] * 7, 8, 1), ([16] * 20, [5_000_000] * 20, 2, 8),
