@@ -81,6 +81,7 @@ struct Shape {
   static constexpr size_t kRing = kWarps * kRingOne, kSlots = kWarps * kSlotOne;
   static constexpr size_t kSums = size_t{2} * kWarps * kRows * 8;
   static constexpr size_t kFixed = kRing + kSlots + kSums;
+  static constexpr size_t bytes(int batch) { return kFixed + (static_cast<size_t>(batch) * (NB == 1 ? 4 : 5) + 2) * 4; }
 };
 
 struct Kv4AttnParams {
@@ -851,8 +852,8 @@ Plan plan_of(const sv_kv4_attn_args &a) {
 template <int D, int NB>
 cudaError_t launch_shape(const Kv4AttnParams &P, int ctas, cudaStream_t s) {
   using Sh = Shape<D, NB>;
-  const size_t smem = Sh::kFixed + (static_cast<size_t>(P.batch) * (NB == 1 ? 4 : 5) + 2) * 4;
-  return launch_after_previous(kv4_attn_kernel<D, NB>, dim3(ctas), Sh::kThreads, smem, s, P);
+  static SharedLimit limit(Sh::bytes(kMaxBatch));
+  return launch_after_previous(kv4_attn_kernel<D, NB>, limit, dim3(ctas), Sh::kThreads, Sh::bytes(P.batch), s, P);
 }
 template <int D>
 cudaError_t launch_rows(int nb, const Kv4AttnParams &P, int ctas, cudaStream_t s) {

@@ -698,12 +698,24 @@ uint32_t short_factor(float x) {
   return h | h << 16;
 }
 
+// Shared memory behind the ring: the exchange, and what all layouts have (at most: 8 rows of 132
+// pairs, 16 lanes of weights).
+constexpr size_t swap_bytes(Layout layout) { return layout == kFar ? kNT * kPad * sizeof(float) : 0; }
+constexpr size_t turn_bytes(int rows, int pairs, int lanes) {
+  return (static_cast<size_t>(rows) * 2 * pairs + 32 * lanes) * sizeof(float);
+}
+
+template <typename T, Output OUT, Layout LAYOUT>
+cudaError_t launch_rows(dim3 grid, size_t turns, cudaStream_t s, const NormRopeParams &P) {
+  constexpr size_t before = kRing<T, OUT> + swap_bytes(LAYOUT);
+  static SharedLimit limit(before + turn_bytes(8, 132, 16));
+  return launch_after_previous(norm_rope_kernel<T, OUT, LAYOUT>, limit, grid, kNT, before + turns, s, P);
+}
 template <typename T, Output OUT>
 cudaError_t launch_layout(Layout layout, dim3 grid, size_t turns, cudaStream_t s, const NormRopeParams &P) {
-  const size_t smem = kRing<T, OUT> + (layout == kFar ? kNT * kPad * sizeof(float) : 0) + turns;
-  return layout == kPaired       ? launch_after_previous(norm_rope_kernel<T, OUT, kPaired>, grid, kNT, smem, s, P)
-         : layout == kNeighbours ? launch_after_previous(norm_rope_kernel<T, OUT, kNeighbours>, grid, kNT, smem, s, P)
-                                 : launch_after_previous(norm_rope_kernel<T, OUT, kFar>, grid, kNT, smem, s, P);
+  return layout == kPaired       ? launch_rows<T, OUT, kPaired>(grid, turns, s, P)
+         : layout == kNeighbours ? launch_rows<T, OUT, kNeighbours>(grid, turns, s, P)
+                                 : launch_rows<T, OUT, kFar>(grid, turns, s, P);
 }
 
 sv_status check_norm(const sv_norm_args &n, const char *who) {
@@ -798,7 +810,7 @@ sv_status run_rows(const sv_rope_args &a, const sv_norm_args &n, const sv_kv4_ca
   P.heads_per_cta = static_cast<int>(std::min<int64_t>(P.heads, (heads + at_once - 1) / at_once * at_once));
   const dim3 grid(static_cast<unsigned>(row_ctas),
                   static_cast<unsigned>((P.heads + P.heads_per_cta - 1) / P.heads_per_cta));
-  const size_t turns = (static_cast<size_t>(rows_per_cta) * 2 * P.pairs + (32u << P.lane_shift)) * sizeof(float);
+  const size_t turns = turn_bytes(rows_per_cta, P.pairs, 1 << P.lane_shift);
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e;
   if (a.dtype == SV_BF16)
@@ -956,10 +968,11 @@ SV_API sv_status spec_kv4_read(const sv_kv4_read_args *a, void *stream) {
   const dim3 grid(static_cast<unsigned>((P.slots + rows_per_cta - 1) / rows_per_cta),
                   static_cast<unsigned>(slices));
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  static SharedLimit none(0);
   const cudaError_t e =
-      a->dtype == SV_BF16  ? launch_after_previous(kv4_read_kernel<uint16_t>, grid, kNT, size_t{0}, s, P)
-      : a->dtype == SV_F32 ? launch_after_previous(kv4_read_kernel<float>, grid, kNT, size_t{0}, s, P)
-                           : launch_after_previous(kv4_read_kernel<uint8_t>, grid, kNT, size_t{0}, s, P);
+      a->dtype == SV_BF16  ? launch_after_previous(kv4_read_kernel<uint16_t>, none, grid, kNT, size_t{0}, s, P)
+      : a->dtype == SV_F32 ? launch_after_previous(kv4_read_kernel<float>, none, grid, kNT, size_t{0}, s, P)
+                           : launch_after_previous(kv4_read_kernel<uint8_t>, none, grid, kNT, size_t{0}, s, P);
   if (e != cudaSuccess) return record_error(SV_ERR_CUDA, "%s launch: %s", who, cudaGetErrorString(e));
   return SV_OK;
 }

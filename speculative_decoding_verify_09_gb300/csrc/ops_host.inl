@@ -5,6 +5,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "spec_ops.h"
 
 namespace sv {
@@ -46,14 +48,32 @@ inline cudaError_t launch_behind(void (*kernel)(Params), dim3 grid, int threads,
   return e;
 }
 
-// The same for a kernel that takes more dynamic shared memory than the default allows.
+// The most dynamic shared memory that calls of one kernel take.  What the driver allows a kernel is
+// raised to it once per device, and never set to what one call needs: that would be the limit of
+// another host thread's launch, too.
+struct SharedLimit {
+  const size_t most;
+  std::atomic<uint64_t> ready{0};                   // a bit per device
+  explicit SharedLimit(size_t bytes) : most(bytes) {}
+  cudaError_t raise(const void *kernel) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = uint64_t{1} << (dev & 63);
+    if (dev < 64 && (ready.load(std::memory_order_acquire) & bit)) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(most));
+    if (e == cudaSuccess) ready.fetch_or(bit, std::memory_order_release);
+    return e;
+  }
+};
+
+// launch_behind for a kernel whose calls may take more dynamic shared memory than the default allows.
 template <typename Params>
-inline cudaError_t launch_after_previous(void (*kernel)(Params), dim3 grid, int threads, size_t smem,
-                                         cudaStream_t s, const Params &params) {
-  if (smem > 48 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void *>(kernel),
-                                               cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               static_cast<int>(smem));
+inline cudaError_t launch_after_previous(void (*kernel)(Params), SharedLimit &limit, dim3 grid, int threads,
+                                         size_t smem, cudaStream_t s, const Params &params) {
+  if (smem > limit.most) return cudaErrorInvalidValue;
+  if (limit.most > 48 * 1024) {
+    const cudaError_t e = limit.raise(reinterpret_cast<const void *>(kernel));
     if (e != cudaSuccess) {
       cudaGetLastError();
       return e;
