@@ -61,6 +61,9 @@ constexpr int kMaxUnits = 65536;                     // sequences times KV heads
 // log2 the maximum may grow before sums are rescaled (0: 61.3 us, 8: 58.6; weights up to 2^8 lose
 // nothing in f16).
 constexpr float kLate = 8.0f;
+// Maxima from here on are far: the fp32 rounding of a score, which the maximum is, differs from the exact
+// product of the sum and its scale by more than an exponent may be off, so that products are rounded too.
+constexpr float kFarMax = 0x1p22f;
 
 // Warps and stages of a warp's ring; NB: 8-row columns of a part.  As many warps as registers
 // allow (128, 168, 255 a thread; 12 instead of 16 warps with three stages: 116 us against 105
@@ -93,6 +96,7 @@ struct Kv4AttnParams {
                                                      // below 2^32 / g; 0: g is 1
   int64_t num_rows, q_stride;
   float scale_log2;                                  // of a score, k_scale and log2 e in it
+  float scale_inverse;                               // 1 / scale_log2
   const int32_t *cu_q, *kv_len;
   const uint16_t *q;
   uint16_t *out;
@@ -453,6 +457,7 @@ __global__ void __launch_bounds__(Shape<D, NB>::kThreads, 1) kv4_attn_kernel(con
 #pragma unroll
       for (int x = 0; x < MT; ++x) o[x][nb][0] = o[x][nb][1] = o[x][nb][2] = o[x][nb][3] = 0.0f;
     }
+    bool far = false;                                // a maximum is
     int nan_from = 0x7fffffff;                       // block token whose V has NaN in this lane's elements
     // (columns that have no rows are not computed)
     auto run_tiles = [&](auto columns) {
@@ -549,7 +554,7 @@ __global__ void __launch_bounds__(Shape<D, NB>::kThreads, 1) kv4_attn_kernel(con
                 if (key + (x >> 1) * 8 > lim[nb][x & 1]) sc[sl][nb][x] = -INFINITY;
           }
         }
-        bool grows = false;
+        bool grows = far;
 #pragma unroll
         for (int nb = 0; nb < NC; ++nb)
 #pragma unroll
@@ -557,6 +562,7 @@ __global__ void __launch_bounds__(Shape<D, NB>::kThreads, 1) kv4_attn_kernel(con
             grows |= fmaxf(fmaxf(sc[0][nb][x], sc[0][nb][2 + x]), fmaxf(sc[1][nb][x], sc[1][nb][2 + x])) *
                          P.scale_log2 > m[nb][x] + kLate;
         if (__any_sync(0xffffffffu, grows)) {
+          far = false;
 #pragma unroll
           for (int nb = 0; nb < NC; ++nb)
 #pragma unroll
@@ -568,6 +574,7 @@ __global__ void __launch_bounds__(Shape<D, NB>::kThreads, 1) kv4_attn_kernel(con
               const float f = now == -INFINITY ? 1.0f : fast_exp2(m[nb][x] - now);
               m[nb][x] = now;
               mu[nb][x] = now == -INFINITY ? 0.0f : now;
+              far |= fabsf(mu[nb][x]) >= kFarMax;
               sum[nb][x] *= f;
 #pragma unroll
               for (int y = 0; y < MT; ++y) {
@@ -575,6 +582,19 @@ __global__ void __launch_bounds__(Shape<D, NB>::kThreads, 1) kv4_attn_kernel(con
                 o[y][nb][2 + x] *= f;
               }
             }
+          far = __any_sync(0xffffffffu, far);
+          if (far) {                                   // scores less their maximum, which is 0 then
+#pragma unroll
+            for (int nb = 0; nb < NC; ++nb) {
+#pragma unroll
+              for (int sl = 0; sl < 2; ++sl)
+#pragma unroll
+                for (int x = 0; x < 4; ++x)
+                  sc[sl][nb][x] = __fmul_rn(__fsub_rn(__fmul_rn(sc[sl][nb][x], P.scale_log2), mu[nb][x & 1]),
+                                            P.scale_inverse);
+              mu[nb][0] = mu[nb][1] = 0.0f;
+            }
+          }
         }
         uint32_t pf[2][NC][2];
 #pragma unroll
@@ -947,6 +967,7 @@ SV_API sv_status spec_kv4_attn(const sv_kv4_attn_args *a, void *ws, size_t ws_by
   const double scale = a->scale != 0.0f ? a->scale : 1.0 / std::sqrt(static_cast<double>(a->cache.head_dim));
   // (kept a normal number: 0 or infinity times a masked score of -inf or a score of 0 were NaN)
   P.scale_log2 = static_cast<float>(std::min(std::max(scale * P.cache.k_scale * 1.4426950408889634, 0x1p-126), 0x1p127));
+  P.scale_inverse = 1.0f / P.scale_log2;
   P.cu_q = a->cu_q;
   P.kv_len = a->kv_len;
   P.q = static_cast<const uint16_t *>(a->q);
