@@ -172,7 +172,8 @@ SV_API size_t sv_kv4_workspace_bytes(const sv_kv4_attn_args *args);
 
 /* q is rounded to f16 (exact for bf16 values in f16's range; beyond +-65504 it
  * becomes infinite and its own row and head non-finite), scores and sums are fp32,
- * weights are rounded to f16.  What tokens that a row does not see hold, be it
+ * weights are rounded to f16: by 2^-11, or by 2^-32 of the row's largest where that is
+ * more (smaller ones are lost).  What tokens that a row does not see hold, be it
  * NaN, does not reach it.  Sequences whose cu_q / kv_len disagree with the host
  * bounds (SV_DEV_BAD_LENGTH) or whose tokens pass the table (SV_DEV_CAPACITY) are
  * left unwritten; one with a page outside [0, num_pages) gets NaN in the rows of

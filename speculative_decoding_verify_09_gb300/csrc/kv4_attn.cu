@@ -8,7 +8,7 @@
 // byte moved down for three of four conversions) that a matrix instruction of 8 rows
 // takes once.  E2M1 times E4M3 has six significant bits, so the operands are exact and
 // only q (to f16, exact for bf16 in its range), the weights (to f16: 2^-11, below the
-// output's 2^-8) and the fp32 sums are rounded.
+// output's 2^-8, or 2^-32 of the row's largest) and the fp32 sums are rounded.
 //
 // Split: the tiles of 32 tokens of all (sequence, KV head, part of the rows) --
 // segments -- are one list, cut into equal runs, one per warp of a persistent grid
@@ -26,7 +26,7 @@
 // elements in a product is free: a lane takes 16 bytes in a row of a token's K (32
 // elements) and the same elements of q; of V, 8 bytes in a row of four tokens'
 // elements.  The weights' running maximum is kept within 2^8 of the true one, so
-// the sums are rescaled seldom.  The 5th-generation tensor path would want the
+// the sums are rescaled seldom; its token's weight is 2^7, which uses f16's range.  The 5th-generation tensor path would want the
 // operands in shared memory, i.e. 2 x 512 bytes written and read per token and head
 // next to 144 from memory: as long as the register-fed products of 40 rows take.
 //
@@ -58,9 +58,11 @@ constexpr int kMaxParts = 1024;
 constexpr int kMaxCtas = 192;                        // (sizes the workspace on any host)
 constexpr int kCounters = 24 * kMaxCtas;             // first in the workspace, whatever the shape
 constexpr int kMaxUnits = 65536;                     // sequences times KV heads times parts
-// log2 the maximum may grow before sums are rescaled (0: 61.3 us, 8: 58.6; weights up to 2^8 lose
-// nothing in f16).
-constexpr float kLate = 8.0f;
+// log2 the maximum may grow before sums are rescaled (0: 61.3 us, 8: 58.6), and of the weight that the
+// maximum's token has.  Weights reach 2^15, which f16 holds; down to 2^-21 of the largest they keep
+// f16's 11 bits, and those below 2^-32 of it are lost (with a weight of 1 for the maximum it was 2^-25, and
+// 2^18 tokens of that size 0.8 % of the output).
+constexpr float kLate = 8.0f, kUp = 7.0f;
 // Maxima from here on are far: the fp32 rounding of a score, which the maximum is, differs from the exact
 // product of the sum and its scale by more than an exponent may be off, so that products are rounded too.
 constexpr float kFarMax = 0x1p22f;
@@ -573,7 +575,7 @@ __global__ void __launch_bounds__(Shape<D, NB>::kThreads, 1) kv4_attn_kernel(con
               const float now = fmaxf(m[nb][x], top * P.scale_log2);
               const float f = now == -INFINITY ? 1.0f : fast_exp2(m[nb][x] - now);
               m[nb][x] = now;
-              mu[nb][x] = now == -INFINITY ? 0.0f : now;
+              mu[nb][x] = now == -INFINITY ? 0.0f : now - kUp;
               far |= fabsf(mu[nb][x]) >= kFarMax;
               sum[nb][x] *= f;
 #pragma unroll
@@ -585,15 +587,17 @@ __global__ void __launch_bounds__(Shape<D, NB>::kThreads, 1) kv4_attn_kernel(con
           far = __any_sync(0xffffffffu, far);
           if (far) {                                   // scores less their maximum, which is 0 then
 #pragma unroll
-            for (int nb = 0; nb < NC; ++nb) {
+            for (int nb = 0; nb < NC; ++nb)
 #pragma unroll
-              for (int sl = 0; sl < 2; ++sl)
+              for (int x = 0; x < 2; ++x) {
+                const float top = m[nb][x] == -INFINITY ? 0.0f : m[nb][x];
 #pragma unroll
-                for (int x = 0; x < 4; ++x)
-                  sc[sl][nb][x] = __fmul_rn(__fsub_rn(__fmul_rn(sc[sl][nb][x], P.scale_log2), mu[nb][x & 1]),
-                                            P.scale_inverse);
-              mu[nb][0] = mu[nb][1] = 0.0f;
-            }
+                for (int y = 0; y < 4; ++y) {
+                  float &s = sc[y >> 1][nb][2 * (y & 1) + x];
+                  s = __fmul_rn(__fsub_rn(__fmul_rn(s, P.scale_log2), top), P.scale_inverse);
+                }
+                mu[nb][x] = -kUp;
+              }
           }
         }
         uint32_t pf[2][NC][2];

@@ -1,4 +1,7 @@
-"""Attention over the paged 4-bit cache at the ends of its operands' ranges."""
+"""Attention over the paged 4-bit cache at the ends of its operands' ranges.
+
+Weights enter the product with V as f16.  Held here: 2^-11 relative for weights down to 2^-21 of a row's
+largest, and below that an error of at most 2^-32 of the largest each."""
 import numpy as np
 import pytest
 import torch
@@ -44,3 +47,36 @@ def test_scores_far_beyond_exps_range(api, Hq, Hkv, rows, power):
                     seen += 1
                 assert np.isfinite(got[r, h]).all()
     assert seen >= rows * Hq or power < 18
+
+
+@pytest.mark.parametrize("g", [1, 12, 20])                 # one, two and three columns of 8 rows
+@pytest.mark.parametrize("D", [128, 64])
+@pytest.mark.parametrize("power", [-24.6, -25.1, -27.3])
+def test_one_heavy_token_and_many_light_ones(api, g, D, power):
+    """2^18 tokens whose weight is 2^power and whose V is 1, behind one of weight 1 and V 0: N 2^power /
+    (1 + N 2^power).  Wanted within half a step of bf16 and 2^-10: the light tokens' roundings come to 2^18
+    2^-32 = 2^-14, and fp32 sums of 2^18 equal terms to at most 2^18 2^-24 of the result, 2^-6 of less than
+    2^-6.  So many sequences that a warp has most of one (all of the same two pages), so that one running
+    maximum holds for it."""
+    n, page, B, Hkv = 1 << 18, 4096, 700, 4
+    pages = torch.zeros(2, Hkv, page // 16, 18 * D, dtype=torch.uint8, device="cuda")
+    pages[..., 0:8 * D:D // 2] = 2                                  # K: E2M1 1 in element 0, its scales 0
+    pages[..., 9 * D:17 * D] = 0x22                                 # V: 1
+    pages[..., 17 * D:] = 0x38
+    pages[1, :, 0, 8 * D] = 0x38                                    # the first token of page 1: K 1, V 0
+    pages[1, :, 0, 9 * D:9 * D + D // 2] = 0
+    cache = api.Kv4Cache(2, Hkv, D, page_size=page, pages=pages)
+    table = torch.zeros(B, n // page, dtype=torch.int32, device="cuda")
+    table[:, 0] = 1
+    q = torch.zeros(B, Hkv * g, D, dtype=torch.bfloat16, device="cuda")
+    q[..., 0] = 1.0
+    out = torch.zeros_like(q)
+    cu, kv_len = dev(np.arange(B + 1, dtype=np.int32)), dev(np.full(B, n - 1, np.int32))
+    scale = float(np.float32(-power * np.log(2.0)))
+    a = api.kv4_attn_args(cache, table, cu, kv_len, q, out, max_q_rows=1, scale=scale)
+    api.spec_kv4_attn(a, api.kv4_workspace(a))
+    torch.cuda.synchronize()
+    light = (n - 1) * np.exp(-scale)
+    want = light / (1.0 + light)
+    got = oracle.to_f64(host_bits(out))
+    assert np.all(np.abs(got - want) <= 2.0 ** -8 * want + 2.0 ** -10), (got.min(), got.max(), want)
