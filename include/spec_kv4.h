@@ -170,9 +170,12 @@ typedef struct sv_kv4_attn_args {
  * SV_DEV_TIMEOUT it is zeroed again. */
 SV_API size_t sv_kv4_workspace_bytes(const sv_kv4_attn_args *args);
 
-/* q is rounded to f16 (exact for bf16 values in f16's range; beyond +-65504 it
- * becomes infinite and its own row and head non-finite), scores and sums are fp32,
- * weights are rounded to f16: by 2^-11, or by 2^-32 of the row's largest where that is
+/* q is rounded to f16, exact for bf16 values from 2^-17 to 65504.  Smaller ones are
+ * off by up to 2^-25; where scale * k_scale * head_dim passes 16, so that this could
+ * show, rows and heads below 2^15 are multiplied by a power of two first, and elements
+ * are off by up to 2^-40 of the largest.  Beyond +-65504 q becomes infinite and its own
+ * row and head non-finite.  Scores and sums are fp32; weights are
+ * rounded to f16: by 2^-11, or by 2^-32 of the row's largest where that is
  * more (smaller ones are lost).  What tokens that a row does not see hold, be it
  * NaN, does not reach it.  Sequences whose cu_q / kv_len disagree with the host
  * bounds (SV_DEV_BAD_LENGTH) or whose tokens pass the table (SV_DEV_CAPACITY) are

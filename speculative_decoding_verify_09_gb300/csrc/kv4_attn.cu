@@ -7,8 +7,9 @@
 // code becomes an f16 operand (one conversion and one product per two codes, and a
 // byte moved down for three of four conversions) that a matrix instruction of 8 rows
 // takes once.  E2M1 times E4M3 has six significant bits, so the operands are exact and
-// only q (to f16, exact for bf16 in its range), the weights (to f16: 2^-11, below the
-// output's 2^-8, or 2^-32 of the row's largest) and the fp32 sums are rounded.
+// only q (to f16: exact from 2^-17 on, and below that where it could show), the weights
+// (to f16: 2^-11, below the output's 2^-8, or 2^-32 of the row's largest) and the fp32
+// sums are rounded.
 //
 // Split: the tiles of 32 tokens of all (sequence, KV head, part of the rows) --
 // segments -- are one list, cut into equal runs, one per warp of a persistent grid
@@ -43,6 +44,7 @@
 // slowest warps and the joining.
 #include <algorithm>
 #include <cmath>
+#include <cstring>
 #include <type_traits>
 
 #include "kv4.inl"
@@ -99,6 +101,8 @@ struct Kv4AttnParams {
   int64_t num_rows, q_stride;
   float scale_log2;                                  // of a score, k_scale and log2 e in it
   float scale_inverse;                               // 1 / scale_log2
+  uint32_t scale_bits;                               // (SCALED) the same as an fp32 in [1, 2) and the power of
+  int scale_power;                                   // two that it is multiplied by
   const int32_t *cu_q, *kv_len;
   const uint16_t *q;
   uint16_t *out;
@@ -172,7 +176,9 @@ struct __align__(16) Piece {
   int rows, first_row, r0, h;                        // its rows: packed rows of a block at r0, KV head
 };
 
-template <int D, int NB>
+// SCALED: a row and head of q whose largest element is below 2^15 is multiplied by the power of two that
+// brings it there, on its way into f16, and its scores' scale is divided by that.
+template <int D, int NB, bool SCALED>
 __global__ void __launch_bounds__(Shape<D, NB>::kThreads, 1) kv4_attn_kernel(const Kv4AttnParams P) {
   using Sh = Shape<D, NB>;
   constexpr int W = Sh::kWarps, S = Sh::kStages, NT = Sh::kThreads, ROWS = Sh::kRows;
@@ -436,6 +442,31 @@ __global__ void __launch_bounds__(Shape<D, NB>::kThreads, 1) kv4_attn_kernel(con
     v = end;
     if (tile1 <= tile0) continue;
 
+    // (SCALED) [ROWS] the scale of each column's scores; the place is the run's last piece's later
+    float *s_scale = reinterpret_cast<float *>(s_ml + (2 * w + 1) * ROWS);
+    if constexpr (SCALED) {
+      __syncwarp();
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) {
+        uint32_t top = 0;                              // the row's largest element, without its sign
+#pragma unroll
+        for (int x = 0; x < WORDS; ++x)
+          for (const uint32_t two : {q[nb][x].x, q[nb][x].y, q[nb][x].z, q[nb][x].w})
+            top = __vmaxu2(top, two & 0x7FFF7FFFu);
+        top = max(top & 0xFFFFu, top >> 16);
+        for (int d = 1; d < 4; d <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
+        const int power = min(126, max(0, 142 - static_cast<int>(top >> 7)));    // (infinities and NaN: 0)
+        const uint32_t f = (127 + power) * 0x800080u;
+#pragma unroll
+        for (int x = 0; x < WORDS; ++x)
+          for (uint32_t *two : {&q[nb][x].x, &q[nb][x].y, &q[nb][x].z, &q[nb][x].w}) *two = mul_bf16x2(*two, f);
+        // (a normal number: 0 or infinity times a masked score of -inf or a score of 0 were NaN)
+        if (c == 0)
+          s_scale[8 * nb + r] = __uint_as_float(
+              P.scale_bits + (static_cast<uint32_t>(min(max(P.scale_power - power, -126), 126)) << 23));
+      }
+      __syncwarp();
+    }
     uint32_t qf[NB][STEPS][2];
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb)
@@ -545,6 +576,15 @@ __global__ void __launch_bounds__(Shape<D, NB>::kThreads, 1) kv4_attn_kernel(con
         }
 
         // ---- weights
+        float scale[NC][2];                            // of this lane's columns
+#pragma unroll
+        for (int nb = 0; nb < NC; ++nb) {
+          scale[nb][0] = scale[nb][1] = P.scale_log2;
+          if constexpr (SCALED) {
+            const float2 two = *reinterpret_cast<const float2 *>(s_scale + 8 * nb + 2 * c);
+            scale[nb][0] = two.x, scale[nb][1] = two.y;
+          }
+        }
         if (edge) {
 #pragma unroll
           for (int sl = 0; sl < 2; ++sl) {
@@ -562,7 +602,7 @@ __global__ void __launch_bounds__(Shape<D, NB>::kThreads, 1) kv4_attn_kernel(con
 #pragma unroll
           for (int x = 0; x < 2; ++x)
             grows |= fmaxf(fmaxf(sc[0][nb][x], sc[0][nb][2 + x]), fmaxf(sc[1][nb][x], sc[1][nb][2 + x])) *
-                         P.scale_log2 > m[nb][x] + kLate;
+                         scale[nb][x] > m[nb][x] + kLate;
         if (__any_sync(0xffffffffu, grows)) {
           far = false;
 #pragma unroll
@@ -572,7 +612,7 @@ __global__ void __launch_bounds__(Shape<D, NB>::kThreads, 1) kv4_attn_kernel(con
               float top = fmaxf(fmaxf(sc[0][nb][x], sc[0][nb][2 + x]), fmaxf(sc[1][nb][x], sc[1][nb][2 + x]));
 #pragma unroll
               for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-              const float now = fmaxf(m[nb][x], top * P.scale_log2);
+              const float now = fmaxf(m[nb][x], top * scale[nb][x]);
               const float f = now == -INFINITY ? 1.0f : fast_exp2(m[nb][x] - now);
               m[nb][x] = now;
               mu[nb][x] = now == -INFINITY ? 0.0f : now - kUp;
@@ -591,10 +631,11 @@ __global__ void __launch_bounds__(Shape<D, NB>::kThreads, 1) kv4_attn_kernel(con
 #pragma unroll
               for (int x = 0; x < 2; ++x) {
                 const float top = m[nb][x] == -INFINITY ? 0.0f : m[nb][x];
+                const float inverse = SCALED ? 1.0f / scale[nb][x] : P.scale_inverse;
 #pragma unroll
                 for (int y = 0; y < 4; ++y) {
                   float &s = sc[y >> 1][nb][2 * (y & 1) + x];
-                  s = __fmul_rn(__fsub_rn(__fmul_rn(s, P.scale_log2), top), P.scale_inverse);
+                  s = __fmul_rn(__fsub_rn(__fmul_rn(s, scale[nb][x]), top), inverse);
                 }
                 mu[nb][x] = -kUp;
               }
@@ -608,7 +649,7 @@ __global__ void __launch_bounds__(Shape<D, NB>::kThreads, 1) kv4_attn_kernel(con
             float e[4];
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
-              e[x] = fast_exp2(fmaf(sc[sl][nb][x], P.scale_log2, -mu[nb][x & 1]));
+              e[x] = fast_exp2(fmaf(sc[sl][nb][x], scale[nb][x & 1], -mu[nb][x & 1]));
               sum[nb][x & 1] += e[x];
             }
             pf[sl][nb][0] = movmatrix_trans(pack_f16x2(e[0], e[1]));
@@ -873,17 +914,18 @@ Plan plan_of(const sv_kv4_attn_args &a) {
   return p;
 }
 
-template <int D, int NB>
+template <int D, int NB, bool SCALED>
 cudaError_t launch_shape(const Kv4AttnParams &P, int ctas, cudaStream_t s) {
   using Sh = Shape<D, NB>;
   static SharedLimit limit(Sh::bytes(kMaxBatch));
-  return launch_after_previous(kv4_attn_kernel<D, NB>, limit, dim3(ctas), Sh::kThreads, Sh::bytes(P.batch), s, P);
+  return launch_after_previous(kv4_attn_kernel<D, NB, SCALED>, limit, dim3(ctas), Sh::kThreads, Sh::bytes(P.batch),
+                               s, P);
 }
-template <int D>
+template <int D, bool SCALED>
 cudaError_t launch_rows(int nb, const Kv4AttnParams &P, int ctas, cudaStream_t s) {
-  return nb == 1   ? launch_shape<D, 1>(P, ctas, s)
-         : nb == 2 ? launch_shape<D, 2>(P, ctas, s)
-                   : launch_shape<D, 3>(P, ctas, s);
+  return nb == 1   ? launch_shape<D, 1, SCALED>(P, ctas, s)
+         : nb == 2 ? launch_shape<D, 2, SCALED>(P, ctas, s)
+                   : launch_shape<D, 3, SCALED>(P, ctas, s);
 }
 
 sv_status check_attn4(const sv_kv4_attn_args *a, bool tensors) {
@@ -969,9 +1011,20 @@ SV_API sv_status spec_kv4_attn(const sv_kv4_attn_args *a, void *ws, size_t ws_by
   P.num_rows = a->num_rows;
   P.q_stride = a->q_stride ? a->q_stride : static_cast<int64_t>(P.Hq) * a->cache.head_dim;
   const double scale = a->scale != 0.0f ? a->scale : 1.0 / std::sqrt(static_cast<double>(a->cache.head_dim));
+  const double all = scale * P.cache.k_scale * 1.4426950408889634;
+  // An element of q below 2^-17 is off by up to 2^-25 in f16: by D scale k_scale 2^-25 of a row's largest
+  // code * scale in a score, all of them together.  From here on its row is scaled (four sequences of
+  // 128k tokens 105.5 us against 104.4, ragged verify rows 60.3 against 58.9).
+  const bool scaled = scale * P.cache.k_scale * a->cache.head_dim > 16.0;
   // (kept a normal number: 0 or infinity times a masked score of -inf or a score of 0 were NaN)
-  P.scale_log2 = static_cast<float>(std::min(std::max(scale * P.cache.k_scale * 1.4426950408889634, 0x1p-126), 0x1p127));
+  P.scale_log2 = static_cast<float>(std::min(std::max(all, 0x1p-126), 0x1p127));
   P.scale_inverse = 1.0f / P.scale_log2;
+  if (scaled) {
+    const int power = std::ilogb(all);
+    const float one = static_cast<float>(std::ldexp(all, -power));
+    P.scale_power = power;                           // (one may be 2: its bits add up all the same)
+    std::memcpy(&P.scale_bits, &one, sizeof one);
+  }
   P.cu_q = a->cu_q;
   P.kv_len = a->kv_len;
   P.q = static_cast<const uint16_t *>(a->q);
@@ -984,8 +1037,9 @@ SV_API sv_status spec_kv4_attn(const sv_kv4_attn_args *a, void *ws, size_t ws_by
   P.spin_limit = limit ? limit : 1u << 22;
   const int ctas = std::min(sms, kMaxCtas);
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = a->cache.head_dim == 128 ? launch_rows<128>(p.nb, P, ctas, s)
-                                                  : launch_rows<64>(p.nb, P, ctas, s);
+  const cudaError_t e = a->cache.head_dim == 128
+                            ? scaled ? launch_rows<128, true>(p.nb, P, ctas, s) : launch_rows<128, false>(p.nb, P, ctas, s)
+                        : scaled ? launch_rows<64, true>(p.nb, P, ctas, s) : launch_rows<64, false>(p.nb, P, ctas, s);
   if (e != cudaSuccess) return record_error(SV_ERR_CUDA, "%s launch: %s", who, cudaGetErrorString(e));
   return SV_OK;
 }

@@ -8,7 +8,7 @@ import torch
 
 import oracle
 from gpu_util import dev, host_bits
-from test_gpu_kv4 import Attn
+from test_gpu_kv4 import Attn, close
 
 pytestmark = pytest.mark.gpu
 
@@ -80,3 +80,53 @@ def test_one_heavy_token_and_many_light_ones(api, g, D, power):
     want = light / (1.0 + light)
     got = oracle.to_f64(host_bits(out))
     assert np.all(np.abs(got - want) <= 2.0 ** -8 * want + 2.0 ** -10), (got.min(), got.max(), want)
+
+
+@pytest.mark.parametrize("Hq,Hkv,rows", [(2, 2, 1), (12, 1, 1), (20, 1, 1), (4, 1, 5)])
+@pytest.mark.parametrize("power", [-14, -20, -25, -30, -60, -126])
+def test_queries_of_small_magnitude(api, Hq, Hkv, rows, power):
+    """q times 2^power with a scale of 2^-power (in two factors where fp32 has no such one): the same
+    exact scores, and the same tolerance, as of q itself."""
+    c = Attn(api, [300, 33], [rows, rows], Hq, Hkv, 128, 16, seed=rows)
+    small = dict(scale=2.0 ** min(-power, 100) / 12)
+    c.q *= 2.0 ** power
+    if power < -100:
+        c.cache.k_scale = 0.5 * 2.0 ** (-power - 100)
+    c.run(**small)
+    close(c.out, c.q.contiguous(), c.pages, c.table, 16, c.cu, c.kv_len, small["scale"],
+          (c.cache.k_scale, 0.25))
+    assert int(c.status.item()) == 0
+
+
+def test_rows_and_heads_of_different_magnitude(api):
+    """Each row and head by itself: neighbours of other magnitudes, zeros among them, change no bit."""
+    c = Attn(api, [300], [3], 8, 2, 128, 16)
+    c.q *= 2.0 ** -30
+    c.run(scale=2.0 ** 30 / 12)
+    want = c.out.clone()
+    c.check(scale=2.0 ** 30 / 12)
+    keep = [(0, 1), (1, 4), (2, 7)]
+    other = torch.ones(3, 8, dtype=torch.bool)
+    for r, h in keep:
+        other[r, h] = False
+    c.q[other.cuda()] *= 2.0 ** 20
+    c.q[1, 0], c.q[2, 5] = 0, float("inf")
+    c.run(scale=2.0 ** 30 / 12)
+    for r, h in keep:
+        assert torch.equal(c.out[r, h], want[r, h])
+    assert bool(c.out[1, 0].isfinite().all()) and not bool(c.out[2, 5].isfinite().any())
+
+
+def test_elements_of_different_magnitude(api):
+    """Elements of a row down to 2^-31 of its largest keep their bits: the largest meets zeros of K alone."""
+    D, page, n = 64, 16, 48
+    c = Attn(api, [n - 1], [1], 1, 1, D, page)
+    for t in range(n):
+        codes, scales = (x[-1].copy() for x in oracle.kv4_load(c.pages, c.table, page, 0, t + 1, 0, 0))
+        codes[:8] = 0
+        oracle.kv4_store(c.pages, c.table, page, 0, t, 0, 0, codes, scales)
+    c.cache.pages.copy_(dev(c.pages))
+    c.q *= 2.0 ** -16
+    c.q[..., :8] = 1.49 * 2.0 ** 13
+    c.run(scale=2.0 ** 13)
+    c.check(scale=2.0 ** 13)
