@@ -95,8 +95,8 @@ SV_API sv_status spec_norm_rope_rows(const sv_norm_rope_args *args, void *stream
  * quantized: with f the tensor's scale and m the largest magnitude of 16
  * elements,
  *   s = e4m3(m / (6 f)),   c = e2m1(x / (s f)),
- * both rounded to nearest even and saturating; where s is 0 the codes are 0.  16
- * elements with a NaN among them get a scale of NaN.  q goes to q_out as in
+ * both rounded to nearest even and saturating, of fp32 quotients; where s is 0 the
+ * codes are 0.  16 elements with a NaN among them get a scale of NaN.  q goes to q_out as in
  * spec_norm_rope_rows (num_q_heads 0: none). */
 typedef struct sv_kv4_append_args {
   sv_rope_args rows;        /* q, k, v, q_out, positions by cu_q and kv_len (positions

@@ -128,7 +128,6 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   asm("max.NaN.f32 %0, %1, %2;\n" : "=f"(r) : "f"(a), "f"(b));
   return r;
 }
-
 // Host: checks of sv_kv4_cache in the name of entry point `who`, and its view.
 sv_status check_cache(const sv_kv4_cache *c, const char *who);
 Kv4View view_of(const sv_kv4_cache &c);

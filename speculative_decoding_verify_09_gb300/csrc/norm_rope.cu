@@ -47,7 +47,7 @@ struct NormRopeParams {
   int64_t num_rows, slots;
   int64_t q_stride, k_stride, v_stride;
   float mscale, k_scale, v_scale, k_inverse, v_inverse;
-  float k_sixth, v_sixth;                            // 1 / (6 scale)
+  float2 k_sixth, v_sixth;                           // 1 / (6 scale): rounded down, and the rest
   float eps, weight_offset, inverse_D;
   const float *q_weight, *k_weight;
   const uint64_t *turns;
@@ -113,12 +113,13 @@ __device__ __forceinline__ F2 f2_fma(F2 a, F2 b, F2 c) {
   return r;
 }
 
-// Scale of 16 elements whose largest magnitude is m, times_sixth being 1 / (6 factor);
-// unit = scale * factor is what a code of 1 stands for.  (With a factor that is a power
-// of two the product meets the ties of two scales: 1 / 3 in fp32 is off by 2^-25, less
-// than half a step of any tie, which has five significant bits.)
-__device__ __forceinline__ uint32_t scale_code(float m, float times_sixth, float factor, float &unit) {
-  const uint32_t s = e4m3x2_of(__fmul_rn(m, times_sixth), 0.0f) & 0xFFu;
+// Scale of 16 elements whose largest magnitude is m: the E4M3 of m / (6 factor), and unit = scale *
+// factor, what a code of 1 stands for.  The quotient is m times 1 / (6 factor) in two parts, which
+// rounds it to fp32 as a division would: by one part it is off by a step, and then meets a tie of
+// two scales that the quotient misses, or the other way round.  (Both parts are positive, so that an
+// infinite m stays infinite.)
+__device__ __forceinline__ uint32_t scale_code(float m, float2 sixth, float factor, float &unit) {
+  const uint32_t s = e4m3x2_of(__fmaf_rn(m, sixth.x, __fmul_rn(m, sixth.y)), 0.0f) & 0xFFu;
   unit = __fmul_rn(e4m3_to_f32(s), factor);
   return s;
 }
@@ -379,7 +380,7 @@ __global__ void __launch_bounds__(kNT, kCtas<T, OUT, LAYOUT>) norm_rope_kernel(c
     const bool normed = kind == 0 ? P.q_weight != nullptr : kind == 1 && P.k_weight != nullptr;
     const bool changed = turns || normed;
     const float factor = kind == 1 ? P.k_scale : P.v_scale, inverse = kind == 1 ? P.k_inverse : P.v_inverse;
-    const float sixth = kind == 1 ? P.k_sixth : P.v_sixth;
+    const float2 sixth = kind == 1 ? P.k_sixth : P.v_sixth;
     const float4 *w4 = reinterpret_cast<const float4 *>(s_weight + (is_q ? 0 : 16 * lanes)) + 2 * c;
     const int64_t out = is_q ? row * P.Hq * P.D : row * P.Hkv * P.D;
     T *to = static_cast<T *>(is_q ? P.q_out : kind == 1 ? P.k_out : P.v_out) + out + (begin + hl) * P.D;
@@ -688,6 +689,13 @@ float exact_inverse(float x) {                       // 1 / x where x is a power
   return std::frexp(x, &e) == 0.5f && std::isnormal(inv) ? inv : 0.0f;
 }
 
+float2 sixth_of(float x) {                           // 1 / (6 x), x > 0, as two positive numbers
+  const double all = 1.0 / (6.0 * static_cast<double>(x));
+  float down = static_cast<float>(all);
+  if (down >= all) down = std::nextafter(down, 0.0f);
+  return make_float2(down, static_cast<float>(all - down));
+}
+
 // f16x2 of `x` if it is a power of two in [2^-5, 2^5], else 0.  A scale (2^-9 .. 448, four
 // significant bits) times such an x is exact in f16, and so is that times a code: six bits
 // from 2^-15 on, or beyond f16's range where E4M3 saturates all the same.
@@ -782,8 +790,8 @@ sv_status run_rows(const sv_rope_args &a, const sv_norm_args &n, const sv_kv4_ca
   }
   P.k_inverse = exact_inverse(P.k_scale);
   P.v_inverse = exact_inverse(P.v_scale);
-  P.k_sixth = static_cast<float>(1.0 / (6.0 * P.k_scale));
-  P.v_sixth = static_cast<float>(1.0 / (6.0 * P.v_scale));
+  P.k_sixth = sixth_of(P.k_scale);
+  P.v_sixth = sixth_of(P.v_scale);
   if (P.num_rows == 0 || P.slots == 0 || P.heads == 0) return SV_OK;
   const int sms = device_sms();
   if (sms <= 0) return record_error(SV_ERR_CUDA, "%s: no current CUDA device", who);
