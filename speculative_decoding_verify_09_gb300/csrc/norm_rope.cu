@@ -23,6 +23,7 @@
 #include <cmath>
 
 #include "kv4.inl"
+#include "kv4_quotient.inl"
 #include "ops_host.inl"
 #include "rows.inl"
 
@@ -123,22 +124,26 @@ __device__ __forceinline__ uint32_t scale_code(float m, float2 sixth, float fact
   unit = __fmul_rn(e4m3_to_f32(s), factor);
   return s;
 }
-// Codes of x / unit.  The quotient by the reciprocal and one correction with the exact
-// remainder: where it is a tie of two codes (x = t unit) the remainder is exact too, so
-// it is met exactly.  A saturated scale (or NaN) may come with quotients that overflow:
-// these are divided.
+struct One {
+  typedef float T;
+  static __device__ __forceinline__ float fma(float a, float b, float c) { return __fmaf_rn(a, b, c); }
+};
+struct Two {
+  typedef F2 T;
+  static __device__ __forceinline__ F2 mul(F2 a, F2 b) { return f2_mul(a, b); }
+  static __device__ __forceinline__ F2 fma(F2 a, F2 b, F2 c) { return f2_fma(a, b, c); }
+};
+// Codes of x / unit.  A saturated scale (or NaN) may come with quotients that overflow: these are
+// divided.
 __device__ __forceinline__ uint32_t codes_of(const F2 (&x)[4], float unit, uint32_t scale) {
   float y[8];
   if (scale - 1u < 0x7Du) {
-    float inv;
-    asm("rcp.approx.ftz.f32 %0, %1;\n" : "=f"(inv) : "f"(unit));
-    inv = fmaf(fmaf(-unit, inv, 1.0f), inv, inv);
+    float near;
+    asm("rcp.approx.ftz.f32 %0, %1;\n" : "=f"(near) : "f"(unit));
+    const float inv = refined_reciprocal<One>(-unit, near, 1.0f);
     const F2 inv2 = f2(inv, inv), neg = f2(-unit, -unit);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const F2 q = f2_mul(x[i], inv2);
-      f2_get(f2_fma(f2_fma(q, neg, x[i]), inv2, q), y[2 * i], y[2 * i + 1]);
-    }
+    for (int i = 0; i < 4; ++i) f2_get(corrected_quotient<Two>(x[i], neg, inv2), y[2 * i], y[2 * i + 1]);
   } else {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
