@@ -273,6 +273,8 @@ def _launch(fn, args, stream, ws=None):
     device = args._device
     if torch._C._cuda_getDevice() != device:
         raise ValueError(f"tensors are on cuda:{device}, not on the current device")
+    if ws is not None and ws.buf.device.index != device:
+        raise ValueError(f"tensors are on cuda:{device}, the workspace on {ws.buf.device}")
     if stream is None:
         raw = torch._C._cuda_getCurrentRawStream(device)
     elif stream.device_index != device:
@@ -633,6 +635,8 @@ def kv4_attn_args(cache, table, cu_q, kv_len, q, out, *, max_q_rows, scale=0.0, 
 def kv4_workspace(args, stream=None):
     """A zeroed Workspace for spec_kv4_attn with these argument shapes; calls that follow one another
     on a stream may share one that is large enough for each."""
+    if torch._C._cuda_getDevice() != args._device:
+        raise ValueError(f"tensors are on cuda:{args._device}, not on the current device")
     n = lib.sv_kv4_workspace_bytes(ctypes.byref(args))
     if n == 0:
         _check(1)
