@@ -93,7 +93,7 @@ struct Shape {
 
 struct Kv4AttnParams {
   Kv4View cache;
-  int batch, Hq, g, max_q_rows, parts;               // parts: of max_q_rows * g rows
+  int batch, Hq, g, max_q_rows;                      // g: query heads of a KV head
   int slab_shift;                                    // log2 of a page's slabs, or -1
   int weighted;                                      // costs of tiles by their columns (NB > 1)
   uint32_t g_inverse;                                // 2^32 / g rounded up: exact quotients of rows
@@ -1004,7 +1004,6 @@ SV_API sv_status spec_kv4_attn(const sv_kv4_attn_args *a, void *ws, size_t ws_by
     if (P.cache.slabs == 1 << x) P.slab_shift = x;
   P.g_inverse = P.g == 1 ? 0 : static_cast<uint32_t>(((uint64_t{1} << 32) + P.g - 1) / P.g);
   P.max_q_rows = a->max_q_rows;
-  P.parts = p.parts;
   const int64_t units = static_cast<int64_t>(P.batch) * P.cache.heads * p.parts,
                 tiles = (static_cast<int64_t>(P.cache.max_pages) * P.cache.page_size + kTile - 1) / kTile;
   P.weighted = units * ((3 + 2 * p.nb) * tiles + 6 * kHead) < (int64_t{1} << 32);
