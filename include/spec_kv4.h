@@ -80,8 +80,8 @@ typedef struct sv_norm_args {
 /* spec_rope_rows (whose contract holds for all else) with norms in front of the
  * rotation.  rope.turns may be NULL: norms only (rot_dim is then ignored, cu_q
  * and kv_len, or positions, still say which rows there are).  All arithmetic in
- * fp32, rounded once to the output type; sums of squares in fp32.  A row of
- * zeros with eps 0 is NaN.  Weights 4-byte aligned. */
+ * fp32, rounded once to the output type; sums of squares in fp32 (a head whose sum
+ * passes fp32's range comes out as zeros).  A row of zeros with eps 0 is NaN.  Weights 4-byte aligned. */
 typedef struct sv_norm_rope_args {
   sv_rope_args rope;
   sv_norm_args norm;
@@ -110,7 +110,8 @@ typedef struct sv_kv4_append_args {
 /* A sequence whose cu_q / kv_len disagree with the host bounds is left unwritten
  * with SV_DEV_BAD_LENGTH, rows behind the table's last page with
  * SV_DEV_CAPACITY and rows whose page is outside [0, num_pages) with
- * SV_DEV_BAD_PARAM are not stored (their q_out is written).  Two sequences may not
+ * SV_DEV_BAD_PARAM are not stored (their q_out is written).  Where cu_q does not
+ * ascend, rows of other sequences may be left unwritten too.  Two sequences may not
  * append to the same page's same tokens. */
 SV_API sv_status spec_kv4_append(const sv_kv4_append_args *args, void *stream);
 

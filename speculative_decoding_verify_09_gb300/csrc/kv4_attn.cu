@@ -27,12 +27,14 @@
 // elements in a product is free: a lane takes 16 bytes in a row of a token's K (32
 // elements) and the same elements of q; of V, 8 bytes in a row of four tokens'
 // elements.  The weights' running maximum is kept within 2^8 of the true one, so
-// the sums are rescaled seldom; its token's weight is 2^7, which uses f16's range.  The 5th-generation tensor path would want the
-// operands in shared memory, i.e. 2 x 512 bytes written and read per token and head
-// next to 144 from memory: as long as the register-fed products of 40 rows take.
+// the sums are rescaled seldom; its token's weight is 2^7, which uses f16's range.
+// The 5th-generation tensor path is not used: single rows gain nothing by it, since the
+// conversions stay.  Blocks of more than 8 rows would: 1024 bytes of f16 operands
+// written to shared memory and read per token and head are 8 clocks (half with K in tensor
+// memory) beside 4.2 of conversions done once, against 17.8 that the ragged rows below take.
 //
 // Bounds, D = 128, 8 KV heads, device time per call: 4 sequences of 128k tokens,
-// single rows, 104 us = 5.8 TB/s (0.86 of the measured copy rate), 614 instructions a
+// single rows, 104 us = 5.8 TB/s (0.85 of the measured copy rate), 614 instructions a
 // tile of 32 tokens issued at 2.6 of 4 per clock, the ALU pipe (conversions, byte
 // moves) at 0.46; 16 and 24 rows take 151 and 208 us, 67 instructions more a tile for
 // each 8 rows but 12 and 8 warps, and fewer registers free to overlap in.  Blocks of
