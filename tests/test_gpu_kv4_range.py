@@ -20,6 +20,30 @@ def api():
     return pkg.load()
 
 
+def check_heaviest(c, scale):
+    """Rows whose scores tell their largest one from all others have its V; how many do."""
+    Hq, Hkv = c.q.shape[1], c.pages.shape[1]
+    got, q = oracle.to_f64(host_bits(c.out)), oracle.to_f64(host_bits(c.q.contiguous()))
+    seen, g = 0, Hq // Hkv
+    for i in range(2):
+        for r in range(c.cu[i], c.cu[i + 1]):
+            n = int(c.kv_len[i]) + r - int(c.cu[i]) + 1
+            for h in range(Hq):
+                if np.abs(q[r, h]).max() > 65504:      # (infinite in f16: 2^14 times 4 and more)
+                    assert not np.isfinite(got[r, h]).any()
+                    continue
+                K, V = (oracle.kv4_values(*oracle.kv4_load(c.pages, c.table, 16, i, n, h // g, w), f)
+                        for w, f in ((0, 0.5), (1, 0.25)))
+                s = K @ q[r, h]
+                order = np.argsort(s)
+                gap, unsure = s[order[-1]] - s[order[-2]], (np.abs(K) @ np.abs(q[r, h])).max() * 272 * 2.0 ** -24
+                if gap > 2 * unsure and (gap - unsure) * scale > 90:
+                    assert np.array_equal(got[r, h], V[order[-1]]), (r, h)
+                    seen += 1
+                assert np.isfinite(got[r, h]).all()
+    return seen
+
+
 @pytest.mark.parametrize("Hq,Hkv,rows", [(2, 2, 1), (12, 1, 1), (20, 1, 1), (4, 1, 5)])
 @pytest.mark.parametrize("power", [12, 18, 21, 23, 25, 27, 30, 45, 90])
 def test_scores_far_beyond_exps_range(api, Hq, Hkv, rows, power):
@@ -31,22 +55,22 @@ def test_scores_far_beyond_exps_range(api, Hq, Hkv, rows, power):
     c = Attn(api, [700, 33], [rows, rows], Hq, Hkv, 128, 16, seed=power)
     scale = 2.0 ** power / 30
     c.run(scale=scale)
-    got, q = oracle.to_f64(host_bits(c.out)), oracle.to_f64(host_bits(c.q.contiguous()))
-    seen, g = 0, Hq // Hkv
-    for i in range(2):
-        for r in range(c.cu[i], c.cu[i + 1]):
-            n = int(c.kv_len[i]) + r - int(c.cu[i]) + 1
-            for h in range(Hq):
-                K, V = (oracle.kv4_values(*oracle.kv4_load(c.pages, c.table, 16, i, n, h // g, w), f)
-                        for w, f in ((0, 0.5), (1, 0.25)))
-                s = K @ q[r, h]
-                order = np.argsort(s)
-                gap, unsure = s[order[-1]] - s[order[-2]], (np.abs(K) @ np.abs(q[r, h])).max() * 272 * 2.0 ** -24
-                if gap > 2 * unsure and (gap - unsure) * scale > 90:
-                    assert np.array_equal(got[r, h], V[order[-1]]), (r, h)
-                    seen += 1
-                assert np.isfinite(got[r, h]).all()
+    seen = check_heaviest(c, scale)
     assert seen >= rows * Hq or power < 18
+
+
+@pytest.mark.parametrize("Hq,Hkv,rows", [(2, 2, 1), (12, 1, 1), (20, 1, 1), (4, 1, 5)])
+@pytest.mark.parametrize("power", [6, 10, 12, 14])
+def test_far_scores_of_large_queries_and_keys(api, Hq, Hkv, rows, power):
+    """The same with an ordinary scale: scores of up to 2^power 2^8 30 / 11.3."""
+    c = Attn(api, [700, 33], [rows, rows], Hq, Hkv, 128, 16, seed=power)
+    scales = c.pages[..., 8 * 128:9 * 128]
+    scales[scales != 0xFF] += 64                                    # (0.01 .. 1.7 before: 2^8 times)
+    assert int(scales[scales != 0xFF].max()) < 0x7F
+    c.cache.pages.copy_(dev(c.pages))
+    c.q *= 2.0 ** power
+    c.run()
+    assert check_heaviest(c, 1 / np.sqrt(128)) >= rows * Hq
 
 
 @pytest.mark.parametrize("g", [1, 12, 20])                 # one, two and three columns of 8 rows
